@@ -71,6 +71,8 @@ extern "C" {
 #define LINEAR_E_CAPTURE  9  /* the first activation epilogue on a device was called under stream capture */
 #define LINEAR_E_WORKSPACE 10 /* indexed contraction: workspace misaligned or below linear_indexed_workspace_bytes */
 #define LINEAR_E_SCRATCH  11  /* linear_f16_indexed_noalloc: the call needs more than LINEAR_NOALLOC_SCRATCH_BYTES */
+#define LINEAR_E_VALUE    12  /* unknown activation or tensor type, or a negative or NaN max_norm */
+#define LINEAR_E_MEMORY   13  /* linear_grad_clip: no host memory for the overlap check */
 
 /*
  * Path selectors for linear_f16_ex / linear_f16_plan.  The path and the tile are
@@ -354,6 +356,178 @@ int32_t linear_f16_indexed_noalloc(const uint16_t* x, int64_t ldx,
                                    uint16_t* y, int64_t ldy,
                                    int64_t E, int64_t M, int64_t N, int64_t K,
                                    void* stream);
+
+/*
+ * The gated feed-forward block: both projections, the activation and the product
+ * ("Tracing a Model", the gated feed-forward section), in one kernel:
+ *
+ *     g[m, n] = sum_k x[m, k] * wg[n, k]        u[m, n] = sum_k x[m, k] * wu[n, k]
+ *     h[m, n] = RNE_E( act(g[m, n]) * u[m, n] )
+ *
+ * act: LINEAR_EPI_SILU, LINEAR_EPI_GELU_TANH or LINEAR_EPI_GELU_ERF (any other
+ * code is LINEAR_E_VALUE).  The sums are FP32; the activation and the product are
+ * taken in FP32 on the unrounded sums and rounded once (unlike an epilogue
+ * program, whose every primitive rounds to E).  exp, erfc and the reciprocal are
+ * FP32 approximations within a few FP32 ulps.
+ *
+ * x: [M, K]; wg, wu: [N, K] each with its own row stride (the two halves of one
+ * [2N, K] weight are wg = w, wu = w + N * ldw).  h: [M, N].  gate and up: [M, N]
+ * or NULL; where given, RNE_E(g) and RNE_E(u) are stored there for the backward
+ * call.  Outputs may not overlap the inputs or each other (LINEAR_E_ALIAS).
+ * M == 0 or N == 0 is a no-op; K == 0 gives +0 (act(0) * 0).  M, N and K of this
+ * and the gradients' calls are at most 2^31 - 65536, row strides below 2^31.
+ */
+int32_t linear_f16_gated(const uint16_t* x, int64_t ldx,
+                         const uint16_t* wg, int64_t ldwg,
+                         const uint16_t* wu, int64_t ldwu,
+                         int32_t act,
+                         uint16_t* h, int64_t ldh,
+                         uint16_t* gate, int64_t ldgate,
+                         uint16_t* up, int64_t ldup,
+                         int64_t M, int64_t N, int64_t K, void* stream);
+int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
+                          const uint16_t* wg, int64_t ldwg,
+                          const uint16_t* wu, int64_t ldwu,
+                          int32_t act,
+                          uint16_t* h, int64_t ldh,
+                          uint16_t* gate, int64_t ldgate,
+                          uint16_t* up, int64_t ldup,
+                          int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * The gated block's gradients, from dh [M, N] and the projections gate and up
+ * [M, N] that the forward call stored:
+ *
+ *     dg = RNE_E( dh * u * act'(g) )     du = RNE_E( dh * act(g) )      (FP32 inside)
+ *     dx[m, k]  = RNE_E( sum_n dg[m, n] * wg[n, k] + du[m, n] * wu[n, k] )
+ *     dwg[n, k] = RNE_E( sum_m dg[m, n] * x[m, k] )      dwu likewise from du
+ *
+ * dg and du are rounded to E because they are the matrix unit's operands; a
+ * binary16 gradient past 65504 becomes infinite there.  dx may be NULL (not
+ * wanted; the weights are then not read), and dwg and dwu may both be NULL (x is
+ * then not read); one of the two groups must be given.  N == 0 gives dx = +0,
+ * M == 0 gives dwg = dwu = +0.
+ *
+ * workspace: linear_gated_workspace_bytes(M, N, K) bytes of device memory (it
+ * holds dg and du), 16-byte aligned, owned by the caller, overwritten, free again
+ * once the call's work on `stream` has finished; two calls in flight at once
+ * need two workspaces.  It may not overlap any other argument.
+ */
+int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int32_t linear_f16_gated_backward(const uint16_t* dh, int64_t lddh,
+                                  const uint16_t* x, int64_t ldx,
+                                  const uint16_t* wg, int64_t ldwg,
+                                  const uint16_t* wu, int64_t ldwu,
+                                  const uint16_t* gate, int64_t ldgate,
+                                  const uint16_t* up, int64_t ldup,
+                                  int32_t act,
+                                  uint16_t* dx, int64_t lddx,
+                                  uint16_t* dwg, int64_t lddwg,
+                                  uint16_t* dwu, int64_t lddwu,
+                                  int64_t M, int64_t N, int64_t K,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_gated_backward(const uint16_t* dh, int64_t lddh,
+                                   const uint16_t* x, int64_t ldx,
+                                   const uint16_t* wg, int64_t ldwg,
+                                   const uint16_t* wu, int64_t ldwu,
+                                   const uint16_t* gate, int64_t ldgate,
+                                   const uint16_t* up, int64_t ldup,
+                                   int32_t act,
+                                   uint16_t* dx, int64_t lddx,
+                                   uint16_t* dwg, int64_t lddwg,
+                                   uint16_t* dwu, int64_t lddwu,
+                                   int64_t M, int64_t N, int64_t K,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The layer's gradients, from dy [M, N]:
+ *
+ *     _backward_input:   dx[m, k] = RNE_E( sum_n dy[m, n] * weight[n, k] )
+ *     _backward_weight:  dw[n, k] = RNE_E( sum_m dy[m, n] * x[m, k] )
+ *                        db[n]    = RNE_E( sum_m dy[m, n] )         (db may be NULL)
+ *
+ * FP32 sums, rounded once; operands are read in place, no transposed copies.
+ * The projection's rounding and the bias addition's are taken as the identity,
+ * as usual for gradients.  The _f32out forms store the unrounded FP32 sums in dw
+ * and db (floats), or with accumulate != 0 add them to what dw and db hold
+ * (gradients summed over several batches).  N == 0 gives dx = +0; M == 0 gives
+ * dw = db = +0 (or leaves them, when accumulating).  Reruns are bit-identical.
+ *
+ * workspace: linear_backward_workspace_bytes(M, N, K) bytes of device memory for
+ * any of these calls, 16-byte aligned; ownership and overlaps as for the gated
+ * block's.
+ */
+int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int32_t linear_f16_backward_input(const uint16_t* dy, int64_t lddy,
+                                  const uint16_t* weight, int64_t ldw,
+                                  uint16_t* dx, int64_t lddx,
+                                  int64_t M, int64_t N, int64_t K,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_backward_input(const uint16_t* dy, int64_t lddy,
+                                   const uint16_t* weight, int64_t ldw,
+                                   uint16_t* dx, int64_t lddx,
+                                   int64_t M, int64_t N, int64_t K,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_f16_backward_weight(const uint16_t* dy, int64_t lddy,
+                                   const uint16_t* x, int64_t ldx,
+                                   uint16_t* dw, int64_t lddw, uint16_t* db,
+                                   int64_t M, int64_t N, int64_t K,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_backward_weight(const uint16_t* dy, int64_t lddy,
+                                    const uint16_t* x, int64_t ldx,
+                                    uint16_t* dw, int64_t lddw, uint16_t* db,
+                                    int64_t M, int64_t N, int64_t K,
+                                    void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_f16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
+                                          const uint16_t* x, int64_t ldx,
+                                          float* dw, int64_t lddw, float* db, int32_t accumulate,
+                                          int64_t M, int64_t N, int64_t K,
+                                          void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
+                                           const uint16_t* x, int64_t ldx,
+                                           float* dw, int64_t lddw, float* db, int32_t accumulate,
+                                           int64_t M, int64_t N, int64_t K,
+                                           void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The global norm of a set of gradients, and clipping by it.
+ *
+ *     linear_grad_norm:  norm[0] = FP32( sqrt( sum over all tensors and elements of g^2 ) )
+ *     linear_grad_clip:  out = RNE( g * s ),  s = min(1, max_norm / (norm[0] + 1e-6)) in FP32
+ *
+ * Squares are taken and summed in FP64 in a fixed order, so no finite gradient
+ * overflows and reruns are bit-identical.  A NaN norm makes every output NaN; an
+ * infinite one (an infinite gradient) makes s zero.  The two calls are apart so
+ * that a sharded caller can combine norms in between.
+ *
+ * Tensors are [rows, cols] with row stride ld (elements; a vector is one row, whose
+ * ld is not read), of any mix of types, any alignment; cols up to 2^46, rows and ld
+ * below 2^31.  The arrays of linear_tensor are host memory, read during the call.
+ * out == NULL clips in place; else out[i] has grads[i]'s shape and type and is
+ * grads[i] itself or overlaps no tensor of the call (LINEAR_E_ALIAS); a tensor
+ * listed twice may not be clipped in place.  norm is device memory.  count up to
+ * LINEAR_GRAD_MAX_TENSORS; count == 0 gives norm 0.  max_norm: not negative or NaN
+ * (LINEAR_E_VALUE).
+ *
+ * workspace of linear_grad_norm: linear_grad_workspace_bytes(count) bytes, 16-byte
+ * aligned, as above.
+ */
+#define LINEAR_TYPE_F16  0
+#define LINEAR_TYPE_BF16 1
+#define LINEAR_TYPE_F32  2
+#define LINEAR_GRAD_MAX_TENSORS 65536
+
+typedef struct linear_tensor {
+    void* data;
+    int64_t rows, cols, ld;
+    int64_t type;            /* LINEAR_TYPE_* */
+} linear_tensor;
+
+int64_t linear_grad_workspace_bytes(int64_t count);   /* -1 if out of range */
+int32_t linear_grad_norm(const linear_tensor* grads, int64_t count, float* norm,
+                         void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, int64_t count,
+                         const float* norm, float max_norm, void* stream);
 
 /* Which kernels a call would launch: the host-side plan of "The Graph IR" (op
  * table, MatMul row: GEMV versus GEMM chosen at plan time; section "Host-side

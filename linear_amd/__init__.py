@@ -1,8 +1,9 @@
 """MI355X (gfx950) FP16 linear layer: y = FP16(FP16(x @ weight.T) + b).
 
 Also its bfloat16 form, the unrounded FP32 sums, multi-step epilogue programs,
-and the grouped and indexed (per-row expert) contractions.  A thin ctypes
-binding over the C ABI of ``liblinear_amd.so`` (declared in
+the grouped and indexed (per-row expert) contractions, the gated feed-forward
+block with its gradients, the layer's gradients, and the global gradient norm
+with clipping.  A thin ctypes binding over the C ABI of ``liblinear_amd.so`` (declared in
 ``include/linear_amd.h``).  The functions carry the C entry points' names and
 only marshal arguments: every step of the computation runs in the library's
 HIP kernels.  PyTorch supplies device memory and the stream.  If the library
@@ -10,6 +11,8 @@ is missing the calls raise; there is no fallback.
 """
 from __future__ import annotations
 
+import array
+import contextlib
 import ctypes
 import os
 
@@ -30,6 +33,8 @@ LINEAR_E_EPILOGUE = 8
 LINEAR_E_CAPTURE = 9
 LINEAR_E_WORKSPACE = 10
 LINEAR_E_SCRATCH = 11
+LINEAR_E_VALUE = 12
+LINEAR_E_MEMORY = 13
 
 # scratch the no-allocation indexed call holds per GPU (include/linear_amd.h)
 NOALLOC_SCRATCH_BYTES = 1 << 20
@@ -54,6 +59,12 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_indexed_workspace_bytes",
                 "linear_f16_indexed", "linear_bf16_indexed", "linear_f16_indexed_f32out", "linear_bf16_indexed_f32out",
                 "linear_f16_indexed_noalloc",
+                "linear_f16_gated", "linear_bf16_gated", "linear_gated_workspace_bytes",
+                "linear_f16_gated_backward", "linear_bf16_gated_backward", "linear_backward_workspace_bytes",
+                "linear_f16_backward_input", "linear_bf16_backward_input",
+                "linear_f16_backward_weight", "linear_bf16_backward_weight",
+                "linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out",
+                "linear_grad_workspace_bytes", "linear_grad_norm", "linear_grad_clip",
                 "linear_f16_plan", "linear_status_string", "linear_last_hip_error")
 
 
@@ -129,6 +140,30 @@ def _lib():
     lib.linear_f16_indexed_noalloc.restype = i32
     lib.linear_indexed_workspace_bytes.argtypes = [i64, i64]
     lib.linear_indexed_workspace_bytes.restype = i64
+    for name in ("linear_f16_gated", "linear_bf16_gated"):
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
+        getattr(lib, name).restype = i32
+    for name in ("linear_f16_gated_backward", "linear_bf16_gated_backward"):
+        getattr(lib, name).argtypes = ([vp, i64] * 6 + [i32] + [vp, i64] * 3 + [i64, i64, i64, vp, i64, vp])
+        getattr(lib, name).restype = i32
+    for name in ("linear_f16_backward_input", "linear_bf16_backward_input"):
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp]
+        getattr(lib, name).restype = i32
+    for name in ("linear_f16_backward_weight", "linear_bf16_backward_weight"):
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, i64, vp, i64, vp]
+        getattr(lib, name).restype = i32
+    for name in ("linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out"):
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp]
+        getattr(lib, name).restype = i32
+    for name in ("linear_gated_workspace_bytes", "linear_backward_workspace_bytes"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = i64
+    lib.linear_grad_workspace_bytes.argtypes = [i64]
+    lib.linear_grad_workspace_bytes.restype = i64
+    lib.linear_grad_norm.argtypes = [vp, i64, vp, vp, i64, vp]
+    lib.linear_grad_norm.restype = i32
+    lib.linear_grad_clip.argtypes = [vp, vp, i64, vp, ctypes.c_float, vp]
+    lib.linear_grad_clip.restype = i32
     lib.linear_f16_plan.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, i32,
                                     ctypes.POINTER(_Plan)]
     lib.linear_f16_plan.restype = i32
@@ -480,6 +515,297 @@ def linear_f16_indexed_f32out(x, w, idx, out=None, stream=None, workspace=None):
 
 def linear_bf16_indexed_f32out(x, w, idx, out=None, stream=None, workspace=None):
     return _indexed_call(torch.bfloat16, x, w, idx, out, True, stream, workspace)
+
+
+def _on(stream, device):
+    """A context in which new tensors belong to the stream of the launch, so that their
+    memory is not reused by other work before the launch has run."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = int(getattr(stream, "cuda_stream", stream))
+        if handle == 0:
+            stream = torch.cuda.default_stream(device)
+        else:
+            stream = torch.cuda.ExternalStream(handle, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _operand(t, name, dtype, shape):
+    """Pointer and row stride of a tensor that must have this type and shape."""
+    if tuple(t.shape) != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    return _mat(t, name, dtype)
+
+
+def _output(t, name, dtype, shape, device):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    return (t, *_operand(t, name, dtype, shape))
+
+
+def _scratch(workspace, need, device):
+    """The call's workspace: the caller's uint8 tensor, or a new one."""
+    if need < 0:
+        raise ValueError("shapes out of range")
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or workspace.numel() < need or (
+            workspace.numel() > 1 and workspace.stride(0) != 1):
+        raise ValueError("workspace must be a contiguous uint8 tensor of at least %d bytes" % need)
+    return workspace
+
+
+def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
+    if x.dim() != 2 or wg.dim() != 2:
+        raise ValueError("x must be [M, K] and wg, wu [N, K]")
+    M, K = x.shape
+    N = wg.shape[0]
+    xp, ldx = _mat(x, "x", dtype)
+    gp, ldg = _operand(wg, "wg", dtype, (N, K))
+    up_, ldu = _operand(wu, "wu", dtype, (N, K))
+    handle = _stream_handle(stream, x, wg, wu, out, gate, up)
+    with _on(stream, x.device):
+        out, hp, ldh = _output(out, "out", dtype, (M, N), x.device)
+        kept = []
+        for name, t in (("gate", gate), ("up", up)):
+            kept += _output(t, name, dtype, (M, N), x.device) if keep or t is not None else (None, None, 0)
+    name = "linear_%s_gated" % tag
+    rc = getattr(_lib(), name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K,
+                               handle)
+    _check(rc, name)
+    return (out, kept[0], kept[3]) if keep else out
+
+
+def linear_f16_gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: int = EPI_SILU, keep: bool = False,
+                     out=None, gate=None, up=None, stream=None):
+    """h = act(x @ wg.T) * (x @ wu.T) in one kernel, rounded once to binary16 (x [M, K], wg and wu
+    [N, K]; act EPI_SILU, EPI_GELU_TANH or EPI_GELU_ERF).  keep: also return the two rounded
+    projections, which the backward call takes: (h, gate, up).  out, gate, up: tensors to write."""
+    return _gated_call("f16", torch.float16, x, wg, wu, act, keep, out, gate, up, stream)
+
+
+def linear_bf16_gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: int = EPI_SILU, keep: bool = False,
+                      out=None, gate=None, up=None, stream=None):
+    """linear_f16_gated on bfloat16 operands and outputs."""
+    return _gated_call("bf16", torch.bfloat16, x, wg, wu, act, keep, out, gate, up, stream)
+
+
+def gated_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of device workspace a gated backward call needs."""
+    n = _lib().linear_gated_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
+    return n
+
+
+def _gated_backward_call(tag, dtype, dh, x, wg, wu, gate, up, act, need_dx, need_dw, dx, dwg, dwu, workspace, stream):
+    if x.dim() != 2 or wg.dim() != 2:
+        raise ValueError("x must be [M, K] and wg, wu [N, K]")
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dwg is not None or dwu is not None
+    if not (need_dx or need_dw):
+        raise ValueError("nothing to compute: neither dx nor the weights' gradients are wanted")
+    M, K = x.shape
+    N = wg.shape[0]
+    args = []
+    for name, t, shape in (("dh", dh, (M, N)), ("x", x, (M, K)), ("wg", wg, (N, K)), ("wu", wu, (N, K)),
+                           ("gate", gate, (M, N)), ("up", up, (M, N))):
+        args += _operand(t, name, dtype, shape)
+    handle = _stream_handle(stream, dh, x, wg, wu, gate, up, dx, dwg, dwu, workspace)
+    none = (None, None, 0)
+    with _on(stream, x.device):
+        dx, *dxa = _output(dx, "dx", dtype, (M, K), x.device) if need_dx else none
+        dwg, *dga = _output(dwg, "dwg", dtype, (N, K), x.device) if need_dw else none
+        dwu, *dua = _output(dwu, "dwu", dtype, (N, K), x.device) if need_dw else none
+        workspace = _scratch(workspace, gated_workspace_bytes(M, N, K), x.device)
+    name = "linear_%s_gated_backward" % tag
+    rc = getattr(_lib(), name)(*args, int(act), *dxa, *dga, *dua, M, N, K, workspace.data_ptr(), workspace.numel(), handle)
+    _check(rc, name)
+    return dx, dwg, dwu
+
+
+def linear_f16_gated_backward(dh, x, wg, wu, gate, up, act: int = EPI_SILU, need_dx: bool = True, need_dw: bool = True,
+                              dx=None, dwg=None, dwu=None, workspace=None, stream=None):
+    """The gated block's gradients (dx [M, K], dwg [N, K], dwu [N, K]) from dh [M, N] and the
+    projections that the forward call kept; those not wanted are None.  workspace: a uint8 device
+    tensor of at least gated_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    return _gated_backward_call("f16", torch.float16, dh, x, wg, wu, gate, up, act, need_dx, need_dw, dx, dwg, dwu,
+                                workspace, stream)
+
+
+def linear_bf16_gated_backward(dh, x, wg, wu, gate, up, act: int = EPI_SILU, need_dx: bool = True, need_dw: bool = True,
+                               dx=None, dwg=None, dwu=None, workspace=None, stream=None):
+    """linear_f16_gated_backward on bfloat16 operands and outputs."""
+    return _gated_backward_call("bf16", torch.bfloat16, dh, x, wg, wu, gate, up, act, need_dx, need_dw, dx, dwg, dwu,
+                                workspace, stream)
+
+
+def backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of device workspace the layer's backward calls need."""
+    n = _lib().linear_backward_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
+    return n
+
+
+def _backward_input_call(tag, dtype, dy, weight, out, workspace, stream):
+    if dy.dim() != 2 or weight.dim() != 2:
+        raise ValueError("dy must be [M, N] and weight [N, K]")
+    M, N = dy.shape
+    K = weight.shape[1]
+    yp, ldy = _mat(dy, "dy", dtype)
+    wp, ldw = _operand(weight, "weight", dtype, (N, K))
+    handle = _stream_handle(stream, dy, weight, out, workspace)
+    with _on(stream, dy.device):
+        out, xp, ldx = _output(out, "out", dtype, (M, K), dy.device)
+        workspace = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
+    name = "linear_%s_backward_input" % tag
+    rc = getattr(_lib(), name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, workspace.data_ptr(), workspace.numel(), handle)
+    _check(rc, name)
+    return out
+
+
+def linear_f16_backward_input(dy: torch.Tensor, weight: torch.Tensor, out=None, workspace=None, stream=None):
+    """dx = dy @ weight (dy [M, N], weight [N, K], float16), FP32 sums rounded once.  workspace: a uint8
+    device tensor of at least backward_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    return _backward_input_call("f16", torch.float16, dy, weight, out, workspace, stream)
+
+
+def linear_bf16_backward_input(dy: torch.Tensor, weight: torch.Tensor, out=None, workspace=None, stream=None):
+    """linear_f16_backward_input on bfloat16 operands."""
+    return _backward_input_call("bf16", torch.bfloat16, dy, weight, out, workspace, stream)
+
+
+def _backward_weight_call(tag, dtype, f32, dy, x, bias, accumulate, out, db, workspace, stream):
+    if dy.dim() != 2 or x.dim() != 2:
+        raise ValueError("dy must be [M, N] and x [M, K]")
+    M, N = dy.shape
+    K = x.shape[1]
+    bias = bias or db is not None
+    if accumulate and (out is None or (bias and db is None)):
+        raise ValueError("accumulate adds to tensors that are there: give out (and db)")
+    yp, ldy = _mat(dy, "dy", dtype)
+    xp, ldx = _operand(x, "x", dtype, (M, K))
+    handle = _stream_handle(stream, dy, x, out, db, workspace)
+    odt = torch.float32 if f32 else dtype
+    with _on(stream, dy.device):
+        out, wp, ldw = _output(out, "out", odt, (N, K), dy.device)
+        if bias and db is None:
+            db = torch.empty((N,), dtype=odt, device=dy.device)
+        workspace = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
+    if bias and (db.dtype != odt or tuple(db.shape) != (N,) or (N > 1 and db.stride(0) != 1)):
+        raise ValueError("db must be a contiguous %s [N] tensor" % odt)
+    bp = db.data_ptr() if bias else None
+    name = "linear_%s_backward_weight%s" % (tag, "_f32out" if f32 else "")
+    flag = (int(bool(accumulate)),) if f32 else ()
+    rc = getattr(_lib(), name)(yp, ldy, xp, ldx, wp, ldw, bp, *flag, M, N, K, workspace.data_ptr(), workspace.numel(),
+                               handle)
+    _check(rc, name)
+    return out, (db if bias else None)
+
+
+def linear_f16_backward_weight(dy: torch.Tensor, x: torch.Tensor, bias: bool = False, out=None, db=None, workspace=None,
+                               stream=None):
+    """(dw, db): dw = dy.T @ x [N, K] and, with bias, db = dy.sum(0) [N] (else None); dy [M, N], x [M, K],
+    float16, FP32 sums rounded once.  workspace as for linear_f16_backward_input."""
+    return _backward_weight_call("f16", torch.float16, False, dy, x, bias, False, out, db, workspace, stream)
+
+
+def linear_bf16_backward_weight(dy: torch.Tensor, x: torch.Tensor, bias: bool = False, out=None, db=None, workspace=None,
+                                stream=None):
+    """linear_f16_backward_weight on bfloat16 operands."""
+    return _backward_weight_call("bf16", torch.bfloat16, False, dy, x, bias, False, out, db, workspace, stream)
+
+
+def linear_f16_backward_weight_f32out(dy: torch.Tensor, x: torch.Tensor, bias: bool = False, accumulate: bool = False,
+                                      out=None, db=None, workspace=None, stream=None):
+    """linear_f16_backward_weight with the unrounded FP32 sums; accumulate: added to what out (and db) hold."""
+    return _backward_weight_call("f16", torch.float16, True, dy, x, bias, accumulate, out, db, workspace, stream)
+
+
+def linear_bf16_backward_weight_f32out(dy: torch.Tensor, x: torch.Tensor, bias: bool = False, accumulate: bool = False,
+                                       out=None, db=None, workspace=None, stream=None):
+    """linear_f16_backward_weight_f32out on bfloat16 operands."""
+    return _backward_weight_call("bf16", torch.bfloat16, True, dy, x, bias, accumulate, out, db, workspace, stream)
+
+
+# linear_tensor.type (include/linear_amd.h, LINEAR_TYPE_*)
+_TENSOR_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+GRAD_MAX_TENSORS = 65536
+
+
+def grad_workspace_bytes(count: int) -> int:
+    """Bytes of device workspace a norm over `count` tensors needs."""
+    n = _lib().linear_grad_workspace_bytes(count)
+    if n < 0:
+        raise ValueError("at most %d tensors" % GRAD_MAX_TENSORS)
+    return n
+
+
+def _tensor_table(tensors, name):
+    """The tensors as an array of linear_tensor (five 64-bit fields each): contiguous ones of any
+    shape, and matrices with unit inner stride."""
+    flat = []
+    for t in tensors:
+        kind = _TENSOR_TYPES.get(t.dtype)
+        if kind is None:
+            raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
+        if t.is_contiguous():
+            n = t.numel()
+            flat += (t.data_ptr(), 1, n, n, kind)
+        elif t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1) and t.stride(0) >= t.shape[1]:
+            flat += (t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), kind)
+        else:
+            raise ValueError("%s must be contiguous, or matrices with unit inner stride" % name)
+    return array.array("q", flat)
+
+
+def linear_grad_norm(grads, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """The global 2-norm of the gradients (a sequence of float16, bfloat16 and float32 tensors), as a
+    float32 [1] tensor.  workspace: a uint8 device tensor of at least grad_workspace_bytes(len(grads))
+    bytes (allocated per call when None)."""
+    grads = list(grads)
+    table = _tensor_table(grads, "grads")
+    if not grads and out is None:
+        raise ValueError("no gradients and no out: the device is not known")
+    handle = _stream_handle(stream, *grads, out, workspace)
+    device = (grads[0] if grads else out).device
+    with _on(stream, device):
+        if out is None:
+            out = torch.empty(1, dtype=torch.float32, device=device)
+        workspace = _scratch(workspace, grad_workspace_bytes(len(grads)), device)
+    if out.dtype != torch.float32 or out.numel() != 1:
+        raise ValueError("out must be a float32 tensor of one value")
+    rc = _lib().linear_grad_norm(table.buffer_info()[0], len(grads), out.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel(), handle)
+    _check(rc, "linear_grad_norm")
+    return out
+
+
+def linear_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None, stream=None):
+    """The gradients times min(1, max_norm / (norm + 1e-6)), rounded to their types: into the tensors
+    of out (same shapes and types), or in place.  norm: the float32 tensor of linear_grad_norm."""
+    grads = list(grads)
+    table = _tensor_table(grads, "grads")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be a float32 tensor of one value")
+    outs = None
+    if out is not None:
+        out = list(out)
+        if [(t.shape, t.dtype) for t in out] != [(t.shape, t.dtype) for t in grads]:
+            raise ValueError("out must have the gradients' shapes and types")
+        # the two tables must agree in their rows: a matrix with padded rows on one side
+        # is described by its rows on both
+        outs = _tensor_table(out, "out")
+        for i, (a, b) in enumerate(zip(grads, out)):
+            if outs[5 * i + 1] != table[5 * i + 1]:
+                for t, row in ((a, table), (b, outs)):
+                    row[5 * i + 1:5 * i + 4] = array.array("q", (t.shape[0], t.shape[1], t.stride(0)))
+    handle = _stream_handle(stream, *grads, norm, *(out or ()))
+    rc = _lib().linear_grad_clip(table.buffer_info()[0], outs.buffer_info()[0] if outs else None, len(grads),
+                                 norm.data_ptr(), float(max_norm), handle)
+    _check(rc, "linear_grad_clip")
+    return out if out is not None else grads
 
 
 def linear_f16_plan(x: torch.Tensor, weight: torch.Tensor, b: torch.Tensor | None = None,

@@ -20,7 +20,8 @@ PROBE_OUT = os.path.join(HERE, "liblinear_probe.so")
 PROBE_SOURCES = ["probe.hip"]
 BUILD_DIR = os.path.join(ROOT, "_build")
 
-SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "indexed.hip", "linear_abi.hip"]
+SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "indexed.hip", "product.hip", "gradnorm.hip",
+           "linear_abi.hip", "train_abi.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

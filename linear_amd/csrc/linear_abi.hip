@@ -13,39 +13,26 @@
 #include <atomic>
 
 #include "../../include/linear_amd.h"
+#include "abi.h"
 #include "kernels.h"
 
 namespace {
 
+using lin::check_device;
+using lin::DevInfo;
+using lin::Extent;
+using lin::extent;
+using lin::kMaxDim;
+using lin::kMaxGridX;
+using lin::kMaxGridY;
+using lin::kMaxLdIn;
+using lin::kMaxLdOut;
+using lin::kWholeMI355X;
+using lin::overlaps;
+
 thread_local int32_t g_last_hip_error = 0;
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxLdIn = (int64_t(1) << 22) - 1;
-constexpr int64_t kMaxLdOut = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxGridX = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxGridY = 65535;
 constexpr int kSkinnyMaxM = 16;   // AUTO sends M <= 16 to the skinny path
-
-// The compute units and XCDs of the device a call runs on, read from the device
-// (a partitioned part has fewer).  Plans made without a usable device (the
-// pure-host linear_f16_plan) assume a whole MI355X: 256 CUs in 8 XCDs.
-struct DevInfo {
-    int cus;
-    int xcd_shift;   // log2 of the XCD count; 0 (no XCD-aware remap) when not a power of two
-};
-constexpr DevInfo kWholeMI355X{256, 3};
-
-struct Extent {
-    uintptr_t lo, hi;  // [lo, hi) in bytes; hi == lo when empty
-};
-
-Extent extent(const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t elem_bytes = 2) {
-    Extent e{(uintptr_t)p, (uintptr_t)p};
-    if (p && rows > 0 && cols > 0) e.hi = e.lo + (uintptr_t)(((rows - 1) * ld + cols) * elem_bytes);
-    return e;
-}
-
-bool overlaps(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
 
 struct Request {
     const uint16_t* x;
@@ -271,9 +258,13 @@ int32_t plan(const Request& r, linear_plan* p, int cus) {
     return LINEAR_OK;
 }
 
+}  // namespace
+
+namespace lin {
+
 // Device check, cached per device: the current device must be a gfx950.  Also
 // caches its compute units and XCDs for the tile rules and the tile remap.
-int32_t check_device(int* dev_out, DevInfo* info = nullptr) {
+int32_t check_device(int* dev_out, DevInfo* info) {
     // per device: 0 unknown, 1 gfx950, 2 other (callers may be on several threads);
     // the CU and XCD figures are stored before the state is published
     static std::atomic<int> cached[64];
@@ -305,6 +296,12 @@ int32_t check_device(int* dev_out, DevInfo* info = nullptr) {
     if (info) *info = DevInfo{cus[dev], xcd_shift[dev]};
     return LINEAR_OK;
 }
+
+void set_last_hip_error(int32_t e) { g_last_hip_error = e; }
+
+}  // namespace lin
+
+namespace {
 
 // The current device's figures when a usable device is current, else a whole
 // MI355X's (leaves the thread's last HIP error as it was).
@@ -707,14 +704,16 @@ const char* linear_status_string(int32_t status) {
         case LINEAR_E_NULL: return "a required pointer is NULL";
         case LINEAR_E_SHAPE: return "invalid shape: M, N or K negative or too large";
         case LINEAR_E_STRIDE: return "invalid row stride: ldx/ldw < K, ldy < N, or beyond the stride limit";
-        case LINEAR_E_ALIAS: return "y overlaps x, weight, b or an epilogue input";
+        case LINEAR_E_ALIAS: return "an output overlaps an input, another output or the workspace";
         case LINEAR_E_PATH: return "unknown path selector";
         case LINEAR_E_DEVICE: return "no usable gfx950 device is current";
         case LINEAR_E_LAUNCH: return "kernel launch failed";
         case LINEAR_E_EPILOGUE: return "invalid epilogue program: step count or step code";
         case LINEAR_E_CAPTURE: return "the first activation epilogue on a device cannot run under stream capture";
-        case LINEAR_E_WORKSPACE: return "workspace not 16-byte aligned or smaller than linear_indexed_workspace_bytes";
+        case LINEAR_E_WORKSPACE: return "workspace not 16-byte aligned or smaller than its linear_*_workspace_bytes";
         case LINEAR_E_SCRATCH: return "the call needs more routing scratch than LINEAR_NOALLOC_SCRATCH_BYTES";
+        case LINEAR_E_VALUE: return "unknown activation or tensor type, or a negative or NaN max_norm";
+        case LINEAR_E_MEMORY: return "no host memory for the call's checks";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,91 @@
+// train.h -- launch interface of the gated feed-forward block, the layer's
+// gradients and the gradient norm.
+#pragma once
+
+#include "common.h"
+#include "kernels.h"
+
+namespace lin {
+
+// Activations of the gated block (the epilogue program's step codes).
+constexpr bool is_activation(int op) { return op == kEpiSilu || op == kEpiGeluTanh || op == kEpiGeluErf; }
+
+// One product of 16-bit operands with an FP32 accumulator, operands addressed by
+// element strides, in up to two segments s:
+//     acc[r, c] = sum_s sum_{k < L} a[s][r * sar + k * sak] * b[s][c * sbr[s] + k * sbk[s]]
+// The gated block instead keeps the two segments apart (acc_s each).
+struct ProductArgs {
+    const uint16_t* a[2];
+    const uint16_t* b[2];
+    int64_t sar, sak;
+    int64_t sbr[2], sbk[2];
+    int segs;
+    int R, C, L;             // output rows and columns, contraction length
+    int tiles_r, tiles_c;
+    void* y;                 // [R, C], row stride ldy: 16-bit words or floats
+    int64_t ldy;
+    int accumulate;          // FP32 output: y += acc
+    // gated block: y is h; the projections are stored where the pointers are given
+    uint16_t *gate, *up;
+    int64_t ldgate, ldup;
+    int act;
+};
+
+enum : int { kProdRound = 0, kProdF32 = 1, kProdGated = 2 };
+
+// Any layout; tiles of kProdTile x kProdTile outputs.
+constexpr int kProdTile = 64;
+hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStream_t stream);
+
+// dg = dh * u * act'(g), du = dh * act(g), rounded to the element type, into the
+// two halves of d [M, 2 * Np]: columns [0, N) and [Np, Np + N); columns between
+// N and Np are zeroed.
+struct GatedGradArgs {
+    const uint16_t *dh, *gate, *up;
+    int64_t lddh, ldgate, ldup;
+    uint16_t* d;
+    int M, N, Np;
+    int act;
+    int vec;                 // 16-byte loads of dh, gate and up
+};
+hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream);
+
+// Column sums of dy [M, N]: db[n] = sum_m dy[m, n].
+struct ColumnSumArgs {
+    const uint16_t* dy;
+    int64_t lddy;
+    float* partial;          // [splits, N]
+    void* db;                // 16-bit words or floats
+    int M, N, splits;
+    int f32, accumulate;
+};
+constexpr int kColSumRows = 64;          // least rows of one partial sum
+constexpr int kColSumMaxSplits = 128;
+inline int64_t column_sum_splits(int64_t M) {
+    const int64_t s = (M + kColSumRows - 1) / kColSumRows;
+    return s < 1 ? 1 : (s > kColSumMaxSplits ? kColSumMaxSplits : s);
+}
+hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t stream);
+
+// The global gradient norm and clipping: tensors in tables of kGradTensors,
+// passed as kernel arguments.
+constexpr int kGradTensors = 64;
+constexpr int kGradChunk = 8192;         // elements of one workgroup step
+constexpr int kGradGrid = 2048;          // most workgroups (and partial sums) of one table
+enum : int { kGradF16 = 0, kGradBF16 = 1, kGradF32 = 2 };
+struct GradTable {
+    const void* src[kGradTensors];
+    void* dst[kGradTensors];
+    int64_t cols[kGradTensors];
+    int64_t ld[kGradTensors], ldd[kGradTensors];   // row strides of src and dst
+    int64_t first[kGradTensors + 1];               // first chunk of each tensor; the last: all chunks
+    uint8_t type[kGradTensors];
+    uint8_t vec[kGradTensors];                     // rows 16-byte aligned (src, and dst when clipping)
+    int count;
+};
+static_assert(sizeof(GradTable) <= 3840, "the table travels as kernel arguments");
+hipError_t launch_grad_partials(const GradTable& t, double* partial, int grid, hipStream_t stream);
+hipError_t launch_grad_norm(const double* partial, int count, float* norm, hipStream_t stream);
+hipError_t launch_grad_clip(const GradTable& t, const float* norm, float max_norm, int grid, hipStream_t stream);
+
+}  // namespace lin

@@ -1,0 +1,496 @@
+// train_abi.hip -- the C ABI of the gated feed-forward block, the layer's
+// gradients and the gradient norm: argument checks, kernel choice, launches.
+// The conventions are linear_abi.hip's: every check runs on the host before
+// anything is enqueued, and only kernels are enqueued.
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <algorithm>
+#include <memory>
+#include <new>
+
+#include "../../include/linear_amd.h"
+#include "abi.h"
+#include "train.h"
+
+namespace {
+
+using lin::DevInfo;
+using lin::Extent;
+using lin::extent;
+using lin::kMaxDim;
+using lin::kMaxGridX;
+using lin::kMaxLdOut;
+using lin::overlaps;
+
+static_assert(lin::kGradF16 == LINEAR_TYPE_F16 && lin::kGradBF16 == LINEAR_TYPE_BF16 && lin::kGradF32 == LINEAR_TYPE_F32,
+              "tensor types");
+
+int32_t launched(hipError_t e) {
+    if (e == hipSuccess) return LINEAR_OK;
+    lin::set_last_hip_error((int32_t)e);
+    return LINEAR_E_LAUNCH;
+}
+
+// Elements that one operand may span: byte addresses stay far inside 64 bits.
+constexpr int64_t kMaxElems = int64_t(1) << 58;
+
+// Sizes leave room below 2^31 for the last tile's rows and columns.
+constexpr int64_t kMaxSize = kMaxDim - 65535;
+
+bool dims_ok(int64_t M, int64_t N, int64_t K) {
+    return M >= 0 && N >= 0 && K >= 0 && M <= kMaxSize && N <= kMaxSize && K <= kMaxSize;
+}
+
+// A [rows, cols] operand of a call: its checks in the order NULL, stride.
+struct Operand {
+    const void* p;
+    int64_t rows, ld, cols;
+    int64_t bytes = 2;
+    bool empty() const { return rows == 0 || cols == 0; }
+    Extent range() const { return extent(p, rows, ld, cols, bytes); }
+};
+
+int32_t check_operand(const Operand& o) {
+    if (o.empty()) return LINEAR_OK;
+    if (!o.p) return LINEAR_E_NULL;
+    if (o.ld < o.cols || (o.rows > 1 && o.ld > kMaxLdOut)) return LINEAR_E_STRIDE;
+    if ((o.rows - 1) * o.ld > kMaxElems - o.cols) return LINEAR_E_STRIDE;
+    return LINEAR_OK;
+}
+
+// The operands' own checks, then: no output may overlap an input or another output.
+template <int NI, int NO>
+int32_t check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
+    int32_t st = LINEAR_OK;
+    auto first = [&](int32_t want) {
+        for (const Operand& o : in)
+            if (check_operand(o) == want) return true;
+        for (const Operand& o : out)
+            if (o.p && check_operand(o) == want) return true;
+        return false;
+    };
+    for (int32_t code : {LINEAR_E_NULL, LINEAR_E_STRIDE})
+        if (st == LINEAR_OK && first(code)) st = code;
+    if (st != LINEAR_OK) return st;
+    for (int i = 0; i < NO; ++i) {
+        if (!out[i].p || out[i].empty()) continue;
+        for (const Operand& o : in)
+            if (!o.empty() && overlaps(out[i].range(), o.range())) return LINEAR_E_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (out[j].p && !out[j].empty() && overlaps(out[i].range(), out[j].range())) return LINEAR_E_ALIAS;
+    }
+    return LINEAR_OK;
+}
+
+int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+bool any_grid_ok(int64_t R, int64_t C) { return tiles_of(R, lin::kProdTile) * tiles_of(C, lin::kProdTile) <= kMaxGridX; }
+
+// A one-segment product with its output shape.
+lin::ProductArgs product(const uint16_t* a, int64_t sar, int64_t sak, const uint16_t* b, int64_t sbr, int64_t sbk, void* y,
+                         int64_t ldy, int64_t R, int64_t C, int64_t L) {
+    lin::ProductArgs p;
+    memset(&p, 0, sizeof p);
+    p.a[0] = a;
+    p.b[0] = b;
+    p.sar = sar;
+    p.sak = sak;
+    p.sbr[0] = sbr;
+    p.sbk[0] = sbk;
+    p.segs = 1;
+    p.R = (int)R;
+    p.C = (int)C;
+    p.L = (int)L;
+    p.tiles_r = (int)tiles_of(R, lin::kProdTile);
+    p.tiles_c = (int)tiles_of(C, lin::kProdTile);
+    p.y = y;
+    p.ldy = ldy;
+    return p;
+}
+
+int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
+                  int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
+                  int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
+    if (!dims_ok(M, N, K)) return LINEAR_E_SHAPE;
+    if (!lin::is_activation(act)) return LINEAR_E_VALUE;
+    if (M == 0 || N == 0) return LINEAR_OK;
+    if (!h) return LINEAR_E_NULL;
+    const Operand in[] = {{x, M, ldx, K}, {wg, N, ldwg, K}, {wu, N, ldwu, K}};
+    const Operand out[] = {{h, M, ldh, N}, {gate, M, ldgate, N}, {up, M, ldup, N}};
+    int32_t st = check_operands(in, out);
+    if (st != LINEAR_OK) return st;
+    if (!any_grid_ok(M, N)) return LINEAR_E_SHAPE;
+    int dev = 0;
+    DevInfo di;
+    st = lin::check_device(&dev, &di);
+    if (st != LINEAR_OK) return st;
+    lin::ProductArgs p = product(x, ldx, 1, wg, ldwg, 1, h, ldh, M, N, K);
+    p.segs = 2;
+    p.b[1] = wu;
+    p.sbr[1] = ldwu;
+    p.sbk[1] = 1;
+    p.gate = gate;
+    p.ldgate = ldgate;
+    p.up = up;
+    p.ldup = ldup;
+    p.act = act;
+    return launched(lin::launch_product_any(elem, lin::kProdGated, p, (hipStream_t)stream));
+}
+
+int32_t check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (need == 0) return LINEAR_OK;
+    if (!ws) return LINEAR_E_NULL;
+    if (have < need || (uintptr_t)ws % 16 != 0) return LINEAR_E_WORKSPACE;
+    return LINEAR_OK;
+}
+
+// dx [M, K] = dy [M, N] . weight [N, K].
+int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uint16_t* w, int64_t ldw, uint16_t* dx,
+                           int64_t lddx, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes, void* stream) {
+    if (!dims_ok(M, N, K)) return LINEAR_E_SHAPE;
+    if (M == 0 || K == 0) return LINEAR_OK;
+    if (!dx) return LINEAR_E_NULL;
+    const int64_t need = linear_backward_workspace_bytes(M, N, K);
+    const Operand in[] = {{dy, M, lddy, N}, {w, N, ldw, K}};
+    const Operand out[] = {{dx, M, lddx, K}, {ws, 1, need, need, 1}};
+    int32_t st = check_operands(in, out);
+    if (st != LINEAR_OK) return st;
+    st = check_workspace(ws, ws_bytes, need);
+    if (st != LINEAR_OK) return st;
+    if (!any_grid_ok(M, K)) return LINEAR_E_SHAPE;
+    int dev = 0;
+    DevInfo di;
+    st = lin::check_device(&dev, &di);
+    if (st != LINEAR_OK) return st;
+    const lin::ProductArgs p = product(dy, lddy, 1, w, 1, ldw, dx, lddx, M, K, N);
+    return launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+}
+
+// dw [N, K] = dy [M, N]^T . x [M, K], db [N] = column sums of dy.
+int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, void* dw,
+                            int64_t lddw, void* db, int32_t accumulate, int64_t M, int64_t N, int64_t K, void* ws,
+                            int64_t ws_bytes, void* stream) {
+    if (!dims_ok(M, N, K)) return LINEAR_E_SHAPE;
+    if (N == 0 || (K == 0 && !db)) return LINEAR_OK;
+    if (K > 0 && !dw) return LINEAR_E_NULL;
+    const int64_t eb = f32 ? 4 : 2;
+    const int64_t need = linear_backward_workspace_bytes(M, N, K);
+    const Operand in[] = {{dy, M, lddy, N}, {x, M, ldx, K}};
+    const Operand out[] = {{dw, N, lddw, K, eb}, {db, 1, N, N, eb}, {ws, 1, need, need, 1}};
+    int32_t st = check_operands(in, out);
+    if (st != LINEAR_OK) return st;
+    st = check_workspace(ws, ws_bytes, need);
+    if (st != LINEAR_OK) return st;
+    if (!any_grid_ok(N, K)) return LINEAR_E_SHAPE;
+    int dev = 0;
+    DevInfo di;
+    st = lin::check_device(&dev, &di);
+    if (st != LINEAR_OK) return st;
+    if (db) {
+        lin::ColumnSumArgs c;
+        c.dy = dy;
+        c.lddy = lddy;
+        c.partial = (float*)ws;
+        c.db = db;
+        c.M = (int)M;
+        c.N = (int)N;
+        c.splits = (int)lin::column_sum_splits(M);
+        c.f32 = f32;
+        c.accumulate = accumulate != 0;
+        st = launched(lin::launch_column_sum(elem, c, (hipStream_t)stream));
+        if (st != LINEAR_OK) return st;
+    }
+    if (K == 0) return LINEAR_OK;
+    lin::ProductArgs p = product(dy, 1, lddy, x, 1, ldx, dw, lddw, N, K, M);
+    p.accumulate = f32 && accumulate != 0;
+    return launched(lin::launch_product_any(elem, f32 ? lin::kProdF32 : lin::kProdRound, p, (hipStream_t)stream));
+}
+
+// The gated block's dg | du matrix: columns of one half, a whole number of 64-wide slices.
+int64_t gated_half(int64_t N) { return (N + 63) / 64 * 64; }
+
+int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,
+                           int64_t ldwg, const uint16_t* wu, int64_t ldwu, const uint16_t* gate, int64_t ldgate,
+                           const uint16_t* up, int64_t ldup, int32_t act, uint16_t* dx, int64_t lddx, uint16_t* dwg,
+                           int64_t lddwg, uint16_t* dwu, int64_t lddwu, int64_t M, int64_t N, int64_t K, void* ws,
+                           int64_t ws_bytes, void* stream) {
+    if (!dims_ok(M, N, K)) return LINEAR_E_SHAPE;
+    if (!lin::is_activation(act)) return LINEAR_E_VALUE;
+    if (K == 0 || (M == 0 && N == 0)) return LINEAR_OK;
+    if ((dwg == nullptr) != (dwu == nullptr)) return LINEAR_E_NULL;
+    const bool want_dx = dx && M > 0, want_dw = dwg && N > 0;
+    if (!want_dx && !want_dw) return dx || dwg ? LINEAR_OK : LINEAR_E_NULL;
+    const int64_t need = linear_gated_workspace_bytes(M, N, K);
+    if (need < 0) return LINEAR_E_SHAPE;
+    const Operand in[] = {{dh, M, lddh, N}, {x, M, ldx, want_dw ? K : 0}, {wg, N, ldwg, want_dx ? K : 0},
+                          {wu, N, ldwu, want_dx ? K : 0}, {gate, M, ldgate, N}, {up, M, ldup, N}};
+    const Operand out[] = {{dx, M, lddx, K}, {dwg, N, lddwg, K}, {dwu, N, lddwu, K}, {ws, 1, need, need, 1}};
+    int32_t st = check_operands(in, out);
+    if (st != LINEAR_OK) return st;
+    st = check_workspace(ws, ws_bytes, need);
+    if (st != LINEAR_OK) return st;
+    const int64_t Np = gated_half(N);
+    if ((want_dx && !any_grid_ok(M, K)) || (want_dw && !any_grid_ok(N, K)) || 2 * Np > kMaxLdOut) return LINEAR_E_SHAPE;
+    int dev = 0;
+    DevInfo di;
+    st = lin::check_device(&dev, &di);
+    if (st != LINEAR_OK) return st;
+    uint16_t* d = (uint16_t*)ws;
+    if (M > 0 && N > 0) {
+        lin::GatedGradArgs g;
+        g.dh = dh;
+        g.gate = gate;
+        g.up = up;
+        g.lddh = lddh;
+        g.ldgate = ldgate;
+        g.ldup = ldup;
+        g.d = d;
+        g.M = (int)M;
+        g.N = (int)N;
+        g.Np = (int)Np;
+        g.act = act;
+        auto al16 = [](const void* q, int64_t ld) { return (uintptr_t)q % 16 == 0 && ld % 8 == 0; };
+        g.vec = al16(dh, lddh) && al16(gate, ldgate) && al16(up, ldup);
+        st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
+        if (st != LINEAR_OK) return st;
+    }
+    if (want_dx) {
+        lin::ProductArgs p = product(d, 2 * Np, 1, wg, 1, ldwg, dx, lddx, M, K, N);
+        p.segs = 2;
+        p.a[1] = d + Np;
+        p.b[1] = wu;
+        p.sbr[1] = 1;
+        p.sbk[1] = ldwu;
+        st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+        if (st != LINEAR_OK) return st;
+    }
+    if (want_dw) {
+        for (int s = 0; s < 2; ++s) {
+            const lin::ProductArgs p = product(d + s * Np, 1, 2 * Np, x, 1, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
+            st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+            if (st != LINEAR_OK) return st;
+        }
+    }
+    return LINEAR_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping
+
+int64_t type_bytes(int64_t type) { return type == LINEAR_TYPE_F32 ? 4 : 2; }
+
+int32_t check_tensor(const linear_tensor& t) {
+    if (t.type != LINEAR_TYPE_F16 && t.type != LINEAR_TYPE_BF16 && t.type != LINEAR_TYPE_F32) return LINEAR_E_VALUE;
+    if (t.rows < 0 || t.cols < 0 || t.rows > kMaxDim || t.cols > (int64_t(1) << 46)) return LINEAR_E_SHAPE;
+    if (t.rows == 0 || t.cols == 0) return LINEAR_OK;
+    if (!t.data) return LINEAR_E_NULL;
+    if (t.rows > 1 && (t.ld < t.cols || t.ld > kMaxLdOut || (t.rows - 1) * t.ld > kMaxElems - t.cols))
+        return LINEAR_E_STRIDE;
+    return LINEAR_OK;
+}
+
+// Tables of up to kGradTensors tensors, empty ones left out; rows without gaps
+// between them count as one row.  f(table, chunks) launches each.
+template <typename F>
+int32_t each_table(const linear_tensor* src, const linear_tensor* dst, int64_t count, F f) {
+    lin::GradTable t;
+    memset(&t, 0, sizeof t);
+    for (int64_t i = 0; i < count; ++i) {
+        const linear_tensor& s = src[i];
+        if (s.rows > 0 && s.cols > 0) {
+            const linear_tensor& d = dst ? dst[i] : s;
+            const int k = t.count;
+            const bool one = s.rows == 1 || (s.ld == s.cols && d.ld == s.cols);
+            const int64_t rows = one ? 1 : s.rows;
+            t.src[k] = s.data;
+            t.dst[k] = d.data;
+            t.cols[k] = one ? s.rows * s.cols : s.cols;
+            t.ld[k] = one ? 0 : s.ld;
+            t.ldd[k] = one ? 0 : d.ld;
+            t.type[k] = (uint8_t)s.type;
+            const int64_t eb = type_bytes(s.type);
+            t.vec[k] = (uintptr_t)s.data % 16 == 0 && (uintptr_t)d.data % 16 == 0 && t.ld[k] * eb % 16 == 0 &&
+                       t.ldd[k] * eb % 16 == 0;
+            t.first[k + 1] = t.first[k] + rows * ((t.cols[k] + lin::kGradChunk - 1) / lin::kGradChunk);
+            t.count = k + 1;
+        }
+        if (t.count == lin::kGradTensors || (i + 1 == count && t.count > 0)) {
+            const int32_t st = f(t, (int)std::min<int64_t>(t.first[t.count], lin::kGradGrid));
+            if (st != LINEAR_OK) return st;
+            t.count = 0;
+        }
+    }
+    return LINEAR_OK;
+}
+
+struct Range {
+    Extent e;
+    bool out;
+};
+
+}  // namespace
+
+extern "C" {
+
+int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!dims_ok(M, N, K) || (M > 0 && gated_half(N) > kMaxElems / 4 / M)) return -1;
+    return M * gated_half(N) * 2 * 2;
+}
+
+int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!dims_ok(M, N, K)) return -1;
+    return lin::column_sum_splits(M) * N * 4;
+}
+
+int32_t linear_f16_gated(const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
+                         int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
+                         int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
+    return run_gated(lin::kF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, stream);
+}
+
+int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
+                          int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
+                          int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
+    return run_gated(lin::kBF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, stream);
+}
+
+int32_t linear_f16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,
+                                  int64_t ldwg, const uint16_t* wu, int64_t ldwu, const uint16_t* gate, int64_t ldgate,
+                                  const uint16_t* up, int64_t ldup, int32_t act, uint16_t* dx, int64_t lddx, uint16_t* dwg,
+                                  int64_t lddwg, uint16_t* dwu, int64_t lddwu, int64_t M, int64_t N, int64_t K,
+                                  void* workspace, int64_t workspace_bytes, void* stream) {
+    return run_gated_backward(lin::kF16, dh, lddh, x, ldx, wg, ldwg, wu, ldwu, gate, ldgate, up, ldup, act, dx, lddx, dwg,
+                              lddwg, dwu, lddwu, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int32_t linear_bf16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,
+                                   int64_t ldwg, const uint16_t* wu, int64_t ldwu, const uint16_t* gate, int64_t ldgate,
+                                   const uint16_t* up, int64_t ldup, int32_t act, uint16_t* dx, int64_t lddx, uint16_t* dwg,
+                                   int64_t lddwg, uint16_t* dwu, int64_t lddwu, int64_t M, int64_t N, int64_t K,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+    return run_gated_backward(lin::kBF16, dh, lddh, x, ldx, wg, ldwg, wu, ldwu, gate, ldgate, up, ldup, act, dx, lddx, dwg,
+                              lddwg, dwu, lddwu, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int32_t linear_f16_backward_input(const uint16_t* dy, int64_t lddy, const uint16_t* weight, int64_t ldw, uint16_t* dx,
+                                  int64_t lddx, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
+    return run_backward_input(lin::kF16, dy, lddy, weight, ldw, dx, lddx, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int32_t linear_bf16_backward_input(const uint16_t* dy, int64_t lddy, const uint16_t* weight, int64_t ldw, uint16_t* dx,
+                                   int64_t lddx, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                                   void* stream) {
+    return run_backward_input(lin::kBF16, dy, lddy, weight, ldw, dx, lddx, M, N, K, workspace, workspace_bytes, stream);
+}
+
+int32_t linear_f16_backward_weight(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, uint16_t* dw,
+                                   int64_t lddw, uint16_t* db, int64_t M, int64_t N, int64_t K, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+    return run_backward_weight(lin::kF16, false, dy, lddy, x, ldx, dw, lddw, db, 0, M, N, K, workspace, workspace_bytes,
+                               stream);
+}
+
+int32_t linear_bf16_backward_weight(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, uint16_t* dw,
+                                    int64_t lddw, uint16_t* db, int64_t M, int64_t N, int64_t K, void* workspace,
+                                    int64_t workspace_bytes, void* stream) {
+    return run_backward_weight(lin::kBF16, false, dy, lddy, x, ldx, dw, lddw, db, 0, M, N, K, workspace, workspace_bytes,
+                               stream);
+}
+
+int32_t linear_f16_backward_weight_f32out(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, float* dw,
+                                          int64_t lddw, float* db, int32_t accumulate, int64_t M, int64_t N, int64_t K,
+                                          void* workspace, int64_t workspace_bytes, void* stream) {
+    return run_backward_weight(lin::kF16, true, dy, lddy, x, ldx, dw, lddw, db, accumulate, M, N, K, workspace,
+                               workspace_bytes, stream);
+}
+
+int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy, const uint16_t* x, int64_t ldx, float* dw,
+                                           int64_t lddw, float* db, int32_t accumulate, int64_t M, int64_t N, int64_t K,
+                                           void* workspace, int64_t workspace_bytes, void* stream) {
+    return run_backward_weight(lin::kBF16, true, dy, lddy, x, ldx, dw, lddw, db, accumulate, M, N, K, workspace,
+                               workspace_bytes, stream);
+}
+
+int64_t linear_grad_workspace_bytes(int64_t count) {
+    if (count < 0 || count > LINEAR_GRAD_MAX_TENSORS) return -1;
+    return (count + lin::kGradTensors - 1) / lin::kGradTensors * lin::kGradGrid * 8;
+}
+
+int32_t linear_grad_norm(const linear_tensor* grads, int64_t count, float* norm, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+    const int64_t need = linear_grad_workspace_bytes(count);
+    if (need < 0) return LINEAR_E_SHAPE;
+    if (!norm || (count > 0 && !grads)) return LINEAR_E_NULL;
+    int32_t st;
+    const Extent en = extent(norm, 1, 1, 1, 4), ew = extent(workspace, 1, need, need, 1);
+    for (int64_t i = 0; i < count; ++i)
+        if ((st = check_tensor(grads[i])) != LINEAR_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != LINEAR_OK) return st;
+    if (overlaps(en, ew)) return LINEAR_E_ALIAS;
+    for (int64_t i = 0; i < count; ++i) {
+        const linear_tensor& t = grads[i];
+        const Extent e = extent(t.data, t.rows, t.ld, t.cols, type_bytes(t.type));
+        if (overlaps(e, en) || overlaps(e, ew)) return LINEAR_E_ALIAS;
+    }
+    int dev = 0;
+    if ((st = lin::check_device(&dev)) != LINEAR_OK) return st;
+    double* partial = (double*)workspace;
+    int used = 0;
+    st = each_table(grads, nullptr, count, [&](const lin::GradTable& t, int grid) {
+        const int32_t r = launched(lin::launch_grad_partials(t, partial + used, grid, (hipStream_t)stream));
+        used += grid;
+        return r;
+    });
+    if (st != LINEAR_OK) return st;
+    return launched(lin::launch_grad_norm(partial, used, norm, (hipStream_t)stream));
+}
+
+int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, int64_t count, const float* norm,
+                         float max_norm, void* stream) {
+    if (count < 0 || count > LINEAR_GRAD_MAX_TENSORS) return LINEAR_E_SHAPE;
+    if (isnan(max_norm) || max_norm < 0.f) return LINEAR_E_VALUE;
+    if (count == 0) return LINEAR_OK;
+    if (!grads || !norm) return LINEAR_E_NULL;
+    int32_t st;
+    for (int64_t i = 0; i < count; ++i) {
+        if ((st = check_tensor(grads[i])) != LINEAR_OK) return st;
+        if (!out) continue;
+        if ((st = check_tensor(out[i])) != LINEAR_OK) return st;
+        if (out[i].type != grads[i].type) return LINEAR_E_VALUE;
+        if (out[i].rows != grads[i].rows || out[i].cols != grads[i].cols) return LINEAR_E_SHAPE;
+    }
+    // every output must be apart from every other tensor and from the norm, but a
+    // tensor may be its own output: sorted by address, an output may not begin
+    // before an earlier range ends, nor an input before an earlier output ends
+    std::unique_ptr<Range[]> ranges(new (std::nothrow) Range[2 * count + 1]);
+    if (!ranges) return LINEAR_E_MEMORY;
+    int64_t n = 0;
+    ranges[n++] = {extent(norm, 1, 1, 1, 4), false};
+    for (int64_t i = 0; i < count; ++i) {
+        const linear_tensor &s = grads[i], &d = out ? out[i] : grads[i];
+        if (s.rows == 0 || s.cols == 0) continue;
+        const int64_t eb = type_bytes(s.type);
+        ranges[n++] = {extent(d.data, d.rows, d.ld, d.cols, eb), true};
+        const bool in_place = d.data == s.data && (d.rows == 1 || d.ld == s.ld);
+        if (!in_place) ranges[n++] = {extent(s.data, s.rows, s.ld, s.cols, eb), false};
+    }
+    std::sort(ranges.get(), ranges.get() + n, [](const Range& a, const Range& b) { return a.e.lo < b.e.lo; });
+    uintptr_t all = 0, outs = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const Range& r = ranges[i];
+        if (r.e.lo < (r.out ? all : outs)) return LINEAR_E_ALIAS;
+        all = std::max(all, r.e.hi);
+        if (r.out) outs = std::max(outs, r.e.hi);
+    }
+    int dev = 0;
+    if ((st = lin::check_device(&dev)) != LINEAR_OK) return st;
+    return each_table(grads, out, count, [&](const lin::GradTable& t, int grid) {
+        return launched(lin::launch_grad_clip(t, norm, max_norm, grid, (hipStream_t)stream));
+    });
+}
+
+}  // extern "C"
