@@ -32,6 +32,7 @@
 
 #include <type_traits>
 
+#include "activation.h"
 #include "common.h"
 #include "kernels.h"
 #include "sched.h"
@@ -343,6 +344,60 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, unsigned char* 
     }
 }
 
+// The end of a gated tile (BN = twice its BC output columns): a wave's blocks
+// alternate between the two projections, so acc[2p] and acc[2p + 1] hold g and u of
+// the same outputs in the same lanes.  h = act(g) u in FP32, rounded once, and the
+// kept projections leave one after the other, each staged in the freed ring like a
+// rounded tile and stored in 16-byte row chunks.
+template <int BM, int BN, int WM, int WN, int E, int R, typename AccT>
+__device__ __forceinline__ void finish_gated(const LinearArgs& a, unsigned char* smem,
+                                             AccT (&acc)[BN / WN / R][BM / WM / R], int m0, int c0, int wave,
+                                             int lane) {
+    constexpr int NT = WM * WN * 64;
+    constexpr int TM = BM / WM, TC = BN / WN / 2, BC = BN / 2;
+    constexpr int FM = TM / R, FP = TC / R;
+    constexpr int G = R * R / 256;
+    constexpr int CPR = BC / 8;                      // chunks per staged row
+    constexpr int CHT = BM * CPR / NT;
+    static_assert((BM * CPR) % NT == 0, "chunks must divide evenly over the threads");
+    const int wn = wave % WN, wm = wave / WN;
+    const int lr = lane % R, lh = lane / R;
+    static_for<0, 3>([&]<int q>() {
+        uint16_t* out = q == 0 ? (uint16_t*)a.y : q == 1 ? a.gate : a.up;
+        const int64_t ld = q == 0 ? a.ldy : q == 1 ? a.ldgate : a.ldup;
+        if (!out) return;                            // uniform
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < FP; ++p)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int cl = wn * TC + p * R + g * 8 + lh * 4;
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const int ml = wm * TM + j * R + lr;
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float gv = acc[2 * p][j][g * 4 + e], uv = acc[2 * p + 1][j][g * 4 + e];
+                        w[e] = narrow<E>(q == 0 ? gated_act(a.act, gv) * uv : q == 1 ? gv : uv);
+                    }
+                    uint2 u;
+                    u.x = w[0] | (w[1] << 16);
+                    u.y = w[2] | (w[3] << 16);
+                    *(uint2*)(smem + (ml * CPR + ((cl / 8) ^ (ml % CPR))) * 16 + ((cl / 4) & 1) * 8) = u;
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < CHT; ++k) {
+            const int c = (int)threadIdx.x + k * NT, r = c / CPR, c8 = c % CPR;
+            const u32x4 v = *(const u32x4*)(smem + (r * CPR + (c8 ^ (r % CPR))) * 16);
+            const int m = m0 + r, n = c0 + c8 * 8;
+            store8(out + (int64_t)m * ld + n, m < a.M, n, a.N, a.vec_gated & (1 << q), v);
+        }
+    });
+}
+
 // Tile (tm, tn) of this workgroup, with its group entered.  One group: the XCD
 // walk of tile_coords over blockIdx.x.  Several groups (grid z): the groups' row
 // tiles are stacked into one column of G x tiles_m row tiles and walked as one
@@ -387,6 +442,11 @@ __device__ inline void stream_tile(LinearArgs& a, int& tm, int& tn) {
 // swizzle puts there.  With BK = 64 every load instruction covers whole 128-byte
 // rows.
 //
+// Gated block (kOutGated): the tile's BN weight rows are BN / 2 rows of each weight,
+// alternating in blocks of R rows (the MFMA block), so that one wave's accumulators
+// hold both projections of its outputs; x is read once for both, and h leaves
+// without g and u ever going to memory.
+//
 // WHOLE (tiles with one MFMA per wave and K step): a K step's fragment reads
 // would have a single MFMA to hide behind, so each slice's fragments are read at
 // once and its MFMAs run as they land; and only slices that exist are requested,
@@ -426,10 +486,13 @@ gemm_stream(LinearArgs a) {
 
     int tm, tn;
     stream_tile<MODE>(a, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    constexpr bool GATED = MODE == kOutGated;
+    const int m0 = tm * BM, n0 = tn * (GATED ? BN / 2 : BN);
     const int K = a.K;
     const __amdgpu_buffer_rsrc_t rw = matrix_rsrc(a.w, n0, a.N, a.ldw, K);
     const __amdgpu_buffer_rsrc_t rx = matrix_rsrc(a.x, m0, a.M, a.ldx, K);
+    const __amdgpu_buffer_rsrc_t rw2 = GATED ? matrix_rsrc(a.w2, n0, a.N, a.ldw2, K) : rw;
+    static_assert(!GATED || ((TN / R) % 2 == 0 && R % RPL == 0), "a wave holds whole pairs of blocks, a load one block");
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // uniform
@@ -465,10 +528,12 @@ gemm_stream(LinearArgs a) {
         const int g = wave * GPW + j;
         const bool isw = g < BN / RPL;
         const int tr = g * RPL + lane / CPR;       // row within the slot (weight rows first)
-        const int r = isw ? tr : tr - BN;          // row within its matrix tile
+        const int wr = GATED ? tr / (2 * R) * R + tr % R : tr;
+        const int r = isw ? wr : tr - BN;          // row within its matrix tile
+        const int64_t ldw = GATED && (tr / R) % 2 ? a.ldw2 : a.ldw;
         const int c = (lane % CPR) ^ ((tr / RP) % CPR);
         if (j < GPER) gk[j] = c * 8;
-        goff[j] = (uint32_t)(((int64_t)r * (isw ? a.ldw : a.ldx) + c * 8) * 2);
+        goff[j] = (uint32_t)(((int64_t)r * (isw ? ldw : a.ldx) + c * 8) * 2);
     }
 
     const int nk = (K + BK - 1) / BK;
@@ -480,7 +545,8 @@ gemm_stream(LinearArgs a) {
         const uint32_t kb__ = (uint32_t)(t__ * BK) * 2u;                                 \
         const int g__ = wave * GPW + (j_);                                               \
         const bool kin__ = t__ * BK + gk[(j_) % GPER] < K;                               \
-        lds_dma16(g__ < BN / RPL ? rw : rx, slot__ + g__ * 1024, kin__ ? goff[(j_)] + kb__ : kOOB); \
+        lds_dma16(g__ < BN / RPL ? (GATED && (g__ * RPL / R) % 2 ? rw2 : rw) : rx, slot__ + g__ * 1024, \
+                  kin__ ? goff[(j_)] + kb__ : kOOB);                                     \
     } while (0)
 
     // The loads of slice t + STAGES go into the slot that the barrier after slice
@@ -672,8 +738,11 @@ gemm_stream(LinearArgs a) {
     if constexpr (MODE == kOutBias && LATE_BIAS) {
         if (nk == 0) request_bias();
     }
-    finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(a, smem, acc, m0, n0, wave, lane,
-                                                           MODE == kOutBias ? &bias8 : nullptr);
+    if constexpr (GATED)
+        finish_gated<BM, BN, WM, WN, E, R>(a, smem, acc, m0, n0, wave, lane);
+    else
+        finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(a, smem, acc, m0, n0, wave, lane,
+                                                               MODE == kOutBias ? &bias8 : nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -709,6 +778,19 @@ hipError_t launch_gemm_t(int cfg, const LinearArgs& a, int mode, hipStream_t str
     switch (cfg) {
         case 0: return launch(regstaged_fn<128, 128, 2, 2, E>(mode), a, 256, stream);
         case 1: return launch(regstaged_fn<64, 64, 2, 2, E>(mode), a, 256, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+// The gated block's tiles; bn counts the rows of both weights.
+template <int E>
+hipError_t launch_gated_stream_t(int cfg, const LinearArgs& a, hipStream_t stream) {
+    switch (cfg) {
+        case 0: return launch((const void*)gemm_stream<256, 256, 2, 4, 2, 64, E, kOutGated, 1, false, true>, a, 512, stream);
+        case 1: return launch((const void*)gemm_stream<256, 128, 4, 2, 3, 64, E, kOutGated, 2>, a, 512, stream);
+        case 2: return launch((const void*)gemm_stream<128, 256, 2, 4, 4, 32, E, kOutGated, 0>, a, 512, stream);
+        case 3: return launch((const void*)gemm_stream<128, 128, 2, 2, 4, 64, E, kOutGated, 2>, a, 256, stream);
+        case 4: return launch((const void*)gemm_stream<64, 128, 2, 2, 4, 64, E, kOutGated, 2>, a, 256, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -33,6 +33,27 @@ inline constexpr GemmConfig kGemmConfigs[kNumGemmConfigs] = {
 // a.tiles_m / a.tiles_n must match the chosen configuration; mode is kOut*.
 template <int E> hipError_t launch_gemm_t(int cfg, const LinearArgs& a, int mode, hipStream_t stream);
 template <int E> hipError_t launch_gemm_stream_t(int cfg, const LinearArgs& a, int mode, hipStream_t stream);
+template <int E> hipError_t launch_gated_stream_t(int cfg, const LinearArgs& a, hipStream_t stream);
+// each element type's kernels are instantiated in one file
+extern template hipError_t launch_gemm_t<kF16>(int, const LinearArgs&, int, hipStream_t);
+extern template hipError_t launch_gemm_t<kBF16>(int, const LinearArgs&, int, hipStream_t);
+extern template hipError_t launch_gemm_stream_t<kF16>(int, const LinearArgs&, int, hipStream_t);
+extern template hipError_t launch_gemm_stream_t<kBF16>(int, const LinearArgs&, int, hipStream_t);
+extern template hipError_t launch_gated_stream_t<kF16>(int, const LinearArgs&, hipStream_t);
+extern template hipError_t launch_gated_stream_t<kBF16>(int, const LinearArgs&, hipStream_t);
+
+// The gated block's streaming kernels: bn counts the rows of both weights (an
+// output tile has bn / 2 columns); a.tiles_n counts bn / 2-column tiles.
+inline constexpr GemmConfig kGatedConfigs[kNumStreamConfigs] = {
+    {256, 256, 2, 4, 2, 64},
+    {256, 128, 4, 2, 3, 64},
+    {128, 256, 2, 4, 4, 32},
+    {128, 128, 2, 2, 4, 64},
+    {64, 128, 2, 2, 4, 64},
+};
+inline hipError_t launch_gated_stream(int elem, int cfg, const LinearArgs& a, hipStream_t stream) {
+    return elem == kBF16 ? launch_gated_stream_t<kBF16>(cfg, a, stream) : launch_gated_stream_t<kF16>(cfg, a, stream);
+}
 
 inline hipError_t launch_gemm(int elem, int cfg, const LinearArgs& a, int mode, hipStream_t stream) {
     return elem == kBF16 ? launch_gemm_t<kBF16>(cfg, a, mode, stream) : launch_gemm_t<kF16>(cfg, a, mode, stream);

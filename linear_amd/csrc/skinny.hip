@@ -189,32 +189,6 @@ skinny_kernel(LinearArgs a) {
     }
 }
 
-// v + (v of lane CTRL's source) on every lane, by a DPP operand (no LDS trip).
-template <int CTRL>
-__device__ inline float dpp_add(float v) {
-    return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf,
-                                                                    false));
-}
-
-__device__ inline float lane_value(float v, int l) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-}
-
-// The sum of v over the wave's 64 lanes, in one fixed order of FP32 additions:
-// pairs, then quads (quad permutations), then the two halves of each row of 8
-// and the two halves of each row of 16 (mirrors), then the four row sums in
-// order.  Each step adds a lane's value to a partner's, and FP32 addition is
-// commutative, so every lane of a group ends with the same bits.  Against the
-// butterfly through LDS permutes (six round trips) this takes 0.2 us off the
-// M = 1 decode launch.
-__device__ inline float wave_sum(float v) {
-    v = dpp_add<0xB1>(v);     // quad_perm [1, 0, 3, 2]
-    v = dpp_add<0x4E>(v);     // quad_perm [2, 3, 0, 1]
-    v = dpp_add<0x141>(v);    // row_half_mirror
-    v = dpp_add<0x140>(v);    // row_mirror
-    return ((lane_value(v, 0) + lane_value(v, 16)) + lane_value(v, 32)) + lane_value(v, 48);
-}
-
 template <int E, int MODE>
 __global__ void __launch_bounds__(kGemvRows * 64)
 gemv_stream(LinearArgs a) {

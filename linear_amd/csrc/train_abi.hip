@@ -111,6 +111,29 @@ lin::ProductArgs product(const uint16_t* a, int64_t sar, int64_t sak, const uint
     return p;
 }
 
+bool al16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
+
+// Tile choice of the streaming kernels, as for the layer: the first (fastest) tile
+// that gives every CU one, else the tile that keeps the most CUs busy at its rate.
+// rows and cols count what the configuration's bm and bn count.
+int choose_tile(const lin::GemmConfig* cfgs, const double* rates, int n, int64_t rows, int64_t cols, int cus) {
+    int best = n - 1;
+    double best_score = -1.0;
+    for (int c = 0; c < n; ++c) {
+        const int64_t tiles = tiles_of(rows, cfgs[c].bm) * tiles_of(cols, cfgs[c].bn);
+        if (tiles >= cus) return c;
+        const double score = (double)tiles * rates[c];
+        if (score > best_score) {
+            best_score = score;
+            best = c;
+        }
+    }
+    return best;
+}
+
+// The layer's rates for the same tiles (relative to the 256 x 256 tile).
+const double kGatedRates[lin::kNumStreamConfigs] = {1.00, 0.94, 0.85, 0.80, 0.65};
+
 int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
                   int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
                   int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
@@ -127,6 +150,35 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
     DevInfo di;
     st = lin::check_device(&dev, &di);
     if (st != LINEAR_OK) return st;
+    if (al16(x, ldx) && al16(wg, ldwg) && al16(wu, ldwu) && K % 8 == 0 && ldx <= lin::kMaxLdIn && ldwg <= lin::kMaxLdIn &&
+        ldwu <= lin::kMaxLdIn) {
+        lin::LinearArgs a;
+        memset(&a, 0, sizeof a);
+        a.x = x;
+        a.w = wg;
+        a.w2 = wu;
+        a.y = h;
+        a.gate = gate;
+        a.up = up;
+        a.ldx = ldx;
+        a.ldw = ldwg;
+        a.ldw2 = ldwu;
+        a.ldy = ldh;
+        a.ldgate = ldgate;
+        a.ldup = ldup;
+        a.M = (int)M;
+        a.N = (int)N;
+        a.K = (int)K;
+        a.act = act;
+        a.vec_gated = (al16(h, ldh) ? 1 : 0) | (al16(gate, ldgate) ? 2 : 0) | (al16(up, ldup) ? 4 : 0);
+        a.groups = 1;
+        a.xcd_shift = di.xcd_shift;
+        const int c = choose_tile(lin::kGatedConfigs, kGatedRates, lin::kNumStreamConfigs, M, 2 * N, di.cus);
+        const lin::GemmConfig& g = lin::kGatedConfigs[c];
+        a.tiles_m = (int)tiles_of(M, g.bm);
+        a.tiles_n = (int)tiles_of(2 * N, g.bn);
+        return launched(lin::launch_gated_stream(elem, c, a, (hipStream_t)stream));
+    }
     lin::ProductArgs p = product(x, ldx, 1, wg, ldwg, 1, h, ldh, M, N, K);
     p.segs = 2;
     p.b[1] = wu;
@@ -252,7 +304,6 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         g.N = (int)N;
         g.Np = (int)Np;
         g.act = act;
-        auto al16 = [](const void* q, int64_t ld) { return (uintptr_t)q % 16 == 0 && ld % 8 == 0; };
         g.vec = al16(dh, lddh) && al16(gate, ldgate) && al16(up, ldup);
         st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
