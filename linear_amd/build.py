@@ -21,7 +21,7 @@ PROBE_SOURCES = ["probe.hip"]
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "indexed.hip", "product.hip", "gradnorm.hip",
-           "gated_f16.hip", "gated_bf16.hip",
+           "gated_f16.hip", "gated_bf16.hip", "grad_f16.hip", "grad_bf16.hip",
            "linear_abi.hip", "train_abi.hip"]
 
 HIPCC_FLAGS = [

@@ -66,7 +66,8 @@ enum : int { kF16 = 0, kBF16 = 1 };
 // Output modes: round the FP32 sum to the element type and add the bias (then
 // round again); round only; store the FP32 sum itself; or round and run the
 // epilogue program of a.epi.  kOutGated: two projections per output, act(g) * u.
-enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 4 };
+// kOutF32Add: add the FP32 sum to the output.
+enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 4, kOutF32Add = 5 };
 
 // Grouped contraction: group g is the activation slice x + g * gsx, the weight
 // block of rows g * N .. g * N + N - 1, y + g * gsy and the bias words g * N ..

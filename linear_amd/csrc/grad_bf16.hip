@@ -1,0 +1,8 @@
+// The gradients' streaming kernels for bfloat16 words.
+#include "grad_impl.h"
+
+namespace lin {
+
+template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);
+
+}  // namespace lin

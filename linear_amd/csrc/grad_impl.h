@@ -1,0 +1,292 @@
+// grad_impl.h -- the streaming MFMA kernels of the gradients' products (templates).
+//
+//     dx [M, K] = dy [M, N] . weight [N, K]        contraction over n
+//     dw [N, K] = dy [M, N]^T . x [M, K]           contraction over m
+//
+// In both the operand that supplies the output columns (weight, x) is contraction-
+// major: one contraction index is a row of memory.  So is dy in dw.  A matrix-core
+// operand holds 8 consecutive contraction indices per lane, so these panels are
+// read out of LDS with the transposing read ds_read_b64_tr_b16: within each group
+// of 16 lanes, lane i receives the elements that lanes 4j + i/4 (j = 0..3) address
+// at their offset i % 4; when the lanes address 4 contraction rows x 16 columns in
+// 8-byte pieces, lane i receives 4 consecutive contraction indices of column i.
+// Nothing is transposed in memory.
+//
+// The tile is the layer's own: columns are the MFMA A operand and rows the B
+// operand, so a lane ends with four consecutive columns of a row; slices of 64
+// contraction indices stream through an LDS ring by direct-to-LDS loads; the
+// fragments of the next K step are read while the MFMAs of the current one run;
+// ends in finish_tile.  v_mfma_f32_16x16x32 throughout.
+//
+// Layout in LDS of a panel slice: 64 rows of B columns (2B bytes), 32-byte column
+// pair u of row k at pair u ^ swz(k), swz(k) = 2 (k mod 4) + (k / 8) mod 2.  The LDS
+// serves a 64-lane 8-byte read 32 lanes at a time: those fetch the pieces of rows
+// 4i .. 4i + 3 and 4i + 8 .. 4i + 11 in one pair, which swz sends to eight
+// different 32-byte bank groups.  A contraction-contiguous row operand (dy in dx)
+// is laid out as in the layer's kernel.
+//
+// The resources are made anew for each slice, from its own first row and with its
+// own length: offsets within a slice stay small whatever the operand's size, rows
+// past the contraction's end read as zero, and a lane's offsets never change.
+#pragma once
+
+#include "gemm_impl.h"
+#include "train.h"
+
+namespace lin {
+
+__host__ __device__ constexpr int panel_swz(int k) { return 2 * (k & 3) | ((k >> 3) & 1); }
+
+// Direct-to-LDS load as lds_dma16, in inline assembly: the compiler does not see an
+// LDS write, so it puts no wait for every load in flight (vmcnt 0) before the
+// transposing reads, which name no LDS bytes it could tell apart.  The ring's own
+// waits (an explicit vmcnt and a barrier per slice) order the two.  There is no
+// register output.  The s_nop covers the wait states after the write of m0, and
+// those between a vector write of a resource word and its use.
+__device__ __forceinline__ void lds_dma16_raw(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r));
+}
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) unsigned char lds_byte;
+
+// LDS bytes at an address (constant offsets from it go into the read instruction).
+__device__ __forceinline__ lds_byte* lds_at(uint32_t addr) { return (lds_byte*)(uintptr_t)addr; }
+
+// The transposing read of 8 bytes per lane.
+__device__ __forceinline__ uint2 lds_tr(lds_byte* p) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)p));
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+    return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+
+// A resource over `bytes` bytes from p (none when negative).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_rsrc(const uint16_t* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, max(bytes, 0), kRsrcWord3);
+}
+
+// Workgroup: one BM x BN tile of one group's output.  ROWT: the row operand is
+// contraction-major too (dw); else contraction-contiguous (dx).
+template <int BM, int BN, int WM, int WN, int STAGES, bool ROWT, int E, int MODE>
+__global__ void __launch_bounds__(WM * WN * 64)
+grad_stream(StreamProduct a) {
+    constexpr int BK = 64, R = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
+    constexpr int NW = WM * WN;
+    constexpr int TM = BM / WM, TN = BN / WN;
+    constexpr int FM = TM / R, FN = TN / R;
+    constexpr int CROW = 2 * BN, RROW = ROWT ? 2 * BM : 2 * BK;   // LDS bytes per row of each panel
+    constexpr int CBYTES = BK * CROW, RBYTES = BM * BK * 2;
+    constexpr int SLICE = CBYTES + RBYTES;
+    constexpr int GC = CBYTES / 1024 / NW, GR = RBYTES / 1024 / NW;   // loads per wave and slice
+    constexpr int GPW = GC + GR;
+    static_assert(CBYTES % (1024 * NW) == 0 && RBYTES % (1024 * NW) == 0, "loads must divide evenly over the waves");
+    static_assert(BN >= 128 && BM >= 128, "the pair swizzle takes 8 pairs per row");
+    static_assert(TM % R == 0 && TN % R == 0, "whole fragments");
+    static_assert(STAGES >= 2 && STAGES * SLICE <= 160 * 1024, "LDS ring too large");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[STAGES * SLICE];
+
+    int tr, tc;
+    tile_coords(blockIdx.x, a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
+    const int group = tr / a.tiles_r;
+    const int r0 = (tr - group * a.tiles_r) * BM, c0 = tc * BN;
+    const uint16_t* rbase = a.r + group * a.rgroup;
+
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t base = lds_address(smem);
+
+    // This wave's loads: GC of the column panel, then GR of the row operand; lane l
+    // lands at byte 16 l of its KB and fetches what the layout places there.
+    uint32_t goff[GPW];
+    // contiguous row operand: the first contraction index fetched, which repeats every
+    // second load (8 rows each, a swizzle of period 16)
+    static_assert(GR % 2 == 0, "a wave's first load must start the swizzle's period");
+    int gk[2];
+#pragma unroll
+    for (int j = 0; j < GPW; ++j) {
+        const bool col = j < GC;
+        const int byte = (col ? wave * GC + j : wave * GR + j - GC) * 1024 + 16 * lane;
+        if (col || ROWT) {
+            const int row = col ? CROW : RROW;
+            const int k = byte / row, c = (byte % row / 16) ^ (2 * panel_swz(k));
+            const int at = (col ? c0 : r0) + 8 * c;
+            goff[j] = at < (col ? a.C : a.R) ? (uint32_t)((k * (int)(col ? a.ldc[0] : a.ldr) + at) * 2) : kOOB;
+        } else {
+            const int r = byte / RROW, c = (byte % RROW / 16) ^ ((r >> 1) & 7);
+            gk[(j - GC) % 2] = 8 * c;
+            goff[j] = r0 + r < a.R ? (uint32_t)((r * (int)a.ldr + 8 * c) * 2) : kOOB;
+        }
+    }
+
+    // slices: each segment's contraction in slices of BK, the segments one after the other
+    const int per = (a.L + BK - 1) / BK;
+    const int nk = per * a.segs;
+
+    // the next slice to request: its LDS slot and resources, from running scalar state.
+    // A row's last 16-byte chunk is read whole (a partly valid one would be dropped): it
+    // is aligned, so it lies in the page of its valid words, and what it holds past
+    // them goes to outputs that are not stored.  With nothing left the lengths are not positive (ld >= its columns), so the
+    // column panel and a contraction-major row operand read zeros; a contiguous one is
+    // masked by its lanes' own indices.
+    const uint16_t* cp = a.c[0];
+    const uint16_t* rp = ROWT ? rbase : rbase + r0 * a.ldr;
+    int left = a.L, seg = 0;                          // contraction indices left in the segment
+    uint32_t fill = base;
+    const int ldc = (int)a.ldc[0], ldr = (int)a.ldr;
+    const int cend = (a.C + 7) & ~7, rend = (a.R + 7) & ~7;
+    const int rbytes = ((min(BM, a.R - r0) - 1) * ldr + BK) * 2;
+    auto request = [&]<int J0, int J1>() {
+        const int n = min(left, BK);
+        const __amdgpu_buffer_rsrc_t rc = slice_rsrc(cp, ((n - 1) * ldc + cend) * 2);
+        const __amdgpu_buffer_rsrc_t rr = slice_rsrc(rp, ROWT ? ((n - 1) * ldr + rend) * 2 : rbytes);
+        static_for<J0, J1>([&]<int j>() {
+            if constexpr (j < GC) lds_dma16_raw(rc, fill + (wave * GC + j) * 1024, goff[j]);
+            else if constexpr (ROWT) lds_dma16_raw(rr, fill + CBYTES + (wave * GR + j - GC) * 1024, goff[j]);
+            else
+                lds_dma16_raw(rr, fill + CBYTES + (wave * GR + j - GC) * 1024, gk[(j - GC) % 2] < left ? goff[j] : kOOB);
+        });
+    };
+    auto next = [&]() {
+        fill = fill == base + (STAGES - 1) * SLICE ? base : fill + SLICE;
+        left -= BK;
+        cp += BK * ldc;
+        rp += ROWT ? BK * ldr : BK;
+        if (left <= 0 && seg + 1 < a.segs) {
+            ++seg;
+            left = a.L;
+            cp = a.c[1];
+        }
+    };
+
+    const int wn = wave % WN, wm = wave / WN;
+    // transposing reads: lane (q = lane / 16, s = lane % 16) addresses row 32 ks + 8 q +
+    // s / 4 (+ 4 for the second read) and the 8-byte piece at column 4 (s % 4) of its
+    // fragment's 16; the row's swizzle is the same for both reads and every ks
+    const int q = lane >> 4, s = lane & 15;
+    const int kq = 8 * q + (s >> 2), sw = panel_swz(kq);
+    uint32_t coff[FN], roff[ROWT ? FM : KS];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+        coff[i] = kq * CROW + ((((wn * TN) / 16 + i) ^ sw) << 5) + 8 * (s & 3);
+    if constexpr (ROWT) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            roff[j] = CBYTES + kq * RROW + ((((wm * TM) / 16 + j) ^ sw) << 5) + 8 * (s & 3);
+    } else {
+        // row lr of fragment j, chunk 4 ks + q: the swizzle (r / 2) % 8 is the same for every j
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) roff[ks] = CBYTES + (wm * TM + s) * RROW + (((4 * ks + q) ^ ((s >> 1) & 7)) << 4);
+    }
+    auto read_col = [&]<int ks, int i>(uint32_t slot) {
+        lds_byte* p = lds_at(slot + coff[i]);
+        const uint2 lo = lds_tr(p + 32 * ks * CROW), hi = lds_tr(p + (32 * ks + 4) * CROW);
+        return (u32x4){lo.x, lo.y, hi.x, hi.y};
+    };
+    auto read_row = [&]<int ks, int j>(uint32_t slot) {
+        if constexpr (ROWT) {
+            lds_byte* p = lds_at(slot + roff[j]);
+            const uint2 lo = lds_tr(p + 32 * ks * RROW), hi = lds_tr(p + (32 * ks + 4) * RROW);
+            return (u32x4){lo.x, lo.y, hi.x, hi.y};
+        } else {
+            return *(lds_u32x4*)(lds_at(slot + roff[ks]) + j * R * RROW);
+        }
+    };
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = (f32x4){};
+
+    if (nk > 0) {
+        // requests past the last slice carry empty resources, so every wait is static
+#pragma unroll
+        for (int t = 0; t < STAGES; ++t) {
+            request.template operator()<0, GPW>();
+            next();
+        }
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 1) * GPW) : "memory");
+        lds_barrier();
+        // the column fragments are double buffered; a row fragment's next value is read
+        // right after the MFMAs that use it
+        u32x4 ca[2][FN], rb[FM];
+        static_for<0, FN>([&]<int i>() { ca[0][i] = read_col.template operator()<0, i>(base); });
+        static_for<0, FM>([&]<int j>() { rb[j] = read_row.template operator()<0, j>(base); });
+        // the MFMAs of the step in buffer CUR while step NKS of the slice at `slot` is read
+        auto step = [&]<int CUR, int NKS, bool LOADS>(uint32_t slot) {
+            static_for<0, FN>([&]<int i>() { ca[CUR ^ 1][i] = read_col.template operator()<NKS, i>(slot); });
+            __builtin_amdgcn_sched_barrier(0);
+            static_for<0, FM>([&]<int j>() {
+#pragma unroll
+                for (int i = 0; i < FN; ++i) acc[i][j] = mfma16x16x32<E>(ca[CUR][i], rb[j], acc[i][j]);
+                __builtin_amdgcn_sched_barrier(0);   // the read takes the registers just used
+                rb[j] = read_row.template operator()<NKS, j>(slot);
+                if constexpr (LOADS) {
+                    constexpr int J0 = GPW * j / FM, J1 = GPW * (j + 1) / FM;
+                    if constexpr (J1 > J0) request.template operator()<J0, J1>();
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        };
+        uint32_t slot = base;
+        for (int t = 0; t + 1 < nk; ++t) {
+            step.template operator()<0, 1, false>(slot);
+            slot = (t + 1) % STAGES == 0 ? base : slot + SLICE;
+            // slice t + 1 has landed, and every wave has read slot t's last step
+            asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 2) * GPW) : "memory");
+            lds_barrier();
+            step.template operator()<1, 0, true>(slot);
+            next();
+        }
+        step.template operator()<0, 1, false>(slot);
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+#pragma unroll
+            for (int i = 0; i < FN; ++i) acc[i][j] = mfma16x16x32<E>(ca[1][i], rb[j], acc[i][j]);
+        // the empty requests past the end must land before the LDS is used again
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
+
+    LinearArgs o;
+    o.y = a.y[0];
+    o.ldy = a.ldy[0];
+    if (group) {
+        o.y = a.y[1];
+        o.ldy = a.ldy[1];
+    }
+    o.M = a.R;
+    o.N = a.C;
+    o.vec_store = (a.vec >> group) & 1;
+    o.epi.vec16 = (a.vec >> group) & 1;
+    finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
+}
+
+static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
+    StreamProduct args = a;
+    void* params[] = {&args};
+    return hipLaunchKernel(fn, dim3((unsigned)(a.groups * a.tiles_r * a.tiles_c)), dim3(threads), params, 0, stream);
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int E>
+static const void* grad_fn(bool rowt, int mode) {
+    if (!rowt) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutRound>;
+    if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32>;
+    if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32Add>;
+    return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutRound>;
+}
+
+template <int E>
+hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream) {
+    switch (cfg) {
+        case 0: return launch_product(grad_fn<256, 256, 2, 4, 2, E>(rowt, mode), a, 512, stream);
+        case 1: return launch_product(grad_fn<256, 128, 4, 2, 3, E>(rowt, mode), a, 512, stream);
+        case 2: return launch_product(grad_fn<128, 128, 2, 2, 4, E>(rowt, mode), a, 256, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace lin

@@ -37,6 +37,39 @@ enum : int { kProdRound = 0, kProdF32 = 1, kProdGated = 2 };
 constexpr int kProdTile = 64;
 hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStream_t stream);
 
+// The streaming products of the gradients (16-byte aligned layouts):
+//     y[g][r, c] = sum over segments s, k < L of row(g)[r, s Lp + k] * c[s][k, c]
+// Columns c[s] are contraction-major [L, C].  The row operand is [L, R] per group, at
+// columns g * rgroup of r (contraction-major: dw, one segment), or [R, segs * Lp]
+// contraction-contiguous (dx, one group); Lp is L rounded up to whole slices when
+// there are two segments.
+struct StreamProduct {
+    const uint16_t* r;
+    const uint16_t* c[2];
+    int64_t ldr, ldc[2], rgroup;
+    void* y[2];
+    int64_t ldy[2];
+    int R, C, L;
+    int segs, groups;
+    int tiles_r, tiles_c;
+    int vec;                 // bit g: y[g] takes 16-byte stores
+    int xcd_shift;
+};
+constexpr int kNumGradConfigs = 3;
+inline constexpr GemmConfig kGradConfigs[kNumGradConfigs] = {
+    {256, 256, 2, 4, 2, 64},
+    {256, 128, 4, 2, 3, 64},
+    {128, 128, 2, 2, 4, 64},
+};
+// rowt: contraction-major row operand; mode kOutRound, or with rowt kOutF32 or kOutF32Add.
+template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
+extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
+extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);
+inline hipError_t launch_grad_stream(int elem, int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream) {
+    return elem == kBF16 ? launch_grad_stream_t<kBF16>(cfg, rowt, mode, a, stream)
+                         : launch_grad_stream_t<kF16>(cfg, rowt, mode, a, stream);
+}
+
 // dg = dh * u * act'(g), du = dh * act(g), rounded to the element type, into the
 // two halves of d [M, 2 * Np]: columns [0, N) and [Np, Np + N); columns between
 // N and Np are zeroed.

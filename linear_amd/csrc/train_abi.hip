@@ -113,18 +113,18 @@ lin::ProductArgs product(const uint16_t* a, int64_t sar, int64_t sak, const uint
 
 bool al16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 
-// Tile choice of the streaming kernels, as for the layer: the first (fastest) tile
-// that gives every CU one, else the tile that keeps the most CUs busy at its rate.
+// Tile choice of the streaming kernels: the least rounds of tiles over the CUs, each
+// round as long as a tile's outputs at its rate; the earlier (larger) tile of equals.
 // rows and cols count what the configuration's bm and bn count.
-int choose_tile(const lin::GemmConfig* cfgs, const double* rates, int n, int64_t rows, int64_t cols, int cus) {
-    int best = n - 1;
-    double best_score = -1.0;
+int choose_tile(const lin::GemmConfig* cfgs, const double* rates, int n, int64_t groups, int64_t rows, int64_t cols,
+                int cus) {
+    int best = 0;
+    double best_cost = -1.0;
     for (int c = 0; c < n; ++c) {
-        const int64_t tiles = tiles_of(rows, cfgs[c].bm) * tiles_of(cols, cfgs[c].bn);
-        if (tiles >= cus) return c;
-        const double score = (double)tiles * rates[c];
-        if (score > best_score) {
-            best_score = score;
+        const int64_t tiles = groups * tiles_of(rows, cfgs[c].bm) * tiles_of(cols, cfgs[c].bn);
+        const double cost = (double)tiles_of(tiles, cus) * cfgs[c].bm * cfgs[c].bn / rates[c];
+        if (best_cost < 0 || cost < best_cost) {
+            best_cost = cost;
             best = c;
         }
     }
@@ -173,7 +173,7 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
         a.vec_gated = (al16(h, ldh) ? 1 : 0) | (al16(gate, ldgate) ? 2 : 0) | (al16(up, ldup) ? 4 : 0);
         a.groups = 1;
         a.xcd_shift = di.xcd_shift;
-        const int c = choose_tile(lin::kGatedConfigs, kGatedRates, lin::kNumStreamConfigs, M, 2 * N, di.cus);
+        const int c = choose_tile(lin::kGatedConfigs, kGatedRates, lin::kNumStreamConfigs, 1, M, 2 * N, di.cus);
         const lin::GemmConfig& g = lin::kGatedConfigs[c];
         a.tiles_m = (int)tiles_of(M, g.bm);
         a.tiles_n = (int)tiles_of(2 * N, g.bn);
@@ -191,6 +191,24 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
     p.act = act;
     return launched(lin::launch_product_any(elem, lin::kProdGated, p, (hipStream_t)stream));
 }
+
+const double kGradRates[lin::kNumGradConfigs] = {1.00, 0.94, 0.80};
+
+// A streaming product's shape, tile and launch; the operands are set by the caller.
+hipError_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, const DevInfo& di, hipStream_t stream) {
+    const int c = choose_tile(lin::kGradConfigs, kGradRates, lin::kNumGradConfigs, a.groups, a.R, a.C, di.cus);
+    const lin::GemmConfig& g = lin::kGradConfigs[c];
+    a.tiles_r = (int)tiles_of(a.R, g.bm);
+    a.tiles_c = (int)tiles_of(a.C, g.bn);
+    a.xcd_shift = di.xcd_shift;
+    const int64_t eb = mode == lin::kOutRound ? 2 : 4;
+    for (int i = 0; i < a.groups; ++i)
+        if ((uintptr_t)a.y[i] % 16 == 0 && a.ldy[i] * eb % 16 == 0) a.vec |= 1 << i;
+    return lin::launch_grad_stream(elem, c, rowt, mode, a, stream);
+}
+
+// What the streaming kernels read: 16-byte chunks of rows, offsets of a tile's rows in 32 bits.
+bool streamable(const void* p, int64_t ld) { return al16(p, ld) && ld <= lin::kMaxLdIn; }
 
 int32_t check_workspace(const void* ws, int64_t have, int64_t need) {
     if (need == 0) return LINEAR_OK;
@@ -217,6 +235,21 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
     DevInfo di;
     st = lin::check_device(&dev, &di);
     if (st != LINEAR_OK) return st;
+    if (streamable(dy, lddy) && streamable(w, ldw) && N % 8 == 0) {
+        lin::StreamProduct a;
+        memset(&a, 0, sizeof a);
+        a.r = dy;
+        a.ldr = lddy;
+        a.c[0] = w;
+        a.ldc[0] = ldw;
+        a.y[0] = dx;
+        a.ldy[0] = lddx;
+        a.R = (int)M;
+        a.C = (int)K;
+        a.L = (int)N;
+        a.segs = a.groups = 1;
+        return launched(launch_stream(elem, false, lin::kOutRound, a, di, (hipStream_t)stream));
+    }
     const lin::ProductArgs p = product(dy, lddy, 1, w, 1, ldw, dx, lddx, M, K, N);
     return launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
 }
@@ -256,6 +289,22 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
         if (st != LINEAR_OK) return st;
     }
     if (K == 0) return LINEAR_OK;
+    if (streamable(dy, lddy) && streamable(x, ldx)) {
+        lin::StreamProduct a;
+        memset(&a, 0, sizeof a);
+        a.r = dy;
+        a.ldr = lddy;
+        a.c[0] = x;
+        a.ldc[0] = ldx;
+        a.y[0] = dw;
+        a.ldy[0] = lddw;
+        a.R = (int)N;
+        a.C = (int)K;
+        a.L = (int)M;
+        a.segs = a.groups = 1;
+        const int mode = !f32 ? lin::kOutRound : accumulate ? lin::kOutF32Add : lin::kOutF32;
+        return launched(launch_stream(elem, true, mode, a, di, (hipStream_t)stream));
+    }
     lin::ProductArgs p = product(dy, 1, lddy, x, 1, ldx, dw, lddw, N, K, M);
     p.accumulate = f32 && accumulate != 0;
     return launched(lin::launch_product_any(elem, f32 ? lin::kProdF32 : lin::kProdRound, p, (hipStream_t)stream));
@@ -308,7 +357,25 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
-    if (want_dx) {
+    const bool dx_streams = streamable(wg, ldwg) && ldwu == ldwg && al16(wu, ldwu) && 2 * Np <= lin::kMaxLdIn;
+    if (want_dx && dx_streams) {
+        lin::StreamProduct a;
+        memset(&a, 0, sizeof a);
+        a.r = d;
+        a.ldr = 2 * Np;
+        a.c[0] = wg;
+        a.c[1] = wu;
+        a.ldc[0] = a.ldc[1] = ldwg;
+        a.y[0] = dx;
+        a.ldy[0] = lddx;
+        a.R = (int)M;
+        a.C = (int)K;
+        a.L = (int)N;
+        a.segs = 2;
+        a.groups = 1;
+        st = launched(launch_stream(elem, false, lin::kOutRound, a, di, (hipStream_t)stream));
+        if (st != LINEAR_OK) return st;
+    } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, 1, wg, 1, ldwg, dx, lddx, M, K, N);
         p.segs = 2;
         p.a[1] = d + Np;
@@ -318,7 +385,26 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
-    if (want_dw) {
+    if (want_dw && streamable(x, ldx) && 2 * Np <= lin::kMaxLdIn) {
+        lin::StreamProduct a;
+        memset(&a, 0, sizeof a);
+        a.r = d;
+        a.ldr = 2 * Np;
+        a.rgroup = Np;
+        a.c[0] = x;
+        a.ldc[0] = ldx;
+        a.y[0] = dwg;
+        a.y[1] = dwu;
+        a.ldy[0] = lddwg;
+        a.ldy[1] = lddwu;
+        a.R = (int)N;
+        a.C = (int)K;
+        a.L = (int)M;
+        a.segs = 1;
+        a.groups = 2;
+        st = launched(launch_stream(elem, true, lin::kOutRound, a, di, (hipStream_t)stream));
+        if (st != LINEAR_OK) return st;
+    } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
             const lin::ProductArgs p = product(d + s * Np, 1, 2 * Np, x, 1, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
             st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));

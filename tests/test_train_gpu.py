@@ -16,6 +16,8 @@ SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1024, 768), (1, 4096, 4096), (1, 24, 40000
           (16, 256, 128), (16, 2048, 1536), (17, 520, 264), (64, 64, 64), (65, 127, 130), (128, 512, 256), (130, 72, 4096),
           (200, 300, 520), (257, 264, 1032), (300, 1000, 768), (512, 768, 512), (1000, 328, 2056), (2050, 200, 264),
           (1040, 2560, 1288)]
+# enough tiles for each of the larger tile sizes to be the choice
+LARGE = [(4100, 2056, 136), (2100, 1032, 520), (4100, 1032, 72), (120, 16392, 200), (600, 520, 264)]
 
 
 def fn(name, t):
@@ -43,9 +45,9 @@ def make(M, N, K, t, seed=0):
 
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
-@pytest.mark.parametrize("i", range(len(SHAPES)), ids=["%dx%dx%d" % s for s in SHAPES])
+@pytest.mark.parametrize("i", range(len(SHAPES + LARGE)), ids=["%dx%dx%d" % s for s in SHAPES + LARGE])
 def test_gated(i, t):
-    M, N, K = SHAPES[i]
+    M, N, K = (SHAPES + LARGE)[i]
     act = ACTS[i % 3]
     x, wg, wu, _ = make(M, N, K, t)
     want, bound = ref.gated64(x, wg, wu, act, t)
@@ -227,7 +229,9 @@ def test_linear_backward(i, wide, t):
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 @pytest.mark.parametrize("M,N,K", [(1, 8, 8), (3, 64, 136), (70, 65, 33), (128, 256, 256), (300, 1000, 264), (520, 264, 776),
-                                   (1030, 2056, 520), (4100, 300, 328)])
+                                   (1030, 2056, 520), (4100, 300, 328),
+                                   (200, 2568, 2560), (333, 4104, 4100), (4100, 333, 4104), (2568, 200, 2560), (2564, 2568, 24),
+                                   (4100, 4104, 72)])
 def test_linear_backward_of_small_integers_is_exact(M, N, K, t):
     """Words -2 .. 2: every sum is an integer far below 2^24, so FP32 holds it exactly in any order."""
     gen = torch.Generator().manual_seed(M)
