@@ -22,7 +22,8 @@
 // pair u of row k at pair u ^ swz(k), swz(k) = 2 (k mod 4) + (k / 8) mod 2.  The LDS
 // serves a 64-lane 8-byte read 32 lanes at a time: those fetch the pieces of rows
 // 4i .. 4i + 3 and 4i + 8 .. 4i + 11 in one pair, which swz sends to eight
-// different 32-byte bank groups.  A contraction-contiguous row operand (dy in dx)
+// different 32-byte bank groups.  A 64-column panel has four pairs a row and two rows
+// in 256 bytes: there swz(k) = (k / 2) mod 2 + 2 ((k / 8) mod 2).  A contraction-contiguous row operand (dy in dx)
 // is laid out as in the layer's kernel.
 //
 // The resources are made anew for each slice, from its own first row and with its
@@ -35,7 +36,10 @@
 
 namespace lin {
 
-__host__ __device__ constexpr int panel_swz(int k) { return 2 * (k & 3) | ((k >> 3) & 1); }
+template <int B>
+__host__ __device__ constexpr int panel_swz(int k) {
+    return B == 64 ? ((k >> 1) & 1) | (((k >> 3) & 1) << 1) : 2 * (k & 3) | ((k >> 3) & 1);
+}
 
 // Direct-to-LDS load as lds_dma16, in inline assembly: the compiler does not see an
 // LDS write, so it puts no wait for every load in flight (vmcnt 0) before the
@@ -84,15 +88,17 @@ grad_stream(StreamProduct a) {
     constexpr int GC = CBYTES / 1024 / NW, GR = RBYTES / 1024 / NW;   // loads per wave and slice
     constexpr int GPW = GC + GR;
     static_assert(CBYTES % (1024 * NW) == 0 && RBYTES % (1024 * NW) == 0, "loads must divide evenly over the waves");
-    static_assert(BN >= 128 && BM >= 128, "the pair swizzle takes 8 pairs per row");
+    static_assert(BN >= 64 && BM >= 64, "panel rows of 4 or more pairs");
     static_assert(TM % R == 0 && TN % R == 0, "whole fragments");
     static_assert(STAGES >= 2 && STAGES * SLICE <= 160 * 1024, "LDS ring too large");
     __shared__ __attribute__((aligned(1024))) unsigned char smem[STAGES * SLICE];
 
     int tr, tc;
-    tile_coords(blockIdx.x, a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
-    const int group = tr / a.tiles_r;
-    const int r0 = (tr - group * a.tiles_r) * BM, c0 = tc * BN;
+    // row tiles of every group of every split, stacked into one grid
+    tile_coords(blockIdx.x, a.splits * a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
+    const int stack = tr / a.tiles_r;                 // split * groups + group
+    const int split = stack / a.groups, group = stack - split * a.groups;
+    const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
 
     const int lane = threadIdx.x & 63;
@@ -112,7 +118,7 @@ grad_stream(StreamProduct a) {
         const int byte = (col ? wave * GC + j : wave * GR + j - GC) * 1024 + 16 * lane;
         if (col || ROWT) {
             const int row = col ? CROW : RROW;
-            const int k = byte / row, c = (byte % row / 16) ^ (2 * panel_swz(k));
+            const int k = byte / row, c = (byte % row / 16) ^ (2 * (col ? panel_swz<BN>(k) : panel_swz<BM>(k)));
             const int at = (col ? c0 : r0) + 8 * c;
             goff[j] = at < (col ? a.C : a.R) ? (uint32_t)((k * (int)(col ? a.ldc[0] : a.ldr) + at) * 2) : kOOB;
         } else {
@@ -123,8 +129,10 @@ grad_stream(StreamProduct a) {
     }
 
     // slices: each segment's contraction in slices of BK, the segments one after the other
+    // (split s takes a contiguous share of all of them)
     const int per = (a.L + BK - 1) / BK;
-    const int nk = per * a.segs;
+    const int t0 = (int)((int64_t)per * a.segs * split / a.splits);
+    const int nk = (int)((int64_t)per * a.segs * (split + 1) / a.splits) - t0;
 
     // the next slice to request: its LDS slot and resources, from running scalar state.
     // A row's last 16-byte chunk is read whole (a partly valid one would be dropped): it
@@ -132,9 +140,12 @@ grad_stream(StreamProduct a) {
     // them goes to outputs that are not stored.  With nothing left the lengths are not positive (ld >= its columns), so the
     // column panel and a contraction-major row operand read zeros; a contiguous one is
     // masked by its lanes' own indices.
-    const uint16_t* cp = a.c[0];
-    const uint16_t* rp = ROWT ? rbase : rbase + r0 * a.ldr;
-    int left = a.L, seg = 0;                          // contraction indices left in the segment
+    int seg = t0 >= per ? 1 : 0;
+    const int first = (t0 - seg * per) * BK;
+    const uint16_t* cp = a.c[seg] + first * a.ldc[0];
+    const uint16_t* rp = ROWT ? rbase + first * a.ldr : rbase + r0 * a.ldr + (int64_t)t0 * BK;
+    int left = nk > 0 ? a.L - first : 0;              // contraction indices left in the segment
+    int todo = nk;                                    // slices left to request
     uint32_t fill = base;
     const int ldc = (int)a.ldc[0], ldr = (int)a.ldr;
     const int cend = (a.C + 7) & ~7, rend = (a.R + 7) & ~7;
@@ -160,6 +171,7 @@ grad_stream(StreamProduct a) {
             left = a.L;
             cp = a.c[1];
         }
+        if (--todo <= 0) left = 0;
     };
 
     const int wn = wave % WN, wm = wave / WN;
@@ -167,15 +179,15 @@ grad_stream(StreamProduct a) {
     // s / 4 (+ 4 for the second read) and the 8-byte piece at column 4 (s % 4) of its
     // fragment's 16; the row's swizzle is the same for both reads and every ks
     const int q = lane >> 4, s = lane & 15;
-    const int kq = 8 * q + (s >> 2), sw = panel_swz(kq);
+    const int kq = 8 * q + (s >> 2);
     uint32_t coff[FN], roff[ROWT ? FM : KS];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
-        coff[i] = kq * CROW + ((((wn * TN) / 16 + i) ^ sw) << 5) + 8 * (s & 3);
+        coff[i] = kq * CROW + ((((wn * TN) / 16 + i) ^ panel_swz<BN>(kq)) << 5) + 8 * (s & 3);
     if constexpr (ROWT) {
 #pragma unroll
         for (int j = 0; j < FM; ++j)
-            roff[j] = CBYTES + kq * RROW + ((((wm * TM) / 16 + j) ^ sw) << 5) + 8 * (s & 3);
+            roff[j] = CBYTES + kq * RROW + ((((wm * TM) / 16 + j) ^ panel_swz<BM>(kq)) << 5) + 8 * (s & 3);
     } else {
         // row lr of fragment j, chunk 4 ks + q: the swizzle (r / 2) % 8 is the same for every j
 #pragma unroll
@@ -252,28 +264,33 @@ grad_stream(StreamProduct a) {
     }
 
     LinearArgs o;
-    o.y = a.y[0];
-    o.ldy = a.ldy[0];
-    if (group) {
-        o.y = a.y[1];
-        o.ldy = a.ldy[1];
-    }
     o.M = a.R;
     o.N = a.C;
-    o.vec_store = (a.vec >> group) & 1;
-    o.epi.vec16 = (a.vec >> group) & 1;
+    if (a.splits > 1) {                               // FP32 partial sums (kOutF32)
+        o.y = a.partial + (int64_t)stack * a.R * a.ldp;
+        o.ldy = a.ldp;
+        o.vec_store = o.epi.vec16 = 1;
+    } else {
+        o.y = group ? a.y[1] : a.y[0];
+        o.ldy = group ? a.ldy[1] : a.ldy[0];
+        o.vec_store = o.epi.vec16 = (a.vec >> group) & 1;
+    }
     finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
 }
 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
     StreamProduct args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)(a.groups * a.tiles_r * a.tiles_c)), dim3(threads), params, 0, stream);
+    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c)), dim3(threads), params, 0,
+                           stream);
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, int E>
 static const void* grad_fn(bool rowt, int mode) {
-    if (!rowt) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutRound>;
+    if (!rowt) {
+        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutF32>;
+        return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutRound>;
+    }
     if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32>;
     if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32Add>;
     return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutRound>;
@@ -284,7 +301,8 @@ hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduc
     switch (cfg) {
         case 0: return launch_product(grad_fn<256, 256, 2, 4, 2, E>(rowt, mode), a, 512, stream);
         case 1: return launch_product(grad_fn<256, 128, 4, 2, 3, E>(rowt, mode), a, 512, stream);
-        case 2: return launch_product(grad_fn<128, 128, 2, 2, 4, E>(rowt, mode), a, 256, stream);
+        case 2: return launch_product(grad_fn<128, 128, 2, 4, 4, E>(rowt, mode), a, 512, stream);
+        case 3: return launch_product(grad_fn<64, 64, 2, 2, 4, E>(rowt, mode), a, 256, stream);
         default: return hipErrorInvalidValue;
     }
 }

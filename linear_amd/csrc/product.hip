@@ -95,6 +95,58 @@ __global__ void __launch_bounds__(256) product_any(ProductArgs p) {
     }
 }
 
+// One thread per four columns of a row; the splits are added in their order.
+template <int E, bool F32>
+__global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
+    const int chunks = (a.C + 3) / 4;
+    const int64_t total = (int64_t)a.groups * a.R * chunks, plane = (int64_t)a.groups * a.R * a.ldp;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t gr = i / chunks;                   // group * R + row
+        const int c = (int)(i - gr * chunks) * 4;
+        const float* p = a.partial + gr * a.ldp + c;
+        f32x4 v = *(const f32x4*)p;
+        int s = 1;
+        for (; s + 3 < a.splits; s += 4) {              // four loads in flight
+            f32x4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = *(const f32x4*)(p + (s + j) * plane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v += w[j];
+        }
+        f32x4 w[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) w[j] = s + j < a.splits ? *(const f32x4*)(p + (s + j) * plane) : (f32x4){};
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (s + j < a.splits) v += w[j];
+        const int g = gr >= a.R ? 1 : 0;
+        const int64_t at = (gr - (int64_t)g * a.R) * a.ldy[g] + c;
+        const bool vec = ((a.vec >> g) & 1) && c + 3 < a.C;
+        if constexpr (F32) {
+            float* y = (float*)a.y[g] + at;
+            if (vec) {
+                *(f32x4*)y = a.accumulate ? *(const f32x4*)y + v : v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.C) y[e] = a.accumulate ? y[e] + v[e] : v[e];
+            }
+        } else {
+            uint16_t* y = (uint16_t*)a.y[g] + at;
+            uint2 u;
+            u.x = (uint32_t)narrow<E>(v[0]) | ((uint32_t)narrow<E>(v[1]) << 16);
+            u.y = (uint32_t)narrow<E>(v[2]) | ((uint32_t)narrow<E>(v[3]) << 16);
+            if (vec) {
+                *(uint2*)y = u;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < a.C) y[e] = narrow<E>(v[e]);
+            }
+        }
+    }
+}
+
 template <int E>
 __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     const int chunks = g.Np / 8;                     // 8-column pieces of a row of one half
@@ -122,35 +174,63 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     }
 }
 
-// Partial sums of one split of the rows: thread t of 256 takes column
-// 64 blockIdx.x + t % 64 and every fourth row; the four are added in order.
-template <int E>
-__global__ void __launch_bounds__(256) column_partials(ColumnSumArgs c) {
-    __shared__ float part[4][64];
-    const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-    const int n = blockIdx.x * 64 + lane, s = blockIdx.y;
-    const int m0 = (int)((int64_t)c.M * s / c.splits), m1 = (int)((int64_t)c.M * (s + 1) / c.splits);
-    float sum = 0.f;
-    if (n < c.N)
-        for (int m = m0 + g; m < m1; m += 4) sum += widen<E>(c.dy[(int64_t)m * c.lddy + n]);
-    part[g][lane] = sum;
-    __syncthreads();
-    if (g == 0 && n < c.N)
-        c.partial[(int64_t)s * c.N + n] = ((part[0][lane] + part[1][lane]) + part[2][lane]) + part[3][lane];
-}
-
-template <int E>
-__global__ void __launch_bounds__(64) column_finish(ColumnSumArgs c) {
-    const int n = blockIdx.x * 64 + threadIdx.x;
-    if (n >= c.N) return;
-    float sum = 0.f;
-    for (int s = 0; s < c.splits; ++s) sum += c.partial[(int64_t)s * c.N + n];
+__device__ inline void store_sum(const ColumnSumArgs& c, int elem, int n, float sum) {
     if (c.f32) {
         float* y = (float*)c.db + n;
         *y = c.accumulate ? *y + sum : sum;
     } else {
-        ((uint16_t*)c.db)[n] = narrow<E>(sum);
+        ((uint16_t*)c.db)[n] = elem == kBF16 ? narrow<kBF16>(sum) : narrow<kF16>(sum);
     }
+}
+
+// Column sums over one split of the rows, 64 columns per workgroup: thread t takes
+// the 8 columns 8 (t % 8) of every 128th row from t / 8, four rows' loads in flight;
+// then 16 threads per column add 8 row groups each, and one adds the 16.  A single
+// split stores db itself.  (8192 x 4096 bf16, 64 MB: 16 splits.)
+template <int E>
+__global__ void __launch_bounds__(1024) column_partials(ColumnSumArgs c) {
+    __shared__ float part[128][65];
+    __shared__ float part2[16][64];
+    const int tid = threadIdx.x, c8 = (tid & 7) * 8, g = tid >> 3;
+    const int n = blockIdx.x * 64 + c8, s = blockIdx.y;
+    const int m0 = (int)((int64_t)c.M * s / c.splits), m1 = (int)((int64_t)c.M * (s + 1) / c.splits);
+    float sum[8] = {};
+    for (int64_t m = m0 + g; m < m1; m += 512) {
+        u32x4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = load8(c.dy + (m + 128 * j) * c.lddy + n, m + 128 * j < m1, n, c.N, c.vec);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += widen<E>((uint16_t)(v[j][e >> 1] >> (16 * (e & 1))));
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[g][c8 + e] = sum[e];
+    __syncthreads();
+    const int col = tid & 63, h = tid >> 6;
+    float t = part[8 * h][col];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t += part[8 * h + i][col];
+    part2[h][col] = t;
+    __syncthreads();
+    const int out = blockIdx.x * 64 + tid;
+    if (tid >= 64 || out >= c.N) return;
+    t = part2[0][tid];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) t += part2[i][tid];
+    if (c.splits == 1) store_sum(c, E, out, t);
+    else c.partial[(int64_t)s * c.N + out] = t;
+}
+
+// The splits' sums, in their order.
+template <int E>
+__global__ void __launch_bounds__(64) column_finish(ColumnSumArgs c) {
+    const int n = blockIdx.x * 64 + threadIdx.x;
+    if (n >= c.N) return;
+    float sum = c.partial[n];
+#pragma unroll 8
+    for (int s = 1; s < c.splits; ++s) sum += c.partial[(int64_t)s * c.N + n];
+    store_sum(c, E, n, sum);
 }
 
 template <int E>
@@ -169,6 +249,15 @@ hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStrea
                            dim3((unsigned)(p.tiles_r * p.tiles_c)), dim3(256), params, 0, stream);
 }
 
+hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStream_t stream) {
+    StreamProduct args = a;
+    void* params[] = {&args};
+    const int64_t blocks = ((int64_t)a.groups * a.R * ((a.C + 3) / 4) + 255) / 256;
+    const void* fn = f32 ? (const void*)split_sum<kF16, true>
+                         : elem == kBF16 ? (const void*)split_sum<kBF16, false> : (const void*)split_sum<kF16, false>;
+    return hipLaunchKernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
+}
+
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream) {
     GatedGradArgs args = g;
     void* params[] = {&args};
@@ -182,8 +271,8 @@ hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t strea
     void* params[] = {&args};
     const unsigned gx = (unsigned)((c.N + 63) / 64);
     hipError_t e = hipLaunchKernel(elem == kBF16 ? (const void*)column_partials<kBF16> : (const void*)column_partials<kF16>,
-                                   dim3(gx, (unsigned)c.splits), dim3(256), params, 0, stream);
-    if (e != hipSuccess) return e;
+                                   dim3(gx, (unsigned)c.splits), dim3(1024), params, 0, stream);
+    if (e != hipSuccess || c.splits == 1) return e;
     return hipLaunchKernel(elem == kBF16 ? (const void*)column_finish<kBF16> : (const void*)column_finish<kF16>,
                            dim3(gx), dim3(64), params, 0, stream);
 }

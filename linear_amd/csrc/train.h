@@ -54,14 +54,21 @@ struct StreamProduct {
     int tiles_r, tiles_c;
     int vec;                 // bit g: y[g] takes 16-byte stores
     int xcd_shift;
+    // the contraction's slices shared among `splits` sets of tiles (more than one:
+    // FP32 partial sums [splits, groups, R] rows of ldp, added by launch_split_sum)
+    int splits;
+    float* partial;
+    int64_t ldp;
+    int accumulate;          // launch_split_sum into floats: y += sum
 };
-constexpr int kNumGradConfigs = 3;
+constexpr int kNumGradConfigs = 4;
 inline constexpr GemmConfig kGradConfigs[kNumGradConfigs] = {
     {256, 256, 2, 4, 2, 64},
     {256, 128, 4, 2, 3, 64},
-    {128, 128, 2, 2, 4, 64},
+    {128, 128, 2, 4, 4, 64},
+    {64, 64, 2, 2, 4, 64},
 };
-// rowt: contraction-major row operand; mode kOutRound, or with rowt kOutF32 or kOutF32Add.
+// rowt: contraction-major row operand; mode kOutRound, kOutF32, or with rowt kOutF32Add.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);
@@ -69,6 +76,9 @@ inline hipError_t launch_grad_stream(int elem, int cfg, bool rowt, int mode, con
     return elem == kBF16 ? launch_grad_stream_t<kBF16>(cfg, rowt, mode, a, stream)
                          : launch_grad_stream_t<kF16>(cfg, rowt, mode, a, stream);
 }
+
+// y[g] = the partial sums' total, in order of the splits: rounded to elem's type, or floats.
+hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStream_t stream);
 
 // dg = dh * u * act'(g), du = dh * act(g), rounded to the element type, into the
 // two halves of d [M, 2 * Np]: columns [0, N) and [Np, Np + N); columns between
@@ -87,16 +97,18 @@ hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t strea
 struct ColumnSumArgs {
     const uint16_t* dy;
     int64_t lddy;
-    float* partial;          // [splits, N]
+    float* partial;          // [splits, N] (more than one split)
     void* db;                // 16-bit words or floats
     int M, N, splits;
     int f32, accumulate;
+    int vec;                 // 16-byte loads of dy
 };
-constexpr int kColSumRows = 64;          // least rows of one partial sum
-constexpr int kColSumMaxSplits = 128;
+// One launch up to 2048 rows (a second one costs what it would save), then a split
+// per 512 rows, up to 64.
 inline int64_t column_sum_splits(int64_t M) {
-    const int64_t s = (M + kColSumRows - 1) / kColSumRows;
-    return s < 1 ? 1 : (s > kColSumMaxSplits ? kColSumMaxSplits : s);
+    if (M <= 2048) return 1;
+    const int64_t s = (M + 511) / 512;
+    return s > 64 ? 64 : s;
 }
 hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t stream);
 

@@ -192,19 +192,107 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
     return launched(lin::launch_product_any(elem, lin::kProdGated, p, (hipStream_t)stream));
 }
 
-const double kGradRates[lin::kNumGradConfigs] = {1.00, 0.94, 0.80};
+// A streaming product's plan: the tile, the splits of the contraction, and, where the
+// last round of tiles would leave much of the chip idle, the first output column of a
+// second launch with a tile of its own (0: one launch).
+struct StreamPlan {
+    int cfg, splits;
+    int64_t c1;
+    int cfg1;
+};
 
-// A streaming product's shape, tile and launch; the operands are set by the caller.
-hipError_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, const DevInfo& di, hipStream_t stream) {
-    const int c = choose_tile(lin::kGradConfigs, kGradRates, lin::kNumGradConfigs, a.groups, a.R, a.C, di.cus);
-    const lin::GemmConfig& g = lin::kGradConfigs[c];
+// The time of a launch in microseconds, from measurements on a whole MI355X at 16 and 64
+// slices: rounds of tiles (of which the small tile runs two per CU), each a start and
+// end plus a time per slice of 64; the splits' partial sums cost a launch and their
+// traffic (0.65 us per MB written and read back).
+struct TileTime {
+    double fixed, slice;
+    int per_cu;
+};
+constexpr TileTime kGradTimes[lin::kNumGradConfigs] = {{7.0, 1.55, 1}, {5.5, 0.85, 1}, {4.2, 0.49, 1}, {3.2, 0.39, 2}};
+constexpr int kPlanCus = 256;      // plans (and so workspaces) do not depend on the device
+constexpr double kLaunchGap = 4.0;
+
+double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t slices, int64_t splits) {
+    const lin::GemmConfig& g = lin::kGradConfigs[cfg];
+    const TileTime& t = kGradTimes[cfg];
+    const int64_t tiles = splits * groups * tiles_of(R, g.bm) * tiles_of(C, g.bn);
+    const double main = (double)tiles_of(tiles, kPlanCus * t.per_cu) * (t.fixed + t.slice * (double)tiles_of(slices, splits));
+    return splits == 1 ? main : main + 2.0 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
+}
+
+StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
+    StreamPlan p{0, 1, 0, 0};
+    double best = tile_time(0, groups, R, C, slices, 1);
+    for (int c = 0; c < lin::kNumGradConfigs; ++c)
+        for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
+            const double t = tile_time(c, groups, R, C, slices, s);
+            if (t < best) {
+                best = t;
+                p.cfg = c;
+                p.splits = (int)s;
+            }
+        }
+    const lin::GemmConfig& g = lin::kGradConfigs[0];
+    const int64_t rows = groups * tiles_of(R, g.bm), cols = tiles_of(C, g.bn);
+    const int64_t whole = rows > 0 ? rows * cols / kPlanCus * kPlanCus / rows : 0;   // column tiles in whole rounds
+    if (whole > 0 && whole < cols) {
+        const double head = tile_time(0, groups, R, whole * g.bn, slices, 1) + kLaunchGap;
+        for (int c = 0; c < lin::kNumGradConfigs; ++c) {
+            const double t = head + tile_time(c, groups, R, C - whole * g.bn, slices, 1);
+            if (t < best) {
+                best = t;
+                p = StreamPlan{0, 1, whole * g.bn, c};
+            }
+        }
+    }
+    return p;
+}
+
+// Bytes of partial sums of a product's plan.
+int64_t partial_bytes(int64_t groups, int64_t R, int64_t C, int64_t slices) {
+    const StreamPlan p = plan_stream(groups, R, C, slices);
+    return p.splits > 1 ? p.splits * groups * R * ((C + 7) / 8 * 8) * 4 : 0;
+}
+
+int64_t slices_of(int64_t L) { return (L + 63) / 64; }
+
+// A streaming product's shape, tile and launches; the operands are set by the caller.
+// partial: device memory of partial_bytes.
+int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, const DevInfo& di, void* partial,
+                      hipStream_t stream) {
+    const StreamPlan p = plan_stream(a.groups, a.R, a.C, slices_of(a.L) * a.segs);
+    const lin::GemmConfig& g = lin::kGradConfigs[p.cfg];
     a.tiles_r = (int)tiles_of(a.R, g.bm);
     a.tiles_c = (int)tiles_of(a.C, g.bn);
     a.xcd_shift = di.xcd_shift;
+    a.splits = p.splits;
     const int64_t eb = mode == lin::kOutRound ? 2 : 4;
     for (int i = 0; i < a.groups; ++i)
         if ((uintptr_t)a.y[i] % 16 == 0 && a.ldy[i] * eb % 16 == 0) a.vec |= 1 << i;
-    return lin::launch_grad_stream(elem, c, rowt, mode, a, stream);
+    if (p.c1 > 0) {
+        lin::StreamProduct head = a;
+        head.C = (int)p.c1;
+        head.tiles_c = (int)(p.c1 / g.bn);
+        const int32_t st = launched(lin::launch_grad_stream(elem, p.cfg, rowt, mode, head, stream));
+        if (st != LINEAR_OK) return st;
+        const lin::GemmConfig& g1 = lin::kGradConfigs[p.cfg1];
+        a.C -= (int)p.c1;
+        a.tiles_r = (int)tiles_of(a.R, g1.bm);
+        a.tiles_c = (int)tiles_of(a.C, g1.bn);
+        for (int i = 0; i < 2; ++i) {
+            if (a.c[i]) a.c[i] += p.c1;
+            if (a.y[i]) a.y[i] = (char*)a.y[i] + p.c1 * eb;
+        }
+        return launched(lin::launch_grad_stream(elem, p.cfg1, rowt, mode, a, stream));
+    }
+    if (p.splits == 1) return launched(lin::launch_grad_stream(elem, p.cfg, rowt, mode, a, stream));
+    a.partial = (float*)partial;
+    a.ldp = ((int64_t)a.C + 7) / 8 * 8;
+    a.accumulate = mode == lin::kOutF32Add;
+    const int32_t st = launched(lin::launch_grad_stream(elem, p.cfg, rowt, lin::kOutF32, a, stream));
+    if (st != LINEAR_OK) return st;
+    return launched(lin::launch_split_sum(elem, mode != lin::kOutRound, a, stream));
 }
 
 // What the streaming kernels read: 16-byte chunks of rows, offsets of a tile's rows in 32 bits.
@@ -248,7 +336,7 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
         a.C = (int)K;
         a.L = (int)N;
         a.segs = a.groups = 1;
-        return launched(launch_stream(elem, false, lin::kOutRound, a, di, (hipStream_t)stream));
+        return launch_stream(elem, false, lin::kOutRound, a, di, ws, (hipStream_t)stream);
     }
     const lin::ProductArgs p = product(dy, lddy, 1, w, 1, ldw, dx, lddx, M, K, N);
     return launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
@@ -285,6 +373,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
         c.splits = (int)lin::column_sum_splits(M);
         c.f32 = f32;
         c.accumulate = accumulate != 0;
+        c.vec = al16(dy, lddy);
         st = launched(lin::launch_column_sum(elem, c, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
@@ -303,7 +392,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
         a.L = (int)M;
         a.segs = a.groups = 1;
         const int mode = !f32 ? lin::kOutRound : accumulate ? lin::kOutF32Add : lin::kOutF32;
-        return launched(launch_stream(elem, true, mode, a, di, (hipStream_t)stream));
+        return launch_stream(elem, true, mode, a, di, ws, (hipStream_t)stream);
     }
     lin::ProductArgs p = product(dy, 1, lddy, x, 1, ldx, dw, lddw, N, K, M);
     p.accumulate = f32 && accumulate != 0;
@@ -373,7 +462,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         a.L = (int)N;
         a.segs = 2;
         a.groups = 1;
-        st = launched(launch_stream(elem, false, lin::kOutRound, a, di, (hipStream_t)stream));
+        st = launch_stream(elem, false, lin::kOutRound, a, di, d + M * 2 * Np, (hipStream_t)stream);
         if (st != LINEAR_OK) return st;
     } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, 1, wg, 1, ldwg, dx, lddx, M, K, N);
@@ -402,7 +491,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         a.L = (int)M;
         a.segs = 1;
         a.groups = 2;
-        st = launched(launch_stream(elem, true, lin::kOutRound, a, di, (hipStream_t)stream));
+        st = launch_stream(elem, true, lin::kOutRound, a, di, d + M * 2 * Np, (hipStream_t)stream);
         if (st != LINEAR_OK) return st;
     } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
@@ -474,12 +563,14 @@ extern "C" {
 
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K) || (M > 0 && gated_half(N) > kMaxElems / 4 / M)) return -1;
-    return M * gated_half(N) * 2 * 2;
+    return M * gated_half(N) * 2 * 2 +
+           std::max(partial_bytes(1, M, K, 2 * slices_of(N)), partial_bytes(2, N, K, slices_of(M)));
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K)) return -1;
-    return lin::column_sum_splits(M) * N * 4;
+    return std::max({lin::column_sum_splits(M) * N * 4, partial_bytes(1, M, K, slices_of(N)),
+                     partial_bytes(1, N, K, slices_of(M))});
 }
 
 int32_t linear_f16_gated(const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
