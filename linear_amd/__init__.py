@@ -14,6 +14,7 @@ from __future__ import annotations
 import array
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -517,11 +518,31 @@ def linear_bf16_indexed_f32out(x, w, idx, out=None, stream=None, workspace=None)
     return _indexed_call(torch.bfloat16, x, w, idx, out, True, stream, workspace)
 
 
+def _launch_stream(stream, *tensors):
+    """_stream_handle's checks for tensors on one device and the current stream, the usual
+    call, at less host time; anything else goes through it."""
+    if stream is None:
+        index = None
+        for t in tensors:
+            if t is not None:
+                i = t.get_device()                       # -1 on the host
+                if i < 0 or (index is not None and i != index):
+                    break
+                index = i
+        else:
+            if index is not None and index == torch.cuda.current_device():
+                return torch._C._cuda_getCurrentRawStream(index)
+    return _stream_handle(stream, *tensors)
+
+
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _on(stream, device):
     """A context in which new tensors belong to the stream of the launch, so that their
     memory is not reused by other work before the launch has run."""
     if stream is None or device.type != "cuda":
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     if not isinstance(stream, torch.cuda.Stream):
         handle = int(getattr(stream, "cuda_stream", stream))
         if handle == 0:
@@ -545,15 +566,17 @@ def _output(t, name, dtype, shape, device):
 
 
 def _scratch(workspace, need, device):
-    """The call's workspace: the caller's uint8 tensor, or a new one."""
-    if need < 0:
-        raise ValueError("shapes out of range")
+    """The call's workspace, its address and its size: the caller's uint8 tensor, or a new one
+    where the call needs any."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), need
     if workspace.dtype != torch.uint8 or workspace.dim() != 1 or workspace.numel() < need or (
             workspace.numel() > 1 and workspace.stride(0) != 1):
         raise ValueError("workspace must be a contiguous uint8 tensor of at least %d bytes" % need)
-    return workspace
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
@@ -564,7 +587,7 @@ def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
     xp, ldx = _mat(x, "x", dtype)
     gp, ldg = _operand(wg, "wg", dtype, (N, K))
     up_, ldu = _operand(wu, "wu", dtype, (N, K))
-    handle = _stream_handle(stream, x, wg, wu, out, gate, up)
+    handle = _launch_stream(stream, x, wg, wu, out, gate, up)
     with _on(stream, x.device):
         out, hp, ldh = _output(out, "out", dtype, (M, N), x.device)
         kept = []
@@ -591,6 +614,7 @@ def linear_bf16_gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: 
     return _gated_call("bf16", torch.bfloat16, x, wg, wu, act, keep, out, gate, up, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def gated_workspace_bytes(M: int, N: int, K: int) -> int:
     """Bytes of device workspace a gated backward call needs."""
     n = _lib().linear_gated_workspace_bytes(M, N, K)
@@ -611,15 +635,15 @@ def _gated_backward_call(tag, dtype, dh, x, wg, wu, gate, up, act, need_dx, need
     for name, t, shape in (("dh", dh, (M, N)), ("x", x, (M, K)), ("wg", wg, (N, K)), ("wu", wu, (N, K)),
                            ("gate", gate, (M, N)), ("up", up, (M, N))):
         args += _operand(t, name, dtype, shape)
-    handle = _stream_handle(stream, dh, x, wg, wu, gate, up, dx, dwg, dwu, workspace)
+    handle = _launch_stream(stream, dh, x, wg, wu, gate, up, dx, dwg, dwu, workspace)
     none = (None, None, 0)
     with _on(stream, x.device):
         dx, *dxa = _output(dx, "dx", dtype, (M, K), x.device) if need_dx else none
         dwg, *dga = _output(dwg, "dwg", dtype, (N, K), x.device) if need_dw else none
         dwu, *dua = _output(dwu, "dwu", dtype, (N, K), x.device) if need_dw else none
-        workspace = _scratch(workspace, gated_workspace_bytes(M, N, K), x.device)
+        workspace, wsp, wsn = _scratch(workspace, gated_workspace_bytes(M, N, K), x.device)
     name = "linear_%s_gated_backward" % tag
-    rc = getattr(_lib(), name)(*args, int(act), *dxa, *dga, *dua, M, N, K, workspace.data_ptr(), workspace.numel(), handle)
+    rc = getattr(_lib(), name)(*args, int(act), *dxa, *dga, *dua, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return dx, dwg, dwu
 
@@ -640,6 +664,7 @@ def linear_bf16_gated_backward(dh, x, wg, wu, gate, up, act: int = EPI_SILU, nee
                                 workspace, stream)
 
 
+@functools.lru_cache(maxsize=256)
 def backward_workspace_bytes(M: int, N: int, K: int) -> int:
     """Bytes of device workspace the layer's backward calls need."""
     n = _lib().linear_backward_workspace_bytes(M, N, K)
@@ -655,12 +680,12 @@ def _backward_input_call(tag, dtype, dy, weight, out, workspace, stream):
     K = weight.shape[1]
     yp, ldy = _mat(dy, "dy", dtype)
     wp, ldw = _operand(weight, "weight", dtype, (N, K))
-    handle = _stream_handle(stream, dy, weight, out, workspace)
+    handle = _launch_stream(stream, dy, weight, out, workspace)
     with _on(stream, dy.device):
         out, xp, ldx = _output(out, "out", dtype, (M, K), dy.device)
-        workspace = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
+        workspace, wsp, wsn = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
     name = "linear_%s_backward_input" % tag
-    rc = getattr(_lib(), name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, workspace.data_ptr(), workspace.numel(), handle)
+    rc = getattr(_lib(), name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return out
 
@@ -686,20 +711,19 @@ def _backward_weight_call(tag, dtype, f32, dy, x, bias, accumulate, out, db, wor
         raise ValueError("accumulate adds to tensors that are there: give out (and db)")
     yp, ldy = _mat(dy, "dy", dtype)
     xp, ldx = _operand(x, "x", dtype, (M, K))
-    handle = _stream_handle(stream, dy, x, out, db, workspace)
+    handle = _launch_stream(stream, dy, x, out, db, workspace)
     odt = torch.float32 if f32 else dtype
     with _on(stream, dy.device):
         out, wp, ldw = _output(out, "out", odt, (N, K), dy.device)
         if bias and db is None:
             db = torch.empty((N,), dtype=odt, device=dy.device)
-        workspace = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
+        workspace, wsp, wsn = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
     if bias and (db.dtype != odt or tuple(db.shape) != (N,) or (N > 1 and db.stride(0) != 1)):
         raise ValueError("db must be a contiguous %s [N] tensor" % odt)
     bp = db.data_ptr() if bias else None
     name = "linear_%s_backward_weight%s" % (tag, "_f32out" if f32 else "")
     flag = (int(bool(accumulate)),) if f32 else ()
-    rc = getattr(_lib(), name)(yp, ldy, xp, ldx, wp, ldw, bp, *flag, M, N, K, workspace.data_ptr(), workspace.numel(),
-                               handle)
+    rc = getattr(_lib(), name)(yp, ldy, xp, ldx, wp, ldw, bp, *flag, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return out, (db if bias else None)
 
@@ -734,6 +758,7 @@ _TENSOR_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 GRAD_MAX_TENSORS = 65536
 
 
+@functools.lru_cache(maxsize=256)
 def grad_workspace_bytes(count: int) -> int:
     """Bytes of device workspace a norm over `count` tensors needs."""
     n = _lib().linear_grad_workspace_bytes(count)
@@ -744,20 +769,31 @@ def grad_workspace_bytes(count: int) -> int:
 
 def _tensor_table(tensors, name):
     """The tensors as an array of linear_tensor (five 64-bit fields each): contiguous ones of any
-    shape, and matrices with unit inner stride."""
-    flat = []
-    for t in tensors:
-        kind = _TENSOR_TYPES.get(t.dtype)
-        if kind is None:
-            raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, t.dtype))
-        if t.is_contiguous():
-            n = t.numel()
-            flat += (t.data_ptr(), 1, n, n, kind)
-        elif t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1) and t.stride(0) >= t.shape[1]:
-            flat += (t.data_ptr(), t.shape[0], t.shape[1], t.stride(0), kind)
-        else:
-            raise ValueError("%s must be contiguous, or matrices with unit inner stride" % name)
-    return array.array("q", flat)
+    shape, as one row, and matrices with unit inner stride."""
+    try:
+        kinds = [_TENSOR_TYPES[t.dtype] for t in tensors]
+    except KeyError as e:
+        raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, e)) from None
+    n = len(tensors)
+    table = array.array("q", bytes(40 * n))
+    table[0::5] = array.array("q", [t.data_ptr() for t in tensors])
+    sizes = array.array("q", [t.numel() for t in tensors])
+    table[1::5] = array.array("q", [1]) * n
+    table[2::5] = sizes
+    table[3::5] = sizes
+    table[4::5] = array.array("q", kinds)
+    packed = [t.is_contiguous() for t in tensors]
+    if not all(packed):
+        for i, t in enumerate(tensors):
+            if not packed[i]:
+                if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
+                    raise ValueError("%s must be contiguous, or matrices with unit inner stride" % name)
+                _by_rows(table, i, t)
+    return table
+
+
+def _by_rows(table, i, t):
+    table[5 * i + 1:5 * i + 4] = array.array("q", (t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]))
 
 
 def linear_grad_norm(grads, out=None, workspace=None, stream=None) -> torch.Tensor:
@@ -768,23 +804,22 @@ def linear_grad_norm(grads, out=None, workspace=None, stream=None) -> torch.Tens
     table = _tensor_table(grads, "grads")
     if not grads and out is None:
         raise ValueError("no gradients and no out: the device is not known")
-    handle = _stream_handle(stream, *grads, out, workspace)
+    handle = _launch_stream(stream, *grads, out, workspace)
     device = (grads[0] if grads else out).device
     with _on(stream, device):
         if out is None:
             out = torch.empty(1, dtype=torch.float32, device=device)
-        workspace = _scratch(workspace, grad_workspace_bytes(len(grads)), device)
+        workspace, wsp, wsn = _scratch(workspace, grad_workspace_bytes(len(grads)), device)
     if out.dtype != torch.float32 or out.numel() != 1:
         raise ValueError("out must be a float32 tensor of one value")
-    rc = _lib().linear_grad_norm(table.buffer_info()[0], len(grads), out.data_ptr(), workspace.data_ptr(),
-                                 workspace.numel(), handle)
+    rc = _lib().linear_grad_norm(table.buffer_info()[0], len(grads), out.data_ptr(), wsp, wsn, handle)
     _check(rc, "linear_grad_norm")
     return out
 
 
 def linear_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None, stream=None):
     """The gradients times min(1, max_norm / (norm + 1e-6)), rounded to their types: into the tensors
-    of out (same shapes and types), or in place.  norm: the float32 tensor of linear_grad_norm."""
+    of out (the same sizes and types), or in place.  norm: the float32 tensor of linear_grad_norm."""
     grads = list(grads)
     table = _tensor_table(grads, "grads")
     if norm.dtype != torch.float32 or norm.numel() != 1:
@@ -792,16 +827,18 @@ def linear_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None, strea
     outs = None
     if out is not None:
         out = list(out)
-        if [(t.shape, t.dtype) for t in out] != [(t.shape, t.dtype) for t in grads]:
-            raise ValueError("out must have the gradients' shapes and types")
-        # the two tables must agree in their rows: a matrix with padded rows on one side
-        # is described by its rows on both
         outs = _tensor_table(out, "out")
-        for i, (a, b) in enumerate(zip(grads, out)):
-            if outs[5 * i + 1] != table[5 * i + 1]:
-                for t, row in ((a, table), (b, outs)):
-                    row[5 * i + 1:5 * i + 4] = array.array("q", (t.shape[0], t.shape[1], t.stride(0)))
-    handle = _stream_handle(stream, *grads, norm, *(out or ()))
+        if len(out) != len(grads) or outs[4::5] != table[4::5]:
+            raise ValueError("out must have as many tensors as grads, of the same types")
+        if outs[1::5] != table[1::5] or outs[2::5] != table[2::5]:
+            if any(a.shape != b.shape for a, b in zip(out, grads)):
+                raise ValueError("out must have the gradients' shapes")
+            # a matrix with padded rows on one side is described by its rows on both
+            for i, (a, b) in enumerate(zip(grads, out)):
+                if outs[5 * i + 1] != table[5 * i + 1]:
+                    _by_rows(table, i, a)
+                    _by_rows(outs, i, b)
+    handle = _launch_stream(stream, *grads, norm, *(out or ()))
     rc = _lib().linear_grad_clip(table.buffer_info()[0], outs.buffer_info()[0] if outs else None, len(grads),
                                  norm.data_ptr(), float(max_norm), handle)
     _check(rc, "linear_grad_clip")

@@ -359,8 +359,7 @@ __device__ __forceinline__ void finish_gated(const LinearArgs& a, unsigned char*
     constexpr int FM = TM / R, FP = TC / R;
     constexpr int G = R * R / 256;
     constexpr int CPR = BC / 8;                      // chunks per staged row
-    constexpr int CHT = BM * CPR / NT;
-    static_assert((BM * CPR) % NT == 0, "chunks must divide evenly over the threads");
+    constexpr int CHT = (BM * CPR + NT - 1) / NT;    // (threads past a small tile's chunks store none)
     const int wn = wave % WN, wm = wave / WN;
     const int lr = lane % R, lh = lane / R;
     static_for<0, 3>([&]<int q>() {
@@ -392,6 +391,7 @@ __device__ __forceinline__ void finish_gated(const LinearArgs& a, unsigned char*
 #pragma unroll
         for (int k = 0; k < CHT; ++k) {
             const int c = (int)threadIdx.x + k * NT, r = c / CPR, c8 = c % CPR;
+            if ((BM * CPR) % NT != 0 && c >= BM * CPR) break;
             const u32x4 v = *(const u32x4*)(smem + (r * CPR + (c8 ^ (r % CPR))) * 16);
             const int m = m0 + r, n = c0 + c8 * 8;
             store8(out + (int64_t)m * ld + n, m < a.M, n, a.N, a.vec_gated & (1 << q), v);
@@ -789,9 +789,9 @@ hipError_t launch_gated_stream_t(int cfg, const LinearArgs& a, hipStream_t strea
     switch (cfg) {
         case 0: return launch((const void*)gemm_stream<256, 256, 2, 4, 2, 64, E, kOutGated, 1, false, true>, a, 512, stream);
         case 1: return launch((const void*)gemm_stream<256, 128, 4, 2, 3, 64, E, kOutGated, 2>, a, 512, stream);
-        case 2: return launch((const void*)gemm_stream<128, 256, 2, 4, 4, 32, E, kOutGated, 0>, a, 512, stream);
-        case 3: return launch((const void*)gemm_stream<128, 128, 2, 2, 4, 64, E, kOutGated, 2>, a, 256, stream);
-        case 4: return launch((const void*)gemm_stream<64, 128, 2, 2, 4, 64, E, kOutGated, 2>, a, 256, stream);
+        case 2: return launch((const void*)gemm_stream<128, 128, 2, 2, 4, 64, E, kOutGated, 2>, a, 256, stream);
+        case 3: return launch((const void*)gemm_stream<64, 64, 2, 2, 4, 64, E, kOutGated, 1, false, true>, a, 256, stream);
+        case 4: return launch((const void*)gemm_stream<32, 32, 2, 1, 6, 64, E, kOutGated, 1, false, true>, a, 128, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -44,12 +44,13 @@ extern template hipError_t launch_gated_stream_t<kBF16>(int, const LinearArgs&, 
 
 // The gated block's streaming kernels: bn counts the rows of both weights (an
 // output tile has bn / 2 columns); a.tiles_n counts bn / 2-column tiles.
-inline constexpr GemmConfig kGatedConfigs[kNumStreamConfigs] = {
+constexpr int kNumGatedConfigs = 5;
+inline constexpr GemmConfig kGatedConfigs[kNumGatedConfigs] = {
     {256, 256, 2, 4, 2, 64},
     {256, 128, 4, 2, 3, 64},
-    {128, 256, 2, 4, 4, 32},
     {128, 128, 2, 2, 4, 64},
-    {64, 128, 2, 2, 4, 64},
+    {64, 64, 2, 2, 4, 64},
+    {32, 32, 2, 1, 6, 64},
 };
 inline hipError_t launch_gated_stream(int elem, int cfg, const LinearArgs& a, hipStream_t stream) {
     return elem == kBF16 ? launch_gated_stream_t<kBF16>(cfg, a, stream) : launch_gated_stream_t<kF16>(cfg, a, stream);
@@ -77,6 +78,8 @@ constexpr int kGemvRows = 4;
 constexpr int kGemvSeg = 512;      // K values per 1 KB wave load (64 lanes x 8)
 constexpr int kGemvMaxK = 32768;   // 64 KB of x in LDS
 hipError_t launch_gemv(int elem, const LinearArgs& a, int mode, hipStream_t stream);
+// The gated block's one-row kernel (M = 1, 16-byte aligned layouts, K <= kGemvMaxK).
+hipError_t launch_gated_gemv(int elem, const LinearArgs& a, hipStream_t stream);
 
 // Indexed contraction (x [M, K] against expert tables W [E, K, N], row m against
 // expert idx[m]).

@@ -113,26 +113,37 @@ lin::ProductArgs product(const uint16_t* a, int64_t sar, int64_t sak, const uint
 
 bool al16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 
-// Tile choice of the streaming kernels: the least rounds of tiles over the CUs, each
-// round as long as a tile's outputs at its rate; the earlier (larger) tile of equals.
-// rows and cols count what the configuration's bm and bn count.
-int choose_tile(const lin::GemmConfig* cfgs, const double* rates, int n, int64_t groups, int64_t rows, int64_t cols,
-                int cus) {
+// The time of a streaming launch in microseconds, from measurements on a whole MI355X
+// at 12 to 64 slices: rounds of tiles over the CUs (the small tiles run several per
+// CU), each a start and end plus a time per slice of 64.
+struct TileTime {
+    double fixed, slice;
+    int per_cu;
+};
+
+double rounds_time(const TileTime& t, int64_t tiles, int64_t slices, int cus) {
+    return (double)tiles_of(tiles, (int64_t)cus * t.per_cu) * (t.fixed + t.slice * (double)slices);
+}
+
+// kGatedConfigs' times.  The 32-row tile with 16 columns of each weight serves few
+// rows (its many small workgroups keep the weights' read at the memory's rate: 16 x
+// 4000 x 4096 in 14 us, 21 with the 64-row tile).
+constexpr TileTime kGatedTimes[lin::kNumGatedConfigs] = {{6.5, 1.60, 1}, {5.3, 0.80, 1}, {4.9, 0.50, 1}, {2.0, 0.42, 2},
+                                                         {2.0, 0.30, 3}};
+
+int choose_gated(int64_t M, int64_t N, int64_t K, int cus) {
     int best = 0;
-    double best_cost = -1.0;
-    for (int c = 0; c < n; ++c) {
-        const int64_t tiles = groups * tiles_of(rows, cfgs[c].bm) * tiles_of(cols, cfgs[c].bn);
-        const double cost = (double)tiles_of(tiles, cus) * cfgs[c].bm * cfgs[c].bn / rates[c];
-        if (best_cost < 0 || cost < best_cost) {
-            best_cost = cost;
+    double best_time = -1.0;
+    for (int c = 0; c < lin::kNumGatedConfigs; ++c) {
+        const lin::GemmConfig& g = lin::kGatedConfigs[c];
+        const double t = rounds_time(kGatedTimes[c], tiles_of(M, g.bm) * tiles_of(2 * N, g.bn), tiles_of(K, 64), cus);
+        if (best_time < 0 || t < best_time) {
+            best_time = t;
             best = c;
         }
     }
     return best;
 }
-
-// The layer's rates for the same tiles (relative to the 256 x 256 tile).
-const double kGatedRates[lin::kNumStreamConfigs] = {1.00, 0.94, 0.85, 0.80, 0.65};
 
 int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
                   int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
@@ -173,7 +184,8 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
         a.vec_gated = (al16(h, ldh) ? 1 : 0) | (al16(gate, ldgate) ? 2 : 0) | (al16(up, ldup) ? 4 : 0);
         a.groups = 1;
         a.xcd_shift = di.xcd_shift;
-        const int c = choose_tile(lin::kGatedConfigs, kGatedRates, lin::kNumStreamConfigs, 1, M, 2 * N, di.cus);
+        if (M == 1 && K <= lin::kGemvMaxK) return launched(lin::launch_gated_gemv(elem, a, (hipStream_t)stream));
+        const int c = choose_gated(M, N, K, di.cus);
         const lin::GemmConfig& g = lin::kGatedConfigs[c];
         a.tiles_m = (int)tiles_of(M, g.bm);
         a.tiles_n = (int)tiles_of(2 * N, g.bn);
@@ -201,31 +213,28 @@ struct StreamPlan {
     int cfg1;
 };
 
-// The time of a launch in microseconds, from measurements on a whole MI355X at 16 and 64
-// slices: rounds of tiles (of which the small tile runs two per CU), each a start and
-// end plus a time per slice of 64; the splits' partial sums cost a launch and their
-// traffic (0.65 us per MB written and read back).
-struct TileTime {
-    double fixed, slice;
-    int per_cu;
-};
+// kGradConfigs' times (16 and 64 slices).  The splits' partial sums cost a launch and
+// their traffic (0.65 us per MB written and read back).
 constexpr TileTime kGradTimes[lin::kNumGradConfigs] = {{7.0, 1.55, 1}, {5.5, 0.85, 1}, {4.2, 0.49, 1}, {3.2, 0.39, 2}};
 constexpr int kPlanCus = 256;      // plans (and so workspaces) do not depend on the device
 constexpr double kLaunchGap = 4.0;
 
 double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t slices, int64_t splits) {
     const lin::GemmConfig& g = lin::kGradConfigs[cfg];
-    const TileTime& t = kGradTimes[cfg];
-    const int64_t tiles = splits * groups * tiles_of(R, g.bm) * tiles_of(C, g.bn);
-    const double main = (double)tiles_of(tiles, kPlanCus * t.per_cu) * (t.fixed + t.slice * (double)tiles_of(slices, splits));
+    const double main = rounds_time(kGradTimes[cfg], splits * groups * tiles_of(R, g.bm) * tiles_of(C, g.bn),
+                                    tiles_of(slices, splits), kPlanCus);
     return splits == 1 ? main : main + 2.0 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
 }
 
 StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
     StreamPlan p{0, 1, 0, 0};
     double best = tile_time(0, groups, R, C, slices, 1);
-    for (int c = 0; c < lin::kNumGradConfigs; ++c)
+    for (int c = 0; c < lin::kNumGradConfigs; ++c) {
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
+            // past twice the chip's tiles a split only adds traffic
+            if (s > 1 && s * groups * tiles_of(R, lin::kGradConfigs[c].bm) * tiles_of(C, lin::kGradConfigs[c].bn) >
+                             2 * kPlanCus * kGradTimes[c].per_cu)
+                break;
             const double t = tile_time(c, groups, R, C, slices, s);
             if (t < best) {
                 best = t;
@@ -233,6 +242,7 @@ StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
                 p.splits = (int)s;
             }
         }
+    }
     const lin::GemmConfig& g = lin::kGradConfigs[0];
     const int64_t rows = groups * tiles_of(R, g.bm), cols = tiles_of(C, g.bn);
     const int64_t whole = rows > 0 ? rows * cols / kPlanCus * kPlanCus / rows : 0;   // column tiles in whole rounds
@@ -569,7 +579,8 @@ int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K)) return -1;
-    return std::max({lin::column_sum_splits(M) * N * 4, partial_bytes(1, M, K, slices_of(N)),
+    const int64_t sums = lin::column_sum_splits(M);
+    return std::max({sums > 1 ? sums * N * 4 : 0, partial_bytes(1, M, K, slices_of(N)),
                      partial_bytes(1, N, K, slices_of(M))});
 }
 

@@ -82,6 +82,10 @@ def test_gated_backward_calls_that_pass_the_checks():
     assert gated_backward(N=0, dh=0, wg=0, wu=0, g=0, u=0, dwg=0, dwu=0) == NODEV
 
 
+# a size whose contraction is split, so that the call needs a workspace
+SPLIT = dict(M=16, N=4096, lddy=4096)
+
+
 def backward_input(dy=DY, lddy=32, w=WG, ldw=64, dx=DX, lddx=64, M=8, N=32, K=64, ws=WS, nws=1 << 20):
     return la._lib().linear_f16_backward_input(dy, lddy, w, ldw, dx, lddx, M, N, K, ws, nws, None)
 
@@ -98,7 +102,8 @@ def backward_weight_f32(acc=0, dw=DWG, db=DB, **kw):
     (dict(M=-1), la.LINEAR_E_SHAPE), (dict(dy=0), la.LINEAR_E_NULL), (dict(w=0), la.LINEAR_E_NULL),
     (dict(dx=0), la.LINEAR_E_NULL), (dict(lddy=31), la.LINEAR_E_STRIDE), (dict(ldw=63), la.LINEAR_E_STRIDE),
     (dict(lddx=63), la.LINEAR_E_STRIDE), (dict(dx=DY), la.LINEAR_E_ALIAS), (dict(dx=WG + 64), la.LINEAR_E_ALIAS),
-    (dict(nws=0), la.LINEAR_E_WORKSPACE), (dict(ws=WS + 4), la.LINEAR_E_WORKSPACE), (dict(ws=DX), la.LINEAR_E_ALIAS),
+    (dict(nws=0, **SPLIT), la.LINEAR_E_WORKSPACE), (dict(ws=WS + 4, **SPLIT), la.LINEAR_E_WORKSPACE),
+    (dict(ws=DX, **SPLIT), la.LINEAR_E_ALIAS), (dict(ws=0, **SPLIT), la.LINEAR_E_NULL),
 ])
 def test_backward_input_refusals(kw, code):
     assert backward_input(**kw) == code
@@ -108,7 +113,8 @@ def test_backward_input_refusals(kw, code):
     (dict(N=-1), la.LINEAR_E_SHAPE), (dict(dy=0), la.LINEAR_E_NULL), (dict(x=0), la.LINEAR_E_NULL),
     (dict(dw=0), la.LINEAR_E_NULL), (dict(lddy=31), la.LINEAR_E_STRIDE), (dict(ldx=63), la.LINEAR_E_STRIDE),
     (dict(lddw=63), la.LINEAR_E_STRIDE), (dict(dw=X), la.LINEAR_E_ALIAS), (dict(db=DY + 62), la.LINEAR_E_ALIAS),
-    (dict(db=DWG + 128), la.LINEAR_E_ALIAS), (dict(nws=100), la.LINEAR_E_WORKSPACE), (dict(ws=DB), la.LINEAR_E_ALIAS),
+    (dict(db=DWG + 128), la.LINEAR_E_ALIAS), (dict(M=4096, nws=100), la.LINEAR_E_WORKSPACE),
+    (dict(M=4096, ws=DB), la.LINEAR_E_ALIAS), (dict(M=4096, ws=0), la.LINEAR_E_NULL),
 ])
 def test_backward_weight_refusals(kw, code):
     assert backward_weight(**kw) == code
