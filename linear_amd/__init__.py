@@ -15,6 +15,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -197,10 +198,11 @@ def _mat(t: torch.Tensor, name: str, dtype=torch.float16):
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if t.dim() != 2:
         raise ValueError("%s must be 2-D, got shape %s" % (name, tuple(t.shape)))
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError("%s must have unit inner stride" % name)
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0), 1)
-    return t.data_ptr(), ld
+    return t.data_ptr(), ld if rows > 1 else max(cols, ld, 1)
 
 
 def _stream_handle(stream, *tensors):
@@ -522,15 +524,10 @@ def _launch_stream(stream, *tensors):
     """_stream_handle's checks for tensors on one device and the current stream, the usual
     call, at less host time; anything else goes through it."""
     if stream is None:
-        index = None
-        for t in tensors:
-            if t is not None:
-                i = t.get_device()                       # -1 on the host
-                if i < 0 or (index is not None and i != index):
-                    break
-                index = i
-        else:
-            if index is not None and index == torch.cuda.current_device():
+        devices = {t.get_device() for t in tensors if t is not None}    # -1 on the host
+        if len(devices) == 1:
+            index = devices.pop()
+            if index >= 0 and index == torch.cuda.current_device():
                 return torch._C._cuda_getCurrentRawStream(index)
     return _stream_handle(stream, *tensors)
 
@@ -554,15 +551,22 @@ def _on(stream, device):
 
 def _operand(t, name, dtype, shape):
     """Pointer and row stride of a tensor that must have this type and shape."""
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     return _mat(t, name, dtype)
 
 
 def _output(t, name, dtype, shape, device):
+    """The output tensor (a new one when not given), its pointer and row stride."""
     if t is None:
         t = torch.empty(shape, dtype=dtype, device=device)
+        return t, t.data_ptr(), max(shape[1], 1)
     return (t, *_operand(t, name, dtype, shape))
+
+
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    return getattr(_lib(), name)
 
 
 def _scratch(workspace, need, device):
@@ -579,6 +583,13 @@ def _scratch(workspace, need, device):
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
+_GATED = {t: "linear_%s_gated" % t for t in ("f16", "bf16")}
+_GATED_BACKWARD = {t: "linear_%s_gated_backward" % t for t in ("f16", "bf16")}
+_BACKWARD_INPUT = {t: "linear_%s_backward_input" % t for t in ("f16", "bf16")}
+_BACKWARD_WEIGHT = {(t, f): "linear_%s_backward_weight%s" % (t, "_f32out" if f else "")
+                    for t in ("f16", "bf16") for f in (False, True)}
+
+
 def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
     if x.dim() != 2 or wg.dim() != 2:
         raise ValueError("x must be [M, K] and wg, wu [N, K]")
@@ -593,8 +604,8 @@ def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
         kept = []
         for name, t in (("gate", gate), ("up", up)):
             kept += _output(t, name, dtype, (M, N), x.device) if keep or t is not None else (None, None, 0)
-    name = "linear_%s_gated" % tag
-    rc = getattr(_lib(), name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K,
+    name = _GATED[tag]
+    rc = _entry(name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K,
                                handle)
     _check(rc, name)
     return (out, kept[0], kept[3]) if keep else out
@@ -642,8 +653,8 @@ def _gated_backward_call(tag, dtype, dh, x, wg, wu, gate, up, act, need_dx, need
         dwg, *dga = _output(dwg, "dwg", dtype, (N, K), x.device) if need_dw else none
         dwu, *dua = _output(dwu, "dwu", dtype, (N, K), x.device) if need_dw else none
         workspace, wsp, wsn = _scratch(workspace, gated_workspace_bytes(M, N, K), x.device)
-    name = "linear_%s_gated_backward" % tag
-    rc = getattr(_lib(), name)(*args, int(act), *dxa, *dga, *dua, M, N, K, wsp, wsn, handle)
+    name = _GATED_BACKWARD[tag]
+    rc = _entry(name)(*args, int(act), *dxa, *dga, *dua, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return dx, dwg, dwu
 
@@ -684,8 +695,8 @@ def _backward_input_call(tag, dtype, dy, weight, out, workspace, stream):
     with _on(stream, dy.device):
         out, xp, ldx = _output(out, "out", dtype, (M, K), dy.device)
         workspace, wsp, wsn = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
-    name = "linear_%s_backward_input" % tag
-    rc = getattr(_lib(), name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, wsp, wsn, handle)
+    name = _BACKWARD_INPUT[tag]
+    rc = _entry(name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return out
 
@@ -721,9 +732,9 @@ def _backward_weight_call(tag, dtype, f32, dy, x, bias, accumulate, out, db, wor
     if bias and (db.dtype != odt or tuple(db.shape) != (N,) or (N > 1 and db.stride(0) != 1)):
         raise ValueError("db must be a contiguous %s [N] tensor" % odt)
     bp = db.data_ptr() if bias else None
-    name = "linear_%s_backward_weight%s" % (tag, "_f32out" if f32 else "")
+    name = _BACKWARD_WEIGHT[tag, f32]
     flag = (int(bool(accumulate)),) if f32 else ()
-    rc = getattr(_lib(), name)(yp, ldy, xp, ldx, wp, ldw, bp, *flag, M, N, K, wsp, wsn, handle)
+    rc = _entry(name)(yp, ldy, xp, ldx, wp, ldw, bp, *flag, M, N, K, wsp, wsn, handle)
     _check(rc, name)
     return out, (db if bias else None)
 
@@ -755,6 +766,7 @@ def linear_bf16_backward_weight_f32out(dy: torch.Tensor, x: torch.Tensor, bias: 
 
 # linear_tensor.type (include/linear_amd.h, LINEAR_TYPE_*)
 _TENSOR_TYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_dtype_of = operator.attrgetter("dtype")
 GRAD_MAX_TENSORS = 65536
 
 
@@ -771,21 +783,20 @@ def _tensor_table(tensors, name):
     """The tensors as an array of linear_tensor (five 64-bit fields each): contiguous ones of any
     shape, as one row, and matrices with unit inner stride."""
     try:
-        kinds = [_TENSOR_TYPES[t.dtype] for t in tensors]
+        kinds = array.array("q", map(_TENSOR_TYPES.__getitem__, map(_dtype_of, tensors)))
     except KeyError as e:
         raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, e)) from None
     n = len(tensors)
+    sizes = array.array("q", map(torch.Tensor.numel, tensors))
     table = array.array("q", bytes(40 * n))
-    table[0::5] = array.array("q", [t.data_ptr() for t in tensors])
-    sizes = array.array("q", [t.numel() for t in tensors])
-    table[1::5] = array.array("q", [1]) * n
+    table[0::5] = array.array("q", map(torch.Tensor.data_ptr, tensors))
+    table[1::5] = array.array("q", (1,)) * n
     table[2::5] = sizes
     table[3::5] = sizes
-    table[4::5] = array.array("q", kinds)
-    packed = [t.is_contiguous() for t in tensors]
-    if not all(packed):
+    table[4::5] = kinds
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
         for i, t in enumerate(tensors):
-            if not packed[i]:
+            if not t.is_contiguous():
                 if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < t.shape[1]:
                     raise ValueError("%s must be contiguous, or matrices with unit inner stride" % name)
                 _by_rows(table, i, t)
