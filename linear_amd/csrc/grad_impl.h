@@ -31,6 +31,7 @@
 // past the contraction's end read as zero, and a lane's offsets never change.
 #pragma once
 
+#include "columns.h"
 #include "gemm_impl.h"
 #include "train.h"
 
@@ -75,8 +76,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_rsrc(const uint16_t* p, 
 
 // Workgroup: one BM x BN tile of one group's output.  ROWT: the row operand is
 // contraction-major too (dw); else contraction-contiguous (dx).
-template <int BM, int BN, int WM, int WN, int STAGES, bool ROWT, int E, int MODE>
-__global__ void __launch_bounds__(WM * WN * 64)
+//
+// KG sets of WM x WN waves share the tile's slices, each set with a ring of its own,
+// and add their sums in LDS at the end: a small tile's slice is bound by the latency of
+// its reads, so several in flight cost one's time (no traffic, unlike a split over
+// workgroups).  The sets run the same number of slices, empty ones at the end.
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
+__global__ void __launch_bounds__(KG * WM * WN * 64)
 grad_stream(StreamProduct a) {
     constexpr int BK = 64, R = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
     constexpr int NW = WM * WN;
@@ -90,8 +96,20 @@ grad_stream(StreamProduct a) {
     static_assert(CBYTES % (1024 * NW) == 0 && RBYTES % (1024 * NW) == 0, "loads must divide evenly over the waves");
     static_assert(BN >= 64 && BM >= 64, "panel rows of 4 or more pairs");
     static_assert(TM % R == 0 && TN % R == 0, "whole fragments");
-    static_assert(STAGES >= 2 && STAGES * SLICE <= 160 * 1024, "LDS ring too large");
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[STAGES * SLICE];
+    constexpr int RING = STAGES * SLICE;
+    static_assert(STAGES >= 2 && KG * RING <= 160 * 1024, "LDS rings too large");
+    static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= KG * RING, "the sets' sums must fit in the rings");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[KG * RING];
+
+    // the bias gradient's share of the launch (small tiles, which leave CUs to spare)
+    if constexpr (ROWT && BM == 64) {
+        const int tiles = a.splits * a.groups * a.tiles_r * a.tiles_c;
+        if ((int)blockIdx.x >= tiles) {
+            static_assert(column_lds(KG * NW * 64) * 4 <= KG * RING, "the column sums fit in the rings");
+            column_block<E, KG * NW * 64>(a.sums, blockIdx.x - tiles, 0, (float*)smem);
+            return;
+        }
+    }
 
     int tr, tc;
     // row tiles of every group of every split, stacked into one grid
@@ -102,8 +120,9 @@ grad_stream(StreamProduct a) {
     const uint16_t* rbase = a.r + group * a.rgroup;
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t base = lds_address(smem);
+    const int set = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / (NW * 64));
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)) - set * NW;
+    const uint32_t base = lds_address(smem) + set * RING;
 
     // This wave's loads: GC of the column panel, then GR of the row operand; lane l
     // lands at byte 16 l of its KB and fetches what the layout places there.
@@ -129,10 +148,12 @@ grad_stream(StreamProduct a) {
     }
 
     // slices: each segment's contraction in slices of BK, the segments one after the other
-    // (split s takes a contiguous share of all of them)
+    // (split s takes a contiguous share of all of them, and a set of it)
     const int per = (a.L + BK - 1) / BK;
-    const int t0 = (int)((int64_t)per * a.segs * split / a.splits);
-    const int nk = (int)((int64_t)per * a.segs * (split + 1) / a.splits) - t0;
+    const int s0 = (int)((int64_t)per * a.segs * split / a.splits);
+    const int s1 = (int)((int64_t)per * a.segs * (split + 1) / a.splits);
+    const int nk = (s1 - s0 + KG - 1) / KG;           // slices a set runs
+    const int t0 = s0 + set * nk, mine = max(min(nk, s1 - t0), 0);
 
     // the next slice to request: its LDS slot and resources, from running scalar state.
     // A row's last 16-byte chunk is read whole (a partly valid one would be dropped): it
@@ -140,12 +161,12 @@ grad_stream(StreamProduct a) {
     // them goes to outputs that are not stored.  With nothing left the lengths are not positive (ld >= its columns), so the
     // column panel and a contraction-major row operand read zeros; a contiguous one is
     // masked by its lanes' own indices.
-    int seg = t0 >= per ? 1 : 0;
+    int seg = t0 >= per && a.segs > 1 ? 1 : 0;
     const int first = (t0 - seg * per) * BK;
-    const uint16_t* cp = a.c[seg] + first * a.ldc[0];
-    const uint16_t* rp = ROWT ? rbase + first * a.ldr : rbase + r0 * a.ldr + (int64_t)t0 * BK;
-    int left = nk > 0 ? a.L - first : 0;              // contraction indices left in the segment
-    int todo = nk;                                    // slices left to request
+    const uint16_t* cp = a.c[seg] + (int64_t)first * a.ldc[0];
+    const uint16_t* rp = ROWT ? rbase + (int64_t)first * a.ldr : rbase + r0 * a.ldr + (int64_t)t0 * BK;
+    int left = mine > 0 ? a.L - first : 0;            // contraction indices left in the segment
+    int todo = mine;                                  // slices left to request
     uint32_t fill = base;
     const int ldc = (int)a.ldc[0], ldr = (int)a.ldr;
     const int cend = (a.C + 7) & ~7, rend = (a.R + 7) & ~7;
@@ -235,7 +256,6 @@ grad_stream(StreamProduct a) {
             static_for<0, FM>([&]<int j>() {
 #pragma unroll
                 for (int i = 0; i < FN; ++i) acc[i][j] = mfma16x16x32<E>(ca[CUR][i], rb[j], acc[i][j]);
-                __builtin_amdgcn_sched_barrier(0);   // the read takes the registers just used
                 rb[j] = read_row.template operator()<NKS, j>(slot);
                 if constexpr (LOADS) {
                     constexpr int J0 = GPW * j / FM, J1 = GPW * (j + 1) / FM;
@@ -263,6 +283,28 @@ grad_stream(StreamProduct a) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
 
+    if constexpr (KG > 1) {
+        // set s > 0 leaves its sums in LDS (thread-contiguous, one accumulator after the
+        // other) and ends; set 0 adds them in order
+        f32x4* sums = (f32x4*)smem;
+        const int t = threadIdx.x % (NW * 64);
+        __syncthreads();
+        if (set > 0) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) sums[((set - 1) * FN * FM + i * FM + j) * NW * 64 + t] = acc[i][j];
+        }
+        __syncthreads();
+        if (set > 0) return;
+#pragma unroll
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] += sums[(g * FN * FM + i * FM + j) * NW * 64 + t];
+    }
+
     LinearArgs o;
     o.M = a.R;
     o.N = a.C;
@@ -275,34 +317,35 @@ grad_stream(StreamProduct a) {
         o.ldy = group ? a.ldy[1] : a.ldy[0];
         o.vec_store = o.epi.vec16 = (a.vec >> group) & 1;
     }
-    finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
+    finish_tile<BM, BN, WM, WN, KG * RING, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
 }
 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
     StreamProduct args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c)), dim3(threads), params, 0,
+    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads), params, 0,
                            stream);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int E>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>
 static const void* grad_fn(bool rowt, int mode) {
     if (!rowt) {
-        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutF32>;
-        return (const void*)grad_stream<BM, BN, WM, WN, STAGES, false, E, kOutRound>;
+        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
+        return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
     }
-    if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32>;
-    if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutF32Add>;
-    return (const void*)grad_stream<BM, BN, WM, WN, STAGES, true, E, kOutRound>;
+    if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;
+    if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32Add>;
+    return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutRound>;
 }
 
 template <int E>
 hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream) {
     switch (cfg) {
-        case 0: return launch_product(grad_fn<256, 256, 2, 4, 2, E>(rowt, mode), a, 512, stream);
-        case 1: return launch_product(grad_fn<256, 128, 4, 2, 3, E>(rowt, mode), a, 512, stream);
-        case 2: return launch_product(grad_fn<128, 128, 2, 4, 4, E>(rowt, mode), a, 512, stream);
-        case 3: return launch_product(grad_fn<64, 64, 2, 2, 4, E>(rowt, mode), a, 256, stream);
+        case 0: return launch_product(grad_fn<256, 256, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
+        case 1: return launch_product(grad_fn<256, 128, 4, 2, 1, 3, E>(rowt, mode), a, 512, stream);
+        case 2: return launch_product(grad_fn<128, 128, 2, 4, 1, 4, E>(rowt, mode), a, 512, stream);
+        case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 4, E>(rowt, mode), a, 256, stream);
+        case 4: return launch_product(grad_fn<64, 64, 2, 2, 2, 4, E>(rowt, mode), a, 512, stream);
         default: return hipErrorInvalidValue;
     }
 }

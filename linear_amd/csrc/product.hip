@@ -9,6 +9,7 @@
 // [row][k]: it takes every alignment, stride and transposition.  It is the path
 // for layouts that the streaming kernels refuse (odd row strides or bases).
 #include "activation.h"
+#include "columns.h"
 #include "train.h"
 
 namespace lin {
@@ -174,52 +175,10 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     }
 }
 
-__device__ inline void store_sum(const ColumnSumArgs& c, int elem, int n, float sum) {
-    if (c.f32) {
-        float* y = (float*)c.db + n;
-        *y = c.accumulate ? *y + sum : sum;
-    } else {
-        ((uint16_t*)c.db)[n] = elem == kBF16 ? narrow<kBF16>(sum) : narrow<kF16>(sum);
-    }
-}
-
-// Column sums over one split of the rows, 64 columns per workgroup: thread t takes
-// the 8 columns 8 (t % 8) of every 128th row from t / 8, four rows' loads in flight;
-// then 16 threads per column add 8 row groups each, and one adds the 16.  A single
-// split stores db itself.  (8192 x 4096 bf16, 64 MB: 16 splits.)
 template <int E>
 __global__ void __launch_bounds__(1024) column_partials(ColumnSumArgs c) {
-    __shared__ float part[128][65];
-    __shared__ float part2[16][64];
-    const int tid = threadIdx.x, c8 = (tid & 7) * 8, g = tid >> 3;
-    const int n = blockIdx.x * 64 + c8, s = blockIdx.y;
-    const int m0 = (int)((int64_t)c.M * s / c.splits), m1 = (int)((int64_t)c.M * (s + 1) / c.splits);
-    float sum[8] = {};
-    for (int64_t m = m0 + g; m < m1; m += 512) {
-        u32x4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = load8(c.dy + (m + 128 * j) * c.lddy + n, m + 128 * j < m1, n, c.N, c.vec);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += widen<E>((uint16_t)(v[j][e >> 1] >> (16 * (e & 1))));
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) part[g][c8 + e] = sum[e];
-    __syncthreads();
-    const int col = tid & 63, h = tid >> 6;
-    float t = part[8 * h][col];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) t += part[8 * h + i][col];
-    part2[h][col] = t;
-    __syncthreads();
-    const int out = blockIdx.x * 64 + tid;
-    if (tid >= 64 || out >= c.N) return;
-    t = part2[0][tid];
-#pragma unroll
-    for (int i = 1; i < 16; ++i) t += part2[i][tid];
-    if (c.splits == 1) store_sum(c, E, out, t);
-    else c.partial[(int64_t)s * c.N + out] = t;
+    __shared__ float lds[column_lds(1024)];
+    column_block<E, 1024>(c, blockIdx.x, blockIdx.y, lds);
 }
 
 // The splits' sums, in their order.
@@ -230,7 +189,7 @@ __global__ void __launch_bounds__(64) column_finish(ColumnSumArgs c) {
     float sum = c.partial[n];
 #pragma unroll 8
     for (int s = 1; s < c.splits; ++s) sum += c.partial[(int64_t)s * c.N + n];
-    store_sum(c, E, n, sum);
+    store_sum<E>(c, n, sum);
 }
 
 template <int E>

@@ -37,6 +37,23 @@ enum : int { kProdRound = 0, kProdF32 = 1, kProdGated = 2 };
 constexpr int kProdTile = 64;
 hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStream_t stream);
 
+// Column sums of dy [M, N]: db[n] = sum_m dy[m, n].
+struct ColumnSumArgs {
+    const uint16_t* dy;
+    int64_t lddy;
+    float* partial;          // [splits, N] (more than one split)
+    void* db;                // 16-bit words or floats
+    int M, N, splits;
+    int f32, accumulate;
+    int vec;                 // 16-byte loads of dy
+};
+// One launch up to 2048 rows (a second one costs what it would save), then a split
+// per 512 rows, up to 64.
+inline int64_t column_sum_splits(int64_t M) {
+    if (M <= 2048) return 1;
+    const int64_t s = (M + 511) / 512;
+    return s > 64 ? 64 : s;
+}
 // The streaming products of the gradients (16-byte aligned layouts):
 //     y[g][r, c] = sum over segments s, k < L of row(g)[r, s Lp + k] * c[s][k, c]
 // Columns c[s] are contraction-major [L, C].  The row operand is [L, R] per group, at
@@ -60,13 +77,22 @@ struct StreamProduct {
     float* partial;
     int64_t ldp;
     int accumulate;          // launch_split_sum into floats: y += sum
+    // the last sum_blocks workgroups take 64 columns of db each instead of a tile
+    // (small tiles of dw, one split)
+    int sum_blocks;
+    ColumnSumArgs sums;
 };
-constexpr int kNumGradConfigs = 4;
-inline constexpr GemmConfig kGradConfigs[kNumGradConfigs] = {
-    {256, 256, 2, 4, 2, 64},
-    {256, 128, 4, 2, 3, 64},
-    {128, 128, 2, 4, 4, 64},
-    {64, 64, 2, 2, 4, 64},
+// Tiles: rows, columns, waves along each, sets of waves that share the slices, ring depth.
+struct GradConfig {
+    int bm, bn, wm, wn, sets, stages;
+};
+constexpr int kNumGradConfigs = 5;
+inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
+    {256, 256, 2, 4, 1, 2},
+    {256, 128, 4, 2, 1, 3},
+    {128, 128, 2, 4, 1, 4},
+    {64, 64, 2, 2, 1, 4},
+    {64, 64, 2, 2, 2, 4},
 };
 // rowt: contraction-major row operand; mode kOutRound, kOutF32, or with rowt kOutF32Add.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
@@ -93,23 +119,6 @@ struct GatedGradArgs {
 };
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream);
 
-// Column sums of dy [M, N]: db[n] = sum_m dy[m, n].
-struct ColumnSumArgs {
-    const uint16_t* dy;
-    int64_t lddy;
-    float* partial;          // [splits, N] (more than one split)
-    void* db;                // 16-bit words or floats
-    int M, N, splits;
-    int f32, accumulate;
-    int vec;                 // 16-byte loads of dy
-};
-// One launch up to 2048 rows (a second one costs what it would save), then a split
-// per 512 rows, up to 64.
-inline int64_t column_sum_splits(int64_t M) {
-    if (M <= 2048) return 1;
-    const int64_t s = (M + 511) / 512;
-    return s > 64 ? 64 : s;
-}
 hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t stream);
 
 // The global gradient norm and clipping: tensors in tables of kGradTensors,
