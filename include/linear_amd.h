@@ -376,7 +376,13 @@ int32_t linear_f16_indexed_noalloc(const uint16_t* x, int64_t ldx,
  * call.  Outputs may not overlap the inputs or each other (LINEAR_E_ALIAS).
  * M == 0 or N == 0 is a no-op; K == 0 gives +0 (act(0) * 0).  M, N and K of this
  * and the gradients' calls are at most 2^31 - 65536, row strides below 2^31.
+ *
+ * workspace: linear_gated_forward_workspace_bytes(M, N, K) bytes of device memory,
+ * 16-byte aligned, owned by the caller, overwritten, free again once the call's work
+ * on `stream` has finished.  It is 0 (and workspace may be NULL) where K is a multiple
+ * of 8 and for a few rows; otherwise it holds copies of the operands with padded rows.
  */
+int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
 int32_t linear_f16_gated(const uint16_t* x, int64_t ldx,
                          const uint16_t* wg, int64_t ldwg,
                          const uint16_t* wu, int64_t ldwu,
@@ -384,7 +390,8 @@ int32_t linear_f16_gated(const uint16_t* x, int64_t ldx,
                          uint16_t* h, int64_t ldh,
                          uint16_t* gate, int64_t ldgate,
                          uint16_t* up, int64_t ldup,
-                         int64_t M, int64_t N, int64_t K, void* stream);
+                         int64_t M, int64_t N, int64_t K,
+                         void* workspace, int64_t workspace_bytes, void* stream);
 int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
                           const uint16_t* wg, int64_t ldwg,
                           const uint16_t* wu, int64_t ldwu,
@@ -392,7 +399,8 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
                           uint16_t* h, int64_t ldh,
                           uint16_t* gate, int64_t ldgate,
                           uint16_t* up, int64_t ldup,
-                          int64_t M, int64_t N, int64_t K, void* stream);
+                          int64_t M, int64_t N, int64_t K,
+                          void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
  * The gated block's gradients, from dh [M, N] and the projections gate and up
@@ -409,7 +417,7 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  * M == 0 gives dwg = dwu = +0.
  *
  * workspace: linear_gated_workspace_bytes(M, N, K) bytes of device memory (it
- * holds dg and du), 16-byte aligned, owned by the caller, overwritten, free again
+ * holds dg and du, partial sums, and copies of operands of odd widths), 16-byte aligned, owned by the caller, overwritten, free again
  * once the call's work on `stream` has finished; two calls in flight at once
  * need two workspaces.  It may not overlap any other argument.
  */

@@ -61,7 +61,7 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_indexed_workspace_bytes",
                 "linear_f16_indexed", "linear_bf16_indexed", "linear_f16_indexed_f32out", "linear_bf16_indexed_f32out",
                 "linear_f16_indexed_noalloc",
-                "linear_f16_gated", "linear_bf16_gated", "linear_gated_workspace_bytes",
+                "linear_f16_gated", "linear_bf16_gated", "linear_gated_forward_workspace_bytes", "linear_gated_workspace_bytes",
                 "linear_f16_gated_backward", "linear_bf16_gated_backward", "linear_backward_workspace_bytes",
                 "linear_f16_backward_input", "linear_bf16_backward_input",
                 "linear_f16_backward_weight", "linear_bf16_backward_weight",
@@ -143,7 +143,8 @@ def _lib():
     lib.linear_indexed_workspace_bytes.argtypes = [i64, i64]
     lib.linear_indexed_workspace_bytes.restype = i64
     for name in ("linear_f16_gated", "linear_bf16_gated"):
-        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp]
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i64, vp, i64, i64, i64, i64, vp,
+                                       i64, vp]
         getattr(lib, name).restype = i32
     for name in ("linear_f16_gated_backward", "linear_bf16_gated_backward"):
         getattr(lib, name).argtypes = ([vp, i64] * 6 + [i32] + [vp, i64] * 3 + [i64, i64, i64, vp, i64, vp])
@@ -157,7 +158,7 @@ def _lib():
     for name in ("linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out"):
         getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp]
         getattr(lib, name).restype = i32
-    for name in ("linear_gated_workspace_bytes", "linear_backward_workspace_bytes"):
+    for name in ("linear_gated_forward_workspace_bytes", "linear_gated_workspace_bytes", "linear_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = i64
     lib.linear_grad_workspace_bytes.argtypes = [i64]
@@ -590,7 +591,16 @@ _BACKWARD_WEIGHT = {(t, f): "linear_%s_backward_weight%s" % (t, "_f32out" if f e
                     for t in ("f16", "bf16") for f in (False, True)}
 
 
-def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
+@functools.lru_cache(maxsize=256)
+def gated_forward_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of device workspace a gated forward call needs: 0 where K is a multiple of 8."""
+    n = _lib().linear_gated_forward_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
+    return n
+
+
+def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, workspace, stream):
     if x.dim() != 2 or wg.dim() != 2:
         raise ValueError("x must be [M, K] and wg, wu [N, K]")
     M, K = x.shape
@@ -598,31 +608,33 @@ def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, stream):
     xp, ldx = _mat(x, "x", dtype)
     gp, ldg = _operand(wg, "wg", dtype, (N, K))
     up_, ldu = _operand(wu, "wu", dtype, (N, K))
-    handle = _launch_stream(stream, x, wg, wu, out, gate, up)
+    handle = _launch_stream(stream, x, wg, wu, out, gate, up, workspace)
     with _on(stream, x.device):
         out, hp, ldh = _output(out, "out", dtype, (M, N), x.device)
         kept = []
         for name, t in (("gate", gate), ("up", up)):
             kept += _output(t, name, dtype, (M, N), x.device) if keep or t is not None else (None, None, 0)
+        workspace, wsp, wsn = _scratch(workspace, gated_forward_workspace_bytes(M, N, K), x.device)
     name = _GATED[tag]
-    rc = _entry(name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K,
-                               handle)
+    rc = _entry(name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K, wsp, wsn,
+                      handle)
     _check(rc, name)
     return (out, kept[0], kept[3]) if keep else out
 
 
 def linear_f16_gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: int = EPI_SILU, keep: bool = False,
-                     out=None, gate=None, up=None, stream=None):
+                     out=None, gate=None, up=None, workspace=None, stream=None):
     """h = act(x @ wg.T) * (x @ wu.T) in one kernel, rounded once to binary16 (x [M, K], wg and wu
     [N, K]; act EPI_SILU, EPI_GELU_TANH or EPI_GELU_ERF).  keep: also return the two rounded
-    projections, which the backward call takes: (h, gate, up).  out, gate, up: tensors to write."""
-    return _gated_call("f16", torch.float16, x, wg, wu, act, keep, out, gate, up, stream)
+    projections, which the backward call takes: (h, gate, up).  out, gate, up: tensors to write.  workspace: a uint8 device
+    tensor of at least gated_forward_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    return _gated_call("f16", torch.float16, x, wg, wu, act, keep, out, gate, up, workspace, stream)
 
 
 def linear_bf16_gated(x: torch.Tensor, wg: torch.Tensor, wu: torch.Tensor, act: int = EPI_SILU, keep: bool = False,
-                      out=None, gate=None, up=None, stream=None):
+                      out=None, gate=None, up=None, workspace=None, stream=None):
     """linear_f16_gated on bfloat16 operands and outputs."""
-    return _gated_call("bf16", torch.bfloat16, x, wg, wu, act, keep, out, gate, up, stream)
+    return _gated_call("bf16", torch.bfloat16, x, wg, wu, act, keep, out, gate, up, workspace, stream)
 
 
 @functools.lru_cache(maxsize=256)

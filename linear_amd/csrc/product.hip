@@ -1,98 +1,236 @@
 // product.hip -- the gated block's and the gradients' products for any layout,
 // the elementwise half of the gated backward, and column sums.
 //
-// product_any computes one 64 x 64 output tile per workgroup of 4 waves with
-// v_mfma_f32_32x32x16 (a 32 x 32 block each; columns as the A operand, rows as B,
-// so a lane holds four consecutive columns of one row).  Both operands are read
-// element by element at their own strides with 64-bit addresses (masked past the
-// edges), along whichever of row and k is contiguous, and staged in LDS as
-// [row][k]: it takes every alignment, stride and transposition.  It is the path
-// for layouts that the streaming kernels refuse (odd row strides or bases).
-#include "activation.h"
+// product_any computes one T x T output tile per workgroup of 4 waves with
+// v_mfma_f32_32x32x16 (a quarter of the tile each; columns as the A operand, rows as
+// B, so a lane holds four consecutive columns of one row).  It is the path for layouts
+// that the streaming kernels refuse (odd row strides or bases): it takes every
+// alignment and stride, with 64-bit addresses.  A thread reads 8 words along an
+// operand's contiguous direction as one 16-byte load of 2-byte alignment (word by word
+// at the edges), the next stage's while this one is multiplied.  A k-contiguous
+// operand is staged as [row][k], a k-major one as [k][row] and read with the
+// transposing read, as in the streaming kernels.
 #include "columns.h"
+#include "grad_impl.h"
 #include "train.h"
 
 namespace lin {
 
 namespace {
 
-constexpr int PB = kProdTile;        // output tile
 constexpr int PK = 32;               // k per stage
-constexpr int PITCH = PK + 8;        // LDS row, in words: 16-byte aligned rows
+constexpr int PITCH = PK + 8;        // words of a [row][k] LDS row: 16-byte aligned rows
 
-// A [PB, PK] operand tile at rows r0.., k0.. into registers: thread t of 256
-// takes 8 elements.  Consecutive threads walk the contiguous direction.
-__device__ inline void any_load(const uint16_t* p, int64_t sr, int64_t sk, int r0, int R, int k0, int L, int tid,
-                                uint16_t (&v)[8]) {
-    const bool along_k = sk == 1;
+// The 8-word pieces of a stage of T rows by PK that thread tid of 256 takes.
+template <int T>
+struct Pieces {
+    u32x4 v[T * PK / 2048];
+};
+
+// ALONG_K: k contiguous (row stride ld), 4 pieces a row; else k-major (ld between
+// k's), T / 8 pieces of 8 rows per k.
+template <int T, bool ALONG_K>
+__device__ inline Pieces<T> any_load(const uint16_t* p, int64_t ld, int r0, int R, int64_t k0, int L, int tid) {
+    Pieces<T> out;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int i = e * 256 + tid;
-        const int r = r0 + (along_k ? i / PK : i % PB), k = k0 + (along_k ? i % PK : i / PB);
-        v[e] = (r < R && k < L) ? p[(int64_t)r * sr + (int64_t)k * sk] : (uint16_t)0;
+    for (int i = 0; i < T * PK / 2048; ++i) {
+        const int c = i * 256 + tid;
+        const int r = r0 + (ALONG_K ? c / (PK / 8) : c % (T / 8) * 8);
+        const int64_t k = k0 + (ALONG_K ? c % (PK / 8) * 8 : c / (T / 8));
+        const bool row = ALONG_K ? r < R : k < L;              // the line that holds the piece
+        const int64_t at = ALONG_K ? k : r, end = ALONG_K ? L : R;
+        const uint16_t* q = p + (ALONG_K ? (int64_t)r : k) * ld + at;
+        if (row && at + 8 <= end) {
+            __builtin_memcpy(&out.v[i], q, 16);
+        } else {
+            out.v[i] = (u32x4){0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (row && at + e < end) out.v[i][e >> 1] |= (uint32_t)q[e] << (16 * (e & 1));
+        }
+    }
+    return out;
+}
+
+// LDS bytes of a stage.
+template <int T, bool ALONG_K>
+constexpr int any_bytes = ALONG_K ? T * PITCH * 2 : PK * T * 2;
+
+template <int T, bool ALONG_K>
+__device__ inline void any_stage(unsigned char* lds, int tid, const Pieces<T>& in) {
+#pragma unroll
+    for (int i = 0; i < T * PK / 2048; ++i) {
+        const int c = i * 256 + tid;
+        if constexpr (ALONG_K) {
+            *(u32x4*)(lds + c / (PK / 8) * PITCH * 2 + c % (PK / 8) * 16) = in.v[i];
+        } else {
+            const int k = c / (T / 8), c8 = c % (T / 8);
+            *(u32x4*)(lds + k * T * 2 + ((c8 ^ (2 * panel_swz<T>(k))) << 4)) = in.v[i];
+        }
     }
 }
-__device__ inline void any_stage(uint16_t* lds, int64_t sk, int tid, const uint16_t (&v)[8]) {
-    const bool along_k = sk == 1;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int i = e * 256 + tid;
-        lds[(along_k ? i / PK : i % PB) * PITCH + (along_k ? i % PK : i / PB)] = v[e];
+
+// The 32-row fragment of rows base .. base + 31 at K step ks: 8 k's from 16 ks + 8 (lane / 32).
+template <int T, bool ALONG_K>
+__device__ inline u32x4 any_frag(const unsigned char* lds, int base, int ks, int lane) {
+    if constexpr (ALONG_K) {
+        return *(const u32x4*)(lds + (base + (lane & 31)) * PITCH * 2 + ks * 32 + (lane >> 5) * 16);
+    } else {
+        // 16 lanes q address rows 16 ks + 8 (q / 2) + s / 4 (+ 4) and the piece at 16 (q % 2) + 4 (s % 4)
+        const int q = lane >> 4, s = lane & 15, k = 16 * ks + 8 * (q >> 1) + (s >> 2);
+        const int r = base + 16 * (q & 1);
+        lds_byte* p = lds_at(lds_address(lds) + k * T * 2 + (((r >> 4) ^ panel_swz<T>(k)) << 5) + 8 * (s & 3));
+        const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * T * 2);
+        return (u32x4){lo.x, lo.y, hi.x, hi.y};
     }
 }
 
-template <int E, int MODE>
+template <int T, int E, int MODE, bool AK, bool BK>
 __global__ void __launch_bounds__(256) product_any(ProductArgs p) {
     constexpr int NB = MODE == kProdGated ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) uint16_t sa[PB * PITCH];
-    __shared__ __attribute__((aligned(16))) uint16_t sb[NB][PB * PITCH];
+    constexpr int F = T / 64;                         // 32 x 32 blocks per wave and direction
+    __shared__ __attribute__((aligned(16))) unsigned char sa[any_bytes<T, AK>];
+    __shared__ __attribute__((aligned(16))) unsigned char sb[NB][any_bytes<T, BK>];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int tr = blockIdx.x / p.tiles_c, tc = blockIdx.x % p.tiles_c;
-    const int r0 = tr * PB, c0 = tc * PB;
-    const int wr = (wave >> 1) * 32, wc = (wave & 1) * 32;
-    const int lr = lane & 31, lh = lane >> 5;
-    f32x16 acc[NB];
+    const int r0 = tr * T, c0 = tc * T;
+    const int wr = (wave >> 1) * (T / 2), wc = (wave & 1) * (T / 2);
+    f32x16 acc[NB][F][F];                             // [operand][column block][row block]
 #pragma unroll
-    for (int b = 0; b < NB; ++b) acc[b] = (f32x16){};
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int j = 0; j < F; ++j) acc[b][i][j] = (f32x16){};
     const int passes = MODE == kProdGated ? 1 : p.segs;
     for (int s = 0; s < passes; ++s) {
-        for (int k0 = 0; k0 < p.L; k0 += PK) {
-            uint16_t va[8], vb[NB][8];
-            any_load(p.a[s], p.sar, p.sak, r0, p.R, k0, p.L, tid, va);
+        Pieces<T> va, vb[NB];
+        auto load = [&](int64_t k0) {
+            va = any_load<T, AK>(p.a[s], p.lda, r0, p.R, k0, p.L, tid);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) any_load(p.b[s + b], p.sbr[s + b], p.sbk[s + b], c0, p.C, k0, p.L, tid, vb[b]);
+            for (int b = 0; b < NB; ++b) vb[b] = any_load<T, BK>(p.b[s + b], p.ldb[s + b], c0, p.C, k0, p.L, tid);
+        };
+        if (p.L > 0) load(0);
+        for (int64_t k0 = 0; k0 < p.L; k0 += PK) {
             __syncthreads();                       // the last stage has been read
-            any_stage(sa, p.sak, tid, va);
+            any_stage<T, AK>(sa, tid, va);
 #pragma unroll
-            for (int b = 0; b < NB; ++b) any_stage(sb[b], p.sbk[s + b], tid, vb[b]);
+            for (int b = 0; b < NB; ++b) any_stage<T, BK>(sb[b], tid, vb[b]);
             __syncthreads();
+            if (k0 + PK < p.L) load(k0 + PK);
 #pragma unroll
             for (int ks = 0; ks < PK / 16; ++ks) {
-                const u32x4 fr = *(const u32x4*)(sa + (wr + lr) * PITCH + ks * 16 + lh * 8);
+                u32x4 fr[F];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    const u32x4 fc = *(const u32x4*)(sb[b] + (wc + lr) * PITCH + ks * 16 + lh * 8);
-                    acc[b] = mfma32x32x16<E>(fc, fr, acc[b]);
+                for (int j = 0; j < F; ++j) fr[j] = any_frag<T, AK>(sa, wr + 32 * j, ks, lane);
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < F; ++i) {
+                        const u32x4 fc = any_frag<T, BK>(sb[b], wc + 32 * i, ks, lane);
+#pragma unroll
+                        for (int j = 0; j < F; ++j) acc[b][i][j] = mfma32x32x16<E>(fc, fr[j], acc[b][i][j]);
+                    }
+            }
+        }
+    }
+    const int lr = lane & 31, lh = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < F; ++j) {
+        const int r = r0 + wr + 32 * j + lr;
+        if (r >= p.R) continue;
+#pragma unroll
+        for (int i = 0; i < F; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int c = c0 + wc + 32 * i + 8 * (v / 4) + 4 * lh + (v % 4);
+                if (c >= p.C) continue;
+                const float sum = acc[0][i][j][v];
+                if constexpr (MODE == kProdF32) {
+                    float* y = (float*)p.y + (int64_t)r * p.ldy + c;
+                    *y = p.accumulate ? *y + sum : sum;
+                } else if constexpr (MODE == kProdRound) {
+                    ((uint16_t*)p.y)[(int64_t)r * p.ldy + c] = narrow<E>(sum);
+                } else {
+                    const float up = acc[NB - 1][i][j][v];
+                    ((uint16_t*)p.y)[(int64_t)r * p.ldy + c] = narrow<E>(gated_act(p.act, sum) * up);
+                    if (p.gate) p.gate[(int64_t)r * p.ldgate + c] = narrow<E>(sum);
+                    if (p.up) p.up[(int64_t)r * p.ldup + c] = narrow<E>(up);
+                }
+            }
+    }
+}
+
+// The gated block's few-row form for any layout: a wave takes one row of both weights
+// and up to 4 rows of x (grid y: row groups), 8 words per lane and step; 4 steps'
+// loads in flight.  (1 x 4001 x 4095 bf16; a 64 x 64 tile per workgroup leaves most
+// CUs without work there.)
+constexpr int ROWS = kAnyRows;
+
+__device__ inline u32x4 any_piece(const uint16_t* p, int k, int K) {
+    u32x4 v = (u32x4){0u, 0u, 0u, 0u};
+    if (k + 8 <= K) __builtin_memcpy(&v, p + k, 16);
+    else
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (k + e < K) v[e >> 1] |= (uint32_t)p[k + e] << (16 * (e & 1));
+    return v;
+}
+
+template <int E>
+__global__ void __launch_bounds__(256) gated_rows_any(ProductArgs p) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n = (int64_t)blockIdx.x * 4 + wave, m0 = (int64_t)blockIdx.y * ROWS;
+    if (n >= p.C) return;
+    const uint16_t *g = p.b[0] + n * p.ldb[0], *u = p.b[1] + n * p.ldb[1];
+    const int rows = (int)min((int64_t)ROWS, p.R - m0);
+    float gs[ROWS] = {}, us[ROWS] = {};
+    for (int64_t k0 = 0; k0 < p.L; k0 += U * 512) {
+        u32x4 gv[U], uv[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t k = min(k0 + j * 512 + lane * 8, (int64_t)p.L);
+            gv[j] = any_piece(g, (int)k, p.L);
+            uv[j] = any_piece(u, (int)k, p.L);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t k = min(k0 + j * 512 + lane * 8, (int64_t)p.L);
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r) {
+                if (r >= rows) break;
+                const u32x4 xv = any_piece(p.a[0] + (m0 + r) * p.lda, (int)k, p.L);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float x = widen<E>((uint16_t)(xv[e >> 1] >> (16 * (e & 1))));
+                    gs[r] = __builtin_fmaf(widen<E>((uint16_t)(gv[j][e >> 1] >> (16 * (e & 1)))), x, gs[r]);
+                    us[r] = __builtin_fmaf(widen<E>((uint16_t)(uv[j][e >> 1] >> (16 * (e & 1)))), x, us[r]);
                 }
             }
         }
     }
-    const int r = r0 + wr + lr;
-    if (r >= p.R) return;
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int c = c0 + wc + 8 * (v / 4) + 4 * lh + (v % 4);
-        if (c >= p.C) continue;
-        if constexpr (MODE == kProdF32) {
-            float* y = (float*)p.y + (int64_t)r * p.ldy + c;
-            *y = p.accumulate ? *y + acc[0][v] : acc[0][v];
-        } else if constexpr (MODE == kProdRound) {
-            ((uint16_t*)p.y)[(int64_t)r * p.ldy + c] = narrow<E>(acc[0][v]);
-        } else {
-            ((uint16_t*)p.y)[(int64_t)r * p.ldy + c] = narrow<E>(gated_act(p.act, acc[0][v]) * acc[NB - 1][v]);
-            if (p.gate) p.gate[(int64_t)r * p.ldgate + c] = narrow<E>(acc[0][v]);
-            if (p.up) p.up[(int64_t)r * p.ldup + c] = narrow<E>(acc[NB - 1][v]);
-        }
+    for (int r = 0; r < ROWS; ++r) {
+        const float gt = wave_sum(gs[r]), ut = wave_sum(us[r]);
+        if (lane != 0 || r >= rows) continue;
+        const int64_t m = m0 + r;
+        ((uint16_t*)p.y)[m * p.ldy + n] = narrow<E>(gated_act(p.act, gt) * ut);
+        if (p.gate) p.gate[m * p.ldgate + n] = narrow<E>(gt);
+        if (p.up) p.up[m * p.ldup + n] = narrow<E>(ut);
+    }
+}
+
+// A matrix [rows, cols] of any stride and base into rows of ldo words (a multiple of
+// 8, 16-byte aligned), the columns past cols zeroed: operands of odd widths become
+// ones that the streaming kernels read.  A thread copies 8 words.
+__global__ void __launch_bounds__(256) repack(const uint16_t* in, int64_t ld, int64_t rows, int cols, uint16_t* out,
+                                              int64_t ldo) {
+    const int64_t chunks = ldo / 8, total = rows * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / chunks;
+        const int c = (int)(i - r * chunks) * 8;
+        *(u32x4*)(out + r * ldo + c) = any_piece(in + r * ld, c, cols);
     }
 }
 
@@ -192,20 +330,39 @@ __global__ void __launch_bounds__(64) column_finish(ColumnSumArgs c) {
     store_sum<E>(c, n, sum);
 }
 
-template <int E>
-const void* any_fn(int mode) {
-    if (mode == kProdF32) return (const void*)product_any<E, kProdF32>;
-    if (mode == kProdGated) return (const void*)product_any<E, kProdGated>;
-    return (const void*)product_any<E, kProdRound>;
+template <int T, int E>
+const void* any_fn(int mode, bool rowt) {
+    if (mode == kProdGated) return (const void*)product_any<T, E, kProdGated, true, true>;
+    if (mode == kProdF32) return (const void*)product_any<T, E, kProdF32, false, false>;
+    return rowt ? (const void*)product_any<T, E, kProdRound, false, false>
+                : (const void*)product_any<T, E, kProdRound, true, false>;
 }
 
 }  // namespace
 
-hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStream_t stream) {
+hipError_t launch_product_any(int elem, int mode, bool rowt, const ProductArgs& p, hipStream_t stream) {
+    if ((mode == kProdF32) > rowt || (mode == kProdGated && rowt)) return hipErrorInvalidValue;
     ProductArgs args = p;
     void* params[] = {&args};
-    return hipLaunchKernel(elem == kBF16 ? any_fn<kBF16>(mode) : any_fn<kF16>(mode),
-                           dim3((unsigned)(p.tiles_r * p.tiles_c)), dim3(256), params, 0, stream);
+    if (mode == kProdGated && p.R <= 8 * ROWS)
+        return hipLaunchKernel(elem == kBF16 ? (const void*)gated_rows_any<kBF16> : (const void*)gated_rows_any<kF16>,
+                               dim3((unsigned)((p.C + 3) / 4), (unsigned)((p.R + ROWS - 1) / ROWS)), dim3(256), params, 0,
+                               stream);
+    const auto tiles = [&](int t) { return ((int64_t)p.R + t - 1) / t * (((int64_t)p.C + t - 1) / t); };
+    const bool large = tiles(128) >= 256;             // enough tiles of 128 for every CU
+    const int t = large ? 128 : kProdTile;
+    args.tiles_c = (p.C + t - 1) / t;
+    const void* fn = elem == kBF16 ? (large ? any_fn<128, kBF16>(mode, rowt) : any_fn<kProdTile, kBF16>(mode, rowt))
+                                   : (large ? any_fn<128, kF16>(mode, rowt) : any_fn<kProdTile, kF16>(mode, rowt));
+    return hipLaunchKernel(fn, dim3((unsigned)tiles(t)), dim3(256), params, 0, stream);
+}
+
+hipError_t launch_repack(const uint16_t* in, int64_t ld, int64_t rows, int cols, uint16_t* out, int64_t ldo,
+                         hipStream_t stream) {
+    void* params[] = {&in, &ld, &rows, &cols, &out, &ldo};
+    const int64_t blocks = (rows * (ldo / 8) + 255) / 256;
+    return hipLaunchKernel((const void*)repack, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0,
+                           stream);
 }
 
 hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStream_t stream) {

@@ -10,18 +10,19 @@ namespace lin {
 // Activations of the gated block (the epilogue program's step codes).
 constexpr bool is_activation(int op) { return op == kEpiSilu || op == kEpiGeluTanh || op == kEpiGeluErf; }
 
-// One product of 16-bit operands with an FP32 accumulator, operands addressed by
-// element strides, in up to two segments s:
-//     acc[r, c] = sum_s sum_{k < L} a[s][r * sar + k * sak] * b[s][c * sbr[s] + k * sbk[s]]
-// The gated block instead keeps the two segments apart (acc_s each).
+// One product of 16-bit operands of any row stride and base with an FP32 accumulator,
+// in up to two segments s:
+//     acc[r, c] = sum_s sum_{k < L} a[s](r, k) * b[s](c, k)
+// a: [R, L] with row stride lda, or, rowt, k-major [L, R]; b: k-major [L, C] with row
+// stride ldb[s].  The gated block has k-contiguous [C, L] operands b and keeps the two
+// segments apart (acc_s each).
 struct ProductArgs {
     const uint16_t* a[2];
     const uint16_t* b[2];
-    int64_t sar, sak;
-    int64_t sbr[2], sbk[2];
+    int64_t lda, ldb[2];
     int segs;
     int R, C, L;             // output rows and columns, contraction length
-    int tiles_r, tiles_c;
+    int tiles_c;             // set by the launch
     void* y;                 // [R, C], row stride ldy: 16-bit words or floats
     int64_t ldy;
     int accumulate;          // FP32 output: y += acc
@@ -33,9 +34,13 @@ struct ProductArgs {
 
 enum : int { kProdRound = 0, kProdF32 = 1, kProdGated = 2 };
 
-// Any layout; tiles of kProdTile x kProdTile outputs.
+// Any layout; the smaller of its two tiles.
 constexpr int kProdTile = 64;
-hipError_t launch_product_any(int elem, int mode, const ProductArgs& p, hipStream_t stream);
+constexpr int kAnyRows = 4;              // rows of x that one pass over the gated weights serves
+hipError_t launch_product_any(int elem, int mode, bool rowt, const ProductArgs& p, hipStream_t stream);
+// out [rows, ldo] = in [rows, cols] with zeros past cols (ldo a multiple of 8).
+hipError_t launch_repack(const uint16_t* in, int64_t ld, int64_t rows, int cols, uint16_t* out, int64_t ldo,
+                         hipStream_t stream);
 
 // Column sums of dy [M, N]: db[n] = sum_m dy[m, n].
 struct ColumnSumArgs {

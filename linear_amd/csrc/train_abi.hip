@@ -90,22 +90,18 @@ int64_t tiles_of(int64_t n, int64_t t) { return (n + t - 1) / t; }
 bool any_grid_ok(int64_t R, int64_t C) { return tiles_of(R, lin::kProdTile) * tiles_of(C, lin::kProdTile) <= kMaxGridX; }
 
 // A one-segment product with its output shape.
-lin::ProductArgs product(const uint16_t* a, int64_t sar, int64_t sak, const uint16_t* b, int64_t sbr, int64_t sbk, void* y,
-                         int64_t ldy, int64_t R, int64_t C, int64_t L) {
+lin::ProductArgs product(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, void* y, int64_t ldy, int64_t R,
+                         int64_t C, int64_t L) {
     lin::ProductArgs p;
     memset(&p, 0, sizeof p);
     p.a[0] = a;
     p.b[0] = b;
-    p.sar = sar;
-    p.sak = sak;
-    p.sbr[0] = sbr;
-    p.sbk[0] = sbk;
+    p.lda = lda;
+    p.ldb[0] = ldb;
     p.segs = 1;
     p.R = (int)R;
     p.C = (int)C;
     p.L = (int)L;
-    p.tiles_r = (int)tiles_of(R, lin::kProdTile);
-    p.tiles_c = (int)tiles_of(C, lin::kProdTile);
     p.y = y;
     p.ldy = ldy;
     return p;
@@ -145,24 +141,67 @@ int choose_gated(int64_t M, int64_t N, int64_t K, int cus) {
     return best;
 }
 
+// What the streaming kernels read: 16-byte chunks of rows, offsets of a tile's rows in 32 bits.
+bool streamable(const void* p, int64_t ld) { return al16(p, ld) && ld <= lin::kMaxLdIn; }
+
+int32_t check_workspace(const void* ws, int64_t have, int64_t need) {
+    if (need == 0) return LINEAR_OK;
+    if (!ws) return LINEAR_E_NULL;
+    if (have < need || (uintptr_t)ws % 16 != 0) return LINEAR_E_WORKSPACE;
+    return LINEAR_OK;
+}
+
+// Operands whose width is not a multiple of 8 are copied into padded rows in the
+// workspace, behind the partial sums (4099 x 4099 x 4099 bf16 dx: 1016 us read in place
+// element by element).
+int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
+bool pack_ok(int64_t rows, int64_t cols) { return rows == 0 || round8(cols) <= kMaxElems / 16 / rows; }
+int64_t packed_bytes(int64_t rows, int64_t cols) { return cols % 8 ? round256(rows * round8(cols) * 2) : 0; }
+
+// The operand p [rows, cols] as the streaming kernels can read it: as it is, or copied
+// to `space`, which then moves on.  contracted: its columns are contraction indices, so
+// the last piece of a row has to hold zeros past them.  (Rows too long for the
+// streaming kernels stay as they are: so does their stride, which those then refuse.)
+int32_t pack_operand(const uint16_t*& p, int64_t& ld, int64_t rows, int64_t cols, bool contracted, unsigned char*& space,
+                     void* stream) {
+    if (cols % 8 == 0 || (streamable(p, ld) && !contracted) || rows == 0 || round8(cols) > lin::kMaxLdIn) return LINEAR_OK;
+    uint16_t* out = (uint16_t*)space;
+    const int32_t st = launched(lin::launch_repack(p, ld, rows, (int)cols, out, round8(cols), (hipStream_t)stream));
+    p = out;
+    ld = round8(cols);
+    space += packed_bytes(rows, cols);
+    return st;
+}
+
 int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
                   int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
-                  int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
+                  int64_t ldup, int64_t M, int64_t N, int64_t K, void* ws, int64_t ws_bytes, void* stream) {
     if (!dims_ok(M, N, K)) return LINEAR_E_SHAPE;
     if (!lin::is_activation(act)) return LINEAR_E_VALUE;
     if (M == 0 || N == 0) return LINEAR_OK;
     if (!h) return LINEAR_E_NULL;
+    const int64_t need = linear_gated_forward_workspace_bytes(M, N, K);
+    if (need < 0) return LINEAR_E_SHAPE;
     const Operand in[] = {{x, M, ldx, K}, {wg, N, ldwg, K}, {wu, N, ldwu, K}};
-    const Operand out[] = {{h, M, ldh, N}, {gate, M, ldgate, N}, {up, M, ldup, N}};
+    const Operand out[] = {{h, M, ldh, N}, {gate, M, ldgate, N}, {up, M, ldup, N}, {ws, 1, need, need, 1}};
     int32_t st = check_operands(in, out);
+    if (st != LINEAR_OK) return st;
+    st = check_workspace(ws, ws_bytes, need);
     if (st != LINEAR_OK) return st;
     if (!any_grid_ok(M, N)) return LINEAR_E_SHAPE;
     int dev = 0;
     DevInfo di;
     st = lin::check_device(&dev, &di);
     if (st != LINEAR_OK) return st;
-    if (al16(x, ldx) && al16(wg, ldwg) && al16(wu, ldwu) && K % 8 == 0 && ldx <= lin::kMaxLdIn && ldwg <= lin::kMaxLdIn &&
-        ldwu <= lin::kMaxLdIn) {
+    if (need > 0) {
+        unsigned char* space = (unsigned char*)ws;
+        if ((st = pack_operand(x, ldx, M, K, true, space, stream)) != LINEAR_OK) return st;
+        if ((st = pack_operand(wg, ldwg, N, K, true, space, stream)) != LINEAR_OK) return st;
+        if ((st = pack_operand(wu, ldwu, N, K, true, space, stream)) != LINEAR_OK) return st;
+    }
+    // whole pieces of K only: the copies have them, with zeros past K
+    if (streamable(x, ldx) && streamable(wg, ldwg) && streamable(wu, ldwu) && (K % 8 == 0 || need > 0)) {
         lin::LinearArgs a;
         memset(&a, 0, sizeof a);
         a.x = x;
@@ -179,29 +218,28 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
         a.ldup = ldup;
         a.M = (int)M;
         a.N = (int)N;
-        a.K = (int)K;
+        a.K = (int)round8(K);
         a.act = act;
         a.vec_gated = (al16(h, ldh) ? 1 : 0) | (al16(gate, ldgate) ? 2 : 0) | (al16(up, ldup) ? 4 : 0);
         a.groups = 1;
         a.xcd_shift = di.xcd_shift;
         if (M == 1 && K <= lin::kGemvMaxK) return launched(lin::launch_gated_gemv(elem, a, (hipStream_t)stream));
-        const int c = choose_gated(M, N, K, di.cus);
+        const int c = choose_gated(M, N, a.K, di.cus);
         const lin::GemmConfig& g = lin::kGatedConfigs[c];
         a.tiles_m = (int)tiles_of(M, g.bm);
         a.tiles_n = (int)tiles_of(2 * N, g.bn);
         return launched(lin::launch_gated_stream(elem, c, a, (hipStream_t)stream));
     }
-    lin::ProductArgs p = product(x, ldx, 1, wg, ldwg, 1, h, ldh, M, N, K);
+    lin::ProductArgs p = product(x, ldx, wg, ldwg, h, ldh, M, N, K);
     p.segs = 2;
     p.b[1] = wu;
-    p.sbr[1] = ldwu;
-    p.sbk[1] = 1;
+    p.ldb[1] = ldwu;
     p.gate = gate;
     p.ldgate = ldgate;
     p.up = up;
     p.ldup = ldup;
     p.act = act;
-    return launched(lin::launch_product_any(elem, lin::kProdGated, p, (hipStream_t)stream));
+    return launched(lin::launch_product_any(elem, lin::kProdGated, false, p, (hipStream_t)stream));
 }
 
 // A streaming product's plan: the tile, the splits of the contraction, and, where the
@@ -315,15 +353,6 @@ int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, cons
     return launched(lin::launch_split_sum(elem, mode != lin::kOutRound, a, stream));
 }
 
-// What the streaming kernels read: 16-byte chunks of rows, offsets of a tile's rows in 32 bits.
-bool streamable(const void* p, int64_t ld) { return al16(p, ld) && ld <= lin::kMaxLdIn; }
-
-int32_t check_workspace(const void* ws, int64_t have, int64_t need) {
-    if (need == 0) return LINEAR_OK;
-    if (!ws) return LINEAR_E_NULL;
-    if (have < need || (uintptr_t)ws % 16 != 0) return LINEAR_E_WORKSPACE;
-    return LINEAR_OK;
-}
 
 // dx [M, K] = dy [M, N] . weight [N, K].
 int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uint16_t* w, int64_t ldw, uint16_t* dx,
@@ -332,6 +361,7 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
     if (M == 0 || K == 0) return LINEAR_OK;
     if (!dx) return LINEAR_E_NULL;
     const int64_t need = linear_backward_workspace_bytes(M, N, K);
+    if (need < 0) return LINEAR_E_SHAPE;
     const Operand in[] = {{dy, M, lddy, N}, {w, N, ldw, K}};
     const Operand out[] = {{dx, M, lddx, K}, {ws, 1, need, need, 1}};
     int32_t st = check_operands(in, out);
@@ -343,7 +373,10 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
     DevInfo di;
     st = lin::check_device(&dev, &di);
     if (st != LINEAR_OK) return st;
-    if (streamable(dy, lddy) && streamable(w, ldw) && N % 8 == 0) {
+    unsigned char* space = (unsigned char*)ws + round256(partial_bytes(1, M, K, slices_of(N)));
+    if ((st = pack_operand(dy, lddy, M, N, true, space, stream)) != LINEAR_OK) return st;
+    if ((st = pack_operand(w, ldw, N, K, false, space, stream)) != LINEAR_OK) return st;
+    if (streamable(dy, lddy) && streamable(w, ldw)) {
         lin::StreamProduct a;
         memset(&a, 0, sizeof a);
         a.r = dy;
@@ -358,8 +391,14 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
         a.segs = a.groups = 1;
         return launch_stream(elem, false, lin::kOutRound, a, di, ws, (hipStream_t)stream);
     }
-    const lin::ProductArgs p = product(dy, lddy, 1, w, 1, ldw, dx, lddx, M, K, N);
-    return launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+    const lin::ProductArgs p = product(dy, lddy, w, ldw, dx, lddx, M, K, N);
+    return launched(lin::launch_product_any(elem, lin::kProdRound, false, p, (hipStream_t)stream));
+}
+
+// The weight call's partial sums: db's and dw's, one after the other in the same space.
+int64_t weight_scratch(int64_t M, int64_t N, int64_t K) {
+    const int64_t sums = lin::column_sum_splits(M);
+    return std::max(sums > 1 ? sums * N * 4 : 0, partial_bytes(1, N, K, slices_of(M)));
 }
 
 // dw [N, K] = dy [M, N]^T . x [M, K], db [N] = column sums of dy.
@@ -371,6 +410,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     if (K > 0 && !dw) return LINEAR_E_NULL;
     const int64_t eb = f32 ? 4 : 2;
     const int64_t need = linear_backward_workspace_bytes(M, N, K);
+    if (need < 0) return LINEAR_E_SHAPE;
     const Operand in[] = {{dy, M, lddy, N}, {x, M, ldx, K}};
     const Operand out[] = {{dw, N, lddw, K, eb}, {db, 1, N, N, eb}, {ws, 1, need, need, 1}};
     int32_t st = check_operands(in, out);
@@ -384,8 +424,6 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     if (st != LINEAR_OK) return st;
     lin::ColumnSumArgs c;
     memset(&c, 0, sizeof c);
-    c.dy = dy;
-    c.lddy = lddy;
     c.partial = (float*)ws;
     c.db = db;
     c.M = (int)M;
@@ -393,8 +431,15 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     c.splits = (int)lin::column_sum_splits(M);
     c.f32 = f32;
     c.accumulate = accumulate != 0;
-    c.vec = al16(dy, lddy);
+    unsigned char* space = (unsigned char*)ws + round256(weight_scratch(M, N, K));
+    if (K > 0) {
+        if ((st = pack_operand(dy, lddy, M, N, false, space, stream)) != LINEAR_OK) return st;
+        if ((st = pack_operand(x, ldx, M, K, false, space, stream)) != LINEAR_OK) return st;
+    }
     const bool streams = K > 0 && streamable(dy, lddy) && streamable(x, ldx);
+    c.dy = dy;
+    c.lddy = lddy;
+    c.vec = al16(dy, lddy);
     const bool with_sums = db && streams && c.splits == 1 && sums_fit(1, N, K, slices_of(M), di.cus);
     if (db && !with_sums) {
         st = launched(lin::launch_column_sum(elem, c, (hipStream_t)stream));
@@ -421,13 +466,18 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
         const int mode = !f32 ? lin::kOutRound : accumulate ? lin::kOutF32Add : lin::kOutF32;
         return launch_stream(elem, true, mode, a, di, ws, (hipStream_t)stream);
     }
-    lin::ProductArgs p = product(dy, 1, lddy, x, 1, ldx, dw, lddw, N, K, M);
+    lin::ProductArgs p = product(dy, lddy, x, ldx, dw, lddw, N, K, M);
     p.accumulate = f32 && accumulate != 0;
-    return launched(lin::launch_product_any(elem, f32 ? lin::kProdF32 : lin::kProdRound, p, (hipStream_t)stream));
+    return launched(lin::launch_product_any(elem, f32 ? lin::kProdF32 : lin::kProdRound, true, p, (hipStream_t)stream));
 }
+
 
 // The gated block's dg | du matrix: columns of one half, a whole number of 64-wide slices.
 int64_t gated_half(int64_t N) { return (N + 63) / 64 * 64; }
+
+int64_t gated_partials(int64_t M, int64_t N, int64_t K) {
+    return std::max(partial_bytes(1, M, K, 2 * slices_of(N)), partial_bytes(2, N, K, slices_of(M)));
+}
 
 int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,
                            int64_t ldwg, const uint16_t* wu, int64_t ldwu, const uint16_t* gate, int64_t ldgate,
@@ -473,6 +523,12 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
+    unsigned char* space = (unsigned char*)(d + M * 2 * Np) + round256(gated_partials(M, N, K));
+    if (want_dx) {
+        if ((st = pack_operand(wg, ldwg, N, K, false, space, stream)) != LINEAR_OK) return st;
+        if ((st = pack_operand(wu, ldwu, N, K, false, space, stream)) != LINEAR_OK) return st;
+    }
+    if (want_dw && (st = pack_operand(x, ldx, M, K, false, space, stream)) != LINEAR_OK) return st;
     const bool dx_streams = streamable(wg, ldwg) && ldwu == ldwg && al16(wu, ldwu) && 2 * Np <= lin::kMaxLdIn;
     if (want_dx && dx_streams) {
         lin::StreamProduct a;
@@ -492,13 +548,12 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         st = launch_stream(elem, false, lin::kOutRound, a, di, d + M * 2 * Np, (hipStream_t)stream);
         if (st != LINEAR_OK) return st;
     } else if (want_dx) {
-        lin::ProductArgs p = product(d, 2 * Np, 1, wg, 1, ldwg, dx, lddx, M, K, N);
+        lin::ProductArgs p = product(d, 2 * Np, wg, ldwg, dx, lddx, M, K, N);
         p.segs = 2;
         p.a[1] = d + Np;
         p.b[1] = wu;
-        p.sbr[1] = 1;
-        p.sbk[1] = ldwu;
-        st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+        p.ldb[1] = ldwu;
+        st = launched(lin::launch_product_any(elem, lin::kProdRound, false, p, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
     if (want_dw && streamable(x, ldx) && 2 * Np <= lin::kMaxLdIn) {
@@ -522,8 +577,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         if (st != LINEAR_OK) return st;
     } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
-            const lin::ProductArgs p = product(d + s * Np, 1, 2 * Np, x, 1, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
-            st = launched(lin::launch_product_any(elem, lin::kProdRound, p, (hipStream_t)stream));
+            const lin::ProductArgs p = product(d + s * Np, 2 * Np, x, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
+            st = launched(lin::launch_product_any(elem, lin::kProdRound, true, p, (hipStream_t)stream));
             if (st != LINEAR_OK) return st;
         }
     }
@@ -588,29 +643,39 @@ struct Range {
 
 extern "C" {
 
+int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    if (!dims_ok(M, N, K) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
+    // a few rows read their weights once, in place
+    return M <= lin::kAnyRows ? 0 : packed_bytes(M, K) + 2 * packed_bytes(N, K);
+}
+
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (!dims_ok(M, N, K) || (M > 0 && gated_half(N) > kMaxElems / 4 / M)) return -1;
-    return M * gated_half(N) * 2 * 2 +
-           std::max(partial_bytes(1, M, K, 2 * slices_of(N)), partial_bytes(2, N, K, slices_of(M)));
+    if (!dims_ok(M, N, K) || !pack_ok(M, gated_half(N)) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
+    const int64_t partials = gated_partials(M, N, K), packed = 2 * packed_bytes(N, K) + packed_bytes(M, K);
+    return M * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (!dims_ok(M, N, K)) return -1;
-    const int64_t sums = lin::column_sum_splits(M);
-    return std::max({sums > 1 ? sums * N * 4 : 0, partial_bytes(1, M, K, slices_of(N)),
-                     partial_bytes(1, N, K, slices_of(M))});
+    if (!dims_ok(M, N, K) || !pack_ok(M, N) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
+    const int64_t in = partial_bytes(1, M, K, slices_of(N)), in_packed = packed_bytes(M, N) + packed_bytes(N, K);
+    const int64_t wt = weight_scratch(M, N, K), wt_packed = packed_bytes(M, N) + packed_bytes(M, K);
+    return std::max(in_packed ? round256(in) + in_packed : in, wt_packed ? round256(wt) + wt_packed : wt);
 }
 
 int32_t linear_f16_gated(const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
                          int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
-                         int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
-    return run_gated(lin::kF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, stream);
+                         int64_t ldup, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+    return run_gated(lin::kF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, workspace,
+                     workspace_bytes, stream);
 }
 
 int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx, const uint16_t* wg, int64_t ldwg, const uint16_t* wu,
                           int64_t ldwu, int32_t act, uint16_t* h, int64_t ldh, uint16_t* gate, int64_t ldgate, uint16_t* up,
-                          int64_t ldup, int64_t M, int64_t N, int64_t K, void* stream) {
-    return run_gated(lin::kBF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, stream);
+                          int64_t ldup, int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                          void* stream) {
+    return run_gated(lin::kBF16, x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, gate, ldgate, up, ldup, M, N, K, workspace,
+                     workspace_bytes, stream);
 }
 
 int32_t linear_f16_gated_backward(const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,

@@ -19,9 +19,9 @@ cpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-d
 
 
 def gated(x=X, ldx=64, wg=WG, ldwg=64, wu=WU, ldwu=64, act=la.EPI_SILU, h=H, ldh=32, g=0, ldg=0, u=0, ldu=0, M=8, N=32,
-          K=64, tag="f16"):
+          K=64, ws=0, nws=0, tag="f16"):
     fn = getattr(la._lib(), "linear_%s_gated" % tag)
-    return fn(x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, g, ldg, u, ldu, M, N, K, None)
+    return fn(x, ldx, wg, ldwg, wu, ldwu, act, h, ldh, g, ldg, u, ldu, M, N, K, ws, nws, None)
 
 
 @pytest.mark.parametrize("tag", ["f16", "bf16"])
@@ -35,6 +35,8 @@ def gated(x=X, ldx=64, wg=WG, ldwg=64, wu=WU, ldwu=64, act=la.EPI_SILU, h=H, ldh
     (dict(ldx=1 << 31), la.LINEAR_E_STRIDE),
     (dict(h=X + 10), la.LINEAR_E_ALIAS), (dict(h=WU - 2), la.LINEAR_E_ALIAS), (dict(g=H, ldg=32), la.LINEAR_E_ALIAS),
     (dict(g=G, ldg=32, u=G + 64, ldu=32), la.LINEAR_E_ALIAS), (dict(u=X, ldu=32), la.LINEAR_E_ALIAS),
+    (dict(K=63), la.LINEAR_E_NULL), (dict(K=63, ws=WS, nws=64), la.LINEAR_E_WORKSPACE),
+    (dict(K=63, ws=WS + 8, nws=1 << 20), la.LINEAR_E_WORKSPACE), (dict(K=63, ws=H, nws=1 << 20), la.LINEAR_E_ALIAS),
 ])
 def test_gated_refusals(tag, kw, code):
     assert gated(tag=tag, **kw) == code
@@ -46,6 +48,7 @@ def test_gated_calls_that_pass_the_checks():
     assert gated(wu=WG) == NODEV                       # one weight for both projections is only read
     assert gated(g=G, ldg=32) == NODEV                 # one projection kept
     assert gated(x=0, wg=0, wu=0, K=0, ldx=0, ldwg=0, ldwu=0) == NODEV
+    assert gated(K=63, ws=WS, nws=1 << 20) == NODEV and gated(K=63, M=3) == NODEV
     assert gated(M=0, x=0, h=0) == la.LINEAR_OK
     assert gated(N=0, wg=0, h=0) == la.LINEAR_OK
 
@@ -198,7 +201,10 @@ def test_workspace_sizes():
     assert la.gated_workspace_bytes(5, 65, 7) >= 5 * 128 * 2 * 2
     assert la.backward_workspace_bytes(4096, 1000, 8) >= 1000 * 4
     assert la.grad_workspace_bytes(0) == 0 and la.grad_workspace_bytes(65) >= 2 * 8
-    for f in (la.gated_workspace_bytes, la.backward_workspace_bytes):
+    assert la.gated_forward_workspace_bytes(4096, 14336, 4096) == 0
+    assert la.gated_forward_workspace_bytes(30, 20, 9) >= (30 + 40) * 16 * 2
+    assert la.backward_workspace_bytes(100, 90, 81) >= (100 * 96 + 90 * 88) * 2
+    for f in (la.gated_forward_workspace_bytes, la.gated_workspace_bytes, la.backward_workspace_bytes):
         with pytest.raises(ValueError):
             f(-1, 2, 3)
     with pytest.raises(ValueError):

@@ -32,6 +32,8 @@ def data(seed, *shapes, scale=None):
 
 def padded(t, pad, shift=0, fill=9.0):
     """The matrix t with `pad` extra columns and a base `shift` words further on, in a sea of `fill`."""
+    if pad < 0:
+        pad = -t.shape[1] % 8 + 8
     flat = torch.full((t.shape[0] * (t.shape[1] + pad) + shift + 64,), fill, dtype=t.dtype, device=t.device)
     v = flat[shift:].as_strided(t.shape, (t.shape[1] + pad, 1))
     v.copy_(t)
@@ -73,7 +75,7 @@ def test_gated_wide_range_of_sums(M, act, t):
         ref.inside(o, w, b, n)
 
 
-LAYOUTS = [(0, 8, 0), (8, 16, 8), (8, 8, 1), (3, 5, 0), (1, 0, 3)]   # pads of rows, and the bases' shift in words
+LAYOUTS = [(0, 8, 0), (8, 16, 8), (8, 8, 1), (3, 5, 0), (1, 0, 3), (-1, 8, 0)]   # pads of rows (-1: to a multiple of 8), and the bases' shift in words
 
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
@@ -83,7 +85,8 @@ def test_gated_strides_bases_and_untouched_surroundings(M, N, K, layout, t):
     p, q, s = layout
     x, wg, wu, _ = make(M, N, K, t)
     want, bound = ref.gated64(x, wg, wu, la.EPI_SILU, t)
-    xs, ws, us = (padded(v, p, s)[0] for v in (x, wg, wu))
+    # NaN around the inputs: nothing read there may reach an output
+    xs, ws, us = (padded(v, p, s, float("nan"))[0] for v in (x, wg, wu))
     outs = [padded(torch.full((M, N), 5.0, dtype=t, device=DEV), q, s) for _ in range(3)]
     fn("gated", t)(xs, ws, us, la.EPI_SILU, keep=True, out=outs[0][0], gate=outs[1][0], up=outs[2][0])
     for (v, flat), w, b, n in zip(outs, want, bound, ("h", "gate", "up")):
@@ -252,7 +255,7 @@ def test_backward_strides_bases_and_untouched_surroundings(M, N, K, layout, t):
     p, q, s = layout
     x, wg, wu, dh = make(M, N, K, t)
     _, g, u = (v.to(t) for v in ref.gated64(x, wg, wu, la.EPI_SILU, t)[0])
-    ins = [padded(v, p, s)[0] for v in (dh, x, wg, wu, g, u)]
+    ins = [padded(v, p, s, float("nan"))[0] for v in (dh, x, wg, wu, g, u)]
 
     def outputs(*specs):
         return [padded(torch.full(sh, 5.0, dtype=o, device=DEV), q, s) for sh, o in specs]
