@@ -528,7 +528,7 @@ def _launch_stream(stream, *tensors):
         devices = {t.get_device() for t in tensors if t is not None}    # -1 on the host
         if len(devices) == 1:
             index = devices.pop()
-            if index >= 0 and index == torch.cuda.current_device():
+            if index >= 0 and index == torch._C._cuda_getDevice():
                 return torch._C._cuda_getCurrentRawStream(index)
     return _stream_handle(stream, *tensors)
 

@@ -47,7 +47,8 @@ __host__ __device__ constexpr int panel_swz(int k) {
 // transposing reads, which name no LDS bytes it could tell apart.  The ring's own
 // waits (an explicit vmcnt and a barrier per slice) order the two.  There is no
 // register output.  The s_nop covers the wait states after the write of m0, and
-// those between a vector write of a resource word and its use.
+// those between a vector write of a resource word and its use.  (m0 is the compiler's
+// reserved register: it writes it anew before each use of its own.)
 __device__ __forceinline__ void lds_dma16_raw(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r));
 }
@@ -330,7 +331,8 @@ static hipError_t launch_product(const void* fn, const StreamProduct& a, int thr
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>
 static const void* grad_fn(bool rowt, int mode) {
     if (!rowt) {
-        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
+        if constexpr (BM < 256)                       // partial sums (split contractions take the smaller tiles)
+            if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
         return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
     }
     if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;

@@ -270,7 +270,9 @@ StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
     double best = tile_time(0, groups, R, C, slices, 1);
     for (int c = 0; c < lin::kNumGradConfigs; ++c) {
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
-            // past twice the chip's tiles a split only adds traffic
+            // the large tiles fill the chip where splitting pays, and past twice the chip's
+            // tiles a split only adds traffic
+            if (s > 1 && lin::kGradConfigs[c].bm == 256) break;
             if (s > 1 && s * groups * tiles_of(R, lin::kGradConfigs[c].bm) * tiles_of(C, lin::kGradConfigs[c].bn) >
                              2 * kPlanCus * kGradTimes[c].per_cu)
                 break;

@@ -17,7 +17,7 @@ SHAPES = [(1, 1, 1), (1, 64, 64), (1, 1024, 768), (1, 4096, 4096), (1, 24, 40000
           (200, 300, 520), (257, 264, 1032), (300, 1000, 768), (512, 768, 512), (1000, 328, 2056), (2050, 200, 264),
           (1040, 2560, 1288)]
 # enough tiles for each of the larger tile sizes to be the choice
-LARGE = [(4100, 2056, 136), (2100, 1032, 520), (4100, 1032, 72), (120, 16392, 200), (600, 520, 264)]
+LARGE = [(4100, 2056, 136), (128, 8200, 264), (2100, 1032, 520), (4100, 1032, 72), (120, 16392, 200), (600, 520, 264)]
 
 
 def fn(name, t):
@@ -210,9 +210,8 @@ def test_gated_gradients_against_differences(act, t):
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 @pytest.mark.parametrize("wide", [False, True], ids=["rounded", "f32out"])
-@pytest.mark.parametrize("i", range(len(SHAPES)), ids=["%dx%dx%d" % s for s in SHAPES])
-def test_linear_backward(i, wide, t):
-    M, N, K = SHAPES[i]
+@pytest.mark.parametrize("M,N,K", SHAPES + [(136, 2568, 2560), (200, 4104, 4100), (4104, 136, 4100)])
+def test_linear_backward(M, N, K, wide, t):
     x, w, _, dy = make(M, N, K, t)
     want, bound = ref.linear_backward64(dy, x, w, t, wide)
     dx = fn("backward_input", t)(dy, w)
@@ -275,6 +274,22 @@ def test_backward_strides_bases_and_untouched_surroundings(M, N, K, layout, t):
         fn("backward_input", t)(ins[0], ins[2], out=outs[0][0])
         fn("backward_weight_f32out" if wide else "backward_weight", t)(ins[0], ins[1], out=outs[1][0], db=outs[2][0][0])
         check(outs, *ref.linear_backward64(dh, x, wg, t, wide))
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_large_views_of_odd_strides(t):
+    """Even sizes in rows of odd stride, enough of them for the larger tile of the any-layout kernel."""
+    for M, N, K in ((2050, 2056, 72), (72, 2056, 2056), (2056, 72, 2056)):
+        x, wg, wu, dh = make(M, N, K, t)
+        xs, gs, us, ds = (padded(v, 3, 1, float("nan"))[0] for v in (x, wg, wu, dh))
+        want, bound = ref.gated64(x, wg, wu, la.EPI_SILU, t)
+        ref.inside(fn("gated", t)(xs, gs, us), want[0], bound[0], "h")
+        for wide in (False, True):
+            want, bound = ref.linear_backward64(dh, x, wg, t, wide)
+            ref.inside(fn("backward_input", t)(ds, gs), want[0], bound[0], "dx")
+            dw, db = fn("backward_weight_f32out" if wide else "backward_weight", t)(ds, xs, bias=True)
+            ref.inside(dw, want[1], bound[1], "dw")
+            ref.inside(db, want[2], bound[2], "db")
 
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
@@ -411,3 +426,60 @@ def test_long_rows_past_32_bits():
     far.copy_(dy)
     assert torch.equal(fn("backward_input", t)(far, w), fn("backward_input", t)(dy, w))
     assert torch.equal(fn("backward_weight", t)(far, x)[0], fn("backward_weight", t)(dy, x)[0])
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_operands_past_2_31_words(t):
+    """Streamed operands whose last rows lie past 2^31 words (and 4 GiB): the contraction over
+    530000 rows, and rows of output that far.  Words -2 .. 2, so FP32 sums are exact (|sum| <=
+    4 * 530000 < 2^24)."""
+    M, W, n = 530000, 4104, 16
+    gen = torch.Generator(device=DEV).manual_seed(7)
+    ints = lambda *s: torch.randint(-2, 3, s, generator=gen, device=DEV, dtype=torch.int8).to(t)   # noqa: E731
+    big, thin, w = ints(M, W), ints(M, n), ints(n, W)
+
+    def chunks(f, *ts):
+        return [f(*(v[i:i + 65536].double() for v in ts)) for i in range(0, M, 65536)]
+
+    dw, db = fn("backward_weight_f32out", t)(thin, big, bias=True)
+    assert torch.equal(dw, sum(chunks(lambda a, b: a.t() @ b, thin, big)).float())
+    assert torch.equal(db, sum(chunks(lambda a: a.sum(0), thin)).float())
+    dw, db = fn("backward_weight_f32out", t)(big, thin, bias=True)
+    assert torch.equal(dw, sum(chunks(lambda a, b: a.t() @ b, big, thin)).float())
+    assert torch.equal(db, sum(chunks(lambda a: a.sum(0), big)).float())
+    wt = w.t().contiguous()                                     # [W, n]: dx [M, n] from dy [M, W]
+    dx = fn("backward_input", t)(big, wt)
+    assert torch.equal(dx, torch.cat(chunks(lambda a: (a @ wt.double()).to(t), big)))
+    dx = fn("backward_input", t)(thin, w)                       # dx [M, W]: the output is the large one
+    for i in range(0, M, 65536):
+        assert torch.equal(dx[i:i + 65536], (thin[i:i + 65536].double() @ w.double()).to(t))
+    _, g, u = fn("gated", t)(big, w, w, keep=True)
+    assert torch.equal(g, torch.cat(chunks(lambda a: (a @ w.double().t()).to(t), big))) and torch.equal(g, u)
+
+
+def test_random_sweep():
+    """Random sizes, types, activations, row pads and base shifts over every call."""
+    import random
+    rng = random.Random(2024)
+    for case in range(60):
+        t = rng.choice(TYPES)
+        M, N, K = (int(round(2 ** rng.uniform(0, 10.5))) for _ in range(3))
+        if rng.random() < 0.6:
+            N, K = (max(8, v // 8 * 8) for v in (N, K))
+        pad, shift, act = rng.choice([0, 8, 16, 3, -1]), rng.choice([0, 0, 0, 8, 1]), rng.choice(ACTS)
+        print("case", case, t, (M, N, K), pad, shift, act, flush=True)
+        x, wg, wu, dh = make(M, N, K, t, seed=case)
+        xs, gs, us, ds = (padded(v, pad, shift, float("nan"))[0] for v in (x, wg, wu, dh))
+        want, bound = ref.gated64(x, wg, wu, act, t)
+        for o, w, b in zip(fn("gated", t)(xs, gs, us, act, keep=True), want, bound):
+            ref.inside(o, w, b, "gated")
+        g, u = want[1].to(t), want[2].to(t)
+        want, bound, _ = ref.gated_backward64(dh, x, wg, wu, g, u, act, t)
+        for o, w, b in zip(fn("gated_backward", t)(ds, xs, gs, us, g, u, act), want, bound):
+            ref.inside(o, w, b, "gated backward")
+        for wide in (False, True):
+            want, bound = ref.linear_backward64(dh, x, wg, t, wide)
+            ref.inside(fn("backward_input", t)(ds, gs), want[0], bound[0], "dx")
+            dw, db = fn("backward_weight_f32out" if wide else "backward_weight", t)(ds, xs, bias=True)
+            ref.inside(dw, want[1], bound[1], "dw")
+            ref.inside(db, want[2], bound[2], "db")
