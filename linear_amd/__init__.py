@@ -557,10 +557,10 @@ def _operand(t, name, dtype, shape):
     return _mat(t, name, dtype)
 
 
-def _output(t, name, dtype, shape, device):
-    """The output tensor (a new one when not given), its pointer and row stride."""
+def _output(t, name, dtype, shape, like):
+    """The output tensor (a new one on the device of `like` when not given), its pointer and row stride."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
         return t, t.data_ptr(), max(shape[1], 1)
     return (t, *_operand(t, name, dtype, shape))
 
@@ -610,10 +610,10 @@ def _gated_call(tag, dtype, x, wg, wu, act, keep, out, gate, up, workspace, stre
     up_, ldu = _operand(wu, "wu", dtype, (N, K))
     handle = _launch_stream(stream, x, wg, wu, out, gate, up, workspace)
     with _on(stream, x.device):
-        out, hp, ldh = _output(out, "out", dtype, (M, N), x.device)
+        out, hp, ldh = _output(out, "out", dtype, (M, N), x)
         kept = []
         for name, t in (("gate", gate), ("up", up)):
-            kept += _output(t, name, dtype, (M, N), x.device) if keep or t is not None else (None, None, 0)
+            kept += _output(t, name, dtype, (M, N), x) if keep or t is not None else (None, None, 0)
         workspace, wsp, wsn = _scratch(workspace, gated_forward_workspace_bytes(M, N, K), x.device)
     name = _GATED[tag]
     rc = _entry(name)(xp, ldx, gp, ldg, up_, ldu, int(act), hp, ldh, kept[1], kept[2], kept[4], kept[5], M, N, K, wsp, wsn,
@@ -661,9 +661,9 @@ def _gated_backward_call(tag, dtype, dh, x, wg, wu, gate, up, act, need_dx, need
     handle = _launch_stream(stream, dh, x, wg, wu, gate, up, dx, dwg, dwu, workspace)
     none = (None, None, 0)
     with _on(stream, x.device):
-        dx, *dxa = _output(dx, "dx", dtype, (M, K), x.device) if need_dx else none
-        dwg, *dga = _output(dwg, "dwg", dtype, (N, K), x.device) if need_dw else none
-        dwu, *dua = _output(dwu, "dwu", dtype, (N, K), x.device) if need_dw else none
+        dx, *dxa = _output(dx, "dx", dtype, (M, K), x) if need_dx else none
+        dwg, *dga = _output(dwg, "dwg", dtype, (N, K), x) if need_dw else none
+        dwu, *dua = _output(dwu, "dwu", dtype, (N, K), x) if need_dw else none
         workspace, wsp, wsn = _scratch(workspace, gated_workspace_bytes(M, N, K), x.device)
     name = _GATED_BACKWARD[tag]
     rc = _entry(name)(*args, int(act), *dxa, *dga, *dua, M, N, K, wsp, wsn, handle)
@@ -705,7 +705,7 @@ def _backward_input_call(tag, dtype, dy, weight, out, workspace, stream):
     wp, ldw = _operand(weight, "weight", dtype, (N, K))
     handle = _launch_stream(stream, dy, weight, out, workspace)
     with _on(stream, dy.device):
-        out, xp, ldx = _output(out, "out", dtype, (M, K), dy.device)
+        out, xp, ldx = _output(out, "out", dtype, (M, K), dy)
         workspace, wsp, wsn = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)
     name = _BACKWARD_INPUT[tag]
     rc = _entry(name)(yp, ldy, wp, ldw, xp, ldx, M, N, K, wsp, wsn, handle)
@@ -737,7 +737,7 @@ def _backward_weight_call(tag, dtype, f32, dy, x, bias, accumulate, out, db, wor
     handle = _launch_stream(stream, dy, x, out, db, workspace)
     odt = torch.float32 if f32 else dtype
     with _on(stream, dy.device):
-        out, wp, ldw = _output(out, "out", odt, (N, K), dy.device)
+        out, wp, ldw = _output(out, "out", odt, (N, K), dy)
         if bias and db is None:
             db = torch.empty((N,), dtype=odt, device=dy.device)
         workspace, wsp, wsn = _scratch(workspace, backward_workspace_bytes(M, N, K), dy.device)

@@ -247,8 +247,7 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, unsigned char* 
     constexpr int TILEB = BM * BN * 2;
     const int wn = wave % WN, wm = wave / WN;
     const int lr = lane % R, lh = lane / R;
-    if constexpr (MODE == kOutF32 || MODE == kOutF32Add) {
-        constexpr bool ADD = MODE == kOutF32Add;
+    if constexpr (MODE == kOutF32) {
         // the FP32 sums go out the same way, staged as floats in the freed ring
         // (in row bands when the whole tile does not fit): row r of a band holds
         // BN / 4 chunks of 16 bytes, chunk c at position c ^ (r % (BN / 4))
@@ -286,18 +285,18 @@ __device__ __forceinline__ void finish_tile(const LinearArgs& a, unsigned char* 
                 if (m >= a.M) continue;
                 float* dst = (float*)a.y + (int64_t)m * a.ldy + n;
                 if (vec && n + 3 < a.N) {
-                    *(f32x4*)dst = ADD ? *(const f32x4*)dst + v : v;
+                    *(f32x4*)dst = v;
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (n + e < a.N) dst[e] = ADD ? dst[e] + v[e] : v[e];
+                        if (n + e < a.N) dst[e] = v[e];
                 }
             }
         }
         return;
     }
 
-    if constexpr (MODE != kOutF32 && MODE != kOutF32Add) {
+    if constexpr (MODE != kOutF32) {
         // stage the rounded tile in the (now free) ring, then finish it in row order:
         // the bias or the epilogue program, and 16-byte stores of whole row chunks
         static_assert(BM * BN * 2 <= RINGB, "the rounded tile must fit in the ring");

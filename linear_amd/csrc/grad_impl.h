@@ -318,7 +318,32 @@ grad_stream(StreamProduct a) {
         o.ldy = group ? a.ldy[1] : a.ldy[0];
         o.vec_store = o.epi.vec16 = (a.vec >> group) & 1;
     }
-    finish_tile<BM, BN, WM, WN, KG * RING, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
+    if constexpr (MODE == kOutF32 || MODE == kOutF32Add) {
+        // FP32 sums leave straight from the registers: the four lanes of a row write 64
+        // bytes of it, the wave's next fragment the 64 beside them, and the workgroup
+        // ends without waiting for its stores (0.5 to 2.5% faster than staged in LDS:
+        // 8192 x 4096 x 4096 214 -> 211 us, adding to the output 224 -> 218)
+        const bool vec = o.vec_store && (uintptr_t)o.y % 16 == 0;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int r = r0 + wm * TM + j * R + s;
+            if (r >= o.M) continue;
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                const int c = c0 + wn * TN + i * R + 4 * q;
+                float* y = (float*)o.y + (int64_t)r * o.ldy + c;
+                if (vec && c + 3 < o.N) {
+                    *(f32x4*)y = MODE == kOutF32Add ? *(const f32x4*)y + acc[i][j] : acc[i][j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < o.N) y[e] = MODE == kOutF32Add ? y[e] + acc[i][j][e] : acc[i][j][e];
+                }
+            }
+        }
+    } else {
+        finish_tile<BM, BN, WM, WN, KG * RING, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
+    }
 }
 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {

@@ -262,7 +262,7 @@ double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t slices, 
     const lin::GradConfig& g = lin::kGradConfigs[cfg];
     const double main = rounds_time(kGradTimes[cfg], splits * groups * tiles_of(R, g.bm) * tiles_of(C, g.bn),
                                     tiles_of(slices, splits), kPlanCus);
-    return splits == 1 ? main : main + 2.0 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
+    return splits == 1 ? main : main + 3.5 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
 }
 
 StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
