@@ -26,10 +26,11 @@
  *    neither allocates, frees nor keeps them after the call returns.
  *  - Work is enqueued on `stream` (a hipStream_t; NULL means the default stream)
  *    and the call returns without synchronising.  Results are visible after the
- *    stream is synchronised.  A call enqueues kernel launches only (one, or two:
- *    a column split of a large GEMM, see linear_plan, and the indexed call's
- *    routing pass), no allocation, copy or memset, so it can be captured into a
- *    HIP graph (the first activation call on a device excepted, see below).
+ *    stream is synchronised.  A call enqueues kernel launches only (one or a few:
+ *    a column split of a large GEMM, see linear_plan, the indexed call's routing
+ *    pass, the parts of a gradient), no allocation, copy or memset, so it can be
+ *    captured into a HIP graph (the first call of an epilogue program with an
+ *    activation on a device excepted, see below).
  *  - Only y[m, n] for m < M, n < N is written; stride padding is never touched.
  *  - Rounding is IEEE round-to-nearest-even with subnormals kept (no flush to
  *    zero) and overflow to infinity; the empty sum (K == 0) is +0.
@@ -69,7 +70,7 @@ extern "C" {
 #define LINEAR_E_LAUNCH   7  /* a kernel launch failed; linear_last_hip_error() has the HIP code */
 #define LINEAR_E_EPILOGUE 8  /* epilogue program: step count outside 0..LINEAR_EPI_MAX_STEPS or an unknown step */
 #define LINEAR_E_CAPTURE  9  /* the first activation epilogue on a device was called under stream capture */
-#define LINEAR_E_WORKSPACE 10 /* indexed contraction: workspace misaligned or below linear_indexed_workspace_bytes */
+#define LINEAR_E_WORKSPACE 10 /* workspace misaligned or smaller than the call's linear_*_workspace_bytes */
 #define LINEAR_E_SCRATCH  11  /* linear_f16_indexed_noalloc: the call needs more than LINEAR_NOALLOC_SCRATCH_BYTES */
 #define LINEAR_E_VALUE    12  /* unknown activation or tensor type, or a negative or NaN max_norm */
 #define LINEAR_E_MEMORY   13  /* linear_grad_clip: no host memory for the overlap check */

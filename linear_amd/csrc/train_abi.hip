@@ -399,7 +399,7 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
 
 // The weight call's partial sums: db's and dw's, one after the other in the same space.
 int64_t weight_scratch(int64_t M, int64_t N, int64_t K) {
-    const int64_t sums = lin::column_sum_splits(M);
+    const int64_t sums = lin::column_sum_splits(M, N);
     return std::max(sums > 1 ? sums * N * 4 : 0, partial_bytes(1, N, K, slices_of(M)));
 }
 
@@ -430,7 +430,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     c.db = db;
     c.M = (int)M;
     c.N = (int)N;
-    c.splits = (int)lin::column_sum_splits(M);
+    c.splits = (int)lin::column_sum_splits(M, N);
     c.f32 = f32;
     c.accumulate = accumulate != 0;
     unsigned char* space = (unsigned char*)ws + round256(weight_scratch(M, N, K));

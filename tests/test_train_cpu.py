@@ -205,6 +205,13 @@ def test_workspace_sizes():
     assert la.gated_forward_workspace_bytes(30, 20, 9) >= (30 + 40) * 16 * 2
     assert la.backward_workspace_bytes(100, 90, 81) >= (100 * 96 + 90 * 88) * 2
     for f in (la.gated_forward_workspace_bytes, la.gated_workspace_bytes, la.backward_workspace_bytes):
+        for zero in range(3):                     # any size may be zero, beside large ones
+            for other in (1, 63, 5000, 70000):
+                sizes = [other] * 3
+                sizes[zero] = 0
+                assert f(*sizes) >= 0
+        assert f(0, 0, 0) >= 0
+    for f in (la.gated_forward_workspace_bytes, la.gated_workspace_bytes, la.backward_workspace_bytes):
         with pytest.raises(ValueError):
             f(-1, 2, 3)
     with pytest.raises(ValueError):

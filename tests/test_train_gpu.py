@@ -138,6 +138,8 @@ def test_empty_and_zero_sums(t):
     dx, dwg, dwu = fn("gated_backward", t)(z(5, 0), z(5, 8), z(0, 8), z(0, 8), z(5, 0), z(5, 0), dx=full(5, 8))
     assert not dx.any() and dwg.shape == (0, 8)
     assert not fn("backward_input", t)(z(5, 0), z(0, 8), out=full(5, 8)).any()
+    assert not fn("backward_input", t)(z(5000, 0), z(0, 8), out=full(5000, 8)).any()
+    assert not fn("gated", t)(z(1, 0), z(7, 0), z(7, 0), out=full(1, 7)).any()
     dw, db = fn("backward_weight", t)(z(0, 7), z(0, 8), out=full(7, 8), db=full(7))
     assert not dw.any() and not db.any()
     dw, db = fn("backward_weight", t)(z(5, 7), z(5, 0), db=full(7))
