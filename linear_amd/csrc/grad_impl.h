@@ -371,7 +371,7 @@ hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduc
         case 0: return launch_product(grad_fn<256, 256, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
         case 1: return launch_product(grad_fn<256, 128, 4, 2, 1, 3, E>(rowt, mode), a, 512, stream);
         case 2: return launch_product(grad_fn<128, 128, 2, 4, 1, 4, E>(rowt, mode), a, 512, stream);
-        case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 4, E>(rowt, mode), a, 256, stream);
+        case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 5, E>(rowt, mode), a, 256, stream);
         case 4: return launch_product(grad_fn<64, 64, 2, 2, 2, 4, E>(rowt, mode), a, 512, stream);
         default: return hipErrorInvalidValue;
     }

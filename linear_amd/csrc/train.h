@@ -100,7 +100,7 @@ inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {256, 256, 2, 4, 1, 2},
     {256, 128, 4, 2, 1, 3},
     {128, 128, 2, 4, 1, 4},
-    {64, 64, 2, 2, 1, 4},
+    {64, 64, 2, 2, 1, 5},
     {64, 64, 2, 2, 2, 4},
 };
 // rowt: contraction-major row operand; mode kOutRound, kOutF32, or with rowt kOutF32Add.

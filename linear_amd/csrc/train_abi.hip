@@ -254,7 +254,7 @@ struct StreamPlan {
 // kGradConfigs' times (16 and 64 slices).  The splits' partial sums cost a launch and
 // their traffic (0.65 us per MB written and read back).
 constexpr TileTime kGradTimes[lin::kNumGradConfigs] = {
-    {7.0, 1.55, 1}, {5.5, 0.85, 1}, {4.6, 0.50, 1}, {3.2, 0.39, 2}, {3.7, 0.205, 1}};
+    {7.0, 1.55, 1}, {5.5, 0.85, 1}, {4.6, 0.50, 1}, {3.5, 0.31, 2}, {3.7, 0.205, 1}};
 constexpr int kPlanCus = 256;      // plans (and so workspaces) do not depend on the device
 constexpr double kLaunchGap = 4.0;
 
