@@ -356,7 +356,7 @@ static hipError_t launch_product(const void* fn, const StreamProduct& a, int thr
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>
 static const void* grad_fn(bool rowt, int mode) {
     if (!rowt) {
-        if constexpr (BM < 256)                       // partial sums (split contractions take the smaller tiles)
+        if constexpr (BM < 256 && STAGES > 2)         // partial sums (the tiles that split contractions take)
             if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
         return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
     }
@@ -373,6 +373,7 @@ hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduc
         case 2: return launch_product(grad_fn<128, 128, 2, 4, 1, 4, E>(rowt, mode), a, 512, stream);
         case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 5, E>(rowt, mode), a, 256, stream);
         case 4: return launch_product(grad_fn<64, 64, 2, 2, 2, 4, E>(rowt, mode), a, 512, stream);
+        case 5: return launch_product(grad_fn<128, 128, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
         default: return hipErrorInvalidValue;
     }
 }

@@ -95,13 +95,14 @@ struct StreamProduct {
 struct GradConfig {
     int bm, bn, wm, wn, sets, stages;
 };
-constexpr int kNumGradConfigs = 5;
+constexpr int kNumGradConfigs = 6;
 inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {256, 256, 2, 4, 1, 2},
     {256, 128, 4, 2, 1, 3},
     {128, 128, 2, 4, 1, 4},
     {64, 64, 2, 2, 1, 5},
     {64, 64, 2, 2, 2, 4},
+    {128, 128, 2, 4, 1, 2},
 };
 // rowt: contraction-major row operand; mode kOutRound, kOutF32, or with rowt kOutF32Add.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);

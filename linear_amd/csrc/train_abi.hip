@@ -251,10 +251,13 @@ struct StreamPlan {
     int cfg1;
 };
 
-// kGradConfigs' times (16 and 64 slices).  The splits' partial sums cost a launch and
-// their traffic (0.65 us per MB written and read back).
-constexpr TileTime kGradTimes[lin::kNumGradConfigs] = {
-    {7.0, 1.55, 1}, {5.5, 0.85, 1}, {4.6, 0.50, 1}, {3.5, 0.31, 2}, {3.7, 0.205, 1}};
+// kGradConfigs' times, from 4096 x 4096 outputs at 1 to 64 slices (and 1024 x 1024 for
+// the small tiles).  128 x 128 comes with a deep ring for a single round and, with two
+// slots, two to a CU, whose ends overlap: 11960 x 2632 outputs of one slice take 21.4 us
+// on the latter, 28 to 33 on the other large tiles.  The splits' partial sums cost a
+// launch and their traffic (0.65 us per MB written and read back).
+constexpr TileTime kGradTimes[lin::kNumGradConfigs] = {{10.2, 1.50, 1}, {7.0, 0.83, 1}, {4.1, 0.50, 1},
+                                                       {2.8, 0.365, 2}, {3.4, 0.20, 1}, {5.7, 0.92, 2}};
 constexpr int kPlanCus = 256;      // plans (and so workspaces) do not depend on the device
 constexpr double kLaunchGap = 4.0;
 
@@ -272,7 +275,7 @@ StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
             // the large tiles fill the chip where splitting pays, and past twice the chip's
             // tiles a split only adds traffic
-            if (s > 1 && lin::kGradConfigs[c].bm == 256) break;
+            if (s > 1 && (lin::kGradConfigs[c].bm == 256 || lin::kGradConfigs[c].stages == 2)) break;
             if (s > 1 && s * groups * tiles_of(R, lin::kGradConfigs[c].bm) * tiles_of(C, lin::kGradConfigs[c].bn) >
                              2 * kPlanCus * kGradTimes[c].per_cu)
                 break;

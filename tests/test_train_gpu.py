@@ -212,7 +212,8 @@ def test_gated_gradients_against_differences(act, t):
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 @pytest.mark.parametrize("wide", [False, True], ids=["rounded", "f32out"])
-@pytest.mark.parametrize("M,N,K", SHAPES + [(136, 2568, 2560), (200, 4104, 4100), (4104, 136, 4100)])
+@pytest.mark.parametrize("M,N,K", SHAPES + [(136, 2568, 2560), (200, 4104, 4100), (4104, 136, 4100), (1100, 2568, 2560),
+                                            (2568, 1100, 2560)])
 def test_linear_backward(M, N, K, wide, t):
     x, w, _, dy = make(M, N, K, t)
     want, bound = ref.linear_backward64(dy, x, w, t, wide)
@@ -485,3 +486,40 @@ def test_random_sweep():
             dw, db = fn("backward_weight_f32out" if wide else "backward_weight", t)(ds, xs, bias=True)
             ref.inside(dw, want[1], bound[1], "dw")
             ref.inside(db, want[2], bound[2], "db")
+
+
+def test_calls_from_four_threads():
+    """Each thread on a stream of its own, without workspaces of the caller's: the words of one thread."""
+    import threading
+    t = torch.bfloat16
+    sets = [make(M, N, K, t, seed=M) for M, N, K in ((300, 1000, 776), (17, 520, 264), (130, 1001, 769), (1, 2048, 1536))]
+
+    def step(x, wg, wu, dh, stream=None):
+        h, g, u = fn("gated", t)(x, wg, wu, keep=True, stream=stream)
+        grads = list(fn("gated_backward", t)(dh, x, wg, wu, g, u, stream=stream))
+        grads += list(fn("backward_weight", t)(dh, x, bias=True, stream=stream))
+        grads.append(fn("backward_input", t)(dh, wg, stream=stream))
+        return [h, *grads, la.linear_grad_norm(grads, stream=stream)]
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    got, errors = [None] * 4, []
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(10):
+                got[i] = step(*sets[i], stream=s)
+            s.synchronize()
+        except Exception as e:                                   # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors
+    for a, b in zip(got, want):
+        for o, w in zip(a, b):
+            assert torch.equal(o, w)
