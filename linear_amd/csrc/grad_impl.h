@@ -82,9 +82,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_rsrc(const uint16_t* p, 
 // and add their sums in LDS at the end: a small tile's slice is bound by the latency of
 // its reads, so several in flight cost one's time (no traffic, unlike a split over
 // workgroups).  The sets run the same number of slices, empty ones at the end.
+template <int BM, int BN, int KG, int STAGES>
+constexpr int grad_lds = KG * STAGES * 64 * (BM + BN) * 2;   // bytes of the rings
+
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
-__global__ void __launch_bounds__(KG * WM * WN * 64)
-grad_stream(StreamProduct a) {
+__device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, unsigned char* smem) {
     constexpr int BK = 64, R = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
     constexpr int NW = WM * WN;
     constexpr int TM = BM / WM, TN = BN / WN;
@@ -100,21 +102,21 @@ grad_stream(StreamProduct a) {
     constexpr int RING = STAGES * SLICE;
     static_assert(STAGES >= 2 && KG * RING <= 160 * 1024, "LDS rings too large");
     static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= KG * RING, "the sets' sums must fit in the rings");
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[KG * RING];
+    static_assert(grad_lds<BM, BN, KG, STAGES> == KG * RING, "the rings' bytes");
 
     // the bias gradient's share of the launch (small tiles, which leave CUs to spare)
     if constexpr (ROWT && BM == 64) {
         const int tiles = a.splits * a.groups * a.tiles_r * a.tiles_c;
-        if ((int)blockIdx.x >= tiles) {
+        if (block >= tiles) {
             static_assert(column_lds(KG * NW * 64) * 4 <= KG * RING, "the column sums fit in the rings");
-            column_block<E, KG * NW * 64>(a.sums, blockIdx.x - tiles, 0, (float*)smem);
+            column_block<E, KG * NW * 64>(a.sums, block - tiles, 0, (float*)smem);
             return;
         }
     }
 
     int tr, tc;
     // row tiles of every group of every split, stacked into one grid
-    tile_coords(blockIdx.x, a.splits * a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
+    tile_coords(block, a.splits * a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
     const int stack = tr / a.tiles_r;                 // split * groups + group
     const int split = stack / a.groups, group = stack - split * a.groups;
     const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
@@ -346,6 +348,30 @@ grad_stream(StreamProduct a) {
     }
 }
 
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
+__global__ void __launch_bounds__(KG * WM * WN * 64)
+grad_stream(StreamProduct a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[grad_lds<BM, BN, KG, STAGES>];
+    grad_tile<BM, BN, WM, WN, KG, STAGES, ROWT, E, MODE>(a, blockIdx.x, smem);
+}
+
+// Two products that do not depend on each other in one launch, the gated block's dx (on
+// 64 x 64 tiles of two sets, or 128 x 128) and dWg, dWu (128 x 128): where each alone
+// leaves CUs idle in its last round, the other's tiles fill them.  dx's tiles, the
+// longer ones, come first.
+template <bool SMALL, int E>
+__global__ void __launch_bounds__(512) grad_pair(StreamProduct a, StreamProduct b) {
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[grad_lds<128, 128, 1, 4>];
+    static_assert(grad_lds<64, 64, 2, 4> <= grad_lds<128, 128, 1, 4>, "one LDS block for both");
+    const int tiles = a.tiles_r * a.tiles_c;
+    if ((int)blockIdx.x < tiles) {
+        if constexpr (SMALL) grad_tile<64, 64, 2, 2, 2, 4, false, E, kOutRound>(a, blockIdx.x, smem);
+        else grad_tile<128, 128, 2, 4, 1, 4, false, E, kOutRound>(a, blockIdx.x, smem);
+    } else {
+        grad_tile<128, 128, 2, 4, 1, 4, true, E, kOutRound>(b, blockIdx.x - tiles, smem);
+    }
+}
+
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
     StreamProduct args = a;
     void* params[] = {&args};
@@ -376,6 +402,15 @@ hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduc
         case 5: return launch_product(grad_fn<128, 128, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
         default: return hipErrorInvalidValue;
     }
+}
+
+template <int E>
+hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream) {
+    StreamProduct aa = a, bb = b;
+    void* params[] = {&aa, &bb};
+    return hipLaunchKernel(small ? (const void*)grad_pair<true, E> : (const void*)grad_pair<false, E>,
+                           dim3((unsigned)(a.tiles_r * a.tiles_c + b.groups * b.tiles_r * b.tiles_c)), dim3(512), params, 0,
+                           stream);
 }
 
 }  // namespace lin

@@ -113,6 +113,16 @@ inline hipError_t launch_grad_stream(int elem, int cfg, bool rowt, int mode, con
                          : launch_grad_stream_t<kF16>(cfg, rowt, mode, a, stream);
 }
 
+// Two unsplit products in one launch: a (rowt false) on kGradConfigs[kPairSmall] or, not
+// small, [kPairTile], then b (rowt true) on [kPairTile]; both rounded.
+constexpr int kPairSmall = 4, kPairTile = 2;
+template <int E> hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream);
+extern template hipError_t launch_grad_pair_t<kF16>(bool, const StreamProduct&, const StreamProduct&, hipStream_t);
+extern template hipError_t launch_grad_pair_t<kBF16>(bool, const StreamProduct&, const StreamProduct&, hipStream_t);
+inline hipError_t launch_grad_pair(int elem, bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream) {
+    return elem == kBF16 ? launch_grad_pair_t<kBF16>(small, a, b, stream) : launch_grad_pair_t<kF16>(small, a, b, stream);
+}
+
 // y[g] = the partial sums' total, in order of the splits: rounded to elem's type, or floats.
 hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStream_t stream);
 

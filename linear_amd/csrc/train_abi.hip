@@ -249,6 +249,7 @@ struct StreamPlan {
     int cfg, splits;
     int64_t c1;
     int cfg1;
+    double time;
 };
 
 // kGradConfigs' times, from 4096 x 4096 outputs at 1 to 64 slices (and 1024 x 1024 for
@@ -269,7 +270,7 @@ double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t slices, 
 }
 
 StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
-    StreamPlan p{0, 1, 0, 0};
+    StreamPlan p{0, 1, 0, 0, 0.0};
     double best = tile_time(0, groups, R, C, slices, 1);
     for (int c = 0; c < lin::kNumGradConfigs; ++c) {
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
@@ -296,10 +297,11 @@ StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
             const double t = head + tile_time(c, groups, R, C - whole * g.bn, slices, 1);
             if (t < best) {
                 best = t;
-                p = StreamPlan{0, 1, whole * g.bn, c};
+                p = StreamPlan{0, 1, whole * g.bn, c, 0.0};
             }
         }
     }
+    p.time = best;
     return p;
 }
 
@@ -313,26 +315,33 @@ bool sums_fit(int64_t groups, int64_t R, int64_t C, int64_t slices, int cus) {
 }
 
 // Bytes of partial sums of a product's plan.
-int64_t partial_bytes(int64_t groups, int64_t R, int64_t C, int64_t slices) {
-    const StreamPlan p = plan_stream(groups, R, C, slices);
+int64_t partial_bytes(const StreamPlan& p, int64_t groups, int64_t R, int64_t C) {
     return p.splits > 1 ? p.splits * groups * R * ((C + 7) / 8 * 8) * 4 : 0;
+}
+int64_t partial_bytes(int64_t groups, int64_t R, int64_t C, int64_t slices) {
+    return partial_bytes(plan_stream(groups, R, C, slices), groups, R, C);
 }
 
 int64_t slices_of(int64_t L) { return (L + 63) / 64; }
 
-// A streaming product's shape, tile and launches; the operands are set by the caller.
-// partial: device memory of partial_bytes.
-int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, const DevInfo& di, void* partial,
-                      hipStream_t stream) {
-    const StreamPlan p = plan_stream(a.groups, a.R, a.C, slices_of(a.L) * a.segs);
+// A product's tiles under a plan and its outputs' alignment (eb: output bytes).
+void set_tiles(lin::StreamProduct& a, const StreamPlan& p, int64_t eb, const DevInfo& di) {
     const lin::GradConfig& g = lin::kGradConfigs[p.cfg];
     a.tiles_r = (int)tiles_of(a.R, g.bm);
     a.tiles_c = (int)tiles_of(a.C, g.bn);
     a.xcd_shift = di.xcd_shift;
     a.splits = p.splits;
-    const int64_t eb = mode == lin::kOutRound ? 2 : 4;
     for (int i = 0; i < a.groups; ++i)
         if ((uintptr_t)a.y[i] % 16 == 0 && a.ldy[i] * eb % 16 == 0) a.vec |= 1 << i;
+}
+
+// A streaming product's launches under its plan; the operands are set by the caller.
+// partial: device memory of the plan's partial sums.
+int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, const StreamPlan& p, const DevInfo& di,
+                      void* partial, hipStream_t stream) {
+    const lin::GradConfig& g = lin::kGradConfigs[p.cfg];
+    const int64_t eb = mode == lin::kOutRound ? 2 : 4;
+    set_tiles(a, p, eb, di);
     if (p.c1 > 0) {
         lin::StreamProduct head = a;
         head.C = (int)p.c1;
@@ -394,7 +403,7 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
         a.C = (int)K;
         a.L = (int)N;
         a.segs = a.groups = 1;
-        return launch_stream(elem, false, lin::kOutRound, a, di, ws, (hipStream_t)stream);
+        return launch_stream(elem, false, lin::kOutRound, a, plan_stream(1, M, K, slices_of(N)), di, ws, (hipStream_t)stream);
     }
     const lin::ProductArgs p = product(dy, lddy, w, ldw, dx, lddx, M, K, N);
     return launched(lin::launch_product_any(elem, lin::kProdRound, false, p, (hipStream_t)stream));
@@ -469,7 +478,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
             a.sums = c;
         }
         const int mode = !f32 ? lin::kOutRound : accumulate ? lin::kOutF32Add : lin::kOutF32;
-        return launch_stream(elem, true, mode, a, di, ws, (hipStream_t)stream);
+        return launch_stream(elem, true, mode, a, plan_stream(1, N, K, slices_of(M)), di, ws, (hipStream_t)stream);
     }
     lin::ProductArgs p = product(dy, lddy, x, ldx, dw, lddw, N, K, M);
     p.accumulate = f32 && accumulate != 0;
@@ -480,8 +489,44 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
 // The gated block's dg | du matrix: columns of one half, a whole number of 64-wide slices.
 int64_t gated_half(int64_t N) { return (N + 63) / 64 * 64; }
 
+// The plans of the gated block's dx and of dWg, dWu.  pair: both run in one launch, where
+// their tiles together, spread over the CUs, take less than two launches.  Whole backward,
+// with and without: 517 x 2720 x 1024 36.8 us, 43.5; 1000 x 1928 x 1296 45.5, 60.1; 2000 x
+// 4096 x 1024 94, 112; 1000 x 11008 x 4096 is large enough for two.  The plans depend on
+// the sizes alone, so either gradient has the same words with and without the other.
+struct GatedPlan {
+    StreamPlan dx, dw;
+    bool pair;
+};
+
+GatedPlan plan_gated(int64_t M, int64_t N, int64_t K) {
+    const int64_t sx = 2 * slices_of(N), sw = slices_of(M);
+    GatedPlan p{plan_stream(1, M, K, sx), plan_stream(2, N, K, sw), false};
+    if (M == 0 || N == 0) return p;
+    double best = p.dx.time + p.dw.time + kLaunchGap;
+    const lin::GradConfig& gw = lin::kGradConfigs[lin::kPairTile];
+    const TileTime& tw = kGradTimes[lin::kPairTile];
+    const double wt = tw.fixed + tw.slice * (double)sw;
+    const double wsum = wt * 2.0 * (double)(tiles_of(N, gw.bm) * tiles_of(K, gw.bn));
+    for (int c : {lin::kPairSmall, lin::kPairTile}) {
+        const lin::GradConfig& g = lin::kGradConfigs[c];
+        const TileTime& t = kGradTimes[c];
+        const double xt = t.fixed + t.slice * (double)sx;
+        const double xsum = xt * (double)(tiles_of(M, g.bm) * tiles_of(K, g.bn));
+        const double all = std::max(std::max(xt, wt), (xsum + wsum) / kPlanCus + 0.5 * wt);
+        if (all < best) {
+            best = all;
+            p.pair = true;
+            p.dx = StreamPlan{c, 1, 0, 0, xt};
+            p.dw = StreamPlan{lin::kPairTile, 1, 0, 0, wt};
+        }
+    }
+    return p;
+}
+
 int64_t gated_partials(int64_t M, int64_t N, int64_t K) {
-    return std::max(partial_bytes(1, M, K, 2 * slices_of(N)), partial_bytes(2, N, K, slices_of(M)));
+    const GatedPlan p = plan_gated(M, N, K);
+    return std::max(partial_bytes(p.dx, 1, M, K), partial_bytes(p.dw, 2, N, K));
 }
 
 int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uint16_t* x, int64_t ldx, const uint16_t* wg,
@@ -535,22 +580,44 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     }
     if (want_dw && (st = pack_operand(x, ldx, M, K, false, space, stream)) != LINEAR_OK) return st;
     const bool dx_streams = streamable(wg, ldwg) && ldwu == ldwg && al16(wu, ldwu) && 2 * Np <= lin::kMaxLdIn;
+    const bool dw_streams = streamable(x, ldx) && 2 * Np <= lin::kMaxLdIn;
+    const GatedPlan plan = plan_gated(M, N, K);
+    lin::StreamProduct px, pw;
+    memset(&px, 0, sizeof px);
+    px.r = d;
+    px.ldr = 2 * Np;
+    px.c[0] = wg;
+    px.c[1] = wu;
+    px.ldc[0] = px.ldc[1] = ldwg;
+    px.y[0] = dx;
+    px.ldy[0] = lddx;
+    px.R = (int)M;
+    px.C = (int)K;
+    px.L = (int)N;
+    px.segs = 2;
+    px.groups = 1;
+    memset(&pw, 0, sizeof pw);
+    pw.r = d;
+    pw.ldr = 2 * Np;
+    pw.rgroup = Np;
+    pw.c[0] = x;
+    pw.ldc[0] = ldx;
+    pw.y[0] = dwg;
+    pw.y[1] = dwu;
+    pw.ldy[0] = lddwg;
+    pw.ldy[1] = lddwu;
+    pw.R = (int)N;
+    pw.C = (int)K;
+    pw.L = (int)M;
+    pw.segs = 1;
+    pw.groups = 2;
+    if (want_dx && want_dw && dx_streams && dw_streams && plan.pair) {
+        set_tiles(px, plan.dx, 2, di);
+        set_tiles(pw, plan.dw, 2, di);
+        return launched(lin::launch_grad_pair(elem, plan.dx.cfg == lin::kPairSmall, px, pw, (hipStream_t)stream));
+    }
     if (want_dx && dx_streams) {
-        lin::StreamProduct a;
-        memset(&a, 0, sizeof a);
-        a.r = d;
-        a.ldr = 2 * Np;
-        a.c[0] = wg;
-        a.c[1] = wu;
-        a.ldc[0] = a.ldc[1] = ldwg;
-        a.y[0] = dx;
-        a.ldy[0] = lddx;
-        a.R = (int)M;
-        a.C = (int)K;
-        a.L = (int)N;
-        a.segs = 2;
-        a.groups = 1;
-        st = launch_stream(elem, false, lin::kOutRound, a, di, d + M * 2 * Np, (hipStream_t)stream);
+        st = launch_stream(elem, false, lin::kOutRound, px, plan.dx, di, d + M * 2 * Np, (hipStream_t)stream);
         if (st != LINEAR_OK) return st;
     } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, wg, ldwg, dx, lddx, M, K, N);
@@ -561,25 +628,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         st = launched(lin::launch_product_any(elem, lin::kProdRound, false, p, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
-    if (want_dw && streamable(x, ldx) && 2 * Np <= lin::kMaxLdIn) {
-        lin::StreamProduct a;
-        memset(&a, 0, sizeof a);
-        a.r = d;
-        a.ldr = 2 * Np;
-        a.rgroup = Np;
-        a.c[0] = x;
-        a.ldc[0] = ldx;
-        a.y[0] = dwg;
-        a.y[1] = dwu;
-        a.ldy[0] = lddwg;
-        a.ldy[1] = lddwu;
-        a.R = (int)N;
-        a.C = (int)K;
-        a.L = (int)M;
-        a.segs = 1;
-        a.groups = 2;
-        st = launch_stream(elem, true, lin::kOutRound, a, di, d + M * 2 * Np, (hipStream_t)stream);
-        if (st != LINEAR_OK) return st;
+    if (want_dw && dw_streams) {
+        return launch_stream(elem, true, lin::kOutRound, pw, plan.dw, di, d + M * 2 * Np, (hipStream_t)stream);
     } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
             const lin::ProductArgs p = product(d + s * Np, 2 * Np, x, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
