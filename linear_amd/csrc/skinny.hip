@@ -190,10 +190,20 @@ skinny_kernel(LinearArgs a) {
     }
 }
 
+// The one-row kernels take x's segments in passes of kGemvPass.  A last pass that is not
+// full reads a segment of zeros instead (x past its end: an infinity there would meet the
+// zero weights): the segments that are staged.
+constexpr int kGemvPass = 8;
+__host__ __device__ constexpr int gemv_segments(int K) {
+    const int s = (K + kGemvSeg - 1) / kGemvSeg;
+    return s % kGemvPass ? s + 1 : s;
+}
+static_assert(gemv_segments(kGemvMaxK) * 1024 <= 65536 && kGemvMaxK % (kGemvSeg * kGemvPass) == 0, "x in 64 KB of LDS");
+
 template <int E, int MODE>
 __global__ void __launch_bounds__(kGemvRows * 64)
 gemv_stream(LinearArgs a) {
-    constexpr int U = 8;                      // segments (1 KB loads per wave) in flight per pass
+    constexpr int U = kGemvPass;              // segments (1 KB loads per wave) in flight per pass
     extern __shared__ __attribute__((aligned(16))) unsigned char xs_row[];   // x: K * 2 bytes
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);        // uniform
@@ -209,7 +219,7 @@ gemv_stream(LinearArgs a) {
         bword = __builtin_amdgcn_raw_buffer_load_b16(rb, (uint32_t)n * 2u, 0, 0);
     }
     // x into LDS, segment s by wave s % kGemvRows
-    for (int s = wave; s < S; s += kGemvRows) {
+    for (int s = wave; s < gemv_segments(K); s += kGemvRows) {
         const int k = s * kGemvSeg + lane * 8;
         lds_dma16(rx, xs_row + s * 1024, k < K ? (uint32_t)k * 2u : kOOB);
     }
@@ -231,8 +241,8 @@ gemv_stream(LinearArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = p + u;
-            // a segment past K has zero weights (out-of-range loads): any x will do
-            const u32x4 xv = *(const u32x4*)(xs_row + (s < S ? s : S - 1) * 1024 + lane * 16);
+            // a segment past K has zero weights (out-of-range loads) and the staged zeros
+            const u32x4 xv = *(const u32x4*)(xs_row + (s < S ? s : S) * 1024 + lane * 16);
             float acc = sums[u];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -264,7 +274,7 @@ gemv_stream(LinearArgs a) {
 template <int E>
 __global__ void __launch_bounds__(kGemvRows * 64)
 gated_gemv(LinearArgs a) {
-    constexpr int U = 8;                      // 1 KB loads per row in flight per pass
+    constexpr int U = kGemvPass;              // 1 KB loads per row in flight per pass
     extern __shared__ __attribute__((aligned(16))) unsigned char xs_row[];   // x: K * 2 bytes
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);        // uniform
@@ -274,7 +284,7 @@ gated_gemv(LinearArgs a) {
     const __amdgpu_buffer_rsrc_t rx = matrix_rsrc(a.x, 0, 1, a.ldx, K);
     const __amdgpu_buffer_rsrc_t rg = matrix_rsrc(a.w, n < a.N ? n : a.N, a.N, a.ldw, K);    // empty past N
     const __amdgpu_buffer_rsrc_t ru = matrix_rsrc(a.w2, n < a.N ? n : a.N, a.N, a.ldw2, K);
-    for (int s = wave; s < S; s += kGemvRows) {
+    for (int s = wave; s < gemv_segments(K); s += kGemvRows) {
         const int k = s * kGemvSeg + lane * 8;
         lds_dma16(rx, xs_row + s * 1024, k < K ? (uint32_t)k * 2u : kOOB);
     }
@@ -297,8 +307,8 @@ gated_gemv(LinearArgs a) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = p + u;
-            // a segment past K has zero weights (out-of-range loads): any x will do
-            const u32x4 xv = *(const u32x4*)(xs_row + (s < S ? s : S - 1) * 1024 + lane * 16);
+            // a segment past K has zero weights (out-of-range loads) and the staged zeros
+            const u32x4 xv = *(const u32x4*)(xs_row + (s < S ? s : S) * 1024 + lane * 16);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float x = widen<E>((uint16_t)(xv[e >> 1] >> (16 * (e & 1))));
@@ -325,7 +335,7 @@ hipError_t launch_gated_gemv(int elem, const LinearArgs& a, hipStream_t stream) 
     if (a.M != 1 || a.K > kGemvMaxK) return hipErrorInvalidValue;
     LinearArgs args = a;
     void* params[] = {&args};
-    const size_t lds = (size_t)((a.K + kGemvSeg - 1) / kGemvSeg) * 1024;
+    const size_t lds = (size_t)gemv_segments(a.K) * 1024;
     return hipLaunchKernel(elem == kBF16 ? (const void*)gated_gemv<kBF16> : (const void*)gated_gemv<kF16>,
                            dim3((unsigned)((a.N + kGemvRows - 1) / kGemvRows)), dim3(kGemvRows * 64), params, lds, stream);
 }
@@ -343,7 +353,7 @@ hipError_t launch_gemv(int elem, const LinearArgs& a, int mode, hipStream_t stre
     LinearArgs args = a;
     void* params[] = {&args};
     const void* fn = elem == kBF16 ? gemv_fn<kBF16>(mode) : gemv_fn<kF16>(mode);
-    const size_t lds = (size_t)((a.K + kGemvSeg - 1) / kGemvSeg) * 1024;
+    const size_t lds = (size_t)gemv_segments(a.K) * 1024;
     return hipLaunchKernel(fn, grid, block, params, lds, stream);
 }
 

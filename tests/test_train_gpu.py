@@ -124,6 +124,68 @@ def test_gated_specials_stay_in_their_rows_and_columns(M, t):
     assert torch.equal(got[:M - 1][:, keep], clean[:M - 1][:, keep])
 
 
+def infinite(signs):
+    """Infinities of these signs, NaN where the factor is zero."""
+    return signs.double() * float("inf")
+
+
+def same(got, want):
+    got = got.double()
+    return bool(((got == want) | (got.isnan() & want.isnan())).all())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,K", [(1, 8), (1, 264), (1, 768), (1, 4100), (1, 9000), (2, 520), (9, 72), (40, 776), (300, 1000)])
+def test_gated_infinite_input(M, K, t):
+    """One infinity in x: each projection of its row is infinite, with its weight's sign, and
+    nothing that a kernel reads past the ends meets it."""
+    x, wg, wu, _ = make(M, 72, K, t)
+    clean = fn("gated", t)(x, wg, wu, keep=True)
+    for k in (0, K // 2, K - 1):
+        v = x.clone()
+        v[M - 1, k] = float("inf")
+        h, g, u = fn("gated", t)(v, wg, wu, keep=True)
+        assert same(g[M - 1], infinite(wg[:, k].sign())), k
+        assert same(u[M - 1], infinite(wu[:, k].sign())), k
+        for a, b in zip((h, g, u), clean):
+            assert torch.equal(a[:M - 1], b[:M - 1])
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 72, 136), (9, 200, 264), (65, 65, 65), (130, 1000, 72), (300, 520, 328), (1000, 72, 520)])
+def test_gradients_infinite_input(M, N, K, t):
+    x, w, _, dy = make(M, N, K, t)
+    clean = fn("backward_input", t)(dy, w)
+    dw0, db0 = fn("backward_weight", t)(dy, x, bias=True)
+    for m, n in ((0, 0), (M - 1, N - 1), (M // 2, N // 2)):
+        v = dy.clone()
+        v[m, n] = float("-inf")
+        rest = torch.arange(M, device=DEV) != m
+        dx = fn("backward_input", t)(v, w)
+        assert same(dx[m], infinite(-w[n].sign())) and torch.equal(dx[rest], clean[rest])
+        rest = torch.arange(N, device=DEV) != n
+        dw, db = fn("backward_weight", t)(v, x, bias=True)
+        assert same(dw[n], infinite(-x[m].sign())) and torch.equal(dw[rest], dw0[rest])
+        assert float(db[n]) == float("-inf") and torch.equal(db[rest], db0[rest])
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 72, 136), (65, 65, 65), (200, 344, 136), (517, 264, 1000)])
+def test_gated_backward_infinite_input(M, N, K, t):
+    x, wg, wu, dh = make(M, N, K, t)
+    _, g, u = fn("gated", t)(x, wg, wu, keep=True)
+    clean = fn("gated_backward", t)(dh, x, wg, wu, g, u)
+    for m, n in ((0, 0), (M - 1, N - 1)):
+        v = dh.clone()
+        v[m, n] = float("inf")
+        dx, dwg, dwu = fn("gated_backward", t)(v, x, wg, wu, g, u)
+        rest = torch.arange(M, device=DEV) != m
+        assert torch.equal(dx[rest], clean[0][rest]) and not bool(dx[m].isfinite().any())
+        rest = torch.arange(N, device=DEV) != n
+        assert torch.equal(dwg[rest], clean[1][rest]) and torch.equal(dwu[rest], clean[2][rest])
+        assert same(dwu[n], infinite((x[m].double() * g[m, n].double()).sign()))
+
+
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 def test_empty_and_zero_sums(t):
     z = lambda *s: torch.zeros(*s, dtype=t, device=DEV)          # noqa: E731
