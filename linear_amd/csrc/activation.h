@@ -39,7 +39,7 @@ __device__ inline void gated_act_grad(int act, float g, float& a, float& d) {
     float z = g, dz = 1.f;
     if (act == kEpiGeluTanh) {
         z = kGeluA * (g + kGeluB * (g * g * g));
-        dz = kGeluA * (1.f + 3.f * kGeluB * (g * g));
+        dz = kGeluA * (1.f + 3.f * kGeluB * fminf(g * g, 1e30f));   // finite: far out it meets a sigmoid of 0
     }
     const float s = sigmoid(z);
     a = g * s;

@@ -161,9 +161,9 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     // the next slice to request: its LDS slot and resources, from running scalar state.
     // A row's last 16-byte chunk is read whole (a partly valid one would be dropped): it
     // is aligned, so it lies in the page of its valid words, and what it holds past
-    // them goes to outputs that are not stored.  With nothing left the lengths are not positive (ld >= its columns), so the
-    // column panel and a contraction-major row operand read zeros; a contiguous one is
-    // masked by its lanes' own indices.
+    // them goes to outputs that are not stored.  With nothing left the lengths are not
+    // positive (ld >= its columns), so the column panel and a contraction-major row
+    // operand read zeros; a contiguous one is masked by its lanes' own indices.
     int seg = t0 >= per && a.segs > 1 ? 1 : 0;
     const int first = (t0 - seg * per) * BK;
     const uint16_t* cp = a.c[seg] + (int64_t)first * a.ldc[0];
@@ -375,8 +375,8 @@ __global__ void __launch_bounds__(512) grad_pair(StreamProduct a, StreamProduct 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
     StreamProduct args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads), params, 0,
-                           stream);
+    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads),
+                           params, 0, stream);
 }
 
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>

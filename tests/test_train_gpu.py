@@ -186,6 +186,19 @@ def test_gated_backward_infinite_input(M, N, K, t):
         assert same(dwu[n], infinite((x[m].double() * g[m, n].double()).sign()))
 
 
+@pytest.mark.parametrize("act", ACTS, ids=list(ref.ACTS.values()))
+def test_gated_gradients_of_large_gates(act):
+    """Far out act is 0 or g and act' is 0 or 1, also where g^2 and g^3 overflow binary32."""
+    g = torch.tensor([[1e3, -1e3, 1e10, -1e10, 1e14, -1e14, 1e20, -1e20, 3e38, -3e38]], dtype=torch.bfloat16, device=DEV)
+    N = g.shape[1]
+    one = torch.ones(1, 8, dtype=torch.bfloat16, device=DEV)
+    w = torch.ones(N, 8, dtype=torch.bfloat16, device=DEV)
+    row = torch.ones_like(g)
+    dx, dwg, dwu = la.linear_bf16_gated_backward(row, one, w, w, g, row, act)
+    assert torch.equal(dwg[:, 0], (g[0] > 0).to(dwg.dtype))
+    assert torch.equal(dwu[:, 0], torch.where(g[0] > 0, g[0], torch.zeros_like(g[0])))
+
+
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 def test_empty_and_zero_sums(t):
     z = lambda *s: torch.zeros(*s, dtype=t, device=DEV)          # noqa: E731
