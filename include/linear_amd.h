@@ -374,13 +374,14 @@ int32_t linear_f16_indexed_noalloc(const uint16_t* x, int64_t ldx,
  * x: [M, K]; wg, wu: [N, K] each with its own row stride (the two halves of one
  * [2N, K] weight are wg = w, wu = w + N * ldw).  h: [M, N].  gate and up: [M, N]
  * or NULL; where given, RNE_E(g) and RNE_E(u) are stored there for the backward
- * call.  Outputs may not overlap the inputs or each other (LINEAR_E_ALIAS).
+ * call.  Outputs may not overlap the inputs or each other (LINEAR_E_ALIAS); columns
+ * of their own in rows of one stride do not (gate and up in one [M, 2N] matrix).
  * M == 0 or N == 0 is a no-op; K == 0 gives +0 (act(0) * 0).  M, N and K of this
  * and the gradients' calls are at most 2^31 - 65536, row strides below 2^31.
  *
  * workspace: linear_gated_forward_workspace_bytes(M, N, K) bytes of device memory,
  * 16-byte aligned, owned by the caller, overwritten, free again once the call's work
- * on `stream` has finished.  It is 0 (and workspace may be NULL) where K is a multiple
+ * on `stream` has finished (two calls in flight at once need two).  It is 0 (and workspace may be NULL) where K is a multiple
  * of 8 and for a few rows; otherwise it holds copies of the operands with padded rows.
  */
 int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
@@ -418,9 +419,10 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  * M == 0 gives dwg = dwu = +0.
  *
  * workspace: linear_gated_workspace_bytes(M, N, K) bytes of device memory (it
- * holds dg and du, partial sums, and copies of operands of odd widths), 16-byte aligned, owned by the caller, overwritten, free again
- * once the call's work on `stream` has finished; two calls in flight at once
- * need two workspaces.  It may not overlap any other argument.
+ * holds dg and du, partial sums, and copies of operands of odd widths), 16-byte
+ * aligned, owned by the caller, overwritten, free again once the call's work on
+ * `stream` has finished; two calls in flight at once need two workspaces.  It may
+ * not overlap any other argument.
  */
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
 int32_t linear_f16_gated_backward(const uint16_t* dh, int64_t lddh,
@@ -513,8 +515,9 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
  * ld is not read), of any mix of types, any alignment; cols up to 2^46, rows and ld
  * below 2^31.  The arrays of linear_tensor are host memory, read during the call.
  * out == NULL clips in place; else out[i] has grads[i]'s shape and type and is
- * grads[i] itself or overlaps no tensor of the call (LINEAR_E_ALIAS); a tensor
- * listed twice may not be clipped in place.  norm is device memory.  count up to
+ * grads[i] itself or overlaps no tensor of the call (LINEAR_E_ALIAS, judged by the
+ * range from a tensor's first word to its last: columns of one matrix overlap); a
+ * tensor listed twice may not be clipped in place.  norm is device memory.  count up to
  * LINEAR_GRAD_MAX_TENSORS; count == 0 gives norm 0.  max_norm: not negative or NaN
  * (LINEAR_E_VALUE).
  *

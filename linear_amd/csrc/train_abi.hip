@@ -61,6 +61,17 @@ int32_t check_operand(const Operand& o) {
     return LINEAR_OK;
 }
 
+// Whether two operands share no byte: apart in memory, or columns of their own in rows of
+// one length (the projections side by side in one [M, 2N] tensor).
+bool apart(const Operand& a, const Operand& b) {
+    if (!overlaps(a.range(), b.range())) return true;
+    if (a.rows == 1 || b.rows == 1 || a.ld * a.bytes != b.ld * b.bytes) return false;
+    const bool swap = (uintptr_t)b.p < (uintptr_t)a.p;
+    const Operand &lo = swap ? b : a, &hi = swap ? a : b;
+    const int64_t row = a.ld * a.bytes, at = (int64_t)(((uintptr_t)hi.p - (uintptr_t)lo.p) % (uintptr_t)row);
+    return at >= lo.cols * lo.bytes && at + hi.cols * hi.bytes <= row;
+}
+
 // The operands' own checks, then: no output may overlap an input or another output.
 template <int NI, int NO>
 int32_t check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
@@ -78,9 +89,9 @@ int32_t check_operands(const Operand (&in)[NI], const Operand (&out)[NO]) {
     for (int i = 0; i < NO; ++i) {
         if (!out[i].p || out[i].empty()) continue;
         for (const Operand& o : in)
-            if (!o.empty() && overlaps(out[i].range(), o.range())) return LINEAR_E_ALIAS;
+            if (!o.empty() && !apart(out[i], o)) return LINEAR_E_ALIAS;
         for (int j = 0; j < i; ++j)
-            if (out[j].p && !out[j].empty() && overlaps(out[i].range(), out[j].range())) return LINEAR_E_ALIAS;
+            if (out[j].p && !out[j].empty() && !apart(out[i], out[j])) return LINEAR_E_ALIAS;
     }
     return LINEAR_OK;
 }

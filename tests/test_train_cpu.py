@@ -249,3 +249,18 @@ def test_host_tensors_and_wrong_arguments_are_refused_before_the_library():
         la.linear_grad_norm([])
     with pytest.raises(ValueError):
         la.linear_grad_clip([x], torch.zeros(1), 1.0, out=[w])
+
+
+@cpu_only
+def test_columns_side_by_side_in_one_tensor():
+    """Matrices of one row stride that share rows but no column do not overlap; one column in
+    common, or rows of another length, do."""
+    half = dict(ldg=64, ldu=64)
+    assert gated(g=G, u=G + 64, **half) == NODEV and gated(u=G, g=G + 64, **half) == NODEV
+    assert gated(h=X + 128, ldh=96, ldx=96) == NODEV                      # behind x's columns
+    assert gated(g=G, u=G + 62, **half) == la.LINEAR_E_ALIAS and gated(u=G, g=G + 62, **half) == la.LINEAR_E_ALIAS
+    assert gated(g=G, u=G + 66, **half) == la.LINEAR_E_ALIAS              # into the next row's first column
+    assert gated(g=G, u=G + 64, ldg=64, ldu=65) == la.LINEAR_E_ALIAS
+    assert gated(g=G, u=G + 64 + 128 * 3, **half) == NODEV                # three rows further down
+    assert gated_backward(dwg=DWG, dwu=DWG + 128, lddwg=128, lddwu=128) == NODEV
+    assert gated_backward(ws=DWG + 128, nws=10 ** 6, lddwg=10 ** 6) == la.LINEAR_E_ALIAS

@@ -598,3 +598,16 @@ def test_calls_from_four_threads():
     for a, b in zip(got, want):
         for o, w in zip(a, b):
             assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(2, 40, 72), (65, 127, 130), (300, 264, 136)])
+def test_projections_and_gradients_side_by_side(M, N, K, t):
+    x, wg, wu, dh = make(M, N, K, t)
+    both, dw = torch.full((M, 2 * N), 5.0, dtype=t, device=DEV), torch.full((N, 2 * K), 5.0, dtype=t, device=DEV)
+    h, g, u = fn("gated", t)(x, wg, wu, keep=True)
+    got = fn("gated", t)(x, wg, wu, keep=True, gate=both[:, :N], up=both[:, N:])
+    assert torch.equal(got[0], h) and torch.equal(both, torch.cat([g, u], 1))
+    dx, dwg, dwu = fn("gated_backward", t)(dh, x, wg, wu, g, u)
+    got = fn("gated_backward", t)(dh, x, wg, wu, both[:, :N], both[:, N:], dwg=dw[:, :K], dwu=dw[:, K:])
+    assert torch.equal(got[0], dx) and torch.equal(dw, torch.cat([dwg, dwu], 1))
