@@ -412,7 +412,9 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  *     dx[m, k]  = RNE_E( sum_n dg[m, n] * wg[n, k] + du[m, n] * wu[n, k] )
  *     dwg[n, k] = RNE_E( sum_m dg[m, n] * x[m, k] )      dwu likewise from du
  *
- * dg and du are rounded to E because they are the matrix unit's operands; a
+ * dg and du are rounded to E because they are the matrix unit's operands (up to 32
+ * rows they are kept as two words, so that only the outputs' own rounding is left;
+ * finite ones then give NaN, not an infinity, with an infinite weight or x); a
  * binary16 gradient past 65504 becomes infinite there.  dx may be NULL (not
  * wanted; the weights are then not read), and dwg and dwu may both be NULL (x is
  * then not read); one of the two groups must be given.  N == 0 gives dx = +0,

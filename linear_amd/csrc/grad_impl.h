@@ -130,6 +130,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     // This wave's loads: GC of the column panel, then GR of the row operand; lane l
     // lands at byte 16 l of its KB and fetches what the layout places there.
     uint32_t goff[GPW];
+    const int lines = ROWT && a.fold ? kLowRow - 1 : BK - 1, whole = ROWT && a.fold ? a.fold : BK;
     // contiguous row operand: the first contraction index fetched, which repeats every
     // second load (8 rows each, a swizzle of period 16)
     static_assert(GR % 2 == 0, "a wave's first load must start the swizzle's period");
@@ -142,7 +143,9 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             const int row = col ? CROW : RROW;
             const int k = byte / row, c = (byte % row / 16) ^ (2 * (col ? panel_swz<BN>(k) : panel_swz<BM>(k)));
             const int at = (col ? c0 : r0) + 8 * c;
-            goff[j] = at < (col ? a.C : a.R) ? (uint32_t)((k * (int)(col ? a.ldc[0] : a.ldr) + at) * 2) : kOOB;
+            const int line = col ? k & lines : k;
+            goff[j] = (int)(at < (col ? a.C : a.R)) & (int)(k % kLowRow < whole)
+                          ? (uint32_t)((line * (int)(col ? a.ldc[0] : a.ldr) + at) * 2) : kOOB;
         } else {
             const int r = byte / RROW, c = (byte % RROW / 16) ^ ((r >> 1) & 7);
             gk[(j - GC) % 2] = 8 * c;
@@ -308,11 +311,33 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
                 for (int j = 0; j < FM; ++j) acc[i][j] += sums[(g * FN * FM + i * FM + j) * NW * 64 + t];
     }
 
+    // the second words' rows, 32 further down, are the same fragments of the tile's other waves
+    if constexpr (!ROWT && BM == 64) {
+        static_assert(WM == 2 && TM == kLowRow, "rows r and kLowRow + r in the waves wm = 0 and 1");
+        if (a.fold) {                                 // uniform
+            f32x4* low = (f32x4*)smem;
+            __syncthreads();
+            if (wm == 1) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) low[((i * FM + j) * WN + wn) * 64 + lane] = acc[i][j];
+            }
+            __syncthreads();
+            if (wm == 0) {
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) acc[i][j] += low[((i * FM + j) * WN + wn) * 64 + lane];
+            }
+        }
+    }
+
     LinearArgs o;
-    o.M = a.R;
+    o.M = !ROWT && a.fold ? a.fold : a.R;
     o.N = a.C;
     if (a.splits > 1) {                               // FP32 partial sums (kOutF32)
-        o.y = a.partial + (int64_t)stack * a.R * a.ldp;
+        o.y = a.partial + (int64_t)stack * o.M * a.ldp;
         o.ldy = a.ldp;
         o.vec_store = o.epi.vec16 = 1;
     } else {

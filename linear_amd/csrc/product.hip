@@ -286,7 +286,14 @@ __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
     }
 }
 
+// What the rounding of v to `word` leaves, rounded: 0 where the word is an infinity or NaN.
 template <int E>
+__device__ inline uint16_t low_word(float v, uint16_t word) {
+    const float rest = v - widen<E>(word);
+    return narrow<E>(__builtin_fabsf(rest) < __builtin_inff() ? rest : 0.f);
+}
+
+template <int E, bool LOW>
 __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     const int chunks = g.Np / 8;                     // 8-column pieces of a row of one half
     const int64_t total = (int64_t)g.M * chunks;
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
         const u32x4 h = load8(g.dh + m * g.lddh + c, true, c, g.N, g.vec);
         const u32x4 a = load8(g.gate + m * g.ldgate + c, true, c, g.N, g.vec);
         const u32x4 u = load8(g.up + m * g.ldup + c, true, c, g.N, g.vec);
-        u32x4 dg = (u32x4){0u, 0u, 0u, 0u}, du = (u32x4){0u, 0u, 0u, 0u};
+        u32x4 dg = (u32x4){0u, 0u, 0u, 0u}, du = dg, dgl = dg, dul = dg;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (c + e >= g.N) continue;
@@ -304,12 +311,23 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
             const float hv = widen<E>((uint16_t)(h[q] >> sh)), uv = widen<E>((uint16_t)(u[q] >> sh));
             float av, dv;
             gated_act_grad(g.act, widen<E>((uint16_t)(a[q] >> sh)), av, dv);
-            dg[q] |= (uint32_t)narrow<E>(hv * uv * dv) << sh;
-            du[q] |= (uint32_t)narrow<E>(hv * av) << sh;
+            const float gf = hv * uv * dv, uf = hv * av;
+            const uint16_t gw = narrow<E>(gf), uw = narrow<E>(uf);
+            dg[q] |= (uint32_t)gw << sh;
+            du[q] |= (uint32_t)uw << sh;
+            if constexpr (LOW) {
+                dgl[q] |= (uint32_t)low_word<E>(gf, gw) << sh;
+                dul[q] |= (uint32_t)low_word<E>(uf, uw) << sh;
+            }
         }
         uint16_t* row = g.d + m * 2 * g.Np + c;
         *(u32x4*)row = dg;
         *(u32x4*)(row + g.Np) = du;
+        if constexpr (LOW) {
+            row += (int64_t)kLowRow * 2 * g.Np;
+            *(u32x4*)row = dgl;
+            *(u32x4*)(row + g.Np) = dul;
+        }
     }
 }
 
@@ -378,8 +396,9 @@ hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t strea
     GatedGradArgs args = g;
     void* params[] = {&args};
     const int64_t blocks = ((int64_t)g.M * (g.Np / 8) + 255) / 256;
-    return hipLaunchKernel(elem == kBF16 ? (const void*)gated_grad<kBF16> : (const void*)gated_grad<kF16>,
-                           dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
+    const void* fn = g.low ? (elem == kBF16 ? (const void*)gated_grad<kBF16, true> : (const void*)gated_grad<kF16, true>)
+                           : (elem == kBF16 ? (const void*)gated_grad<kBF16, false> : (const void*)gated_grad<kF16, false>);
+    return hipLaunchKernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t stream) {

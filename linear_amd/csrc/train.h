@@ -11,15 +11,15 @@ namespace lin {
 constexpr bool is_activation(int op) { return op == kEpiSilu || op == kEpiGeluTanh || op == kEpiGeluErf; }
 
 // One product of 16-bit operands of any row stride and base with an FP32 accumulator,
-// in up to two segments s:
+// in up to four segments s:
 //     acc[r, c] = sum_s sum_{k < L} a[s](r, k) * b[s](c, k)
 // a: [R, L] with row stride lda, or, rowt, k-major [L, R]; b: k-major [L, C] with row
 // stride ldb[s].  The gated block has k-contiguous [C, L] operands b and keeps the two
 // segments apart (acc_s each).
 struct ProductArgs {
-    const uint16_t* a[2];
-    const uint16_t* b[2];
-    int64_t lda, ldb[2];
+    const uint16_t* a[4];
+    const uint16_t* b[4];
+    int64_t lda, ldb[4];
     int segs;
     int R, C, L;             // output rows and columns, contraction length
     int tiles_c;             // set by the launch
@@ -63,6 +63,8 @@ inline int64_t column_sum_splits(int64_t M, int64_t N) {
     const int64_t s = by_rows < by_cus ? by_rows : by_cus;
     return s > 64 ? 64 : s;
 }
+// Few rows: dg and du are kept as two words each (gated_grad), the second in row kLowRow + m.
+constexpr int kLowRow = 32;
 // The streaming products of the gradients (16-byte aligned layouts):
 //     y[g][r, c] = sum over segments s, k < L of row(g)[r, s Lp + k] * c[s][k, c]
 // Columns c[s] are contraction-major [L, C].  The row operand is [L, R] per group, at
@@ -77,6 +79,10 @@ struct StreamProduct {
     int64_t ldy[2];
     int R, C, L;
     int segs, groups;
+    // not 0: the row operand is `fold` rows of two words, the second in row kLowRow + m.
+    // dx (64-row tiles, R = 2 kLowRow): each output row is the sum of the two rows' products.
+    // dw (L = 2 kLowRow, one slice): row kLowRow + m of the columns is row m again.
+    int fold;
     int tiles_r, tiles_c;
     int vec;                 // bit g: y[g] takes 16-byte stores
     int xcd_shift;
@@ -128,13 +134,15 @@ hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStrea
 
 // dg = dh * u * act'(g), du = dh * act(g), rounded to the element type, into the
 // two halves of d [M, 2 * Np]: columns [0, N) and [Np, Np + N); columns between
-// N and Np are zeroed.
+// N and Np are zeroed.  low: what the rounding leaves goes, rounded in turn, to row
+// kLowRow + m (0 where the first word is not finite).
 struct GatedGradArgs {
     const uint16_t *dh, *gate, *up;
     int64_t lddh, ldgate, ldup;
     uint16_t* d;
     int M, N, Np;
     int act;
+    int low;
     int vec;                 // 16-byte loads of dh, gate and up
 };
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream);

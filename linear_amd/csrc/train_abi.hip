@@ -280,10 +280,12 @@ double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t slices, 
     return splits == 1 ? main : main + 3.5 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
 }
 
-StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
-    StreamPlan p{0, 1, 0, 0, 0.0};
-    double best = tile_time(0, groups, R, C, slices, 1);
+// only64: one launch of a 64-row tile.
+StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices, bool only64 = false) {
+    StreamPlan p{only64 ? lin::kPairSmall : 0, 1, 0, 0, 0.0};
+    double best = tile_time(p.cfg, groups, R, C, slices, 1);
     for (int c = 0; c < lin::kNumGradConfigs; ++c) {
+        if (only64 && lin::kGradConfigs[c].bm != 64) continue;
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
             // the large tiles fill the chip where splitting pays, and past twice the chip's
             // tiles a split only adds traffic
@@ -302,7 +304,7 @@ StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices) {
     const lin::GradConfig& g = lin::kGradConfigs[0];
     const int64_t rows = groups * tiles_of(R, g.bm), cols = tiles_of(C, g.bn);
     const int64_t whole = rows > 0 ? rows * cols / kPlanCus * kPlanCus / rows : 0;   // column tiles in whole rounds
-    if (whole > 0 && whole < cols) {
+    if (!only64 && whole > 0 && whole < cols) {
         const double head = tile_time(0, groups, R, whole * g.bn, slices, 1) + kLaunchGap;
         for (int c = 0; c < lin::kNumGradConfigs; ++c) {
             const double t = head + tile_time(c, groups, R, C - whole * g.bn, slices, 1);
@@ -375,6 +377,7 @@ int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, cons
     a.accumulate = mode == lin::kOutF32Add;
     const int32_t st = launched(lin::launch_grad_stream(elem, p.cfg, rowt, lin::kOutF32, a, stream));
     if (st != LINEAR_OK) return st;
+    if (a.fold) a.R = a.fold;
     return launched(lin::launch_split_sum(elem, mode != lin::kOutRound, a, stream));
 }
 
@@ -500,6 +503,13 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
 // The gated block's dg | du matrix: columns of one half, a whole number of 64-wide slices.
 int64_t gated_half(int64_t N) { return (N + 63) / 64 * 64; }
 
+// Up to 32 rows leave half of a 64-row tile, and half of a slice of 64 rows, empty: there
+// dg and du are two words each, the second in the empty half, and their rounding costs the
+// outputs nothing (16 x 2720 x 1024: 21.4 us, 20.7 with one word).  With more rows it would
+// double the products; the outputs' errors are then 1.4 times one rounding's.
+bool low_words(int64_t M) { return M > 0 && M <= lin::kLowRow; }
+int64_t gated_rows(int64_t M) { return low_words(M) ? 2 * lin::kLowRow : M; }
+
 // The plans of the gated block's dx and of dWg, dWu.  pair: both run in one launch, where
 // their tiles together, spread over the CUs, take less than two launches.  Whole backward,
 // with and without: 517 x 2720 x 1024 36.8 us, 43.5; 1000 x 1928 x 1296 45.5, 60.1; 2000 x
@@ -511,8 +521,9 @@ struct GatedPlan {
 };
 
 GatedPlan plan_gated(int64_t M, int64_t N, int64_t K) {
+    const bool low = low_words(M);
     const int64_t sx = 2 * slices_of(N), sw = slices_of(M);
-    GatedPlan p{plan_stream(1, M, K, sx), plan_stream(2, N, K, sw), false};
+    GatedPlan p{plan_stream(1, M, K, sx, low), plan_stream(2, N, K, sw), false};
     if (M == 0 || N == 0) return p;
     double best = p.dx.time + p.dw.time + kLaunchGap;
     const lin::GradConfig& gw = lin::kGradConfigs[lin::kPairTile];
@@ -521,6 +532,7 @@ GatedPlan plan_gated(int64_t M, int64_t N, int64_t K) {
     const double wsum = wt * 2.0 * (double)(tiles_of(N, gw.bm) * tiles_of(K, gw.bn));
     for (int c : {lin::kPairSmall, lin::kPairTile}) {
         const lin::GradConfig& g = lin::kGradConfigs[c];
+        if (low && g.bm != 64) continue;
         const TileTime& t = kGradTimes[c];
         const double xt = t.fixed + t.slice * (double)sx;
         const double xsum = xt * (double)(tiles_of(M, g.bm) * tiles_of(K, g.bn));
@@ -580,11 +592,15 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         g.N = (int)N;
         g.Np = (int)Np;
         g.act = act;
+        g.low = low_words(M);
         g.vec = al16(dh, lddh) && al16(gate, ldgate) && al16(up, ldup);
         st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
-    unsigned char* space = (unsigned char*)(d + M * 2 * Np) + round256(gated_partials(M, N, K));
+    const bool low = low_words(M);
+    uint16_t* partials = d + gated_rows(M) * 2 * Np;
+    const uint16_t* dl = d + (int64_t)lin::kLowRow * 2 * Np;
+    unsigned char* space = (unsigned char*)partials + round256(gated_partials(M, N, K));
     if (want_dx) {
         if ((st = pack_operand(wg, ldwg, N, K, false, space, stream)) != LINEAR_OK) return st;
         if ((st = pack_operand(wu, ldwu, N, K, false, space, stream)) != LINEAR_OK) return st;
@@ -602,7 +618,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     px.ldc[0] = px.ldc[1] = ldwg;
     px.y[0] = dx;
     px.ldy[0] = lddx;
-    px.R = (int)M;
+    px.R = (int)(low ? 2 * lin::kLowRow : M);
+    px.fold = low ? (int)M : 0;
     px.C = (int)K;
     px.L = (int)N;
     px.segs = 2;
@@ -619,7 +636,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     pw.ldy[1] = lddwu;
     pw.R = (int)N;
     pw.C = (int)K;
-    pw.L = (int)M;
+    pw.L = (int)(low ? 2 * lin::kLowRow : M);
+    pw.fold = px.fold;
     pw.segs = 1;
     pw.groups = 2;
     if (want_dx && want_dw && dx_streams && dw_streams && plan.pair) {
@@ -628,22 +646,30 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         return launched(lin::launch_grad_pair(elem, plan.dx.cfg == lin::kPairSmall, px, pw, (hipStream_t)stream));
     }
     if (want_dx && dx_streams) {
-        st = launch_stream(elem, false, lin::kOutRound, px, plan.dx, di, d + M * 2 * Np, (hipStream_t)stream);
+        st = launch_stream(elem, false, lin::kOutRound, px, plan.dx, di, partials, (hipStream_t)stream);
         if (st != LINEAR_OK) return st;
     } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, wg, ldwg, dx, lddx, M, K, N);
-        p.segs = 2;
-        p.a[1] = d + Np;
-        p.b[1] = wu;
-        p.ldb[1] = ldwu;
+        p.segs = low ? 4 : 2;
+        for (int s = 0; s < p.segs; ++s) {
+            p.a[s] = (s < 2 ? d : dl) + s % 2 * Np;
+            p.b[s] = s % 2 ? wu : wg;
+            p.ldb[s] = s % 2 ? ldwu : ldwg;
+        }
         st = launched(lin::launch_product_any(elem, lin::kProdRound, false, p, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
     if (want_dw && dw_streams) {
-        return launch_stream(elem, true, lin::kOutRound, pw, plan.dw, di, d + M * 2 * Np, (hipStream_t)stream);
+        return launch_stream(elem, true, lin::kOutRound, pw, plan.dw, di, partials, (hipStream_t)stream);
     } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
-            const lin::ProductArgs p = product(d + s * Np, 2 * Np, x, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
+            lin::ProductArgs p = product(d + s * Np, 2 * Np, x, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
+            if (low) {
+                p.segs = 2;
+                p.a[1] = dl + s * Np;
+                p.b[1] = x;
+                p.ldb[1] = ldx;
+            }
             st = launched(lin::launch_product_any(elem, lin::kProdRound, true, p, (hipStream_t)stream));
             if (st != LINEAR_OK) return st;
         }
@@ -718,7 +744,7 @@ int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K) || !pack_ok(M, gated_half(N)) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
     const int64_t partials = gated_partials(M, N, K), packed = 2 * packed_bytes(N, K) + packed_bytes(M, K);
-    return M * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
+    return gated_rows(M) * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {

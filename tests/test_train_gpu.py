@@ -611,3 +611,30 @@ def test_projections_and_gradients_side_by_side(M, N, K, t):
     dx, dwg, dwu = fn("gated_backward", t)(dh, x, wg, wu, g, u)
     got = fn("gated_backward", t)(dh, x, wg, wu, both[:, :N], both[:, N:], dwg=dw[:, :K], dwu=dw[:, K:])
     assert torch.equal(got[0], dx) and torch.equal(dw, torch.cat([dwg, dwu], 1))
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 72, 136), (1, 4168, 88), (3, 129, 65), (9, 2720, 1024), (17, 264, 2056), (31, 136, 4096),
+                                   (32, 344, 136), (32, 8192, 512)])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_few_rows_lose_nothing_to_the_inner_rounding(M, N, K, t, aligned):
+    """Up to 32 rows dg and du keep two words (relative u^2, or where the second is subnormal the
+    smallest subnormal's half): against the gradients of the unrounded dg and du the outputs are off
+    by their own rounding, u at most in every value, and FP32's."""
+    x, wg, wu, dh = make(M, N, K, t)
+    if not aligned:
+        x, wg, wu = (padded(v, 1, 1)[0] for v in (x, wg, wu))
+    _, g, u = fn("gated", t)(x, wg, wu, la.EPI_GELU_ERF, keep=True)
+    got = fn("gated_backward", t)(dh, x, wg, wu, g, u, la.EPI_GELU_ERF)
+    X, G, U, D, pg, pu = (v.double() for v in (x, wg, wu, dh, g, u))
+    act, slope, r, es = ref.act64(la.EPI_GELU_ERF, pg)
+    dg, du = D * pu * slope, D * act
+    # their FP32 evaluation, and what two words leave
+    left = [e + ref.half_step(t) ** 2 * v.abs() + ref.tiny(t)
+            for v, e in ((dg, (D * pu).abs() * es + 2 * ref.S * dg.abs()), (du, (r + ref.S) * du.abs() + D.abs() * ref.FLOOR))]
+    pieces = [((dg, G, left[0]), (du, U, left[1])), ((dg.t(), X, left[0].t()),), ((du.t(), X, left[1].t()),)]
+    for o, terms, n in zip(got, pieces, ("dx", "dwg", "dwu")):
+        want = sum(a @ b for a, b, _ in terms)
+        size = sum(a.abs() @ b.abs() for a, b, _ in terms)
+        bound = sum(r @ b.abs() for _, b, r in terms) + ref.acc(2 * (2 * N if n == "dx" else M), size)
+        ref.inside(o, want, ref.rounded(want, bound, t), n)
