@@ -34,7 +34,7 @@ __device__ inline void column_block(const ColumnSumArgs& c, int block, int split
     for (int64_t m = m0 + g; m < m1; m += 4 * G) {
         u32x4 v[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = load8(c.dy + (m + G * j) * c.lddy + n, m + G * j < m1, n, c.N, c.vec);
+        for (int j = 0; j < 4; ++j) v[j] = load8(c.dy + (m + G * j) * c.lddy + n, m + G * j < m1, n, c.N);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -30,7 +30,6 @@ struct EpiArgs {
     int nsteps;
     uint64_t ops;           // step s in byte s (packed: a kernel indexes no array of its arguments,
                             // which would move a modified argument copy to scratch memory)
-    int vec16;              // bits: 1 y, 2 bias, 4 res, 8 mul allow 16-byte (8-word) accesses
 };
 
 __host__ __device__ inline int epi_op(const EpiArgs& ep, int s) { return (int)((ep.ops >> (8 * s)) & 0xff); }
@@ -56,7 +55,6 @@ struct LinearArgs {
     uint16_t *gate, *up; // the kept projections [M, N], or nullptr
     int64_t ldw2, ldgate, ldup;
     int act;             // kEpiSilu, kEpiGeluTanh or kEpiGeluErf
-    int vec_gated;       // bits: 1 h, 2 gate, 4 up allow 16-byte stores
 };
 
 
@@ -280,20 +278,24 @@ __device__ inline void lookup_chunks(lds_u16* win, __amdgpu_buffer_rsrc_t rt, u3
 }
 
 // 8 consecutive words src[0..7] of a row, the valid ones only (col + e < N,
-// row valid); 16-byte load when allowed.
-__device__ inline u32x4 load8(const uint16_t* src, bool row_ok, int col, int N, bool vec) {
-    if (row_ok && vec && col + 7 < N) return *(const u32x4*)src;
+// row valid): a 16-byte load, of any alignment, where all are.  store8 likewise (15 x 6879
+// x 2405 dw, rows of odd length: 2-byte stores took 35 us, these 19).
+__device__ inline u32x4 load8(const uint16_t* src, bool row_ok, int col, int N) {
     u32x4 r = (u32x4){0u, 0u, 0u, 0u};
+    if (row_ok && col + 7 < N) {
+        __builtin_memcpy(&r, src, 16);
+        return r;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e)
         if (row_ok && col + e < N) r[e >> 1] |= (uint32_t)src[e] << (16 * (e & 1));
     return r;
 }
 
-__device__ inline void store8(uint16_t* dst, bool row_ok, int col, int N, bool vec, u32x4 v) {
+__device__ inline void store8(uint16_t* dst, bool row_ok, int col, int N, u32x4 v) {
     if (!row_ok) return;
-    if (vec && col + 7 < N) {
-        *(u32x4*)dst = v;
+    if (col + 7 < N) {
+        __builtin_memcpy(dst, &v, 16);
         return;
     }
 #pragma unroll

@@ -189,7 +189,7 @@ __device__ inline void epi_tile(const LinearArgs& a, const unsigned char* tile, 
         if constexpr (MODE == kOutBias) {       // the layer's own epilogue: one bias step
             u32x4 v[CH];
 #pragma unroll
-            for (int k = 0; k < CH; ++k) v[k] = bias8 ? *bias8 : load8(a.b + cc[k], true, cc[k], a.N, ep.vec16 & 2);
+            for (int k = 0; k < CH; ++k) v[k] = bias8 ? *bias8 : load8(a.b + cc[k], true, cc[k], a.N);
 #pragma unroll
             for (int k = 0; k < CH; ++k) t[k] = binop8<E, false>(t[k], v[k]);
         }
@@ -204,15 +204,15 @@ __device__ inline void epi_tile(const LinearArgs& a, const unsigned char* tile, 
             u32x4 v[CH];
             if (op == kEpiBias) {
 #pragma unroll
-                for (int k = 0; k < CH; ++k) v[k] = load8(ep.bias + cc[k], true, cc[k], a.N, ep.vec16 & 2);
+                for (int k = 0; k < CH; ++k) v[k] = load8(ep.bias + cc[k], true, cc[k], a.N);
             } else if (op == kEpiResidual) {
 #pragma unroll
                 for (int k = 0; k < CH; ++k)
-                    v[k] = load8(ep.res + (int64_t)rr[k] * ep.ldr + cc[k], rr[k] < a.M, cc[k], a.N, ep.vec16 & 4);
+                    v[k] = load8(ep.res + (int64_t)rr[k] * ep.ldr + cc[k], rr[k] < a.M, cc[k], a.N);
             } else {
 #pragma unroll
                 for (int k = 0; k < CH; ++k)
-                    v[k] = load8(ep.mul + (int64_t)rr[k] * ep.ldm + cc[k], rr[k] < a.M, cc[k], a.N, ep.vec16 & 8);
+                    v[k] = load8(ep.mul + (int64_t)rr[k] * ep.ldm + cc[k], rr[k] < a.M, cc[k], a.N);
             }
             if (op == kEpiMul) {
 #pragma unroll
@@ -224,7 +224,7 @@ __device__ inline void epi_tile(const LinearArgs& a, const unsigned char* tile, 
         }
 #pragma unroll
         for (int k = 0; k < CH; ++k)
-            store8((uint16_t*)a.y + (int64_t)rr[k] * a.ldy + cc[k], rr[k] < a.M, cc[k], a.N, ep.vec16 & 1, t[k]);
+            store8((uint16_t*)a.y + (int64_t)rr[k] * a.ldy + cc[k], rr[k] < a.M, cc[k], a.N, t[k]);
     }
 }
 
@@ -393,7 +393,7 @@ __device__ __forceinline__ void finish_gated(const LinearArgs& a, unsigned char*
             if ((BM * CPR) % NT != 0 && c >= BM * CPR) break;
             const u32x4 v = *(const u32x4*)(smem + (r * CPR + (c8 ^ (r % CPR))) * 16);
             const int m = m0 + r, n = c0 + c8 * 8;
-            store8(out + (int64_t)m * ld + n, m < a.M, n, a.N, a.vec_gated & (1 << q), v);
+            store8(out + (int64_t)m * ld + n, m < a.M, n, a.N, v);
         }
     });
 }
@@ -507,7 +507,7 @@ gemm_stream(LinearArgs a) {
     u32x4 bias8 = (u32x4){0u, 0u, 0u, 0u};
     auto request_bias = [&]() {
         const int c = n0 + 8 * ((int)threadIdx.x % (BN / 8));
-        bias8 = load8(a.b + c, true, c, a.N, a.epi.vec16 & 2);
+        bias8 = load8(a.b + c, true, c, a.N);
     };
     constexpr bool LATE_BIAS = M16 && !WHOLE;        // requested after the K loop instead
     if constexpr (MODE == kOutBias && !LATE_BIAS) request_bias();

@@ -339,18 +339,15 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     if (a.splits > 1) {                               // FP32 partial sums (kOutF32)
         o.y = a.partial + (int64_t)stack * o.M * a.ldp;
         o.ldy = a.ldp;
-        o.vec_store = o.epi.vec16 = 1;
     } else {
         o.y = group ? a.y[1] : a.y[0];
         o.ldy = group ? a.ldy[1] : a.ldy[0];
-        o.vec_store = o.epi.vec16 = (a.vec >> group) & 1;
     }
     if constexpr (MODE == kOutF32 || MODE == kOutF32Add) {
         // FP32 sums leave straight from the registers: the four lanes of a row write 64
         // bytes of it, the wave's next fragment the 64 beside them, and the workgroup
         // ends without waiting for its stores (0.5 to 2.5% faster than staged in LDS:
         // 8192 x 4096 x 4096 214 -> 211 us, adding to the output 224 -> 218)
-        const bool vec = o.vec_store && (uintptr_t)o.y % 16 == 0;
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int r = r0 + wm * TM + j * R + s;
@@ -359,8 +356,14 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             for (int i = 0; i < FN; ++i) {
                 const int c = c0 + wn * TN + i * R + 4 * q;
                 float* y = (float*)o.y + (int64_t)r * o.ldy + c;
-                if (vec && c + 3 < o.N) {
-                    *(f32x4*)y = MODE == kOutF32Add ? *(const f32x4*)y + acc[i][j] : acc[i][j];
+                if (c + 3 < o.N) {                     // at any alignment
+                    f32x4 v = acc[i][j];
+                    if constexpr (MODE == kOutF32Add) {
+                        f32x4 old;
+                        __builtin_memcpy(&old, y, 16);
+                        v = old + v;
+                    }
+                    __builtin_memcpy(y, &v, 16);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)

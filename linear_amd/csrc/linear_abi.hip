@@ -347,10 +347,6 @@ int32_t run(const Request& r, void* stream) {
     a.gsx = r.sx;
     a.gsy = r.sy;
     memset(&a.epi, 0, sizeof a.epi);
-    auto al16 = [](const void* q, int64_t ld) { return ((uintptr_t)q % 16 == 0) && (ld % 8 == 0); };
-    // 16-byte row accesses of the staged epilogue: y and the bias (the program's inputs below)
-    a.epi.vec16 = (al16(r.y, r.ldy) && (r.G <= 1 || r.sy % 8 == 0) ? 1 : 0) |
-                  (al16(r.b, 8) && (r.G <= 1 || r.N % 8 == 0) ? 2 : 0);
     int mode = r.f32_out ? lin::kOutF32 : (r.b != nullptr ? lin::kOutBias : lin::kOutRound);
     if (r.epi) {
         mode = lin::kOutEpi;
@@ -361,8 +357,6 @@ int32_t run(const Request& r, void* stream) {
         a.epi.ldr = ep->ldr;
         a.epi.ldm = ep->ldm;
         a.epi.nsteps = ep->nsteps;
-        a.epi.vec16 = (al16(r.y, r.ldy) ? 1 : 0) | (al16(ep->bias, 8) ? 2 : 0) |
-                      (al16(ep->residual, ep->ldr) ? 4 : 0) | (al16(ep->mul, ep->ldm) ? 8 : 0);
         for (int s = 0; s < ep->nsteps; ++s) a.epi.ops |= (uint64_t)(uint8_t)ep->op[s] << (8 * s);
         if (epi_uses(ep, LINEAR_EPI_SILU) || epi_uses(ep, LINEAR_EPI_GELU_TANH) || epi_uses(ep, LINEAR_EPI_GELU_ERF)) {
             hipError_t te = lin::act_tables(r.elem, dev, (hipStream_t)stream, &a.epi.act);

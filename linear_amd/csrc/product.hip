@@ -260,11 +260,16 @@ __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
             if (s + j < a.splits) v += w[j];
         const int g = gr >= a.R ? 1 : 0;
         const int64_t at = (gr - (int64_t)g * a.R) * a.ldy[g] + c;
-        const bool vec = ((a.vec >> g) & 1) && c + 3 < a.C;
+        const bool whole = c + 3 < a.C;                  // stored at any alignment
         if constexpr (F32) {
             float* y = (float*)a.y[g] + at;
-            if (vec) {
-                *(f32x4*)y = a.accumulate ? *(const f32x4*)y + v : v;
+            if (whole) {
+                f32x4 old = (f32x4){};
+                if (a.accumulate) {
+                    __builtin_memcpy(&old, y, 16);
+                    v = old + v;
+                }
+                __builtin_memcpy(y, &v, 16);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -275,8 +280,8 @@ __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
             uint2 u;
             u.x = (uint32_t)narrow<E>(v[0]) | ((uint32_t)narrow<E>(v[1]) << 16);
             u.y = (uint32_t)narrow<E>(v[2]) | ((uint32_t)narrow<E>(v[3]) << 16);
-            if (vec) {
-                *(uint2*)y = u;
+            if (whole) {
+                __builtin_memcpy(y, &u, 8);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -300,9 +305,9 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / chunks;
         const int c = (int)(i - m * chunks) * 8;
-        const u32x4 h = load8(g.dh + m * g.lddh + c, true, c, g.N, g.vec);
-        const u32x4 a = load8(g.gate + m * g.ldgate + c, true, c, g.N, g.vec);
-        const u32x4 u = load8(g.up + m * g.ldup + c, true, c, g.N, g.vec);
+        const u32x4 h = load8(g.dh + m * g.lddh + c, true, c, g.N);
+        const u32x4 a = load8(g.gate + m * g.ldgate + c, true, c, g.N);
+        const u32x4 u = load8(g.up + m * g.ldup + c, true, c, g.N);
         u32x4 dg = (u32x4){0u, 0u, 0u, 0u}, du = dg, dgl = dg, dul = dg;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {

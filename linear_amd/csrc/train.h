@@ -50,7 +50,6 @@ struct ColumnSumArgs {
     void* db;                // 16-bit words or floats
     int M, N, splits;
     int f32, accumulate;
-    int vec;                 // 16-byte loads of dy
 };
 // Splits of the rows: enough workgroups of 64 columns for every CU, of 2048 rows at
 // least; one where the columns alone give half the chip work (a second launch costs
@@ -84,7 +83,6 @@ struct StreamProduct {
     // dw (L = 2 kLowRow, one slice): row kLowRow + m of the columns is row m again.
     int fold;
     int tiles_r, tiles_c;
-    int vec;                 // bit g: y[g] takes 16-byte stores
     int xcd_shift;
     // the contraction's slices shared among `splits` sets of tiles (more than one:
     // FP32 partial sums [splits, groups, R] rows of ldp, added by launch_split_sum)
@@ -143,7 +141,6 @@ struct GatedGradArgs {
     int M, N, Np;
     int act;
     int low;
-    int vec;                 // 16-byte loads of dh, gate and up
 };
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream);
 

@@ -231,7 +231,6 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
         a.N = (int)N;
         a.K = (int)round8(K);
         a.act = act;
-        a.vec_gated = (al16(h, ldh) ? 1 : 0) | (al16(gate, ldgate) ? 2 : 0) | (al16(up, ldup) ? 4 : 0);
         a.groups = 1;
         a.xcd_shift = di.xcd_shift;
         if (M == 1 && K <= lin::kGemvMaxK) return launched(lin::launch_gated_gemv(elem, a, (hipStream_t)stream));
@@ -337,15 +336,13 @@ int64_t partial_bytes(int64_t groups, int64_t R, int64_t C, int64_t slices) {
 
 int64_t slices_of(int64_t L) { return (L + 63) / 64; }
 
-// A product's tiles under a plan and its outputs' alignment (eb: output bytes).
-void set_tiles(lin::StreamProduct& a, const StreamPlan& p, int64_t eb, const DevInfo& di) {
+// A product's tiles under a plan.
+void set_tiles(lin::StreamProduct& a, const StreamPlan& p, const DevInfo& di) {
     const lin::GradConfig& g = lin::kGradConfigs[p.cfg];
     a.tiles_r = (int)tiles_of(a.R, g.bm);
     a.tiles_c = (int)tiles_of(a.C, g.bn);
     a.xcd_shift = di.xcd_shift;
     a.splits = p.splits;
-    for (int i = 0; i < a.groups; ++i)
-        if ((uintptr_t)a.y[i] % 16 == 0 && a.ldy[i] * eb % 16 == 0) a.vec |= 1 << i;
 }
 
 // A streaming product's launches under its plan; the operands are set by the caller.
@@ -354,7 +351,7 @@ int32_t launch_stream(int elem, bool rowt, int mode, lin::StreamProduct& a, cons
                       void* partial, hipStream_t stream) {
     const lin::GradConfig& g = lin::kGradConfigs[p.cfg];
     const int64_t eb = mode == lin::kOutRound ? 2 : 4;
-    set_tiles(a, p, eb, di);
+    set_tiles(a, p, di);
     if (p.c1 > 0) {
         lin::StreamProduct head = a;
         head.C = (int)p.c1;
@@ -467,7 +464,6 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     const bool streams = K > 0 && streamable(dy, lddy) && streamable(x, ldx);
     c.dy = dy;
     c.lddy = lddy;
-    c.vec = al16(dy, lddy);
     const bool with_sums = db && streams && c.splits == 1 && sums_fit(1, N, K, slices_of(M), di.cus);
     if (db && !with_sums) {
         st = launched(lin::launch_column_sum(elem, c, (hipStream_t)stream));
@@ -593,7 +589,6 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         g.Np = (int)Np;
         g.act = act;
         g.low = low_words(M);
-        g.vec = al16(dh, lddh) && al16(gate, ldgate) && al16(up, ldup);
         st = launched(lin::launch_gated_grad(elem, g, (hipStream_t)stream));
         if (st != LINEAR_OK) return st;
     }
@@ -641,8 +636,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     pw.segs = 1;
     pw.groups = 2;
     if (want_dx && want_dw && dx_streams && dw_streams && plan.pair) {
-        set_tiles(px, plan.dx, 2, di);
-        set_tiles(pw, plan.dw, 2, di);
+        set_tiles(px, plan.dx, di);
+        set_tiles(pw, plan.dw, di);
         return launched(lin::launch_grad_pair(elem, plan.dx.cfg == lin::kPairSmall, px, pw, (hipStream_t)stream));
     }
     if (want_dx && dx_streams) {
