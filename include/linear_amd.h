@@ -408,14 +408,18 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  * The gated block's gradients, from dh [M, N] and the projections gate and up
  * [M, N] that the forward call stored:
  *
- *     dg = RNE_E( dh * u * act'(g) )     du = RNE_E( dh * act(g) )      (FP32 inside)
+ *     dg = RNE_E( c * dh * u * act'(g) ) / c     du = RNE_E( c * dh * act(g) ) / c      (FP32 inside)
  *     dx[m, k]  = RNE_E( sum_n dg[m, n] * wg[n, k] + du[m, n] * wu[n, k] )
  *     dwg[n, k] = RNE_E( sum_m dg[m, n] * x[m, k] )      dwu likewise from du
  *
  * dg and du are rounded to E because they are the matrix unit's operands (up to 32
  * rows they are kept as two words, so that only the outputs' own rounding is left;
- * finite ones then give NaN, not an infinity, with an infinite weight or x); a
- * binary16 gradient past 65504 becomes infinite there.  dx may be NULL (not
+ * finite ones then give NaN, not an infinity, with an infinite weight or x).  In
+ * bfloat16 c is 1.  In binary16 c is the power of two that brings the largest finite
+ * |dg| or |du| of the call to 2^14 .. 2^15, and the products' FP32 sums are divided by
+ * it: whatever the gradients' size, none overflows, and those down to 2^-28 of the
+ * largest keep the type's relative precision (smaller ones are off by up to 2^-39 of the
+ * largest).  dx may be NULL (not
  * wanted; the weights are then not read), and dwg and dwu may both be NULL (x is
  * then not read); one of the two groups must be given.  N == 0 gives dx = +0,
  * M == 0 gives dwg = dwu = +0.

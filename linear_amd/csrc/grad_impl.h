@@ -121,6 +121,10 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     const int split = stack / a.groups, group = stack - split * a.groups;
     const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
+    float back = 1.f;                                 // (read here: its latency passes under the loop)
+    if constexpr (E == kF16 && MODE != kOutF32Add) {
+        if (a.unscale) back = *a.unscale;
+    }
 
     const int lane = threadIdx.x & 63;
     const int set = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / (NW * 64));
@@ -330,6 +334,15 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
 #pragma unroll
                     for (int j = 0; j < FM; ++j) acc[i][j] += low[((i * FM + j) * WN + wn) * 64 + lane];
             }
+        }
+    }
+
+    if constexpr (E == kF16 && MODE != kOutF32Add) {
+        if (a.unscale) {                              // uniform
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] *= back;
         }
     }
 

@@ -30,6 +30,7 @@ struct ProductArgs {
     uint16_t *gate, *up;
     int64_t ldgate, ldup;
     int act;
+    const float* unscale;    // rounded outputs, not null: the sums are multiplied by *unscale
 };
 
 enum : int { kProdRound = 0, kProdF32 = 1, kProdGated = 2 };
@@ -82,6 +83,8 @@ struct StreamProduct {
     // dx (64-row tiles, R = 2 kLowRow): each output row is the sum of the two rows' products.
     // dw (L = 2 kLowRow, one slice): row kLowRow + m of the columns is row m again.
     int fold;
+    // not null: the sums are multiplied by *unscale, the power of two that undoes the row operand's
+    const float* unscale;
     int tiles_r, tiles_c;
     int xcd_shift;
     // the contraction's slices shared among `splits` sets of tiles (more than one:
@@ -134,6 +137,15 @@ hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStrea
 // two halves of d [M, 2 * Np]: columns [0, N) and [Np, Np + N); columns between
 // N and Np are zeroed.  low: what the rounding leaves goes, rounded in turn, to row
 // kLowRow + m (0 where the first word is not finite).
+//
+// head, not null (binary16): dg and du are rounded after a multiplication by a power of
+// two that brings the largest finite one of the call to 2^14 .. 2^15.  binary16 ends at
+// 65504 and is subnormal below 6e-5, where the gradients of a mean loss lie: unscaled,
+// dWg of 512 rows of dh of 1e-6 was off by 5%.  A first launch (gated_max) leaves its
+// workgroups' maxima in head; the second derives the factor from them and leaves its
+// inverse in head[0], by which the products' sums are multiplied.
+constexpr int kGradMaxGrid = 512;                              // most workgroups of gated_max
+constexpr int kGradHead = 256 * ((16 + 4 * kGradMaxGrid + 255) / 256);   // bytes of head
 struct GatedGradArgs {
     const uint16_t *dh, *gate, *up;
     int64_t lddh, ldgate, ldup;
@@ -141,6 +153,8 @@ struct GatedGradArgs {
     int M, N, Np;
     int act;
     int low;
+    float* head;
+    int parts;               // set by the launch: maxima in head[4 ..]
 };
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream);
 

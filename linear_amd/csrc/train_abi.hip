@@ -574,9 +574,13 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     DevInfo di;
     st = lin::check_device(&dev, &di);
     if (st != LINEAR_OK) return st;
-    uint16_t* d = (uint16_t*)ws;
+    uint16_t* d = (uint16_t*)((char*)ws + lin::kGradHead);
+    // binary16 words are scaled; the products' sums are then multiplied by the factor's inverse
+    float* const head = elem == lin::kF16 && M > 0 && N > 0 ? (float*)ws : nullptr;
     if (M > 0 && N > 0) {
         lin::GatedGradArgs g;
+        memset(&g, 0, sizeof g);
+        g.head = head;
         g.dh = dh;
         g.gate = gate;
         g.up = up;
@@ -606,6 +610,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     const GatedPlan plan = plan_gated(M, N, K);
     lin::StreamProduct px, pw;
     memset(&px, 0, sizeof px);
+    memset(&pw, 0, sizeof pw);
     px.r = d;
     px.ldr = 2 * Np;
     px.c[0] = wg;
@@ -619,7 +624,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     px.L = (int)N;
     px.segs = 2;
     px.groups = 1;
-    memset(&pw, 0, sizeof pw);
+    px.unscale = pw.unscale = head;
     pw.r = d;
     pw.ldr = 2 * Np;
     pw.rgroup = Np;
@@ -646,6 +651,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, wg, ldwg, dx, lddx, M, K, N);
         p.segs = low ? 4 : 2;
+        p.unscale = head;
         for (int s = 0; s < p.segs; ++s) {
             p.a[s] = (s < 2 ? d : dl) + s % 2 * Np;
             p.b[s] = s % 2 ? wu : wg;
@@ -659,6 +665,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     } else if (want_dw) {
         for (int s = 0; s < 2; ++s) {
             lin::ProductArgs p = product(d + s * Np, 2 * Np, x, ldx, s ? dwu : dwg, s ? lddwu : lddwg, N, K, M);
+            p.unscale = head;
             if (low) {
                 p.segs = 2;
                 p.a[1] = dl + s * Np;
@@ -739,7 +746,7 @@ int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K) || !pack_ok(M, gated_half(N)) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
     const int64_t partials = gated_partials(M, N, K), packed = 2 * packed_bytes(N, K) + packed_bytes(M, K);
-    return gated_rows(M) * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
+    return lin::kGradHead + gated_rows(M) * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
