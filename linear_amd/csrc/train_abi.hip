@@ -558,7 +558,8 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     if (K == 0 || (M == 0 && N == 0)) return LINEAR_OK;
     if ((dwg == nullptr) != (dwu == nullptr)) return LINEAR_E_NULL;
     const bool want_dx = dx && M > 0, want_dw = dwg && N > 0;
-    if (!want_dx && !want_dw) return dx || dwg ? LINEAR_OK : LINEAR_E_NULL;
+    // (an empty output has no address, like one that is not wanted)
+    if (!want_dx && !want_dw) return M == 0 || N == 0 || dx || dwg ? LINEAR_OK : LINEAR_E_NULL;
     const int64_t need = linear_gated_workspace_bytes(M, N, K);
     if (need < 0) return LINEAR_E_SHAPE;
     const Operand in[] = {{dh, M, lddh, N}, {x, M, ldx, want_dw ? K : 0}, {wg, N, ldwg, want_dx ? K : 0},

@@ -1,0 +1,19 @@
+"""Edges of the gated block's and the gradients' entry points that need no GPU: sizes of zero, the
+largest sizes, and operands that a call does not read."""
+import pytest
+
+import linear_amd as la
+from test_train_cpu import gated_backward, needs_lib
+
+pytestmark = needs_lib
+
+
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+def test_gradients_of_an_empty_batch_with_one_group_wanted(tag):
+    """An empty output has no address, like one that is not wanted: nothing is left to compute."""
+    none = dict(dx=0, dwg=0, dwu=0, tag=tag)
+    assert gated_backward(M=0, dh=0, x=0, g=0, u=0, **none) == la.LINEAR_OK
+    assert gated_backward(N=0, dh=0, wg=0, wu=0, g=0, u=0, **none) == la.LINEAR_OK
+    assert gated_backward(K=0, x=0, wg=0, wu=0, **none) == la.LINEAR_OK
+    assert gated_backward(**none) == la.LINEAR_E_NULL                       # every output has elements
+    assert gated_backward(M=0, dh=0, x=0, g=0, u=0, dx=0, dwg=0, tag=tag) == la.LINEAR_E_NULL   # one of a pair
