@@ -443,6 +443,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
     st = check_workspace(ws, ws_bytes, need);
     if (st != LINEAR_OK) return st;
     if (!any_grid_ok(N, K)) return LINEAR_E_SHAPE;
+    if (M == 0 && f32 && accumulate) return LINEAR_OK;   // adds nothing (and leaves a -0)
     int dev = 0;
     DevInfo di;
     st = lin::check_device(&dev, &di);

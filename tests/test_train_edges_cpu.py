@@ -3,7 +3,7 @@ largest sizes, and operands that a call does not read."""
 import pytest
 
 import linear_amd as la
-from test_train_cpu import gated_backward, needs_lib
+from test_train_cpu import DB, DWG, gated_backward, needs_lib
 
 pytestmark = needs_lib
 
@@ -17,3 +17,11 @@ def test_gradients_of_an_empty_batch_with_one_group_wanted(tag):
     assert gated_backward(K=0, x=0, wg=0, wu=0, **none) == la.LINEAR_OK
     assert gated_backward(**none) == la.LINEAR_E_NULL                       # every output has elements
     assert gated_backward(M=0, dh=0, x=0, g=0, u=0, dx=0, dwg=0, tag=tag) == la.LINEAR_E_NULL   # one of a pair
+
+
+@pytest.mark.parametrize("tag", ["f16", "bf16"])
+def test_adding_an_empty_batch_leaves_the_sums(tag):
+    """Nothing is enqueued: adding a zero would turn a -0 into +0."""
+    fn = getattr(la._lib(), "linear_%s_backward_weight_f32out" % tag)
+    assert fn(0, 32, 0, 64, DWG, 64, DB, 1, 0, 32, 64, 0, 0, None) == la.LINEAR_OK
+    assert fn(0, 32, 0, 64, 0, 64, DB, 1, 0, 32, 64, 0, 0, None) == la.LINEAR_E_NULL

@@ -22,3 +22,11 @@ def test_gradients_of_an_empty_batch_with_one_group_wanted(t):
     dx, dwg, dwu = back(z(5, 0), z(5, 8), z(0, 8), z(0, 8), z(5, 0), z(5, 0), need_dw=False,
                         dx=torch.full((5, 8), 3.0, dtype=t, device=DEV))
     assert not dx.any() and dwg is None and dwu is None
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_adding_an_empty_batch_leaves_the_sums(t):
+    z = lambda *s: torch.zeros(*s, dtype=t, device=DEV)          # noqa: E731
+    dw, db = torch.full((7, 8), -0.0, device=DEV), torch.full((7,), -0.0, device=DEV)
+    fn("backward_weight_f32out", t)(z(0, 7), z(0, 8), bias=True, out=dw, db=db, accumulate=True)
+    assert bool(dw.signbit().all()) and bool(db.signbit().all())
