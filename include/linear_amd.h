@@ -413,9 +413,8 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  *     dwg[n, k] = RNE_E( sum_m dg[m, n] * x[m, k] )      dwu likewise from du
  *
  * dg and du are rounded to E because they are the matrix unit's operands (up to 32
- * rows they are kept as two words, so that only the outputs' own rounding is left;
- * finite ones then give NaN, not an infinity, with an infinite weight or x).  In
- * bfloat16 c is 1.  In binary16 c is the power of two that brings the largest finite
+ * rows they are kept as two words, so that only the outputs' own rounding is left).
+ * In bfloat16 c is 1.  In binary16 c is the power of two that brings the largest finite
  * |dg| or |du| of the call to 2^14 .. 2^15, and the products' FP32 sums are divided by
  * it: whatever the gradients' size, none overflows, and those down to 2^-28 of the
  * largest keep the type's relative precision (smaller ones are off by up to 2^-39 of the

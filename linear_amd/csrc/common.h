@@ -277,6 +277,18 @@ __device__ inline void lookup_chunks(lds_u16* win, __amdgpu_buffer_rsrc_t rt, u3
         }
 }
 
+// The 8 words with infinities and NaN as zeros.
+template <int E>
+__device__ inline u32x4 finite_words(u32x4 v) {
+    constexpr uint32_t top = E == kBF16 ? 0x7f80u : 0x7c00u;      // the exponent of both
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if ((v[i] & top) == top) v[i] &= 0xffff0000u;
+        if ((v[i] & (top << 16)) == top << 16) v[i] &= 0xffffu;
+    }
+    return v;
+}
+
 // 8 consecutive words src[0..7] of a row, the valid ones only (col + e < N,
 // row valid): a 16-byte load, of any alignment, where all are.  store8 likewise (15 x 6879
 // x 2405 dw, rows of odd length: 2-byte stores took 35 us, these 19).

@@ -254,6 +254,18 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         }
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"((STAGES - 1) * GPW) : "memory");
         lds_barrier();
+        if constexpr (ROWT) {
+            if (a.fold) {                             // uniform: one slice
+                // rows kLowRow .. of the column panel, which the second words meet: an infinity of x
+                // is the first words' alone, a zero or a word of the other sign would make it NaN (16 x
+                // 14336 x 4096 bf16: 2.5 us of 147)
+                for (int o = (int)threadIdx.x % (NW * 64) * 16; o < a.fold * CROW; o += NW * 1024) {
+                    u32x4* v = (u32x4*)(smem + set * RING + kLowRow * CROW + o);
+                    *v = finite_words<E>(*v);
+                }
+                lds_barrier();
+            }
+        }
         // the column fragments are double buffered; a row fragment's next value is read
         // right after the MFMAs that use it
         u32x4 ca[2][FN], rb[FM];
@@ -332,7 +344,14 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
 #pragma unroll
-                    for (int j = 0; j < FM; ++j) acc[i][j] += low[((i * FM + j) * WN + wn) * 64 + lane];
+                    for (int j = 0; j < FM; ++j) {
+                        // (the second words' sum is left out where the first's is infinite or NaN:
+                        // with an infinite weight it may be of the other sign, or NaN)
+                        const f32x4 lo = low[((i * FM + j) * WN + wn) * 64 + lane];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j][e] += __builtin_fabsf(acc[i][j][e]) < __builtin_inff() ? lo[e] : 0.f;
+                    }
             }
         }
     }

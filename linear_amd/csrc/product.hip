@@ -109,6 +109,12 @@ __global__ void __launch_bounds__(256) product_any(ProductArgs p) {
             va = any_load<T, AK>(p.a[s], p.lda, r0, p.R, k0, p.L, tid);
 #pragma unroll
             for (int b = 0; b < NB; ++b) vb[b] = any_load<T, BK>(p.b[s + b], p.ldb[s + b], c0, p.C, k0, p.L, tid);
+            if constexpr (MODE == kProdRound) {
+                if (p.finite_from && s >= p.finite_from) {
+#pragma unroll
+                    for (int i = 0; i < T * PK / 2048; ++i) vb[0].v[i] = finite_words<E>(vb[0].v[i]);
+                }
+            }
         };
         if (p.L > 0) load(0);
         for (int64_t k0 = 0; k0 < p.L; k0 += PK) {

@@ -21,6 +21,7 @@ struct ProductArgs {
     const uint16_t* b[4];
     int64_t lda, ldb[4];
     int segs;
+    int finite_from;         // not 0, rounded outputs: the segments from which b's infinities and NaN count as zeros
     int R, C, L;             // output rows and columns, contraction length
     int tiles_c;             // set by the launch
     void* y;                 // [R, C], row stride ldy: 16-bit words or floats

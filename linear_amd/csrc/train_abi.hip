@@ -653,6 +653,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     } else if (want_dx) {
         lin::ProductArgs p = product(d, 2 * Np, wg, ldwg, dx, lddx, M, K, N);
         p.segs = low ? 4 : 2;
+        p.finite_from = low ? 2 : 0;                  // the second words'
         p.unscale = head;
         for (int s = 0; s < p.segs; ++s) {
             p.a[s] = (s < 2 ? d : dl) + s % 2 * Np;
@@ -670,6 +671,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
             p.unscale = head;
             if (low) {
                 p.segs = 2;
+                p.finite_from = 1;
                 p.a[1] = dl + s * Np;
                 p.b[1] = x;
                 p.ldb[1] = ldx;
