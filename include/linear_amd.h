@@ -40,6 +40,9 @@
  *  - Every argument error is detected on the host before anything is enqueued;
  *    y is then untouched.  No exception or abort crosses this ABI.
  *  - Limits: M, N, K < 2^31; ldx, ldw < 2^22 and ldy < 2^31 elements.
+ *    A launch holds fewer than 2^32 threads: outputs of more than 2^25 columns are
+ *    computed in parts, and a call that needs a larger launch all the same (some 2^29
+ *    rows) returns LINEAR_E_LAUNCH.
  *  - Fast path: x and weight 16-byte aligned, ldx, ldw and K multiples of 8.
  *    Any other layout is accepted and runs a slower element-wise loader.
  */

@@ -10,6 +10,9 @@ constexpr int64_t kMaxLdIn = (int64_t(1) << 22) - 1;
 constexpr int64_t kMaxLdOut = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxGridX = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxGridY = 65535;
+// Columns of one launch.  The one-row kernels take 64 threads a column and a launch holds
+// fewer than 2^32 (see launch_kernel); wider outputs are taken in parts, each a layer of its own.
+constexpr int64_t kColumnPart = int64_t(1) << 25;
 
 // The compute units and XCDs of the device a call runs on, read from the device
 // (a partitioned part has fewer).  Plans made without a usable device (the

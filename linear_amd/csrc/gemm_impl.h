@@ -769,7 +769,7 @@ static const void* stream_fn(int mode) {
 static hipError_t launch(const void* fn, const LinearArgs& a, int threads, hipStream_t stream) {
     LinearArgs args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)(a.tiles_m * a.tiles_n), 1, (unsigned)a.groups), dim3(threads), params,
+    return launch_kernel(fn, dim3((unsigned)(a.tiles_m * a.tiles_n), 1, (unsigned)a.groups), dim3(threads), params,
                            0, stream);
 }
 

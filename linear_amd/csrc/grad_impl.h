@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(512) grad_pair(StreamProduct a, StreamProduct 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
     StreamProduct args = a;
     void* params[] = {&args};
-    return hipLaunchKernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads),
+    return launch_kernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads),
                            params, 0, stream);
 }
 
@@ -468,7 +468,7 @@ template <int E>
 hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream) {
     StreamProduct aa = a, bb = b;
     void* params[] = {&aa, &bb};
-    return hipLaunchKernel(small ? (const void*)grad_pair<true, E> : (const void*)grad_pair<false, E>,
+    return launch_kernel(small ? (const void*)grad_pair<true, E> : (const void*)grad_pair<false, E>,
                            dim3((unsigned)(a.tiles_r * a.tiles_c + b.groups * b.tiles_r * b.tiles_c)), dim3(512), params, 0,
                            stream);
 }

@@ -159,18 +159,18 @@ __global__ void __launch_bounds__(256) grad_clip(GradTable t, const float* norm,
 hipError_t launch_grad_partials(const GradTable& t, double* partial, int grid, hipStream_t stream) {
     GradTable table = t;
     void* params[] = {&table, &partial};
-    return hipLaunchKernel((const void*)grad_partials, dim3((unsigned)grid), dim3(256), params, 0, stream);
+    return launch_kernel((const void*)grad_partials, dim3((unsigned)grid), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_grad_norm(const double* partial, int count, float* norm, hipStream_t stream) {
     void* params[] = {&partial, &count, &norm};
-    return hipLaunchKernel((const void*)grad_norm, dim3(1), dim3(1024), params, 0, stream);
+    return launch_kernel((const void*)grad_norm, dim3(1), dim3(1024), params, 0, stream);
 }
 
 hipError_t launch_grad_clip(const GradTable& t, const float* norm, float max_norm, int grid, hipStream_t stream) {
     GradTable table = t;
     void* params[] = {&table, &norm, &max_norm};
-    return hipLaunchKernel((const void*)grad_clip, dim3((unsigned)grid), dim3(256), params, 0, stream);
+    return launch_kernel((const void*)grad_clip, dim3((unsigned)grid), dim3(256), params, 0, stream);
 }
 
 }  // namespace lin

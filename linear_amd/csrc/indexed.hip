@@ -919,7 +919,7 @@ hipError_t launch_indexed_routed(int elem, int cfg, const IndexedArgs& a, int mo
     IndexedArgs args = a;
     void* params[] = {&args};
     const int64_t tiles_n = (a.N + g.bn - 1) / g.bn;
-    return hipLaunchKernel(fn, dim3((unsigned)(tiles_n * a.slots)), dim3(g.wm * g.wn * 64), params, 0, stream);
+    return launch_kernel(fn, dim3((unsigned)(tiles_n * a.slots)), dim3(g.wm * g.wn * 64), params, 0, stream);
 }
 
 template <int E>
@@ -932,7 +932,7 @@ hipError_t launch_indexed(int elem, const IndexedArgs& a, int mode, hipStream_t 
     IndexedArgs args = a;
     void* params[] = {&args};
     const dim3 grid((unsigned)((a.N + kIdxCols - 1) / kIdxCols), (unsigned)a.E);
-    return hipLaunchKernel(fn, grid, dim3(kIdxWaves * 64), params, 0, stream);
+    return launch_kernel(fn, grid, dim3(kIdxWaves * 64), params, 0, stream);
 }
 
 }  // namespace lin

@@ -7,6 +7,14 @@
 
 namespace lin {
 
+// hipLaunchKernel for grids of any size: HIP counts a dimension's threads in 32 bits and,
+// past them, enqueues what is left of the product and reports no error (one row of 2^26 + 8
+// outputs: the first two were written).  Such a launch is refused here.
+inline hipError_t launch_kernel(const void* fn, dim3 grid, dim3 block, void** params, size_t lds, hipStream_t stream) {
+    if ((uint64_t)grid.x * block.x >> 32) return hipErrorInvalidConfiguration;
+    return hipLaunchKernel(fn, grid, block, params, lds, stream);
+}
+
 struct GemmConfig {
     int bm, bn, wm, wn;   // tile rows (m), tile columns (n), waves along m and n
     int stages;           // LDS ring depth

@@ -318,6 +318,25 @@ int32_t run(const Request& r, void* stream) {
     int32_t st = validate_all(r);
     if (st != LINEAR_OK) return st;
     if (r.M == 0 || r.N == 0 || r.G == 0) return LINEAR_OK;
+    if (r.N > lin::kColumnPart && r.G == 1) {         // columns in parts
+        for (int64_t n0 = 0; n0 < r.N && st == LINEAR_OK; n0 += lin::kColumnPart) {
+            Request part = r;
+            part.N = std::min(r.N - n0, lin::kColumnPart);
+            part.w = r.w + n0 * r.ldw;
+            if (r.b) part.b = r.b + n0;
+            part.y = (unsigned char*)r.y + n0 * (r.f32_out ? 4 : 2);
+            linear_epilogue epi;
+            if (r.epi) {
+                epi = *r.epi;
+                if (epi.bias) epi.bias += n0;
+                if (epi.residual) epi.residual += n0;
+                if (epi.mul) epi.mul += n0;
+                part.epi = &epi;
+            }
+            st = run(part, stream);
+        }
+        return st;
+    }
     linear_plan p;
     st = plan(r, &p, kWholeMI355X.cus);   // shape errors come before device errors
     if (st != LINEAR_OK) return st;

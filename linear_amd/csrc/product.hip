@@ -10,6 +10,9 @@
 // at the edges), the next stage's while this one is multiplied.  A k-contiguous
 // operand is staged as [row][k], a k-major one as [k][row] and read with the
 // transposing read, as in the streaming kernels.
+#include <algorithm>
+
+#include "abi.h"
 #include "columns.h"
 #include "grad_impl.h"
 #include "train.h"
@@ -441,7 +444,7 @@ hipError_t launch_product_any(int elem, int mode, bool rowt, const ProductArgs& 
     ProductArgs args = p;
     void* params[] = {&args};
     if (mode == kProdGated && p.R <= 8 * ROWS)
-        return hipLaunchKernel(elem == kBF16 ? (const void*)gated_rows_any<kBF16> : (const void*)gated_rows_any<kF16>,
+        return launch_kernel(elem == kBF16 ? (const void*)gated_rows_any<kBF16> : (const void*)gated_rows_any<kF16>,
                                dim3((unsigned)((p.C + 3) / 4), (unsigned)((p.R + ROWS - 1) / ROWS)), dim3(256), params, 0,
                                stream);
     const auto tiles = [&](int t) { return ((int64_t)p.R + t - 1) / t * (((int64_t)p.C + t - 1) / t); };
@@ -450,14 +453,14 @@ hipError_t launch_product_any(int elem, int mode, bool rowt, const ProductArgs& 
     args.tiles_c = (p.C + t - 1) / t;
     const void* fn = elem == kBF16 ? (large ? any_fn<128, kBF16>(mode, rowt) : any_fn<kProdTile, kBF16>(mode, rowt))
                                    : (large ? any_fn<128, kF16>(mode, rowt) : any_fn<kProdTile, kF16>(mode, rowt));
-    return hipLaunchKernel(fn, dim3((unsigned)tiles(t)), dim3(256), params, 0, stream);
+    return launch_kernel(fn, dim3((unsigned)tiles(t)), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_repack(const uint16_t* in, int64_t ld, int64_t rows, int cols, uint16_t* out, int64_t ldo,
                          hipStream_t stream) {
     void* params[] = {&in, &ld, &rows, &cols, &out, &ldo};
     const int64_t blocks = (rows * (ldo / 8) + 255) / 256;
-    return hipLaunchKernel((const void*)repack, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0,
+    return launch_kernel((const void*)repack, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0,
                            stream);
 }
 
@@ -467,7 +470,7 @@ hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStrea
     const int64_t blocks = ((int64_t)a.groups * a.R * ((a.C + 3) / 4) + 255) / 256;
     const void* fn = f32 ? (const void*)split_sum<kF16, true>
                          : elem == kBF16 ? (const void*)split_sum<kBF16, false> : (const void*)split_sum<kF16, false>;
-    return hipLaunchKernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
+    return launch_kernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t stream) {
@@ -478,24 +481,34 @@ hipError_t launch_gated_grad(int elem, const GatedGradArgs& g, hipStream_t strea
     if (g.head) {
         const int64_t parts = (pieces + 1023) / 1024;
         args.parts = (int)(parts < kGradMaxGrid ? parts : kGradMaxGrid);
-        const hipError_t e = hipLaunchKernel((const void*)gated_max<kF16>, dim3((unsigned)args.parts), dim3(1024), params, 0,
+        const hipError_t e = launch_kernel((const void*)gated_max<kF16>, dim3((unsigned)args.parts), dim3(1024), params, 0,
                                              stream);
         if (e != hipSuccess) return e;
     }
     const void* fn = elem == kBF16
                          ? (g.low ? (const void*)gated_grad<kBF16, true, false> : (const void*)gated_grad<kBF16, false, false>)
                          : (g.low ? (const void*)gated_grad<kF16, true, true> : (const void*)gated_grad<kF16, false, true>);
-    return hipLaunchKernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
+    return launch_kernel(fn, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t stream) {
     ColumnSumArgs args = c;
     void* params[] = {&args};
+    if (c.N > kColumnPart) {                          // (one split: so many columns fill the chip)
+        for (int64_t n = 0; n < c.N; n += kColumnPart) {
+            args.dy = c.dy + n;
+            args.db = (char*)c.db + n * (c.f32 ? 4 : 2);
+            args.N = (int)std::min((int64_t)c.N - n, kColumnPart);
+            const hipError_t e = launch_column_sum(elem, args, stream);
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
     const unsigned gx = (unsigned)((c.N + 63) / 64);
-    hipError_t e = hipLaunchKernel(elem == kBF16 ? (const void*)column_partials<kBF16> : (const void*)column_partials<kF16>,
+    hipError_t e = launch_kernel(elem == kBF16 ? (const void*)column_partials<kBF16> : (const void*)column_partials<kF16>,
                                    dim3(gx, (unsigned)c.splits), dim3(1024), params, 0, stream);
     if (e != hipSuccess || c.splits == 1) return e;
-    return hipLaunchKernel(elem == kBF16 ? (const void*)column_finish<kBF16> : (const void*)column_finish<kF16>,
+    return launch_kernel(elem == kBF16 ? (const void*)column_finish<kBF16> : (const void*)column_finish<kF16>,
                            dim3(gx), dim3(64), params, 0, stream);
 }
 

@@ -336,7 +336,7 @@ hipError_t launch_gated_gemv(int elem, const LinearArgs& a, hipStream_t stream) 
     LinearArgs args = a;
     void* params[] = {&args};
     const size_t lds = (size_t)gemv_segments(a.K) * 1024;
-    return hipLaunchKernel(elem == kBF16 ? (const void*)gated_gemv<kBF16> : (const void*)gated_gemv<kF16>,
+    return launch_kernel(elem == kBF16 ? (const void*)gated_gemv<kBF16> : (const void*)gated_gemv<kF16>,
                            dim3((unsigned)((a.N + kGemvRows - 1) / kGemvRows)), dim3(kGemvRows * 64), params, lds, stream);
 }
 
@@ -354,7 +354,7 @@ hipError_t launch_gemv(int elem, const LinearArgs& a, int mode, hipStream_t stre
     void* params[] = {&args};
     const void* fn = elem == kBF16 ? gemv_fn<kBF16>(mode) : gemv_fn<kF16>(mode);
     const size_t lds = (size_t)gemv_segments(a.K) * 1024;
-    return hipLaunchKernel(fn, grid, block, params, lds, stream);
+    return launch_kernel(fn, grid, block, params, lds, stream);
 }
 
 template <int E>
@@ -377,7 +377,7 @@ hipError_t launch_skinny(int elem, const LinearArgs& a, bool vec, int mode, hipS
     LinearArgs args = a;
     void* params[] = {&args};
     const void* fn = elem == kBF16 ? skinny_fn<kBF16>(vec, mode) : skinny_fn<kF16>(vec, mode);
-    return hipLaunchKernel(fn, grid, block, params, 0, stream);
+    return launch_kernel(fn, grid, block, params, 0, stream);
 }
 
 }  // namespace lin

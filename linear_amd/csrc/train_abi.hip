@@ -200,6 +200,12 @@ int32_t run_gated(int elem, const uint16_t* x, int64_t ldx, const uint16_t* wg, 
     if (st != LINEAR_OK) return st;
     st = check_workspace(ws, ws_bytes, need);
     if (st != LINEAR_OK) return st;
+    if (N > lin::kColumnPart) {                       // columns in parts; the workspace serves one after the other
+        for (int64_t n = 0; n < N && st == LINEAR_OK; n += lin::kColumnPart)
+            st = run_gated(elem, x, ldx, wg + n * ldwg, ldwg, wu + n * ldwu, ldwu, act, h + n, ldh, gate ? gate + n : gate,
+                           ldgate, up ? up + n : up, ldup, M, std::min(N - n, lin::kColumnPart), K, ws, ws_bytes, stream);
+        return st;
+    }
     if (!any_grid_ok(M, N)) return LINEAR_E_SHAPE;
     int dev = 0;
     DevInfo di;
