@@ -577,7 +577,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     st = check_workspace(ws, ws_bytes, need);
     if (st != LINEAR_OK) return st;
     const int64_t Np = gated_half(N);
-    if ((want_dx && !any_grid_ok(M, K)) || (want_dw && !any_grid_ok(N, K)) || 2 * Np > kMaxLdOut) return LINEAR_E_SHAPE;
+    if ((want_dx && !any_grid_ok(M, K)) || (want_dw && !any_grid_ok(N, K))) return LINEAR_E_SHAPE;
     int dev = 0;
     DevInfo di;
     st = lin::check_device(&dev, &di);
@@ -754,7 +754,8 @@ int64_t linear_gated_forward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (!dims_ok(M, N, K) || !pack_ok(M, gated_half(N)) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
+    if (!dims_ok(M, N, K) || 2 * gated_half(N) > kMaxLdOut) return -1;   // dg | du in one row
+    if (!pack_ok(M, gated_half(N)) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
     const int64_t partials = gated_partials(M, N, K), packed = 2 * packed_bytes(N, K) + packed_bytes(M, K);
     return lin::kGradHead + gated_rows(M) * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
 }

@@ -25,3 +25,16 @@ def test_adding_an_empty_batch_leaves_the_sums(tag):
     fn = getattr(la._lib(), "linear_%s_backward_weight_f32out" % tag)
     assert fn(0, 32, 0, 64, DWG, 64, DB, 1, 0, 32, 64, 0, 0, None) == la.LINEAR_OK
     assert fn(0, 32, 0, 64, 0, 64, DB, 1, 0, 32, 64, 0, 0, None) == la.LINEAR_E_NULL
+
+
+def test_sizes_of_the_gated_backward_workspace():
+    """dg | du is a matrix of twice N columns (N in whole slices of 64), each row below 2^31 words: the
+    workspace call refuses the sizes that the backward call refuses."""
+    top = (1 << 30) - 64
+    for M in (1, 5000):
+        assert la.gated_workspace_bytes(M, top, 1) > 4 * M * top
+        for N in (top + 1, 1 << 30, (1 << 31) - 65536):
+            with pytest.raises(ValueError):
+                la.gated_workspace_bytes(M, N, 1)
+            assert gated_backward(M=M, N=N, K=1, ldx=1, ldwg=1, ldwu=1, lddx=1, lddwg=1, lddwu=1, lddh=N, ldg=N, ldu=N,
+                                  nws=1 << 62) == la.LINEAR_E_SHAPE
