@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import concurrent.futures
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -23,6 +24,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "indexed.hip", "product.hip", "gradnorm.hip",
            "gated_f16.hip", "gated_bf16.hip", "grad_f16.hip", "grad_bf16.hip",
            "linear_abi.hip", "train_abi.hip"]
+
+# sources whose kernels set m0 in inline assembly (lds_dma16_raw), which the compiler is not told
+RAW_M0_SOURCES = ("grad_f16.hip", "grad_bf16.hip")
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -61,9 +65,28 @@ def _resources(text: str) -> dict:
     return res
 
 
+def _other_m0_uses(asm: str) -> list:
+    """The instructions naming m0 that are not lds_dma16_raw's three: m0's write, the wait states
+    and the direct-to-LDS load that reads it.  Any other would be the compiler's own use, whose
+    value the inline assembly may have overwritten."""
+    code = [l.split(";")[0].split("//")[0].strip() for l in asm.splitlines()]
+    code = [l for l in code if l and not l.startswith(".") and not l.endswith(":")]
+    bad = []
+    for i, line in enumerate(code):
+        if not re.search(r"\bm0\b", line):
+            continue
+        rest = [l.split() for l in code[i + 1:i + 3]] + [[""]] * 2
+        if not (line.startswith("s_mov_b32 m0,") and rest[0] == ["s_nop", "3"] and
+                rest[1][0] == "buffer_load_dwordx4" and rest[1][-1] == "lds"):
+            bad.append(line)
+    return bad
+
+
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
     cmd = [hipcc(), *HIPCC_FLAGS, "-c", os.path.join(CSRC, src), "-o", obj]
+    if src in RAW_M0_SOURCES:
+        cmd.append("-save-temps=obj")
     r = subprocess.run(cmd, capture_output=True, text=True)
     out = r.stdout + r.stderr
     noise = ("is not a recognized feature for this target", "kernel-resource-usage")
@@ -84,6 +107,12 @@ def _compile(src: str) -> str:
             f.write("%s %s\n" % (k, " ".join("%s=%s" % (a.replace(" ", "_"), b) for a, b in v.items())))
     if bad:
         raise RuntimeError("kernels in %s use scratch memory: %s" % (src, ", ".join(sorted(bad))))
+    if src in RAW_M0_SOURCES:
+        asm = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + "-hip-amdgcn-amd-amdhsa-gfx950.s")
+        with open(asm) as f:
+            uses = _other_m0_uses(f.read())
+        if uses:
+            raise RuntimeError("%s: the compiler uses m0 itself beside the inline assembly: %s" % (src, uses[0]))
     return obj
 
 

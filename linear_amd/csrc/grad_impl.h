@@ -47,8 +47,10 @@ __host__ __device__ constexpr int panel_swz(int k) {
 // transposing reads, which name no LDS bytes it could tell apart.  The ring's own
 // waits (an explicit vmcnt and a barrier per slice) order the two.  There is no
 // register output.  The s_nop covers the wait states after the write of m0, and
-// those between a vector write of a resource word and its use.  (m0 is the compiler's
-// reserved register: it writes it anew before each use of its own.)
+// those between a vector write of a resource word and its use.  m0 cannot be named as
+// clobbered (the compiler reserves it): the build checks that no other instruction of
+// these kernels uses it.  (Handing back its old value after each load would need no
+// check, and takes 2 to 4% more of dx: 8192 x 4096 x 4096 bf16 214.5 -> 223.4 us.)
 __device__ __forceinline__ void lds_dma16_raw(__amdgpu_buffer_rsrc_t r, uint32_t lds, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(r));
 }
