@@ -587,6 +587,28 @@ int32_t linear_f16_plan(const uint16_t* x, int64_t ldx,
                         int64_t M, int64_t N, int64_t K,
                         int32_t path, linear_plan* plan);
 
+/*
+ * How a gated backward call of these sizes forms its products (host only, 16-byte
+ * aligned layouts; it depends on the sizes alone): the tiles of dx and of the pair dwg,
+ * dwu, the sets of workgroups that share a contraction (splits), and, where the output
+ * columns from split_c on are a second launch, that launch's tile.  joint: both
+ * products run in one launch.  Returns LINEAR_OK, LINEAR_E_SHAPE or LINEAR_E_NULL.
+ */
+typedef struct linear_product_plan {
+    int32_t tile_m, tile_n;   /* output rows and columns per workgroup */
+    int32_t stages;           /* slices of 64 contraction indices in a workgroup's LDS ring */
+    int32_t sets;             /* sets of waves that share a tile's slices */
+    int32_t splits;
+    int32_t tile_m2, tile_n2; /* the second launch's tile (0: one launch) */
+    int64_t split_c;          /* its first column (0: one launch) */
+} linear_product_plan;
+typedef struct linear_gated_plan {
+    linear_product_plan dx, dw;
+    int32_t joint;
+    int32_t two_words;        /* dg and du are kept as two words each (up to 32 rows) */
+} linear_gated_plan;
+int32_t linear_gated_backward_plan(int64_t M, int64_t N, int64_t K, linear_gated_plan* plan);
+
 /* Static English text for a status code (never NULL). */
 const char* linear_status_string(int32_t status);
 

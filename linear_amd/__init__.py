@@ -67,7 +67,7 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_f16_backward_weight", "linear_bf16_backward_weight",
                 "linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out",
                 "linear_grad_workspace_bytes", "linear_grad_norm", "linear_grad_clip",
-                "linear_f16_plan", "linear_status_string", "linear_last_hip_error")
+                "linear_f16_plan", "linear_gated_backward_plan", "linear_status_string", "linear_last_hip_error")
 
 
 class LinearError(RuntimeError):
@@ -88,6 +88,15 @@ class _Plan(ctypes.Structure):
                 ("tile_k", ctypes.c_int32), ("threads", ctypes.c_int32), ("vector_io", ctypes.c_int32),
                 ("grid", ctypes.c_int64), ("split_n", ctypes.c_int64), ("tile_m2", ctypes.c_int32),
                 ("tile_n2", ctypes.c_int32), ("grid2", ctypes.c_int64), ("stages", ctypes.c_int32)]
+
+
+class _ProductPlan(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int32) for f in ("tile_m", "tile_n", "stages", "sets", "splits", "tile_m2", "tile_n2")] + [
+        ("split_c", ctypes.c_int64)]
+
+
+class _GatedPlan(ctypes.Structure):
+    _fields_ = [("dx", _ProductPlan), ("dw", _ProductPlan), ("joint", ctypes.c_int32), ("two_words", ctypes.c_int32)]
 
 
 class _Epilogue(ctypes.Structure):
@@ -170,6 +179,8 @@ def _lib():
     lib.linear_f16_plan.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, i32,
                                     ctypes.POINTER(_Plan)]
     lib.linear_f16_plan.restype = i32
+    lib.linear_gated_backward_plan.argtypes = [i64, i64, i64, ctypes.POINTER(_GatedPlan)]
+    lib.linear_gated_backward_plan.restype = i32
     lib.linear_status_string.argtypes = [i32]
     lib.linear_status_string.restype = ctypes.c_char_p
     lib.linear_last_hip_error.argtypes = []
@@ -885,6 +896,17 @@ def linear_f16_plan(x: torch.Tensor, weight: torch.Tensor, b: torch.Tensor | Non
                                 x.shape[0], weight.shape[0], x.shape[1], int(path), ctypes.byref(p))
     _check(rc, "linear_f16_plan")
     return {f: getattr(p, f) for f, _ in _Plan._fields_}
+
+
+def linear_gated_backward_plan(M: int, N: int, K: int) -> dict:
+    """How a gated backward call of these sizes forms its products (host only, aligned layouts):
+    dx and dw, each with tile_m, tile_n, stages, sets, splits and, where the columns from split_c
+    on are a second launch, tile_m2 and tile_n2; joint: both in one launch; two_words: dg and du
+    are kept as two words."""
+    p = _GatedPlan()
+    _check(_lib().linear_gated_backward_plan(M, N, K, ctypes.byref(p)), "linear_gated_backward_plan")
+    parts = {n: {f: getattr(getattr(p, n), f) for f, _ in _ProductPlan._fields_} for n in ("dx", "dw")}
+    return {**parts, "joint": bool(p.joint), "two_words": bool(p.two_words)}
 
 
 def linear(x: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,

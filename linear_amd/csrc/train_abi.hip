@@ -760,6 +760,31 @@ int64_t linear_gated_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return lin::kGradHead + gated_rows(M) * gated_half(N) * 2 * 2 + (packed ? round256(partials) + packed : partials);
 }
 
+int32_t linear_gated_backward_plan(int64_t M, int64_t N, int64_t K, linear_gated_plan* plan) {
+    if (linear_gated_workspace_bytes(M, N, K) < 0) return LINEAR_E_SHAPE;
+    if (!plan) return LINEAR_E_NULL;
+    memset(plan, 0, sizeof *plan);
+    const GatedPlan p = plan_gated(M, N, K);
+    auto fill = [](linear_product_plan& out, const StreamPlan& s) {
+        const lin::GradConfig &g = lin::kGradConfigs[s.cfg], &g1 = lin::kGradConfigs[s.cfg1];
+        out.tile_m = g.bm;
+        out.tile_n = g.bn;
+        out.stages = g.stages;
+        out.sets = g.sets;
+        out.splits = s.splits;
+        out.split_c = s.c1;
+        if (s.c1 > 0) {
+            out.tile_m2 = g1.bm;
+            out.tile_n2 = g1.bn;
+        }
+    };
+    fill(plan->dx, p.dx);
+    fill(plan->dw, p.dw);
+    plan->joint = p.pair;
+    plan->two_words = low_words(M);
+    return LINEAR_OK;
+}
+
 int64_t linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!dims_ok(M, N, K) || !pack_ok(M, N) || !pack_ok(M, K) || !pack_ok(N, K)) return -1;
     const int64_t in = partial_bytes(1, M, K, slices_of(N)), in_packed = packed_bytes(M, N) + packed_bytes(N, K);
