@@ -426,6 +426,8 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  * then not read); one of the two groups must be given, unless M or N is 0.
  * N == 0 gives dx = +0, M == 0 gives dwg = dwu = +0.  N is at most
  * 2^30 - 64 (dg and du share rows).
+ * Fast path of dx: both weights with one row stride (16-byte aligned, as everywhere);
+ * weights of two strides run the slower element-wise loader.
  *
  * workspace: linear_gated_workspace_bytes(M, N, K) bytes of device memory (it
  * holds dg and du, partial sums, and copies of operands of odd widths), 16-byte

@@ -151,7 +151,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             const int at = (col ? c0 : r0) + 8 * c;
             const int line = col ? k & lines : k;
             goff[j] = (int)(at < (col ? a.C : a.R)) & (int)(k % kLowRow < whole)
-                          ? (uint32_t)((line * (int)(col ? a.ldc[0] : a.ldr) + at) * 2) : kOOB;
+                          ? (uint32_t)((line * (int)(col ? a.ldc : a.ldr) + at) * 2) : kOOB;
         } else {
             const int r = byte / RROW, c = (byte % RROW / 16) ^ ((r >> 1) & 7);
             gk[(j - GC) % 2] = 8 * c;
@@ -175,12 +175,12 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     // operand read zeros; a contiguous one is masked by its lanes' own indices.
     int seg = t0 >= per && a.segs > 1 ? 1 : 0;
     const int first = (t0 - seg * per) * BK;
-    const uint16_t* cp = a.c[seg] + (int64_t)first * a.ldc[0];
+    const uint16_t* cp = a.c[seg] + (int64_t)first * a.ldc;
     const uint16_t* rp = ROWT ? rbase + (int64_t)first * a.ldr : rbase + r0 * a.ldr + (int64_t)t0 * BK;
     int left = mine > 0 ? a.L - first : 0;            // contraction indices left in the segment
     int todo = mine;                                  // slices left to request
     uint32_t fill = base;
-    const int ldc = (int)a.ldc[0], ldr = (int)a.ldr;
+    const int ldc = (int)a.ldc, ldr = (int)a.ldr;
     const int cend = (a.C + 7) & ~7, rend = (a.R + 7) & ~7;
     const int rbytes = ((min(BM, a.R - r0) - 1) * ldr + BK) * 2;
     auto request = [&]<int J0, int J1>() {

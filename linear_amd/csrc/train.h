@@ -75,7 +75,7 @@ constexpr int kLowRow = 32;
 struct StreamProduct {
     const uint16_t* r;
     const uint16_t* c[2];
-    int64_t ldr, ldc[2], rgroup;
+    int64_t ldr, ldc, rgroup;          // ldc: of every segment (a lane's offsets never change)
     void* y[2];
     int64_t ldy[2];
     int R, C, L;

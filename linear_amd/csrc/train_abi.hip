@@ -413,7 +413,7 @@ int32_t run_backward_input(int elem, const uint16_t* dy, int64_t lddy, const uin
         a.r = dy;
         a.ldr = lddy;
         a.c[0] = w;
-        a.ldc[0] = ldw;
+        a.ldc = ldw;
         a.y[0] = dx;
         a.ldy[0] = lddx;
         a.R = (int)M;
@@ -483,7 +483,7 @@ int32_t run_backward_weight(int elem, bool f32, const uint16_t* dy, int64_t lddy
         a.r = dy;
         a.ldr = lddy;
         a.c[0] = x;
-        a.ldc[0] = ldx;
+        a.ldc = ldx;
         a.y[0] = dw;
         a.ldy[0] = lddw;
         a.R = (int)N;
@@ -613,6 +613,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
         if ((st = pack_operand(wu, ldwu, N, K, false, space, stream)) != LINEAR_OK) return st;
     }
     if (want_dw && (st = pack_operand(x, ldx, M, K, false, space, stream)) != LINEAR_OK) return st;
+    // weights of two row strides run the any-layout kernel, as unaligned ones do
     const bool dx_streams = streamable(wg, ldwg) && ldwu == ldwg && al16(wu, ldwu) && 2 * Np <= lin::kMaxLdIn;
     const bool dw_streams = streamable(x, ldx) && 2 * Np <= lin::kMaxLdIn;
     const GatedPlan plan = plan_gated(M, N, K);
@@ -623,7 +624,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     px.ldr = 2 * Np;
     px.c[0] = wg;
     px.c[1] = wu;
-    px.ldc[0] = px.ldc[1] = ldwg;
+    px.ldc = ldwg;
     px.y[0] = dx;
     px.ldy[0] = lddx;
     px.R = (int)(low ? 2 * lin::kLowRow : M);
@@ -637,7 +638,7 @@ int32_t run_gated_backward(int elem, const uint16_t* dh, int64_t lddh, const uin
     pw.ldr = 2 * Np;
     pw.rgroup = Np;
     pw.c[0] = x;
-    pw.ldc[0] = ldx;
+    pw.ldc = ldx;
     pw.y[0] = dwg;
     pw.y[1] = dwu;
     pw.ldy[0] = lddwg;
