@@ -417,17 +417,17 @@ int32_t linear_bf16_gated(const uint16_t* x, int64_t ldx,
  *
  * dg and du are rounded to E because they are the matrix unit's operands (up to 32
  * rows they are kept as two words, so that only the outputs' own rounding is left).
- * In bfloat16 c is 1.  In binary16 c is the power of two that brings the largest finite
- * |dg| or |du| of the call to 2^14 .. 2^15, and the products' FP32 sums are divided by
- * it: whatever the gradients' size, none overflows, and those down to 2^-28 of the
- * largest keep the type's relative precision (smaller ones are off by up to 2^-39 of the
- * largest).  dx may be NULL (not
- * wanted; the weights are then not read), and dwg and dwu may both be NULL (x is
- * then not read); one of the two groups must be given, unless M or N is 0.
- * N == 0 gives dx = +0, M == 0 gives dwg = dwu = +0.  N is at most
- * 2^30 - 64 (dg and du share rows).
- * Fast path of dx: both weights with one row stride (16-byte aligned, as everywhere);
- * weights of two strides run the slower element-wise loader.
+ * In bfloat16 c is 1.  In binary16 c is the power of two that brings the largest
+ * finite |dg| or |du| of the call to 2^14 .. 2^15, and the products' FP32 sums are
+ * divided by it: whatever the gradients' size none overflows, and those down to 2^-28
+ * of the largest keep the type's relative precision (smaller ones are off by up to
+ * 2^-39 of the largest).
+ *
+ * dx may be NULL (not wanted; the weights are then not read), and dwg and dwu may both
+ * be NULL (x is then not read); one of the two groups must be given, unless M or N is
+ * 0.  N == 0 gives dx = +0, M == 0 gives dwg = dwu = +0.  N is at most 2^30 - 64 (dg and
+ * du share rows).  Fast path of dx: both weights with one row stride (16-byte aligned,
+ * as everywhere); weights of two strides run the slower element-wise loader.
  *
  * workspace: linear_gated_workspace_bytes(M, N, K) bytes of device memory (it
  * holds dg and du, partial sums, and copies of operands of odd widths), 16-byte
@@ -517,9 +517,11 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
  *     linear_grad_norm:  norm[0] = FP32( sqrt( sum over all tensors and elements of g^2 ) )
  *     linear_grad_clip:  out = RNE( g * s ),  s = min(1, max_norm / (norm[0] + 1e-6)) in FP32
  *
- * Squares are taken and summed in FP64 in a fixed order, so no finite gradient
- * overflows and reruns are bit-identical.  A NaN norm makes every output NaN; an
- * infinite one (an infinite gradient) makes s zero.  The two calls are apart so
+ * Squares are taken and summed in FP64 in a fixed order, so the sum of finite
+ * gradients does not overflow and reruns are bit-identical; the norm itself does where
+ * it passes FLT_MAX.  A NaN norm makes every output NaN; an infinite one (an infinite
+ * gradient, or finite ones past FLT_MAX together) makes s zero, so finite gradients
+ * zero and infinite ones NaN, or, with an infinite max_norm, every output NaN.  The two calls are apart so
  * that a sharded caller can combine norms in between.
  *
  * Tensors are [rows, cols] with row stride ld (elements; a vector is one row, whose

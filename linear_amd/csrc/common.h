@@ -291,7 +291,7 @@ __device__ inline u32x4 finite_words(u32x4 v) {
 
 // 8 consecutive words src[0..7] of a row, the valid ones only (col + e < N,
 // row valid): a 16-byte load, of any alignment, where all are.  store8 likewise (15 x 6879
-// x 2405 dw, rows of odd length: 2-byte stores took 35 us, these 19).
+// x 2405 dw, rows of odd length: 2-byte stores took 35 us, these 19 on the same box).
 __device__ inline u32x4 load8(const uint16_t* src, bool row_ok, int col, int N) {
     u32x4 r = (u32x4){0u, 0u, 0u, 0u};
     if (row_ok && col + 7 < N) {

@@ -120,8 +120,8 @@ lin::ProductArgs product(const uint16_t* a, int64_t lda, const uint16_t* b, int6
 
 bool al16(const void* p, int64_t ld) { return (uintptr_t)p % 16 == 0 && ld % 8 == 0; }
 
-// The time of a streaming launch in microseconds, from measurements on a whole MI355X
-// at 12 to 64 slices: rounds of tiles over the CUs (the small tiles run several per
+// The time of a streaming launch in microseconds, from measurements on a whole MI355X:
+// rounds of tiles over the CUs (the small tiles run several per
 // CU), each a start and end plus a time per slice of 64.
 struct TileTime {
     double fixed, slice;
@@ -132,7 +132,7 @@ double rounds_time(const TileTime& t, int64_t tiles, int64_t slices, int cus) {
     return (double)tiles_of(tiles, (int64_t)cus * t.per_cu) * (t.fixed + t.slice * (double)slices);
 }
 
-// kGatedConfigs' times.  The 32-row tile with 16 columns of each weight serves few
+// kGatedConfigs' times, at 12 to 64 slices.  The 32-row tile with 16 columns of each weight serves few
 // rows (its many small workgroups keep the weights' read at the memory's rate: 16 x
 // 4000 x 4096 in 14 us, 21 with the 64-row tile).
 constexpr TileTime kGatedTimes[lin::kNumGatedConfigs] = {{6.5, 1.60, 1}, {5.3, 0.80, 1}, {4.9, 0.50, 1}, {2.0, 0.42, 2},
@@ -163,8 +163,8 @@ int32_t check_workspace(const void* ws, int64_t have, int64_t need) {
 }
 
 // Operands whose width is not a multiple of 8 are copied into padded rows in the
-// workspace, behind the partial sums (4099 x 4099 x 4099 bf16 dx: 1016 us read in place
-// element by element).
+// workspace, behind the partial sums (4099 x 4099 x 4099 bf16 dx: 167 us; 4096 x 4096 x
+// 4096 off 16-byte alignment, which is read in place: 292).
 int64_t round8(int64_t n) { return (n + 7) / 8 * 8; }
 int64_t round256(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 bool pack_ok(int64_t rows, int64_t cols) { return rows == 0 || round8(cols) <= kMaxElems / 16 / rows; }
@@ -508,15 +508,16 @@ int64_t gated_half(int64_t N) { return (N + 63) / 64 * 64; }
 
 // Up to 32 rows leave half of a 64-row tile, and half of a slice of 64 rows, empty: there
 // dg and du are two words each, the second in the empty half, and their rounding costs the
-// outputs nothing (16 x 2720 x 1024: 21.4 us, 20.7 with one word).  With more rows it would
-// double the products; the outputs' errors are then 1.4 times one rounding's.
+// outputs nothing (whole backward of 16 x 14336 x 4096 bf16 146 us, 141 with one word).  With
+// more rows it would double the products; the outputs' errors are then 1.4 times one rounding's.
 bool low_words(int64_t M) { return M > 0 && M <= lin::kLowRow; }
 int64_t gated_rows(int64_t M) { return low_words(M) ? 2 * lin::kLowRow : M; }
 
 // The plans of the gated block's dx and of dWg, dWu.  pair: both run in one launch, where
 // their tiles together, spread over the CUs, take less than two launches.  Whole backward,
-// with and without: 517 x 2720 x 1024 36.8 us, 43.5; 1000 x 1928 x 1296 45.5, 60.1; 2000 x
-// 4096 x 1024 94, 112; 1000 x 11008 x 4096 is large enough for two.  The plans depend on
+// with and without, bf16: 517 x 2720 x 1024 34.1 us, 41.1; 1000 x 1928 x 1296 42.0, 56.9; 2000
+// x 4096 x 1024 89, 106 (f16 40.5, 47.3; 49.0, 63.5; 108, 124); 1000 x 11008 x 4096 is large
+// enough for two.  The plans depend on
 // the sizes alone, so either gradient has the same words with and without the other.
 struct GatedPlan {
     StreamPlan dx, dw;
