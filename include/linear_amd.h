@@ -474,6 +474,9 @@ int32_t linear_bf16_gated_backward(const uint16_t* dh, int64_t lddh,
  * and db (floats), or with accumulate != 0 add them to what dw and db hold
  * (gradients summed over several batches).  N == 0 gives dx = +0; M == 0 gives
  * dw = db = +0 (or leaves them, when accumulating).  Reruns are bit-identical.
+ * The matrix unit aligns a product by its words' exponents, and a binary16 subnormal's
+ * is that of 2^-14: sums of products with subnormal words are as precise as if those
+ * words' magnitude were 2^-14, which only the _f32out forms can show.
  *
  * workspace: linear_backward_workspace_bytes(M, N, K) bytes of device memory for
  * any of these calls, 16-byte aligned; ownership and overlaps as for the gated
