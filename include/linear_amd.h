@@ -515,6 +515,99 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
                                            void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * The softmax cross entropy of a linear head, without the logits in memory:
+ *
+ *     z[m, n] = sum_k x[m, k] * weight[n, k] (+ b[n])          FP32, not rounded
+ *     lse[m]  = log( sum_n exp(z[m, n]) )
+ *     loss[m] = lse[m] - z[m, target[m]]
+ *
+ * N is the vocabulary.  A row whose target lies outside [0, N) does not count: its loss is
+ * 0 (its lse is that of its logits all the same).  loss and lse are [M] floats; either may
+ * be NULL.  target: [M] device int64.  b: [N] or NULL; an entry of -inf takes its column
+ * out.  A row of -inf logits has lse -inf, one with +inf (and no NaN) lse +inf.  N == 0
+ * gives lse -inf; K == 0 gives z = b.  FP32 inside; reruns are bit-identical.
+ *
+ * Limits: M up to LINEAR_CROSS_ENTROPY_MAX_M, K up to LINEAR_CROSS_ENTROPY_MAX_K, N as for
+ * the gated block.  Every layout runs the streaming kernels: operands off 16-byte alignment,
+ * or of rows whose length or stride is not a multiple of 8, are copied into the workspace,
+ * the weight a piece at a time.
+ *
+ * workspace: linear_cross_entropy_workspace_bytes(M, N, K) bytes of device memory, 16-byte
+ * aligned; ownership and overlaps as for the gated block's.
+ */
+#define LINEAR_CROSS_ENTROPY_MAX_M (1 << 24)
+#define LINEAR_CROSS_ENTROPY_MAX_K ((1 << 22) - 8)
+int64_t linear_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int32_t linear_f16_cross_entropy(const uint16_t* x, int64_t ldx,
+                                 const uint16_t* weight, int64_t ldw,
+                                 const uint16_t* b, const int64_t* target,
+                                 float* loss, float* lse,
+                                 int64_t M, int64_t N, int64_t K,
+                                 void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_cross_entropy(const uint16_t* x, int64_t ldx,
+                                  const uint16_t* weight, int64_t ldw,
+                                  const uint16_t* b, const int64_t* target,
+                                  float* loss, float* lse,
+                                  int64_t M, int64_t N, int64_t K,
+                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Its gradients, from dloss [M] and, where lse itself is penalised, dlse [M] (or NULL):
+ *
+ *     dz[m, n] = RNE_E( c * ((d + dlse[m]) * exp(z[m, n] - lse[m]) - d * (n == target[m])) ) / c
+ *     with d = dloss[m], or 0 for a row that does not count
+ *     dx[m, k] = RNE_E( sum_n dz[m, n] * weight[n, k] )
+ *     dw[n, k] = RNE_E( sum_m dz[m, n] * x[m, k] )         db[n] = RNE_E( sum_m dz[m, n] )
+ *
+ * lse is the forward call's.  The logits are formed again, a piece of the vocabulary at a
+ * time; dz of a piece is kept in the workspace as the two products' operand, dx's sums over
+ * the pieces in FP32.  c is 1 in bfloat16; in binary16 it is the power of two that brings
+ * the rows' largest |d + dlse| + |d| to 2^14 .. 2^15, so that neither large nor small dloss
+ * loses precision (the outputs themselves have the type's range: scale dloss, as usual in
+ * binary16).  dz of a row with d = 0 and dlse = 0 is zero whatever its logits are; its x
+ * still meets those zeros in dw (NaN or infinite x there gives NaN).
+ *
+ * dx, dw and db may each be NULL (not wanted), not all three unless they are empty.  N == 0
+ * gives dx = +0, M == 0 gives dw = db = +0.  The _f32out forms store dw and db as floats
+ * (unrounded sums), or with accumulate != 0 add them to what dw and db hold.
+ *
+ * workspace: linear_cross_entropy_backward_workspace_bytes(M, N, K) bytes, as above.
+ */
+int64_t linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int32_t linear_f16_cross_entropy_backward(const float* dloss, const float* dlse,
+                                          const uint16_t* x, int64_t ldx,
+                                          const uint16_t* weight, int64_t ldw,
+                                          const uint16_t* b, const int64_t* target, const float* lse,
+                                          uint16_t* dx, int64_t lddx,
+                                          uint16_t* dw, int64_t lddw, uint16_t* db,
+                                          int64_t M, int64_t N, int64_t K,
+                                          void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_cross_entropy_backward(const float* dloss, const float* dlse,
+                                           const uint16_t* x, int64_t ldx,
+                                           const uint16_t* weight, int64_t ldw,
+                                           const uint16_t* b, const int64_t* target, const float* lse,
+                                           uint16_t* dx, int64_t lddx,
+                                           uint16_t* dw, int64_t lddw, uint16_t* db,
+                                           int64_t M, int64_t N, int64_t K,
+                                           void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_f16_cross_entropy_backward_f32out(const float* dloss, const float* dlse,
+                                                 const uint16_t* x, int64_t ldx,
+                                                 const uint16_t* weight, int64_t ldw,
+                                                 const uint16_t* b, const int64_t* target, const float* lse,
+                                                 uint16_t* dx, int64_t lddx,
+                                                 float* dw, int64_t lddw, float* db, int32_t accumulate,
+                                                 int64_t M, int64_t N, int64_t K,
+                                                 void* workspace, int64_t workspace_bytes, void* stream);
+int32_t linear_bf16_cross_entropy_backward_f32out(const float* dloss, const float* dlse,
+                                                  const uint16_t* x, int64_t ldx,
+                                                  const uint16_t* weight, int64_t ldw,
+                                                  const uint16_t* b, const int64_t* target, const float* lse,
+                                                  uint16_t* dx, int64_t lddx,
+                                                  float* dw, int64_t lddw, float* db, int32_t accumulate,
+                                                  int64_t M, int64_t N, int64_t K,
+                                                  void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * The global norm of a set of gradients, and clipping by it.
  *
  *     linear_grad_norm:  norm[0] = FP32( sqrt( sum over all tensors and elements of g^2 ) )

@@ -66,6 +66,10 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_f16_backward_input", "linear_bf16_backward_input",
                 "linear_f16_backward_weight", "linear_bf16_backward_weight",
                 "linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out",
+                "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes",
+                "linear_f16_cross_entropy", "linear_bf16_cross_entropy",
+                "linear_f16_cross_entropy_backward", "linear_bf16_cross_entropy_backward",
+                "linear_f16_cross_entropy_backward_f32out", "linear_bf16_cross_entropy_backward_f32out",
                 "linear_grad_workspace_bytes", "linear_grad_norm", "linear_grad_clip",
                 "linear_f16_plan", "linear_gated_backward_plan", "linear_status_string", "linear_last_hip_error")
 
@@ -167,7 +171,17 @@ def _lib():
     for name in ("linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out"):
         getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, i64, i64, i64, vp, i64, vp]
         getattr(lib, name).restype = i32
-    for name in ("linear_gated_forward_workspace_bytes", "linear_gated_workspace_bytes", "linear_backward_workspace_bytes"):
+    for name in ("linear_f16_cross_entropy", "linear_bf16_cross_entropy"):
+        getattr(lib, name).argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64, vp, i64, vp]
+        getattr(lib, name).restype = i32
+    for name in ("linear_f16_cross_entropy_backward", "linear_bf16_cross_entropy_backward"):
+        getattr(lib, name).argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, vp, i64, vp]
+        getattr(lib, name).restype = i32
+        getattr(lib, name + "_f32out").argtypes = [vp, vp, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, i32, i64, i64,
+                                                   i64, vp, i64, vp]
+        getattr(lib, name + "_f32out").restype = i32
+    for name in ("linear_gated_forward_workspace_bytes", "linear_gated_workspace_bytes", "linear_backward_workspace_bytes",
+                 "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = i64
     lib.linear_grad_workspace_bytes.argtypes = [i64]
@@ -785,6 +799,148 @@ def linear_bf16_backward_weight_f32out(dy: torch.Tensor, x: torch.Tensor, bias: 
                                        out=None, db=None, workspace=None, stream=None):
     """linear_f16_backward_weight_f32out on bfloat16 operands."""
     return _backward_weight_call("bf16", torch.bfloat16, True, dy, x, bias, accumulate, out, db, workspace, stream)
+
+
+_CROSS_ENTROPY = {t: "linear_%s_cross_entropy" % t for t in ("f16", "bf16")}
+_CROSS_ENTROPY_BACKWARD = {(t, f): "linear_%s_cross_entropy_backward%s" % (t, "_f32out" if f else "")
+                           for t in ("f16", "bf16") for f in (False, True)}
+
+
+@functools.lru_cache(maxsize=256)
+def cross_entropy_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of device workspace a cross entropy call needs."""
+    n = _lib().linear_cross_entropy_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
+    return n
+
+
+@functools.lru_cache(maxsize=256)
+def cross_entropy_backward_workspace_bytes(M: int, N: int, K: int) -> int:
+    """Bytes of device workspace a cross entropy backward call needs."""
+    n = _lib().linear_cross_entropy_backward_workspace_bytes(M, N, K)
+    if n < 0:
+        raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
+    return n
+
+
+def _vector(t, name, dtype, n):
+    """Pointer of a contiguous vector of n values (None: a null pointer)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous %s tensor of %d values" % (name, dtype, n))
+    return t.data_ptr()
+
+
+def _cross_entropy_call(tag, dtype, x, weight, target, b, loss, lse, workspace, stream):
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be [M, K] and weight [N, K]")
+    M, K = x.shape
+    N = weight.shape[0]
+    xp, ldx = _mat(x, "x", dtype)
+    wp, ldw = _operand(weight, "weight", dtype, (N, K))
+    tp = _vector(target, "target", torch.int64, M)
+    bp = _vector(b, "b", dtype, N)
+    handle = _launch_stream(stream, x, weight, target, b, loss, lse, workspace)
+    with _on(stream, x.device):
+        if loss is None:
+            loss = torch.empty(M, dtype=torch.float32, device=x.device)
+        if lse is None:
+            lse = torch.empty(M, dtype=torch.float32, device=x.device)
+        workspace, wsp, wsn = _scratch(workspace, cross_entropy_workspace_bytes(M, N, K), x.device)
+    name = _CROSS_ENTROPY[tag]
+    rc = _entry(name)(xp, ldx, wp, ldw, bp, tp, _vector(loss, "loss", torch.float32, M), _vector(lse, "lse", torch.float32, M),
+                      M, N, K, wsp, wsn, handle)
+    _check(rc, name)
+    return loss, lse
+
+
+def linear_f16_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, b=None, loss=None, lse=None,
+                             workspace=None, stream=None):
+    """(loss, lse) of the head x @ weight.T (+ b) (x [M, K], weight [N, K], b [N], float16; target int64 [M]):
+    lse = log sum exp of a row's logits, loss = lse - the target's logit, float32 [M]; a target outside [0, N)
+    (-100, say) gives loss 0.  The logits are never stored.  loss, lse: tensors to write.  workspace: a uint8
+    device tensor of at least cross_entropy_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    return _cross_entropy_call("f16", torch.float16, x, weight, target, b, loss, lse, workspace, stream)
+
+
+def linear_bf16_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor, b=None, loss=None, lse=None,
+                              workspace=None, stream=None):
+    """linear_f16_cross_entropy on bfloat16 operands."""
+    return _cross_entropy_call("bf16", torch.bfloat16, x, weight, target, b, loss, lse, workspace, stream)
+
+
+def _cross_entropy_backward_call(tag, dtype, f32, dloss, x, weight, target, lse, b, dlse, need_dx, need_dw, bias, accumulate,
+                                 dx, dw, db, workspace, stream):
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x must be [M, K] and weight [N, K]")
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    bias = db is not None or (need_dw and b is not None if bias is None else bias)
+    if not (need_dx or need_dw or bias):
+        raise ValueError("nothing to compute: no gradient is wanted")
+    if accumulate and ((need_dw and dw is None) or (bias and db is None)):
+        raise ValueError("accumulate adds to tensors that are there: give dw (and db)")
+    M, K = x.shape
+    N = weight.shape[0]
+    xp, ldx = _mat(x, "x", dtype)
+    wp, ldw = _operand(weight, "weight", dtype, (N, K))
+    vectors = [_vector(t, n, torch.float32, M) for t, n in ((dloss, "dloss"), (dlse, "dlse"), (lse, "lse"))]
+    tp = _vector(target, "target", torch.int64, M)
+    bp = _vector(b, "b", dtype, N)
+    handle = _launch_stream(stream, dloss, dlse, x, weight, target, lse, b, dx, dw, db, workspace)
+    none = (None, None, 0)
+    odt = torch.float32 if f32 else dtype
+    with _on(stream, x.device):
+        dx, *dxa = _output(dx, "dx", dtype, (M, K), x) if need_dx else none
+        dw, *dwa = _output(dw, "dw", odt, (N, K), x) if need_dw else none
+        if bias and db is None:
+            db = torch.empty(N, dtype=odt, device=x.device)
+        workspace, wsp, wsn = _scratch(workspace, cross_entropy_backward_workspace_bytes(M, N, K), x.device)
+    name = _CROSS_ENTROPY_BACKWARD[tag, f32]
+    flag = (int(bool(accumulate)),) if f32 else ()
+    rc = _entry(name)(vectors[0], vectors[1], xp, ldx, wp, ldw, bp, tp, vectors[2], *dxa, *dwa,
+                      _vector(db, "db", odt, N) if bias else None, *flag, M, N, K, wsp, wsn, handle)
+    _check(rc, name)
+    return dx, dw, (db if bias else None)
+
+
+def linear_f16_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                                      lse: torch.Tensor, b=None, dlse=None, need_dx: bool = True, need_dw: bool = True,
+                                      bias=None, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """(dx [M, K], dw [N, K], db [N]) of linear_f16_cross_entropy from dloss and, where lse enters the objective
+    too, dlse (float32 [M]); lse is the forward call's.  Those not wanted are None; db is wanted with b and dw
+    unless bias says otherwise.  workspace: a uint8 device tensor of at least
+    cross_entropy_backward_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    return _cross_entropy_backward_call("f16", torch.float16, False, dloss, x, weight, target, lse, b, dlse, need_dx, need_dw,
+                                        bias, False, dx, dw, db, workspace, stream)
+
+
+def linear_bf16_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                                       lse: torch.Tensor, b=None, dlse=None, need_dx: bool = True, need_dw: bool = True,
+                                       bias=None, dx=None, dw=None, db=None, workspace=None, stream=None):
+    """linear_f16_cross_entropy_backward on bfloat16 operands and outputs."""
+    return _cross_entropy_backward_call("bf16", torch.bfloat16, False, dloss, x, weight, target, lse, b, dlse, need_dx,
+                                        need_dw, bias, False, dx, dw, db, workspace, stream)
+
+
+def linear_f16_cross_entropy_backward_f32out(dloss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, target: torch.Tensor,
+                                             lse: torch.Tensor, b=None, dlse=None, need_dx: bool = True, need_dw: bool = True,
+                                             bias=None, accumulate: bool = False, dx=None, dw=None, db=None, workspace=None,
+                                             stream=None):
+    """linear_f16_cross_entropy_backward with dw and db as unrounded FP32 sums; accumulate: added to what dw (and
+    db) hold."""
+    return _cross_entropy_backward_call("f16", torch.float16, True, dloss, x, weight, target, lse, b, dlse, need_dx, need_dw,
+                                        bias, accumulate, dx, dw, db, workspace, stream)
+
+
+def linear_bf16_cross_entropy_backward_f32out(dloss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
+                                              target: torch.Tensor, lse: torch.Tensor, b=None, dlse=None,
+                                              need_dx: bool = True, need_dw: bool = True, bias=None, accumulate: bool = False,
+                                              dx=None, dw=None, db=None, workspace=None, stream=None):
+    """linear_f16_cross_entropy_backward_f32out on bfloat16 operands."""
+    return _cross_entropy_backward_call("bf16", torch.bfloat16, True, dloss, x, weight, target, lse, b, dlse, need_dx,
+                                        need_dw, bias, accumulate, dx, dw, db, workspace, stream)
 
 
 # linear_tensor.type (include/linear_amd.h, LINEAR_TYPE_*)

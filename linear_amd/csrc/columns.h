@@ -7,6 +7,7 @@ namespace lin {
 
 template <int E>
 __device__ inline void store_sum(const ColumnSumArgs& c, int n, float sum) {
+    if (c.unscale) sum *= *c.unscale;
     if (c.f32) {
         float* y = (float*)c.db + n;
         *y = c.accumulate ? *y + sum : sum;

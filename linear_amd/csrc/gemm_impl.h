@@ -398,6 +398,14 @@ __device__ __forceinline__ void finish_gated(const LinearArgs& a, unsigned char*
     });
 }
 
+// The ends of the cross entropy's tiles (loss_impl.h).
+template <int BM, int BN, int WM, int WN, int E, int R, typename Args, typename AccT>
+__device__ __forceinline__ void finish_lse(const Args& a, unsigned char* smem, AccT (&acc)[BN / WN / R][BM / WM / R],
+                                           int m0, int n0, int tn, int wave, int lane);
+template <int BM, int BN, int WM, int WN, int RINGB, int E, int R, typename Args, typename AccT>
+__device__ __forceinline__ void finish_dz(const Args& a, unsigned char* smem, AccT (&acc)[BN / WN / R][BM / WM / R],
+                                          int m0, int n0, int wave, int lane);
+
 // Tile (tm, tn) of this workgroup, with its group entered.  One group: the XCD
 // walk of tile_coords over blockIdx.x.  Several groups (grid z): the groups' row
 // tiles are stacked into one column of G x tiles_m row tiles and walked as one
@@ -453,9 +461,9 @@ __device__ inline void stream_tile(LinearArgs& a, int& tm, int& tn) {
 // the wait for slice t choosing at run time how many later slices may still be
 // in flight (no zero-fill requests past K).
 template <int BM, int BN, int WM, int WN, int STAGES, int BK, int E, int MODE, int SPREAD = 1, bool WHOLE = false,
-          bool M16 = false>
+          bool M16 = false, typename Args = LinearArgs>
 __global__ void __launch_bounds__(WM * WN * 64)
-gemm_stream(LinearArgs a) {
+gemm_stream(Args a) {
     constexpr int R = M16 ? 16 : 32;                  // MFMA block rows and columns
     constexpr int KSTEP = M16 ? 32 : 16;              // k values per MFMA
     constexpr int KS = BK / KSTEP;                    // MFMA K steps per slice
@@ -740,6 +748,10 @@ gemm_stream(LinearArgs a) {
     }
     if constexpr (GATED)
         finish_gated<BM, BN, WM, WN, E, R>(a, smem, acc, m0, n0, wave, lane);
+    else if constexpr (MODE == kOutLse)
+        finish_lse<BM, BN, WM, WN, E, R>(a, smem, acc, m0, n0, tn, wave, lane);
+    else if constexpr (MODE == kOutDz)
+        finish_dz<BM, BN, WM, WN, STAGES * SLICE, E, R>(a, smem, acc, m0, n0, wave, lane);
     else
         finish_tile<BM, BN, WM, WN, STAGES * SLICE, E, MODE, R>(a, smem, acc, m0, n0, wave, lane,
                                                                MODE == kOutBias ? &bias8 : nullptr);

@@ -124,7 +124,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
     float back = 1.f;                                 // (read here: its latency passes under the loop)
-    if constexpr (E == kF16 && MODE != kOutF32Add) {
+    if constexpr (E == kF16) {
         if (a.unscale) back = *a.unscale;
     }
 
@@ -358,7 +358,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         }
     }
 
-    if constexpr (E == kF16 && MODE != kOutF32Add) {
+    if constexpr (E == kF16) {
         if (a.unscale) {                              // uniform
 #pragma unroll
             for (int i = 0; i < FN; ++i)
@@ -444,8 +444,8 @@ static hipError_t launch_product(const void* fn, const StreamProduct& a, int thr
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>
 static const void* grad_fn(bool rowt, int mode) {
     if (!rowt) {
-        if constexpr (BM < 256 && STAGES > 2)         // partial sums (the tiles that split contractions take)
-            if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
+        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
+        if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32Add>;
         return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
     }
     if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;

@@ -1,0 +1,61 @@
+// loss.h -- launch interface of the linear head's cross entropy.
+#pragma once
+
+#include "common.h"
+#include "kernels.h"
+
+namespace lin {
+
+// The statistics of one row over one column tile: sum of exp(z - ref), with ref the
+// largest z of the tile (clamped to the finite range).
+struct RowPart {
+    float ref, sum;
+};
+
+// A launch over the columns [col0, col0 + N) of the vocabulary; w and b begin at col0.
+struct LossArgs : LinearArgs {
+    const int64_t* target;   // [M]
+    int64_t col0, cols;      // this launch's first column; the vocabulary
+    // kOutLse
+    RowPart* parts;          // [M, ldparts]: tile tn's statistics of row m at m * ldparts + tn
+    int64_t ldparts;
+    float* at_target;        // [M]: z at the target, where that is one of this launch's columns
+    // kOutDz: y is dz, 16-bit words; columns from N to the next multiple of 8 are zeroed
+    const float *lse, *dloss, *dlse;   // [M]; dlse may be null
+    const float* scale;      // not null: dz is multiplied by *scale before its rounding
+};
+
+constexpr int kNumLossConfigs = 5;
+inline constexpr GemmConfig kLossConfigs[kNumLossConfigs] = {
+    {256, 256, 2, 4, 2, 64},
+    {256, 128, 4, 2, 3, 64},
+    {128, 128, 2, 2, 4, 64},
+    {64, 64, 2, 2, 4, 64},
+    {32, 32, 2, 1, 6, 64},
+};
+// mode kOutLse or kOutDz; a.tiles_m and a.tiles_n match the configuration.
+template <int E> hipError_t launch_loss_stream_t(int cfg, int mode, const LossArgs& a, hipStream_t stream);
+extern template hipError_t launch_loss_stream_t<kF16>(int, int, const LossArgs&, hipStream_t);
+extern template hipError_t launch_loss_stream_t<kBF16>(int, int, const LossArgs&, hipStream_t);
+inline hipError_t launch_loss_stream(int elem, int cfg, int mode, const LossArgs& a, hipStream_t stream) {
+    return elem == kBF16 ? launch_loss_stream_t<kBF16>(cfg, mode, a, stream) : launch_loss_stream_t<kF16>(cfg, mode, a, stream);
+}
+
+// lse and loss [M] (either may be null) from the tiles' statistics.
+struct LossJoinArgs {
+    const RowPart* parts;
+    int64_t ldparts;
+    int64_t count;           // statistics per row
+    const float* at_target;
+    const int64_t* target;
+    int64_t cols;
+    float *lse, *loss;
+};
+hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream);
+
+// head[0], head[1]: the power of two that brings the largest finite |dloss + dlse| + |dloss|
+// of the rows to 2^14 .. 2^15, as its inverse and itself.
+hipError_t launch_loss_scale(const int64_t* target, int64_t cols, const float* dloss, const float* dlse, int64_t M,
+                             float* head, hipStream_t stream);
+
+}  // namespace lin

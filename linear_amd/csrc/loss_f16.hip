@@ -1,0 +1,8 @@
+// The cross entropy's streaming kernels for binary16 words.
+#include "loss_impl.h"
+
+namespace lin {
+
+template hipError_t launch_loss_stream_t<kF16>(int cfg, int mode, const LossArgs& a, hipStream_t stream);
+
+}  // namespace lin

@@ -268,6 +268,7 @@ __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
 #pragma unroll
         for (int j = 0; j < 3; ++j)
             if (s + j < a.splits) v += w[j];
+        if (a.sum_unscale) v *= *a.sum_unscale;
         const int g = gr >= a.R ? 1 : 0;
         const int64_t at = (gr - (int64_t)g * a.R) * a.ldy[g] + c;
         const bool whole = c + 3 < a.C;                  // stored at any alignment

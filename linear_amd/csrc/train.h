@@ -52,6 +52,7 @@ struct ColumnSumArgs {
     void* db;                // 16-bit words or floats
     int M, N, splits;
     int f32, accumulate;
+    const float* unscale;    // not null: the sums are multiplied by *unscale
 };
 // Splits of the rows: enough workgroups of 64 columns for every CU, of 2048 rows at
 // least; one where the columns alone give half the chip work (a second launch costs
@@ -94,6 +95,7 @@ struct StreamProduct {
     float* partial;
     int64_t ldp;
     int accumulate;          // launch_split_sum into floats: y += sum
+    const float* sum_unscale;   // launch_split_sum, not null: the totals are multiplied by *sum_unscale
     // the last sum_blocks workgroups take 64 columns of db each instead of a tile
     // (small tiles of dw, one split)
     int sum_blocks;
@@ -112,7 +114,7 @@ inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {64, 64, 2, 2, 2, 4},
     {128, 128, 2, 4, 1, 2},
 };
-// rowt: contraction-major row operand; mode kOutRound, kOutF32, or with rowt kOutF32Add.
+// rowt: contraction-major row operand; mode kOutRound, kOutF32 or kOutF32Add.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);

@@ -1,0 +1,308 @@
+"""A linear head's cross entropy and its gradients on the GPU against 64-bit forms."""
+import pytest
+import torch
+
+import linear_amd as la
+import loss_refs as ref
+from train_refs import inside
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = [torch.float16, torch.bfloat16]
+IDS = ["f16", "bf16"]
+
+# one row and few, one column, odd sizes, tile edges, rows past each tile, rows copied for their odd length
+SHAPES = [(1, 1, 1), (1, 7, 64), (1, 8200, 4096), (2, 33, 65), (5, 129, 192), (16, 256, 128), (20, 4099, 520), (33, 1000, 72),
+          (64, 64, 64), (65, 127, 130), (130, 515, 93), (257, 264, 1032), (300, 1000, 768), (517, 2049, 264),
+          (1024, 1024, 768), (2100, 1032, 520), (4100, 264, 72), (3, 70000, 8), (4100, 8200, 40)]
+
+
+def fn(name, t):
+    return getattr(la, "linear_%s_cross_entropy%s" % ("bf16" if t == torch.bfloat16 else "f16", name))
+
+
+def make(M, N, K, t, seed=0, bias=True, scale=2.0):
+    gen = torch.Generator().manual_seed(seed + M + 3 * N + 7 * K)
+    x = torch.randn(M, K, generator=gen)
+    w = torch.randn(N, K, generator=gen) * scale * K ** -0.5
+    b = torch.randn(N, generator=gen)
+    target = torch.randint(0, max(N, 1), (M,), generator=gen)
+    if M > 2:
+        target[torch.rand(M, generator=gen) < 0.2] = -100
+        target[1] = N                                 # just outside
+    dloss, dlse = torch.randn(M, generator=gen) * 0.1, torch.randn(M, generator=gen) * 0.01
+    return (x.to(t).to(DEV), w.to(t).to(DEV), target.to(DEV), b.to(t).to(DEV) if bias else None, dloss.to(DEV), dlse.to(DEV))
+
+
+def check_forward(x, w, target, b, t, **kw):
+    want, bound = ref.forward64(x, w, target, b)
+    loss, lse = fn("", t)(x, w, target, b, **kw)
+    inside(loss, want[0], bound[0], "loss")
+    inside(lse, want[1], bound[1], "lse")
+    return loss, lse
+
+
+def check_backward(dloss, dlse, x, w, target, lse, b, t, f32=False, **kw):
+    want, bound = ref.backward64(dloss, dlse, x, w, target, b, t, f32)
+    got = fn("_backward_f32out" if f32 else "_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, bias=True, **kw)
+    for g, v, e, n in zip(got, want, bound, ("dx", "dw", "db")):
+        inside(g, v, e, n)
+    return got
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("i", range(len(SHAPES)), ids=["%dx%dx%d" % s for s in SHAPES])
+def test_loss_and_gradients(i, t):
+    M, N, K = SHAPES[i]
+    x, w, target, b, dloss, dlse = make(M, N, K, t, bias=i % 2 == 0)
+    loss, lse = check_forward(x, w, target, b, t)
+    got = check_backward(dloss, dlse if i % 3 else None, x, w, target, lse, b, t)
+    again = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse if i % 3 else None, bias=True)
+    assert all(torch.equal(u, v) for u, v in zip(got, again)), "reruns give the same bits"
+    assert all(torch.equal(u, v) for u, v in zip((loss, lse), fn("", t)(x, w, target, b)))
+
+
+# the vocabulary in pieces: many rows, and rows that are copied
+PIECES = [(20000, 8300, 64), (40, 17000, 2049), (16400, 8210, 33)]
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", PIECES)
+def test_vocabulary_in_pieces(M, N, K, t):
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = check_forward(x, w, target, b, t)
+    check_backward(dloss, dlse, x, w, target, lse, b, t)
+    check_backward(dloss, None, x, w, target, lse, b, t, f32=True)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 70, 40), (30, 260, 264), (300, 777, 136)])
+def test_f32_gradients_and_accumulation(M, N, K, t):
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = fn("", t)(x, w, target, b)
+    first = check_backward(dloss, dlse, x, w, target, lse, b, t, f32=True)
+    dw, db = torch.full((N, K), 3.0, device=DEV), torch.full((N,), -2.0, device=DEV)
+    fn("_backward_f32out", t)(dloss, x, w, target, lse, b, dlse=dlse, accumulate=True, dw=dw, db=db, need_dx=False)
+    # one FP32 addition: half a step of the sum (and of a partial sum's, where the contraction is split)
+    for got, one, base in ((dw, first[1], 3.0), (db, first[2], -2.0)):
+        want = one.double() + base
+        assert bool(((got.double() - want).abs() <= 2.0 ** -23 * (want.abs() + 1)).all())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("wanted", ["dx", "dw", "db", "dx,db"])
+def test_gradients_that_are_not_wanted(wanted, t):
+    M, N, K = 70, 300, 72
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = fn("", t)(x, w, target, b)
+    every = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse)
+    some = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, need_dx="dx" in wanted, need_dw="dw" in wanted,
+                              bias="db" in wanted)
+    for n, a, c in zip(("dx", "dw", "db"), every, some):
+        assert (c is None) == (n not in wanted)
+        if c is not None:
+            assert torch.equal(a, c)
+
+
+def padded(v, pad, shift, fill):
+    """The matrix v with `pad` extra columns and a base `shift` words further on, in a sea of `fill`."""
+    flat = torch.full((v.shape[0] * (v.shape[1] + pad) + shift + 64,), fill, dtype=v.dtype, device=v.device)
+    out = flat[shift:].as_strided(v.shape, (v.shape[1] + pad, 1))
+    out.copy_(v)
+    return out, flat
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad,out_pad,shift", [(0, 8, 0), (8, 16, 8), (8, 3, 1), (3, 5, 0), (1, 0, 3)])
+@pytest.mark.parametrize("M,N,K", [(1, 72, 64), (40, 264, 136), (300, 513, 93)])
+def test_strides_bases_and_untouched_surroundings(M, N, K, pad, out_pad, shift, t):
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    xs, ws = (padded(v, pad, shift, float("nan"))[0] for v in (x, w))
+    bs = torch.cat([torch.full((3,), float("nan"), dtype=t, device=DEV), b])[3:]
+    vectors = [torch.full((M + 2,), 7.0, device=DEV) for _ in range(2)]
+    loss, lse = check_forward(xs, ws, target, bs, t, loss=vectors[0][1:-1], lse=vectors[1][1:-1])
+    assert all(float(v[0]) == 7.0 and float(v[-1]) == 7.0 for v in vectors)
+    dx, dw = padded(torch.zeros_like(x), out_pad, shift, 9.0), padded(torch.zeros_like(w), out_pad, shift, 9.0)
+    check_backward(dloss, dlse, xs, ws, target, lse, bs, t, dx=dx[0], dw=dw[0])
+    for v, flat in (dx, dw):
+        v.fill_(9.0)
+        assert bool((flat == 9.0).all()), "written outside"
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_rows_that_do_not_count(M, t):
+    """All rows outside the vocabulary: losses and gradients of zero (with dlse, lse's alone); a NaN
+    row that does not count has loss 0 and leaves the other rows' losses and dx alone."""
+    N, K = 270, 136
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    for outside in (-1, N, -100, 2 ** 40, -2 ** 62):
+        off = torch.full_like(target, outside)
+        loss, lse = check_forward(x, w, off, b, t)
+        assert bool((loss == 0).all())
+        for g in fn("_backward", t)(dloss, x, w, off, lse, b):
+            assert bool((g == 0).all())
+        check_backward(dloss, dlse, x, w, off, lse, b, t)
+    if M == 1:
+        return
+    target[M // 2] = -100
+    clean = fn("", t)(x, w, target, b)
+    x[M // 2, 3] = float("nan")
+    dirty = fn("", t)(x, w, target, b)
+    assert torch.equal(clean[0], dirty[0]) and bool(dirty[1][M // 2].isnan())
+    keep = torch.arange(M, device=DEV) != M // 2
+    assert torch.equal(clean[1][keep], dirty[1][keep])
+    dx = fn("_backward", t)(dloss, x, w, target, dirty[1], b, need_dw=False)[0]
+    assert bool((dx[M // 2] == 0).all()) and bool(dx.isfinite().all())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_masked_columns_and_empty_rows(M, t):
+    """A bias of -inf takes its columns out; with all taken out lse is -inf and the loss NaN; an
+    infinite logit gives an infinite lse."""
+    N, K = 517, 64
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    b[::3] = float("-inf")
+    target = target // 3 * 3 + 1
+    want, bound = ref.forward64(x, w, target, b)
+    loss, lse = fn("", t)(x, w, target, b)
+    inside(loss, want[0], bound[0], "loss")
+    inside(lse, want[1], bound[1], "lse")
+    dx, dw, db = fn("_backward", t)(dloss, x, w, target, lse, b)
+    assert bool((dw[::3] == 0).all()) and bool((db[::3] == 0).all()) and bool(dx.isfinite().all())
+    b.fill_(float("-inf"))
+    loss, lse = fn("", t)(x, w, target, b)
+    ok = ref.counted(target, N)
+    assert bool((lse == float("-inf")).all()) and bool(loss[ok].isnan().all()) and bool((loss[~ok] == 0).all())
+    b.zero_()
+    b[N - 1] = float("inf")
+    loss, lse = fn("", t)(x, w, target, b)
+    assert bool((lse == float("inf")).all())
+    ok &= target != N - 1
+    assert bool((loss[ok] == float("inf")).all())
+    # the type's lowest value masks like -inf once another column stays
+    b.zero_()
+    b[::3] = torch.finfo(t).min
+    loss, lse = check_forward(x, w, target, b, t)
+    assert bool(lse.isfinite().all())
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("scale", [1e-3, 30.0])
+def test_flat_and_peaked_rows(scale, t):
+    """Logits all alike, and rows decided by one logit (|z| in the hundreds)."""
+    M, N, K = 100, 1500, 256
+    x, w, target, b, dloss, dlse = make(M, N, K, t, scale=scale, bias=False)
+    _, lse = check_forward(x, w, target, None, t)
+    check_backward(dloss, dlse, x, w, target, lse, None, t)
+
+
+@pytest.mark.parametrize("size", [1e-12, 1e-7, 1.0, 1e3])
+def test_binary16_gradients_of_any_size(size):
+    """dz is scaled before its rounding: FP32 outputs keep their precision for weights of any size."""
+    M, N, K = 48, 700, 128
+    x, w, target, b, dloss, dlse = make(M, N, K, torch.float16)
+    _, lse = fn("", torch.float16)(x, w, target, b)
+    want, bound = ref.backward64(dloss * size, None, x, w, target, b, torch.float16, True)
+    got = fn("_backward_f32out", torch.float16)(dloss * size, x, w, target, lse, b)
+    for g, v, e in zip(got[1:], want[1:], bound[1:]):
+        inside(g, v, e, "size %g" % size)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_empty_sizes(t):
+    x, w, target, b, dloss, dlse = make(6, 9, 16, t)
+    # no rows
+    loss, lse = fn("", t)(x[:0], w, target[:0], b)
+    assert loss.shape == lse.shape == (0,)
+    dw, db = torch.full_like(w, 5.0), torch.full_like(b, 5.0)
+    fn("_backward", t)(dloss[:0], x[:0], w, target[:0], lse, b, dw=dw, db=db)
+    assert bool((dw == 0).all()) and bool((db == 0).all())
+    dw, db = torch.full((9, 16), 5.0, device=DEV), torch.full((9,), 5.0, device=DEV)
+    fn("_backward_f32out", t)(dloss[:0], x[:0], w, target[:0], lse, b, dw=dw, db=db, accumulate=True)
+    assert bool((dw == 5).all()) and bool((db == 5).all())
+    # no vocabulary
+    loss, lse = fn("", t)(x, w[:0], target, b[:0])
+    assert bool((loss == 0).all()) and bool((lse == float("-inf")).all())
+    dx, dw, db = fn("_backward", t)(dloss, x, w[:0], target, lse, b[:0])
+    assert bool((dx == 0).all()) and dw.shape == (0, 16) and db.shape == (0,)
+    # no width: the logits are the bias
+    check_forward(x[:, :0], w[:, :0], target, b, t)
+    _, lse = fn("", t)(x[:, :0], w[:, :0], target, b)
+    db = fn("_backward", t)(dloss, x[:, :0], w[:, :0], target, lse, b)[2]
+    want, bound = ref.backward64(dloss, None, x[:, :0], w[:, :0], target, b, t)
+    inside(db, want[2], bound[2], "db")
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(3, 500, 72), (300, 1030, 93)])
+def test_captured_calls_replayed(M, N, K, t):
+    """A loss and its gradients captured into one graph, replayed on other data with eager calls between."""
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    warm = fn("", t)(x, w, target, b)
+    fn("_backward", t)(dloss, x, w, target, warm[1], b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loss, lse = fn("", t)(x, w, target, b)
+        grads = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse)
+    for seed in range(3):
+        for old, new in zip((x, w, target, b, dloss, dlse), make(M, N, K, t, seed=seed * 100)):
+            old.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = fn("", t)(x, w, target, b)
+        want = fn("_backward", t)(dloss, x, w, target, eager[1], b, dlse=dlse)
+        assert torch.equal(loss, eager[0]) and torch.equal(lse, eager[1])
+        assert all(torch.equal(u, v) for u, v in zip(grads, want))
+
+
+def test_another_stream_and_a_given_workspace():
+    t = torch.bfloat16
+    x, w, target, b, dloss, dlse = make(130, 515, 93, t)
+    want = fn("", t)(x, w, target, b)
+    grads = fn("_backward", t)(dloss, x, w, target, want[1], b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(max(la.cross_entropy_workspace_bytes(130, 515, 93), la.cross_entropy_backward_workspace_bytes(130, 515, 93)),
+                     dtype=torch.uint8, device=DEV)
+    got = fn("", t)(x, w, target, b, workspace=ws, stream=side)
+    mine = fn("_backward", t)(dloss, x, w, target, got[1], b, workspace=ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(got, want)) and all(torch.equal(u, v) for u, v in zip(mine, grads))
+
+
+def test_a_weight_past_2_31_words():
+    """Rows of the weight more than 2^31 words on: the first and last columns decide their rows."""
+    t, M, N, K = torch.bfloat16, 40, 70000, 32768
+    if torch.cuda.mem_get_info()[0] < 30 << 30:
+        pytest.skip("needs 30 GB")
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    x = (torch.randn(M, K, generator=gen, device=DEV) * K ** -0.5).to(t)
+    w = torch.randn(N, K, generator=gen, device=DEV, dtype=t)
+    target = torch.randint(0, N, (M,), generator=gen, device=DEV)
+    target[0], target[1] = N - 1, 0
+    loss, lse = fn("", t)(x, w, target)
+    z = torch.cat([x.double() @ part.double().t() for part in w.split(5000)], 1)
+    want = torch.logsumexp(z, 1)
+    # |z| <= 1 by |x| |w| sums of some 200 in all: acc(K, 210) of train_refs
+    bound = (K / 16 + 48) * 2.0 ** -23 * 210
+    assert float((lse.double() - want).abs().max()) <= bound
+    assert float((loss.double() - (want - z.gather(1, target[:, None])[:, 0])).abs().max()) <= 2 * bound
+    dloss = torch.ones(M, device=DEV)
+    dx, dw, _ = fn("_backward", t)(dloss, x, w, target, lse)
+    dz = torch.exp(z - want[:, None])
+    dz[torch.arange(M, device=DEV), target] -= 1
+    for rows in (slice(0, 50), slice(N - 50, N)):
+        exact = dz[:, rows].t() @ x.double()
+        # the rounding of dz, of dw, and the sums': (1 + 2^-8)^2 - 1 of the products' magnitude and their FP32 sum
+        room = (2.0 ** -8 * 2.1 + 4 * bound) * (dz[:, rows].abs().t() @ x.double().abs()) + 1e-30
+        assert bool(((dw[rows].double() - exact).abs() <= room).all())
+    part = torch.zeros(M, K, dtype=torch.float64, device=DEV)
+    size = torch.zeros_like(part)
+    for n in range(0, N, 5000):
+        piece = w[n:n + 5000].double()
+        part += dz[:, n:n + 5000] @ piece
+        size += dz[:, n:n + 5000].abs() @ piece.abs()
+    assert bool(((dx.double() - part).abs() <= (2.0 ** -8 * 1.1 + 4 * bound) * size + 2.0 ** -8 * part.abs()).all())
