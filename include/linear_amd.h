@@ -650,6 +650,61 @@ int32_t linear_grad_norm(const linear_tensor* grads, int64_t count, float* norm,
 int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, int64_t count,
                          const float* norm, float max_norm, void* stream);
 
+/*
+ * An AdamW step over many tensors in one pass, clipping included:
+ *
+ *     g = grad * s,   s = 1 without norm, else min(1, max_norm / (norm[0] + 1e-6))
+ *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
+ *
+ * in FP32, p rounded to its type once.  params, grads: `count` tensors as for
+ * linear_grad_clip, of the same sizes, each of any type and row stride.  m, v: for each
+ * tensor linear_adamw_state_bytes(rows * cols, state_bits) bytes of device memory, which the
+ * step reads and overwrites; values in row-major order without gaps, whatever the
+ * parameter's stride; all bytes zero before the first step.  copies: NULL, or `count` tensors
+ * of 16-bit types that p is also rounded into (the words of 32-bit weights that the next
+ * forward pass reads).  The arrays and options are host memory, read during the call.
+ *
+ * state_bits 32: floats.  state_bits 8: rows * cols codes, then a byte k + 127 for each block
+ * of LINEAR_ADAMW_BLOCK values, whose codes count in units of 2^k; k is the smallest from -100
+ * on for which the block's largest finite magnitude is under 464 * 2^k (m) or 63488 * 2^k (v).
+ * m: a sign, 4 bits of exponent (bias 7) and 3 of mantissa, subnormals at exponent 0, code 127
+ * NaN (infinities are stored as that).  v: 5 bits of exponent (bias 15), 3 of mantissa, code
+ * 248 infinity, 249 to 255 NaN.  Magnitudes from 1.9375 * 2^127 on count as infinite.  Values are rounded to nearest even from an FP64 m and v (so off
+ * by at most 2^-4 of their value, or half the smallest spacing); a v over zero is at least the
+ * first code.  p is updated with m and v before that rounding.
+ *
+ * norm: device memory (linear_grad_norm's), or NULL; a NaN norm makes everything NaN, an
+ * infinite one s zero, as for linear_grad_clip.  device_lr, device_step: device memory read
+ * instead of lr and step by the step's kernels, for captured graphs (NULL: not used).
+ * LINEAR_E_VALUE: state_bits neither 8 nor 32; lr, eps or weight_decay negative, infinite or
+ * NaN; a beta outside [0, 1); step < 1 (without device_step); max_norm negative or NaN (with
+ * norm); copies of 32-bit type.  No tensor, state, copy or device scalar may overlap another
+ * (LINEAR_E_ALIAS, judged as for linear_grad_clip; a gradient may be listed twice).
+ */
+#define LINEAR_ADAMW_BLOCK 32
+
+typedef struct linear_adamw_options {
+    double lr, beta1, beta2, eps, weight_decay;
+    int64_t step;                  /* 1 for the first update */
+    int32_t state_bits;
+    float max_norm;
+    const float* norm;
+    const float* device_lr;
+    const int64_t* device_step;
+} linear_adamw_options;
+
+int64_t linear_adamw_state_bytes(int64_t n, int32_t state_bits);   /* -1 if out of range */
+int32_t linear_adamw(const linear_tensor* params, const linear_tensor* grads, void* const* m, void* const* v,
+                     const linear_tensor* copies, int64_t count, const linear_adamw_options* options, void* stream);
+
+/*
+ * The numbers that 8-bit states stand for (second != 0: second moments), into bfloat16 or
+ * float tensors (LINEAR_E_VALUE for binary16) of the parameters' sizes.  Every such number is
+ * a bfloat16 number, so the conversion is exact.
+ */
+int32_t linear_adamw_values(const linear_tensor* out, const void* const* states, int32_t second, int64_t count, void* stream);
+
 /* Which kernels a call would launch: the host-side plan of "The Graph IR" (op
  * table, MatMul row: GEMV versus GEMM chosen at plan time; section "Host-side
  * shape inference").  Enqueues nothing and touches no device memory; the tile

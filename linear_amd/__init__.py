@@ -71,6 +71,7 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_f16_cross_entropy_backward", "linear_bf16_cross_entropy_backward",
                 "linear_f16_cross_entropy_backward_f32out", "linear_bf16_cross_entropy_backward_f32out",
                 "linear_grad_workspace_bytes", "linear_grad_norm", "linear_grad_clip",
+                "linear_adamw_state_bytes", "linear_adamw", "linear_adamw_values",
                 "linear_f16_plan", "linear_gated_backward_plan", "linear_status_string", "linear_last_hip_error")
 
 
@@ -101,6 +102,12 @@ class _ProductPlan(ctypes.Structure):
 
 class _GatedPlan(ctypes.Structure):
     _fields_ = [("dx", _ProductPlan), ("dw", _ProductPlan), ("joint", ctypes.c_int32), ("two_words", ctypes.c_int32)]
+
+
+class _AdamwOptions(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_double) for f in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("step", ctypes.c_int64), ("state_bits", ctypes.c_int32), ("max_norm", ctypes.c_float),
+        ("norm", ctypes.c_void_p), ("device_lr", ctypes.c_void_p), ("device_step", ctypes.c_void_p)]
 
 
 class _Epilogue(ctypes.Structure):
@@ -190,6 +197,12 @@ def _lib():
     lib.linear_grad_norm.restype = i32
     lib.linear_grad_clip.argtypes = [vp, vp, i64, vp, ctypes.c_float, vp]
     lib.linear_grad_clip.restype = i32
+    lib.linear_adamw_state_bytes.argtypes = [i64, i32]
+    lib.linear_adamw_state_bytes.restype = i64
+    lib.linear_adamw.argtypes = [vp, vp, vp, vp, vp, i64, ctypes.POINTER(_AdamwOptions), vp]
+    lib.linear_adamw.restype = i32
+    lib.linear_adamw_values.argtypes = [vp, vp, i32, i64, vp]
+    lib.linear_adamw_values.restype = i32
     lib.linear_f16_plan.argtypes = [vp, i64, vp, i64, vp, vp, i64, i64, i64, i64, i32,
                                     ctypes.POINTER(_Plan)]
     lib.linear_f16_plan.restype = i32
@@ -1033,6 +1046,116 @@ def linear_grad_clip(grads, norm: torch.Tensor, max_norm: float, out=None, strea
                                  norm.data_ptr(), float(max_norm), handle)
     _check(rc, "linear_grad_clip")
     return out if out is not None else grads
+
+
+ADAMW_BLOCK = 32
+
+
+def adamw_state(param: torch.Tensor, bits: int = 32) -> torch.Tensor:
+    """A first or second moment of zeros for linear_adamw: float32 of the parameter's shape, or, with
+    bits 8, a uint8 vector of its codes and its blocks' powers of two."""
+    if bits == 32:
+        return torch.zeros(param.shape, dtype=torch.float32, device=param.device)
+    n = _lib().linear_adamw_state_bytes(param.numel(), bits)
+    if n < 0:
+        raise ValueError("bits must be 8 or 32")
+    return torch.zeros(n, dtype=torch.uint8, device=param.device)
+
+
+def _same_sizes(tables, tensors, names):
+    """The tables describe tensors of the first one's shapes; a matrix with padded rows in one is
+    described by its rows in all."""
+    if any(len(t) != len(tables[0]) for t in tables):
+        raise ValueError("%s must have as many tensors as %s" % (" and ".join(names[1:]), names[0]))
+    first = tables[0]
+    for ts, name in zip(tensors[1:], names[1:]):
+        if any(a.shape != b.shape for a, b in zip(ts, tensors[0])):
+            raise ValueError("%s must have the shapes of %s" % (name, names[0]))
+    if all(t[1::5] == first[1::5] for t in tables):
+        return
+    for i in range(len(tensors[0])):
+        if any(t[5 * i + 1] != first[5 * i + 1] for t in tables):
+            for t, ts in zip(tables, tensors):
+                if t[5 * i + 1] == 1:
+                    _by_rows(t, i, ts[i])
+
+
+def _state_pointers(states, sizes, eight, name):
+    """The states' addresses, after a check of their types and sizes."""
+    want = torch.uint8 if eight else torch.float32
+    if len(states) != len(sizes) or any(d != want for d in map(_dtype_of, states)):
+        raise ValueError("%s must have a state for each tensor, all float32 or all uint8" % name)
+    held = [n + -(-n // ADAMW_BLOCK) for n in sizes] if eight else sizes
+    if list(map(torch.Tensor.numel, states)) != list(held) or not all(map(torch.Tensor.is_contiguous, states)):
+        raise ValueError("%s must be contiguous, of adamw_state's sizes" % name)
+    return array.array("q", map(torch.Tensor.data_ptr, states))
+
+
+def _device_scalar(t, name, dtype):
+    if t.dtype != dtype or t.numel() != 1:
+        raise ValueError("%s must be a %s tensor of one value" % (name, dtype))
+    return t.data_ptr()
+
+
+def linear_adamw(params, grads, m, v, *, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                 weight_decay: float = 0.01, norm=None, max_norm=None, copies=None, stream=None):
+    """One AdamW step, in place, over a sequence of parameters (float16, bfloat16, float32) and their gradients (of any
+    of these types).  m, v: the moments of each (adamw_state: all float32 or all 8-bit).  step: 1 for the first update.
+    norm, max_norm: linear_grad_norm's tensor and the norm that gradients are clipped to, within the same pass.
+    copies: 16-bit tensors that the new parameters are also rounded into.  lr and step may be device tensors of one
+    value (float32, int64), read when the step runs: a captured step then follows them.  Returns params."""
+    params, grads, m, v = list(params), list(grads), list(m), list(v)
+    tensors, names = [params, grads], ["params", "grads"]
+    if copies is not None:
+        copies = list(copies)
+        tensors.append(copies)
+        names.append("copies")
+    tables = [_tensor_table(t, n) for t, n in zip(tensors, names)]
+    _same_sizes(tables, tensors, names)
+    eight = bool(m) and m[0].dtype == torch.uint8
+    sizes = list(map(torch.Tensor.numel, params))
+    mp, vp = _state_pointers(m, sizes, eight, "m"), _state_pointers(v, sizes, eight, "v")
+    if (norm is None) != (max_norm is None):
+        raise ValueError("norm and max_norm belong together")
+    o = _AdamwOptions(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, state_bits=8 if eight else 32)
+    scalars = []
+    if norm is not None:
+        o.norm, o.max_norm = _device_scalar(norm, "norm", torch.float32), max_norm
+        scalars.append(norm)
+    if isinstance(lr, torch.Tensor):
+        o.device_lr = _device_scalar(lr, "lr", torch.float32)
+        scalars.append(lr)
+    else:
+        o.lr = lr
+    if isinstance(step, torch.Tensor):
+        o.device_step = _device_scalar(step, "step", torch.int64)
+        scalars.append(step)
+    else:
+        o.step = step
+    handle = _launch_stream(stream, *params, *grads, *m, *v, *scalars, *(copies or ()))
+    rc = _lib().linear_adamw(tables[0].buffer_info()[0], tables[1].buffer_info()[0], mp.buffer_info()[0], vp.buffer_info()[0],
+                             tables[2].buffer_info()[0] if copies is not None else None, len(params), ctypes.byref(o), handle)
+    _check(rc, "linear_adamw")
+    return params
+
+
+def linear_adamw_values(states, second: bool, out=None, like=None, stream=None):
+    """The numbers that 8-bit moments stand for (second: second moments), exactly: into the bfloat16 or float32 tensors
+    of out, or into new bfloat16 tensors of the shapes of `like` (the parameters)."""
+    states = list(states)
+    if out is None:
+        if like is None:
+            raise ValueError("give out, or like: a state does not know its parameter's shape")
+        like = list(like)
+        with _on(stream, like[0].device if like else torch.device("cpu")):
+            out = [torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in like]
+    out = list(out)
+    table = _tensor_table(out, "out")
+    sp = _state_pointers(states, list(map(torch.Tensor.numel, out)), True, "states")
+    handle = _launch_stream(stream, *states, *out)
+    rc = _lib().linear_adamw_values(table.buffer_info()[0], sp.buffer_info()[0], int(bool(second)), len(out), handle)
+    _check(rc, "linear_adamw_values")
+    return out
 
 
 def linear_f16_plan(x: torch.Tensor, weight: torch.Tensor, b: torch.Tensor | None = None,

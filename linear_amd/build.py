@@ -23,8 +23,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "indexed.hip", "product.hip", "gradnorm.hip",
            "gated_f16.hip", "gated_bf16.hip", "grad_f16.hip", "grad_bf16.hip",
-           "loss_f16.hip", "loss_bf16.hip", "loss.hip",
-           "linear_abi.hip", "train_abi.hip", "loss_abi.hip"]
+           "loss_f16.hip", "loss_bf16.hip", "loss.hip", "adamw.hip",
+           "linear_abi.hip", "train_abi.hip", "loss_abi.hip",
+           "adamw_abi.hip"]
 
 # sources whose kernels set m0 in inline assembly (lds_dma16_raw), which the compiler is not told
 RAW_M0_SOURCES = ("grad_f16.hip", "grad_bf16.hip")

@@ -1,0 +1,53 @@
+// adamw.h -- launch interface of the AdamW step.
+#pragma once
+
+#include "common.h"
+#include "kernels.h"
+
+namespace lin {
+
+// Tensors of one launch, in its kernel arguments.
+constexpr int kAdamTensors = 40;
+constexpr int kAdamRun = 8;                           // consecutive values of a thread
+constexpr int kAdamChunk = 256 * kAdamRun;            // values of one workgroup step
+constexpr int kAdamGrid = 2048;                       // most workgroups
+constexpr int kAdamBlock = 32;                        // values that share a power of two (8-bit moments)
+enum : int { kNoCopy = 3 };                           // beside kGradF16, kGradBF16 and kGradF32
+
+struct AdamTable {
+    void* param[kAdamTensors];
+    const void* grad[kAdamTensors];
+    void *m[kAdamTensors], *v[kAdamTensors], *copy[kAdamTensors];
+    int64_t n[kAdamTensors];                          // values
+    int64_t first[kAdamTensors + 1];                  // first chunk of each tensor; the last: all chunks
+    int64_t cols[kAdamTensors];                       // values of a row; 0: no gaps between the rows
+    int32_t ldp[kAdamTensors], ldg[kAdamTensors], ldc[kAdamTensors];
+    uint8_t ptype[kAdamTensors], gtype[kAdamTensors], ctype[kAdamTensors];
+    int count;
+};
+
+struct AdamArgs {
+    double lr, beta1, beta2, weight_decay;
+    double bias1, bias2;             // 1 - beta^step; not read where device_step is given
+    float eps, max_norm;
+    const float* norm;               // null: no clipping
+    const float* device_lr;          // not null: read instead of lr
+    const int64_t* device_step;      // not null: the step
+};
+static_assert(sizeof(AdamTable) + sizeof(AdamArgs) <= 3840, "the table travels as kernel arguments");
+hipError_t launch_adamw(bool eight, const AdamTable& t, const AdamArgs& a, int grid, hipStream_t stream);
+
+// 8-bit moments as the numbers they stand for.
+constexpr int kValueTensors = 64;
+struct ValueTable {
+    const uint8_t* state[kValueTensors];
+    void* out[kValueTensors];
+    int64_t n[kValueTensors], first[kValueTensors + 1], cols[kValueTensors];
+    int32_t ld[kValueTensors];
+    uint8_t f32[kValueTensors];                       // floats, else bfloat16 words
+    int count;
+};
+static_assert(sizeof(ValueTable) <= 3840, "the table travels as kernel arguments");
+hipError_t launch_adamw_values(bool second, const ValueTable& t, int grid, hipStream_t stream);
+
+}  // namespace lin

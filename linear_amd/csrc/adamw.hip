@@ -1,0 +1,393 @@
+// adamw.hip -- an AdamW step over many tensors.
+//
+//     g = grad * s,  s = 1 or min(1, max_norm / (norm + 1e-6))
+//     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
+//     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+//
+// One pass: weights, gradients and moments are read once, weights and moments written.  Up to
+// kAdamTensors tensors go into one launch, their table in the kernel's arguments; a tensor's
+// values, in row-major order, are cut into chunks of kAdamChunk, and workgroup w takes the w-th
+// share of all chunks in their order.  A thread takes 8 consecutive values.
+//
+// 8-bit moments: n codes, then a byte k + 127 for each block of 32 values, whose codes count in
+// units of 2^k.  The first moment's codes are a sign, 4 bits of exponent and 3 of mantissa (the
+// hardware's e4m3: 448 at most, 127 is NaN); the second's have no sign and 5 bits of exponent
+// (the upper bits of a binary16 word: 61440 at most, 248 infinity, past it NaN).  m / sqrt(v)
+// needs about the same range of m and of sqrt(v): 2^17 and 2^16 under a block's largest.  k is
+// the smallest, from -100 on, for which the largest finite value stays under the border where it
+// would round past the last code, 464 or 63488 times 2^k.  A power of two makes the division by
+// it exact, so a stored moment is one rounding (half a step: 2^-4) from its value.  The moments
+// are formed in FP64: sums of such few-bit numbers often lie on, or within FP32's error of, the
+// border between two codes.  A second moment over zero is never stored as zero, which the next
+// step would divide by.
+#include "adamw.h"
+#include "train.h"
+
+namespace lin {
+
+namespace {
+
+constexpr int RUN = kAdamRun;
+
+// 8 consecutive 16-bit words or floats as loaded.
+struct Raw {
+    u32x4 lo, hi;            // hi: floats only
+};
+
+// Where the values i .. i + 7 of a tensor with rows of cols values lie: offsets of a row's first
+// value and of the first value, walked one value at a time.
+struct Walk {
+    int64_t row, col;
+    __device__ Walk(int64_t i, int64_t cols) : row(i / cols), col(i - i / cols * cols) {}
+    __device__ void next(int64_t cols) {
+        if (++col == cols) {
+            col = 0;
+            ++row;
+        }
+    }
+};
+
+__device__ inline Raw raw_load(const void* p, bool f32, int64_t i, int count, int64_t cols, int64_t ld) {
+    Raw r;
+    r.lo = r.hi = (u32x4){0u, 0u, 0u, 0u};
+    if (cols == 0 && count == RUN) {
+        if (f32) {
+            __builtin_memcpy(&r.lo, (const float*)p + i, 16);
+            __builtin_memcpy(&r.hi, (const float*)p + i + 4, 16);
+        } else {
+            __builtin_memcpy(&r.lo, (const uint16_t*)p + i, 16);
+        }
+        return r;
+    }
+    Walk w(i, cols ? cols : INT64_MAX);
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        if (e < count) {
+            const int64_t at = w.row * ld + w.col;
+            if (f32) {
+                const uint32_t u = ((const uint32_t*)p)[at];
+                if (e < 4) r.lo[e] = u;
+                else r.hi[e - 4] = u;
+            } else {
+                r.lo[e >> 1] |= (uint32_t)((const uint16_t*)p)[at] << (16 * (e & 1));
+            }
+        }
+        if (cols) w.next(cols);
+        else ++w.col;
+    }
+    return r;
+}
+
+__device__ inline void widen8(const Raw& r, int type, float (&out)[RUN]) {
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const uint32_t word = e < 4 ? r.lo[e] : r.hi[e - 4];
+        const uint16_t half = (uint16_t)(r.lo[e >> 1] >> (16 * (e & 1)));
+        out[e] = type == kGradF32 ? __builtin_bit_cast(float, word) : type == kGradBF16 ? widen<kBF16>(half) : widen<kF16>(half);
+    }
+}
+
+__device__ inline void store_run(void* p, int type, const float (&v)[RUN], int64_t i, int count, int64_t cols, int64_t ld) {
+    Raw r;
+    if (type == kGradF32) {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) {
+            const uint32_t u = __builtin_bit_cast(uint32_t, v[e]);
+            if (e < 4) r.lo[e] = u;
+            else r.hi[e - 4] = u;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t a = type == kGradBF16 ? narrow<kBF16>(v[2 * q]) : narrow<kF16>(v[2 * q]);
+            const uint32_t b = type == kGradBF16 ? narrow<kBF16>(v[2 * q + 1]) : narrow<kF16>(v[2 * q + 1]);
+            r.lo[q] = a | (b << 16);
+        }
+    }
+    if (cols == 0 && count == RUN) {
+        if (type == kGradF32) {
+            __builtin_memcpy((float*)p + i, &r.lo, 16);
+            __builtin_memcpy((float*)p + i + 4, &r.hi, 16);
+        } else {
+            __builtin_memcpy((uint16_t*)p + i, &r.lo, 16);
+        }
+        return;
+    }
+    Walk w(i, cols ? cols : INT64_MAX);
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        if (e < count) {
+            const int64_t at = w.row * ld + w.col;
+            if (type == kGradF32) ((uint32_t*)p)[at] = e < 4 ? r.lo[e] : r.hi[e - 4];
+            else ((uint16_t*)p)[at] = (uint16_t)(r.lo[e >> 1] >> (16 * (e & 1)));
+        }
+        if (cols) w.next(cols);
+        else ++w.col;
+    }
+}
+
+// 8 codes (zeros past count).
+__device__ inline uint2 load_codes(const uint8_t* p, int count) {
+    uint2 r{0u, 0u};
+    if (count == RUN) {
+        __builtin_memcpy(&r, p, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            if (e < count) (e < 4 ? r.x : r.y) |= (uint32_t)p[e] << (8 * (e & 3));
+    }
+    return r;
+}
+
+__device__ inline void store_codes(uint8_t* p, uint2 c, int count) {
+    if (count == RUN) {
+        __builtin_memcpy(p, &c, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            if (e < count) p[e] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
+    }
+}
+
+// 2^k of a block's byte k + 127 (0 for a byte of 0: a state of zero bytes is a state of zeros).
+__device__ inline float block_unit(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+template <bool SECOND>
+__device__ inline void decode4(uint32_t codes, float unit, float* out) {
+    if constexpr (SECOND) {
+        // a code is bits 7 .. 14 of a binary16 word
+        const uint32_t a = __builtin_amdgcn_perm(0u, codes, 0x0c010c00u) << 7, b = __builtin_amdgcn_perm(0u, codes, 0x0c030c02u) << 7;
+        out[0] = widen<kF16>((uint16_t)a) * unit;
+        out[1] = widen<kF16>((uint16_t)(a >> 16)) * unit;
+        out[2] = widen<kF16>((uint16_t)b) * unit;
+        out[3] = widen<kF16>((uint16_t)(b >> 16)) * unit;
+    } else {
+        typedef float f32x2 __attribute__((ext_vector_type(2)));
+        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
+        out[0] = a[0] * unit;
+        out[1] = a[1] * unit;
+        out[2] = b[0] * unit;
+        out[3] = b[1] * unit;
+    }
+}
+
+template <bool SECOND>
+__device__ inline void decode8(uint2 codes, float unit, float (&out)[RUN]) {
+    decode4<SECOND>(codes.x, unit, out);
+    decode4<SECOND>(codes.y, unit, out + 4);
+}
+
+__device__ inline uint32_t high_word(double v) { return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32); }
+__device__ inline double from_high(uint32_t hi) { return __builtin_bit_cast(double, (uint64_t)hi << 32); }
+
+template <int CTRL>
+__device__ inline uint32_t dpp_max(uint32_t v) {
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+    return v > o ? v : o;
+}
+
+// The codes of 8 values (0 past a tensor's end) and their block's byte; the four lanes of a quad
+// hold a block.
+template <bool SECOND>
+__device__ inline uint2 encode8(const double (&v)[RUN], uint32_t& byte) {
+    // from 1.9375 * 2^127 on a value counts as infinite: rounded, it would leave binary32's range
+    constexpr uint32_t kNotFinite = 0x47ef0000u;
+    // the upper words order the magnitudes as finely as the borders need: those have 5 bits
+    uint32_t top = 0;
+    bool odd = false;
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const uint32_t h = high_word(v[e]) & 0x7fffffffu;
+        odd |= h >= kNotFinite;
+        top = h >= kNotFinite || h < top ? top : h;
+    }
+    top = dpp_max<0xB1>(top);                         // quad_perm [1, 0, 3, 2]
+    top = dpp_max<0x4E>(top);                         // quad_perm [2, 3, 0, 1]
+    // 464 = 1.8125 * 2^8, 63488 = 1.9375 * 2^15: from there on the next power of two
+    const int e = (int)((top + (SECOND ? 0x10000u : 0x30000u)) >> 20) - 1023;
+    const int k = max(e - (SECOND ? 15 : 8), -100);
+    byte = (uint32_t)(k + 127);
+    const double unit = from_high((uint32_t)(1023 - k) << 20);   // 2^-k
+    float r[RUN];
+#pragma unroll
+    for (int i = 0; i < RUN; ++i) {
+        const double y = v[i] * unit;
+        // rounded to 4 significant bits (the subnormals to their spacing) by an addition of
+        // 1.5 * 2^(49 + its exponent)
+        const uint32_t x = max((high_word(y) >> 20) & 0x7ffu, (uint32_t)(1023 - (SECOND ? 14 : 6)));
+        const double big = from_high(((x + 49u) << 20) | 0x80000u);
+        r[i] = (float)((y + big) - big);
+        if constexpr (SECOND) r[i] = v[i] > 0.0 ? fmaxf(r[i], 0x1p-17f) : r[i];
+    }
+    uint2 c;
+    if constexpr (SECOND) {
+        uint32_t w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)                   // exact: the values are binary16's
+            w[q] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(r[2 * q], r[2 * q + 1])) >> 7;
+        c.x = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u);
+        c.y = __builtin_amdgcn_perm(w[3], w[2], 0x06040200u);
+    } else {
+        int a = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false), b = __builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
+        a = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], a, true);
+        b = __builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], b, true);
+        c.x = (uint32_t)a;
+        c.y = (uint32_t)b;
+    }
+    if (odd) {                                        // infinities and NaN
+#pragma unroll
+        for (int i = 0; i < RUN; ++i) {
+            const uint32_t h = high_word(v[i]) & 0x7fffffffu;
+            if (h < kNotFinite) continue;
+            const uint32_t code = !SECOND ? 127u : v[i] != v[i] ? 255u : 248u;
+            uint32_t& word = i < 4 ? c.x : c.y;
+            word = (word & ~(0xffu << (8 * (i & 3)))) | (code << (8 * (i & 3)));
+        }
+    }
+    return c;
+}
+
+// A step's factors.
+struct Factors {
+    double scale;                    // of the gradients
+    float keep, rate, root;          // 1 - lr weight_decay, lr / bias1, 1 / sqrt(bias2)
+};
+
+__device__ inline Factors factors(const AdamArgs& a, Factors* shared) {
+    if (threadIdx.x == 0) {
+        const double lr = a.device_lr ? (double)*a.device_lr : a.lr;
+        double bias1 = a.bias1, bias2 = a.bias2;
+        if (a.device_step) {
+            const double step = (double)*a.device_step;
+            bias1 = 1.0 - pow(a.beta1, step);
+            bias2 = 1.0 - pow(a.beta2, step);
+        }
+        Factors f;
+        f.scale = 1.0;
+        if (a.norm) {
+            const double s = (double)a.max_norm / ((double)*a.norm + 1e-6);
+            f.scale = s >= 1.0 ? 1.0 : s;             // a NaN scale stays
+        }
+        f.keep = (float)(1.0 - lr * a.weight_decay);
+        f.rate = (float)(lr / bias1);
+        f.root = (float)(1.0 / sqrt(bias2));
+        *shared = f;
+    }
+    __syncthreads();
+    return *shared;
+}
+
+// sqrt(v) within 2 FP32 steps, for subnormal v too (which the instruction takes for zero).
+__device__ inline float root_of(float v) {
+    const bool low = v < 0x1p-60f;
+    const float s = __builtin_amdgcn_sqrtf(low ? v * 0x1p80f : v);
+    return low ? s * 0x1p-40f : s;
+}
+
+__device__ inline float updated(float p, float m, float v, const Factors& f, float eps) {
+    return p * f.keep - (f.rate * m) * __builtin_amdgcn_rcpf(root_of(v) * f.root + eps);
+}
+
+template <bool EIGHT>
+__global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
+    __shared__ Factors shared;
+    const Factors f = factors(a, &shared);
+    const int64_t chunks = t.first[t.count];
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+    int i = 0;
+    for (int64_t c = c0; c < c1; ++c) {
+        while (c >= t.first[i + 1]) ++i;
+        const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
+        const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
+        const int64_t cols = t.cols[i];
+        const int ptype = t.ptype[i], gtype = t.gtype[i];
+        float p[RUN], g[RUN];
+        // every load is issued before the first is used; lanes past the end take part in their
+        // block's maximum with zeros
+        const Raw pr = raw_load(t.param[i], ptype == kGradF32, at, count, cols, t.ldp[i]);
+        const Raw gr = raw_load(t.grad[i], gtype == kGradF32, at, count, cols, t.ldg[i]);
+        if constexpr (EIGHT) {
+            uint8_t *mc = (uint8_t*)t.m[i], *vc = (uint8_t*)t.v[i];
+            const int64_t block = n + at / kAdamBlock;
+            const uint2 mw = load_codes(mc + at, count), vw = load_codes(vc + at, count);
+            const float mu = block_unit(count ? mc[block] : 0u), vu = block_unit(count ? vc[block] : 0u);
+            widen8(pr, ptype, p);
+            widen8(gr, gtype, g);
+            float mf[RUN], vf[RUN];
+            decode8<false>(mw, mu, mf);
+            decode8<true>(vw, vu, vf);
+            double m[RUN], v[RUN];
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) {
+                const double gd = (double)g[e] * f.scale;
+                m[e] = (double)mf[e] * a.beta1 + gd * (1.0 - a.beta1);
+                v[e] = (double)vf[e] * a.beta2 + gd * gd * (1.0 - a.beta2);
+                p[e] = updated(p[e], (float)m[e], (float)v[e], f, a.eps);
+            }
+            uint32_t mb, vb;
+            const uint2 mo = encode8<false>(m, mb), vo = encode8<true>(v, vb);
+            store_codes(mc + at, mo, count);
+            store_codes(vc + at, vo, count);
+            if (count && (threadIdx.x & 3) == 0) {
+                mc[block] = (uint8_t)mb;
+                vc[block] = (uint8_t)vb;
+            }
+        } else {
+            float *mp = (float*)t.m[i], *vp = (float*)t.v[i];
+            const Raw mr = raw_load(mp, true, at, count, 0, 0), vr = raw_load(vp, true, at, count, 0, 0);
+            float m[RUN], v[RUN];
+            widen8(pr, ptype, p);
+            widen8(gr, gtype, g);
+            widen8(mr, kGradF32, m);
+            widen8(vr, kGradF32, v);
+            const float b1 = (float)a.beta1, r1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2, r2 = (float)(1.0 - a.beta2);
+            const float s = (float)f.scale;
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) {
+                const float gs = g[e] * s;
+                m[e] = m[e] * b1 + gs * r1;
+                v[e] = v[e] * b2 + gs * gs * r2;
+                p[e] = updated(p[e], m[e], v[e], f, a.eps);
+            }
+            store_run(mp, kGradF32, m, at, count, 0, 0);
+            store_run(vp, kGradF32, v, at, count, 0, 0);
+        }
+        store_run(t.param[i], ptype, p, at, count, cols, t.ldp[i]);
+        if (t.ctype[i] != kNoCopy) store_run(t.copy[i], t.ctype[i], p, at, count, cols, t.ldc[i]);
+    }
+}
+
+template <bool SECOND>
+__global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
+    const int64_t chunks = t.first[t.count];
+    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
+    int i = 0;
+    for (int64_t c = c0; c < c1; ++c) {
+        while (c >= t.first[i + 1]) ++i;
+        const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
+        if (left <= 0) continue;
+        const int count = left >= RUN ? RUN : (int)left;
+        float v[RUN];
+        decode8<SECOND>(load_codes(t.state[i] + at, count), block_unit(t.state[i][n + at / kAdamBlock]), v);
+        store_run(t.out[i], t.f32[i] ? kGradF32 : kGradBF16, v, at, count, t.cols[i], t.ld[i]);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_adamw(bool eight, const AdamTable& t, const AdamArgs& a, int grid, hipStream_t stream) {
+    AdamTable table = t;
+    AdamArgs args = a;
+    void* params[] = {&table, &args};
+    return launch_kernel(eight ? (const void*)adamw<true> : (const void*)adamw<false>, dim3((unsigned)grid), dim3(256), params, 0,
+                         stream);
+}
+
+hipError_t launch_adamw_values(bool second, const ValueTable& t, int grid, hipStream_t stream) {
+    ValueTable table = t;
+    void* params[] = {&table};
+    return launch_kernel(second ? (const void*)adamw_values<true> : (const void*)adamw_values<false>, dim3((unsigned)grid),
+                         dim3(256), params, 0, stream);
+}
+
+}  // namespace lin
