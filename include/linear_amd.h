@@ -561,10 +561,10 @@ int32_t linear_bf16_cross_entropy(const uint16_t* x, int64_t ldx,
  *
  * lse is the forward call's.  The logits are formed again, a piece of the vocabulary at a
  * time; dz of a piece is kept in the workspace as the two products' operand, dx's sums over
- * the pieces in FP32.  c is 1 in bfloat16; in binary16 it is the power of two that brings
- * the rows' largest |d + dlse| + |d| to 2^14 .. 2^15, so that neither large nor small dloss
- * loses precision (the outputs themselves have the type's range: scale dloss, as usual in
- * binary16).  dz of a row with d = 0 and dlse = 0 is zero whatever its logits are; its x
+ * the pieces in FP32.  c is a power of two over the rows' largest |d| that brings their
+ * largest |d + dlse| + |d| to 2^14 .. 2^15: neither large nor small dloss loses precision in
+ * binary16 (the outputs themselves have the type's range: scale dloss, as usual there), and
+ * the -d of rows that share one d, as in a mean, is not rounded at all.  dz of a row with d = 0 and dlse = 0 is zero whatever its logits are; its x
  * still meets those zeros in dw (NaN or infinite x there gives NaN).
  *
  * dx, dw and db may each be NULL (not wanted), not all three unless they are empty.  N == 0

@@ -124,9 +124,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
     float back = 1.f;                                 // (read here: its latency passes under the loop)
-    if constexpr (E == kF16) {
-        if (a.unscale) back = *a.unscale;
-    }
+    if (a.unscale) back = *a.unscale;
 
     const int lane = threadIdx.x & 63;
     const int set = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / (NW * 64));
@@ -358,13 +356,11 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         }
     }
 
-    if constexpr (E == kF16) {
-        if (a.unscale) {                              // uniform
+    if (a.unscale) {                                  // uniform
 #pragma unroll
-            for (int i = 0; i < FN; ++i)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-                for (int j = 0; j < FM; ++j) acc[i][j] *= back;
-        }
+            for (int j = 0; j < FM; ++j) acc[i][j] *= back;
     }
 
     LinearArgs o;

@@ -22,7 +22,7 @@ struct LossArgs : LinearArgs {
     float* at_target;        // [M]: z at the target, where that is one of this launch's columns
     // kOutDz: y is dz, 16-bit words; columns from N to the next multiple of 8 are zeroed
     const float *lse, *dloss, *dlse;   // [M]; dlse may be null
-    const float* scale;      // not null: dz is multiplied by *scale before its rounding
+    const float* scale;      // dz is multiplied by *scale before its rounding
 };
 
 constexpr int kNumLossConfigs = 5;
@@ -53,8 +53,12 @@ struct LossJoinArgs {
 };
 hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream);
 
-// head[0], head[1]: the power of two that brings the largest finite |dloss + dlse| + |dloss|
-// of the rows to 2^14 .. 2^15, as its inverse and itself.
+// head[0], head[1]: the factor that dz is multiplied by before its rounding, as its inverse and
+// itself: 2^e over the largest finite |dloss| of the rows that count, with e such that the
+// largest |dloss + dlse| + |dloss| ends at 2^14 .. 2^15.  dz at a row's target is near -dloss
+// for most rows, the same number in each where the loss is a mean: unscaled, all would be
+// rounded the same way, up to half a step (1024 x 1024 x 768 bf16: dx, dW, db off by 1.9 times
+// one rounding; scaled, that number is a power of two).
 hipError_t launch_loss_scale(const int64_t* target, int64_t cols, const float* dloss, const float* dlse, int64_t M,
                              float* head, hipStream_t stream);
 

@@ -215,8 +215,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
     const LossPlan p = plan_loss(M, N, K, packed);
     const LossSpace at = space_of(p, M, K);
     unsigned char* space = (unsigned char*)ws;
-    // binary16 words are scaled; the products' sums are then multiplied by the factor's inverse
-    float* const head = elem == kF16 && M > 0 && N > 0 ? (float*)ws : nullptr;
+    // dz is scaled; the products' sums are then multiplied by the factor's inverse
+    float* const head = M > 0 && N > 0 ? (float*)ws : nullptr;
     uint16_t* dz = (uint16_t*)(space + at.dz);
     float* sums = (float*)(space + at.dx);
     void* partials = space + at.partials;

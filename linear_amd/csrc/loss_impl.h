@@ -120,7 +120,7 @@ __device__ __forceinline__ void finish_dz(const Args& a, unsigned char* smem, Ac
     constexpr int G = R * R / 256;
     const int wn = wave % WN, wm = wave / WN;
     const int lr = lane % R, lh = lane / R;
-    const float scale = E == kF16 ? *a.scale : 1.f;
+    const float scale = *a.scale;
     const bool ragged = n0 + BN > a.N;               // uniform
     if (a.b) {
 #pragma unroll
