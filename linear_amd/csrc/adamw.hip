@@ -29,124 +29,91 @@ namespace {
 
 constexpr int RUN = kAdamRun;
 
-// 8 consecutive 16-bit words or floats as loaded.
-struct Raw {
-    u32x4 lo, hi;            // hi: floats only
+// 8 consecutive values of type T (kGradF16, kGradBF16 or kGradF32) as loaded.
+template <int T>
+struct Run {
+    u32x4 w[T == kGradF32 ? 2 : 1];
 };
 
-// Where the values i .. i + 7 of a tensor with rows of cols values lie: offsets of a row's first
-// value and of the first value, walked one value at a time.
-struct Walk {
-    int64_t row, col;
-    __device__ Walk(int64_t i, int64_t cols) : row(i / cols), col(i - i / cols * cols) {}
-    __device__ void next(int64_t cols) {
-        if (++col == cols) {
+template <int T>
+__device__ inline Run<T> load_run(const void* p, int64_t i) {
+    Run<T> r;
+    __builtin_memcpy(&r, (const char*)p + i * (T == kGradF32 ? 4 : 2), sizeof r);   // at any alignment
+    return r;
+}
+
+template <int T>
+__device__ inline void widen_run(const Run<T>& r, float (&out)[RUN]) {
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const uint32_t word = r.w[T == kGradF32 ? e >> 2 : 0][e & 3];   // (a bit cast of a vector's element takes its first)
+        if constexpr (T == kGradF32) out[e] = __builtin_bit_cast(float, word);
+        else out[e] = widen<T == kGradBF16 ? kBF16 : kF16>((uint16_t)(r.w[0][e >> 1] >> (16 * (e & 1))));
+    }
+}
+
+template <int T>
+__device__ inline void store_run(void* p, const float (&v)[RUN], int64_t i) {
+    Run<T> r;
+#pragma unroll
+    for (int e = 0; e < RUN; e += 2) {
+        if constexpr (T == kGradF32) {
+            r.w[e >> 2][e & 3] = __builtin_bit_cast(uint32_t, v[e]);
+            r.w[e >> 2][(e & 3) + 1] = __builtin_bit_cast(uint32_t, v[e + 1]);
+        } else {
+            constexpr int E = T == kGradBF16 ? kBF16 : kF16;
+            r.w[0][e >> 1] = (uint32_t)narrow<E>(v[e]) | ((uint32_t)narrow<E>(v[e + 1]) << 16);
+        }
+    }
+    __builtin_memcpy((char*)p + i * (T == kGradF32 ? 4 : 2), &r, sizeof r);
+}
+
+// Value by value: a tensor's last run, and tensors with gaps between their rows.
+__device__ inline float value_at(const void* p, int type, int64_t at) {
+    if (type == kGradF32) return ((const float*)p)[at];
+    const uint16_t u = ((const uint16_t*)p)[at];
+    return type == kGradBF16 ? widen<kBF16>(u) : widen<kF16>(u);
+}
+__device__ inline void put_at(void* p, int type, int64_t at, float v) {
+    if (type == kGradF32) ((float*)p)[at] = v;
+    else ((uint16_t*)p)[at] = type == kGradBF16 ? narrow<kBF16>(v) : narrow<kF16>(v);
+}
+
+// f(e, offset) for the first `count` values from value i on of a tensor with rows of cols values
+// (0: no gaps) and a row stride of ld.
+template <typename F>
+__device__ inline void each_value(int64_t i, int count, int64_t cols, int64_t ld, F f) {
+    int64_t row = cols ? i / cols : 0, col = i - row * cols;
+    const int64_t end = cols ? cols : INT64_MAX;
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        if (e < count) f(e, row * ld + col);
+        if (++col == end) {
             col = 0;
             ++row;
         }
     }
-};
+}
 
-__device__ inline Raw raw_load(const void* p, bool f32, int64_t i, int count, int64_t cols, int64_t ld) {
-    Raw r;
-    r.lo = r.hi = (u32x4){0u, 0u, 0u, 0u};
-    if (cols == 0 && count == RUN) {
-        if (f32) {
-            __builtin_memcpy(&r.lo, (const float*)p + i, 16);
-            __builtin_memcpy(&r.hi, (const float*)p + i + 4, 16);
-        } else {
-            __builtin_memcpy(&r.lo, (const uint16_t*)p + i, 16);
-        }
-        return r;
-    }
-    Walk w(i, cols ? cols : INT64_MAX);
-#pragma unroll
-    for (int e = 0; e < RUN; ++e) {
-        if (e < count) {
-            const int64_t at = w.row * ld + w.col;
-            if (f32) {
-                const uint32_t u = ((const uint32_t*)p)[at];
-                if (e < 4) r.lo[e] = u;
-                else r.hi[e - 4] = u;
-            } else {
-                r.lo[e >> 1] |= (uint32_t)((const uint16_t*)p)[at] << (16 * (e & 1));
-            }
-        }
-        if (cols) w.next(cols);
-        else ++w.col;
-    }
+__device__ inline uint2 load_codes(const uint8_t* p) {
+    uint2 r;
+    __builtin_memcpy(&r, p, 8);
     return r;
 }
+__device__ inline void store_codes(uint8_t* p, uint2 c) { __builtin_memcpy(p, &c, 8); }
 
-__device__ inline void widen8(const Raw& r, int type, float (&out)[RUN]) {
-#pragma unroll
-    for (int e = 0; e < RUN; ++e) {
-        const uint32_t word = e < 4 ? r.lo[e] : r.hi[e - 4];
-        const uint16_t half = (uint16_t)(r.lo[e >> 1] >> (16 * (e & 1)));
-        out[e] = type == kGradF32 ? __builtin_bit_cast(float, word) : type == kGradBF16 ? widen<kBF16>(half) : widen<kF16>(half);
-    }
-}
-
-__device__ inline void store_run(void* p, int type, const float (&v)[RUN], int64_t i, int count, int64_t cols, int64_t ld) {
-    Raw r;
-    if (type == kGradF32) {
-#pragma unroll
-        for (int e = 0; e < RUN; ++e) {
-            const uint32_t u = __builtin_bit_cast(uint32_t, v[e]);
-            if (e < 4) r.lo[e] = u;
-            else r.hi[e - 4] = u;
-        }
-    } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t a = type == kGradBF16 ? narrow<kBF16>(v[2 * q]) : narrow<kF16>(v[2 * q]);
-            const uint32_t b = type == kGradBF16 ? narrow<kBF16>(v[2 * q + 1]) : narrow<kF16>(v[2 * q + 1]);
-            r.lo[q] = a | (b << 16);
-        }
-    }
-    if (cols == 0 && count == RUN) {
-        if (type == kGradF32) {
-            __builtin_memcpy((float*)p + i, &r.lo, 16);
-            __builtin_memcpy((float*)p + i + 4, &r.hi, 16);
-        } else {
-            __builtin_memcpy((uint16_t*)p + i, &r.lo, 16);
-        }
-        return;
-    }
-    Walk w(i, cols ? cols : INT64_MAX);
-#pragma unroll
-    for (int e = 0; e < RUN; ++e) {
-        if (e < count) {
-            const int64_t at = w.row * ld + w.col;
-            if (type == kGradF32) ((uint32_t*)p)[at] = e < 4 ? r.lo[e] : r.hi[e - 4];
-            else ((uint16_t*)p)[at] = (uint16_t)(r.lo[e >> 1] >> (16 * (e & 1)));
-        }
-        if (cols) w.next(cols);
-        else ++w.col;
-    }
-}
-
-// 8 codes (zeros past count).
+// The first `count` of 8 codes (zeros past them).
 __device__ inline uint2 load_codes(const uint8_t* p, int count) {
     uint2 r{0u, 0u};
-    if (count == RUN) {
-        __builtin_memcpy(&r, p, 8);
-    } else {
 #pragma unroll
-        for (int e = 0; e < RUN; ++e)
-            if (e < count) (e < 4 ? r.x : r.y) |= (uint32_t)p[e] << (8 * (e & 3));
-    }
+    for (int e = 0; e < RUN; ++e)
+        if (e < count) (e < 4 ? r.x : r.y) |= (uint32_t)p[e] << (8 * (e & 3));
     return r;
 }
-
 __device__ inline void store_codes(uint8_t* p, uint2 c, int count) {
-    if (count == RUN) {
-        __builtin_memcpy(p, &c, 8);
-    } else {
 #pragma unroll
-        for (int e = 0; e < RUN; ++e)
-            if (e < count) p[e] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
-    }
+    for (int e = 0; e < RUN; ++e)
+        if (e < count) p[e] = (uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3)));
 }
 
 // 2^k of a block's byte k + 127 (0 for a byte of 0: a state of zero bytes is a state of zeros).
@@ -288,6 +255,117 @@ __device__ inline float updated(float p, float m, float v, const Factors& f, flo
     return p * f.keep - (f.rate * m) * __builtin_amdgcn_rcpf(root_of(v) * f.root + eps);
 }
 
+// The moments of 8 values after the step, and the values.
+__device__ inline void step32(const AdamArgs& a, const Factors& f, float (&p)[RUN], const float (&g)[RUN], float (&m)[RUN],
+                              float (&v)[RUN]) {
+    const float b1 = (float)a.beta1, r1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2, r2 = (float)(1.0 - a.beta2);
+    const float s = (float)f.scale;
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const float gs = g[e] * s;
+        m[e] = m[e] * b1 + gs * r1;
+        v[e] = v[e] * b2 + gs * gs * r2;
+        p[e] = updated(p[e], m[e], v[e], f, a.eps);
+    }
+}
+
+__device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN], const float (&g)[RUN], uint2& mc, uint2& vc,
+                             uint32_t& mb, uint32_t& vb) {
+    float mf[RUN], vf[RUN];
+    decode8<false>(mc, block_unit(mb), mf);
+    decode8<true>(vc, block_unit(vb), vf);
+    const double r1 = 1.0 - a.beta1, r2 = 1.0 - a.beta2;
+    double m[RUN], v[RUN];
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        const double gd = (double)g[e] * f.scale;
+        m[e] = (double)mf[e] * a.beta1 + gd * r1;
+        v[e] = (double)vf[e] * a.beta2 + gd * gd * r2;
+        p[e] = updated(p[e], (float)m[e], (float)v[e], f, a.eps);
+    }
+    mc = encode8<false>(m, mb);
+    vc = encode8<true>(v, vb);
+}
+
+// A chunk of a tensor without gaps that lies inside it, of types P and G: every load is issued
+// before the first is used.
+template <bool EIGHT, int P, int G>
+__device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
+    const Run<P> pr = load_run<P>(t.param[i], at);
+    const Run<G> gr = load_run<G>(t.grad[i], at);
+    float p[RUN], g[RUN];
+    if constexpr (EIGHT) {
+        uint8_t *ms = (uint8_t*)t.m[i], *vs = (uint8_t*)t.v[i];
+        const int64_t block = t.n[i] + at / kAdamBlock;
+        uint2 mc = load_codes(ms + at), vc = load_codes(vs + at);
+        uint32_t mb = ms[block], vb = vs[block];
+        widen_run<P>(pr, p);
+        widen_run<G>(gr, g);
+        step8(a, f, p, g, mc, vc, mb, vb);
+        store_codes(ms + at, mc);
+        store_codes(vs + at, vc);
+        if ((threadIdx.x & 3) == 0) {
+            ms[block] = (uint8_t)mb;
+            vs[block] = (uint8_t)vb;
+        }
+    } else {
+        const Run<kGradF32> mr = load_run<kGradF32>(t.m[i], at), vr = load_run<kGradF32>(t.v[i], at);
+        float m[RUN], v[RUN];
+        widen_run<P>(pr, p);
+        widen_run<G>(gr, g);
+        widen_run<kGradF32>(mr, m);
+        widen_run<kGradF32>(vr, v);
+        step32(a, f, p, g, m, v);
+        store_run<kGradF32>(t.m[i], m, at);
+        store_run<kGradF32>(t.v[i], v, at);
+    }
+    store_run<P>(t.param[i], p, at);
+    if (t.ctype[i] == kGradBF16) store_run<kGradBF16>(t.copy[i], p, at);
+    else if (t.ctype[i] == kGradF16) store_run<kGradF16>(t.copy[i], p, at);
+}
+
+// Any chunk.  Lanes past the end take part in their block's maximum with zeros.
+template <bool EIGHT>
+__device__ __forceinline__ void chunk_any(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
+    const int64_t n = t.n[i], left = n - at, cols = t.cols[i];
+    const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
+    float p[RUN] = {}, g[RUN] = {};
+    each_value(at, count, cols, t.ldp[i], [&](int e, int64_t o) { p[e] = value_at(t.param[i], t.ptype[i], o); });
+    each_value(at, count, cols, t.ldg[i], [&](int e, int64_t o) { g[e] = value_at(t.grad[i], t.gtype[i], o); });
+    if constexpr (EIGHT) {
+        uint8_t *ms = (uint8_t*)t.m[i], *vs = (uint8_t*)t.v[i];
+        const int64_t block = n + at / kAdamBlock;
+        uint2 mc = load_codes(ms + at, count), vc = load_codes(vs + at, count);
+        uint32_t mb = count ? ms[block] : 0u, vb = count ? vs[block] : 0u;
+        step8(a, f, p, g, mc, vc, mb, vb);
+        store_codes(ms + at, mc, count);
+        store_codes(vs + at, vc, count);
+        if (count && (threadIdx.x & 3) == 0) {
+            ms[block] = (uint8_t)mb;
+            vs[block] = (uint8_t)vb;
+        }
+    } else {
+        float *mp = (float*)t.m[i] + at, *vp = (float*)t.v[i] + at;
+        float m[RUN] = {}, v[RUN] = {};
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            if (e < count) {
+                m[e] = mp[e];
+                v[e] = vp[e];
+            }
+        step32(a, f, p, g, m, v);
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            if (e < count) {
+                mp[e] = m[e];
+                vp[e] = v[e];
+            }
+    }
+    each_value(at, count, cols, t.ldp[i], [&](int e, int64_t o) { put_at(t.param[i], t.ptype[i], o, p[e]); });
+    if (t.ctype[i] != kNoCopy)
+        each_value(at, count, cols, t.ldc[i], [&](int e, int64_t o) { put_at(t.copy[i], t.ctype[i], o, p[e]); });
+}
+
 template <bool EIGHT>
 __global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
     __shared__ Factors shared;
@@ -297,63 +375,22 @@ __global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
     int i = 0;
     for (int64_t c = c0; c < c1; ++c) {
         while (c >= t.first[i + 1]) ++i;
-        const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
-        const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
-        const int64_t cols = t.cols[i];
-        const int ptype = t.ptype[i], gtype = t.gtype[i];
-        float p[RUN], g[RUN];
-        // every load is issued before the first is used; lanes past the end take part in their
-        // block's maximum with zeros
-        const Raw pr = raw_load(t.param[i], ptype == kGradF32, at, count, cols, t.ldp[i]);
-        const Raw gr = raw_load(t.grad[i], gtype == kGradF32, at, count, cols, t.ldg[i]);
-        if constexpr (EIGHT) {
-            uint8_t *mc = (uint8_t*)t.m[i], *vc = (uint8_t*)t.v[i];
-            const int64_t block = n + at / kAdamBlock;
-            const uint2 mw = load_codes(mc + at, count), vw = load_codes(vc + at, count);
-            const float mu = block_unit(count ? mc[block] : 0u), vu = block_unit(count ? vc[block] : 0u);
-            widen8(pr, ptype, p);
-            widen8(gr, gtype, g);
-            float mf[RUN], vf[RUN];
-            decode8<false>(mw, mu, mf);
-            decode8<true>(vw, vu, vf);
-            double m[RUN], v[RUN];
-#pragma unroll
-            for (int e = 0; e < RUN; ++e) {
-                const double gd = (double)g[e] * f.scale;
-                m[e] = (double)mf[e] * a.beta1 + gd * (1.0 - a.beta1);
-                v[e] = (double)vf[e] * a.beta2 + gd * gd * (1.0 - a.beta2);
-                p[e] = updated(p[e], (float)m[e], (float)v[e], f, a.eps);
-            }
-            uint32_t mb, vb;
-            const uint2 mo = encode8<false>(m, mb), vo = encode8<true>(v, vb);
-            store_codes(mc + at, mo, count);
-            store_codes(vc + at, vo, count);
-            if (count && (threadIdx.x & 3) == 0) {
-                mc[block] = (uint8_t)mb;
-                vc[block] = (uint8_t)vb;
-            }
-        } else {
-            float *mp = (float*)t.m[i], *vp = (float*)t.v[i];
-            const Raw mr = raw_load(mp, true, at, count, 0, 0), vr = raw_load(vp, true, at, count, 0, 0);
-            float m[RUN], v[RUN];
-            widen8(pr, ptype, p);
-            widen8(gr, gtype, g);
-            widen8(mr, kGradF32, m);
-            widen8(vr, kGradF32, v);
-            const float b1 = (float)a.beta1, r1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2, r2 = (float)(1.0 - a.beta2);
-            const float s = (float)f.scale;
-#pragma unroll
-            for (int e = 0; e < RUN; ++e) {
-                const float gs = g[e] * s;
-                m[e] = m[e] * b1 + gs * r1;
-                v[e] = v[e] * b2 + gs * gs * r2;
-                p[e] = updated(p[e], m[e], v[e], f, a.eps);
-            }
-            store_run(mp, kGradF32, m, at, count, 0, 0);
-            store_run(vp, kGradF32, v, at, count, 0, 0);
+        const int64_t begin = (c - t.first[i]) * kAdamChunk, at = begin + threadIdx.x * RUN;
+        if (t.cols[i] || begin + kAdamChunk > t.n[i]) {
+            chunk_any<EIGHT>(t, a, f, i, at);
+            continue;
         }
-        store_run(t.param[i], ptype, p, at, count, cols, t.ldp[i]);
-        if (t.ctype[i] != kNoCopy) store_run(t.copy[i], t.ctype[i], p, at, count, cols, t.ldc[i]);
+        switch (t.ptype[i] * 3 + t.gtype[i]) {        // uniform
+            case 0: chunk_fast<EIGHT, 0, 0>(t, a, f, i, at); break;
+            case 1: chunk_fast<EIGHT, 0, 1>(t, a, f, i, at); break;
+            case 2: chunk_fast<EIGHT, 0, 2>(t, a, f, i, at); break;
+            case 3: chunk_fast<EIGHT, 1, 0>(t, a, f, i, at); break;
+            case 4: chunk_fast<EIGHT, 1, 1>(t, a, f, i, at); break;
+            case 5: chunk_fast<EIGHT, 1, 2>(t, a, f, i, at); break;
+            case 6: chunk_fast<EIGHT, 2, 0>(t, a, f, i, at); break;
+            case 7: chunk_fast<EIGHT, 2, 1>(t, a, f, i, at); break;
+            default: chunk_fast<EIGHT, 2, 2>(t, a, f, i, at); break;
+        }
     }
 }
 
@@ -366,10 +403,19 @@ __global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
         while (c >= t.first[i + 1]) ++i;
         const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
         if (left <= 0) continue;
-        const int count = left >= RUN ? RUN : (int)left;
+        const uint8_t* s = t.state[i];
+        const float unit = block_unit(s[n + at / kAdamBlock]);
         float v[RUN];
-        decode8<SECOND>(load_codes(t.state[i] + at, count), block_unit(t.state[i][n + at / kAdamBlock]), v);
-        store_run(t.out[i], t.f32[i] ? kGradF32 : kGradBF16, v, at, count, t.cols[i], t.ld[i]);
+        if (left >= RUN && t.cols[i] == 0) {
+            decode8<SECOND>(load_codes(s + at), unit, v);
+            if (t.f32[i]) store_run<kGradF32>(t.out[i], v, at);
+            else store_run<kGradBF16>(t.out[i], v, at);
+        } else {
+            const int count = left >= RUN ? RUN : (int)left;
+            decode8<SECOND>(load_codes(s + at, count), unit, v);
+            each_value(at, count, t.cols[i], t.ld[i],
+                       [&](int e, int64_t o) { put_at(t.out[i], t.f32[i] ? kGradF32 : kGradBF16, o, v[e]); });
+        }
     }
 }
 
