@@ -667,12 +667,13 @@ int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, i
  *
  * state_bits 32: floats.  state_bits 8: rows * cols codes, then a byte k + 127 for each block
  * of LINEAR_ADAMW_BLOCK values, whose codes count in units of 2^k; k is the smallest from -100
- * on for which the block's largest finite magnitude is under 464 * 2^k (m) or 63488 * 2^k (v).
- * m: a sign, 4 bits of exponent (bias 7) and 3 of mantissa, subnormals at exponent 0, code 127
- * NaN (infinities are stored as that).  v: 5 bits of exponent (bias 15), 3 of mantissa, code
- * 248 infinity, 249 to 255 NaN.  Magnitudes from 1.9375 * 2^127 on count as infinite.  Values are rounded to nearest even from an FP64 m and v (so off
- * by at most 2^-4 of their value, or half the smallest spacing); a v over zero is at least the
- * first code.  p is updated with m and v before that rounding.
+ * on for which the block's largest finite magnitude, rounded to binary32, is under 464 * 2^k (m)
+ * or 63488 * 2^k (v).  m: a sign, 4 bits of exponent (bias 7) and 3 of mantissa, subnormals at
+ * exponent 0, code 127 NaN (infinities are stored as that).  v: 5 bits of exponent (bias 15), 3
+ * of mantissa, code 248 infinity, 249 to 255 NaN.  Magnitudes from 1.9375 * 2^127 on count as
+ * infinite.  Values are rounded to nearest even from an FP64 m and v (so off by at most 2^-4 of
+ * their value, or half the smallest spacing); a v over zero is at least the first code.  p is
+ * updated with m and v before that rounding.
  *
  * norm: device memory (linear_grad_norm's), or NULL; a NaN norm makes everything NaN, an
  * infinite one s zero, as for linear_grad_clip.  device_lr, device_step: device memory read

@@ -119,72 +119,91 @@ __device__ inline void store_codes(uint8_t* p, uint2 c, int count) {
 // 2^k of a block's byte k + 127 (0 for a byte of 0: a state of zero bytes is a state of zeros).
 __device__ inline float block_unit(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
 
+// The numbers of 4 codes, in units of their block.
 template <bool SECOND>
-__device__ inline void decode4(uint32_t codes, float unit, float* out) {
+__device__ inline void decode4(uint32_t codes, float* out) {
     if constexpr (SECOND) {
         // a code is bits 7 .. 14 of a binary16 word
         const uint32_t a = __builtin_amdgcn_perm(0u, codes, 0x0c010c00u) << 7, b = __builtin_amdgcn_perm(0u, codes, 0x0c030c02u) << 7;
-        out[0] = widen<kF16>((uint16_t)a) * unit;
-        out[1] = widen<kF16>((uint16_t)(a >> 16)) * unit;
-        out[2] = widen<kF16>((uint16_t)b) * unit;
-        out[3] = widen<kF16>((uint16_t)(b >> 16)) * unit;
+        out[0] = widen<kF16>((uint16_t)a);
+        out[1] = widen<kF16>((uint16_t)(a >> 16));
+        out[2] = widen<kF16>((uint16_t)b);
+        out[3] = widen<kF16>((uint16_t)(b >> 16));
     } else {
         typedef float f32x2 __attribute__((ext_vector_type(2)));
         const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(codes, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(codes, true);
-        out[0] = a[0] * unit;
-        out[1] = a[1] * unit;
-        out[2] = b[0] * unit;
-        out[3] = b[1] * unit;
+        out[0] = a[0];
+        out[1] = a[1];
+        out[2] = b[0];
+        out[3] = b[1];
     }
 }
 
 template <bool SECOND>
-__device__ inline void decode8(uint2 codes, float unit, float (&out)[RUN]) {
-    decode4<SECOND>(codes.x, unit, out);
-    decode4<SECOND>(codes.y, unit, out + 4);
+__device__ inline void decode8(uint2 codes, float (&out)[RUN]) {
+    decode4<SECOND>(codes.x, out);
+    decode4<SECOND>(codes.y, out + 4);
 }
 
 __device__ inline uint32_t high_word(double v) { return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32); }
 __device__ inline double from_high(uint32_t hi) { return __builtin_bit_cast(double, (uint64_t)hi << 32); }
 
 template <int CTRL>
-__device__ inline uint32_t dpp_max(uint32_t v) {
-    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
-    return v > o ? v : o;
+__device__ inline float dpp_max(float v) {
+    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false)));
 }
 
-// The codes of 8 values (0 past a tensor's end) and their block's byte; the four lanes of a quad
-// hold a block.
+// The largest over the four lanes of a quad, which hold a block.
+__device__ inline float block_max(float v) { return dpp_max<0x4E>(dpp_max<0xB1>(v)); }   // quad_perm [1, 0, 3, 2], [2, 3, 0, 1]
+
+// From here on a magnitude counts as infinite: rounded to a code, it could leave binary32's range.
+constexpr float kEndless = 0x1.fp127f;
+
+// The codes of 8 values (0 past a tensor's end), given in FP32 too, and their block's byte.  What is
+// rare (infinities, second moments that would round to zero) is looked for once a run and put right
+// behind a branch.
 template <bool SECOND>
-__device__ inline uint2 encode8(const double (&v)[RUN], uint32_t& byte) {
-    // from 1.9375 * 2^127 on a value counts as infinite: rounded, it would leave binary32's range
-    constexpr uint32_t kNotFinite = 0x47ef0000u;
-    // the upper words order the magnitudes as finely as the borders need: those have 5 bits
-    uint32_t top = 0;
-    bool odd = false;
+__device__ inline uint2 encode8(const double (&v)[RUN], const float (&f)[RUN], uint32_t& byte) {
+    float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < RUN; ++e) {
-        const uint32_t h = high_word(v[e]) & 0x7fffffffu;
-        odd |= h >= kNotFinite;
-        top = h >= kNotFinite || h < top ? top : h;
+    for (int e = 0; e < RUN; ++e) top = fmaxf(top, __builtin_fabsf(f[e]));   // (leaves out NaN)
+    top = block_max(top);
+    const bool endless = top >= kEndless;
+    if (endless) {
+        top = 0.f;
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) top = __builtin_fabsf(f[e]) < kEndless ? fmaxf(top, __builtin_fabsf(f[e])) : top;
+        top = block_max(top);                         // (a quad takes this branch as one)
     }
-    top = dpp_max<0xB1>(top);                         // quad_perm [1, 0, 3, 2]
-    top = dpp_max<0x4E>(top);                         // quad_perm [2, 3, 0, 1]
     // 464 = 1.8125 * 2^8, 63488 = 1.9375 * 2^15: from there on the next power of two
-    const int e = (int)((top + (SECOND ? 0x10000u : 0x30000u)) >> 20) - 1023;
-    const int k = max(e - (SECOND ? 15 : 8), -100);
+    const int x = (int)((__builtin_bit_cast(uint32_t, top) + (SECOND ? 0x80000u : 0x180000u)) >> 23) - 127;
+    const int k = max(x - (SECOND ? 15 : 8), -100);
     byte = (uint32_t)(k + 127);
-    const double unit = from_high((uint32_t)(1023 - k) << 20);   // 2^-k
+    const float inverse = __builtin_bit_cast(float, (uint32_t)(127 - k) << 23);
+    const uint32_t low = (uint32_t)(1023 + k - (SECOND ? 14 : 6)) << 20;   // the smallest normal code, as an upper word
     float r[RUN];
 #pragma unroll
-    for (int i = 0; i < RUN; ++i) {
-        const double y = v[i] * unit;
-        // rounded to 4 significant bits (the subnormals to their spacing) by an addition of
-        // 1.5 * 2^(49 + its exponent)
-        const uint32_t x = max((high_word(y) >> 20) & 0x7ffu, (uint32_t)(1023 - (SECOND ? 14 : 6)));
-        const double big = from_high(((x + 49u) << 20) | 0x80000u);
-        r[i] = (float)((y + big) - big);
-        if constexpr (SECOND) r[i] = v[i] > 0.0 ? fmaxf(r[i], 0x1p-17f) : r[i];
+    for (int e = 0; e < RUN; ++e) {
+        // Rounded to 4 significant bits (the subnormals to their spacing) by adding, and taking away,
+        // 2^49 times the number's upper word: the sum's last place is then the code's, and the large
+        // number an even count of those.
+        const uint32_t h = SECOND ? high_word(v[e]) : high_word(v[e]) & 0x7fffffffu;
+        const double big = from_high(max(h, low) + (49u << 20));
+        r[e] = (float)((__builtin_fabs(v[e]) + big) - big) * inverse;
+    }
+    if constexpr (SECOND) {
+        float least = r[0];
+#pragma unroll
+        for (int e = 1; e < RUN; ++e) least = fminf(least, r[e]);
+        if (least == 0.f) {
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) r[e] = r[e] == 0.f && v[e] > 0.0 ? 0x1p-17f : r[e];
+        }
+    }
+    if (endless) {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e)
+            r[e] = __builtin_fabsf(f[e]) >= kEndless ? (SECOND ? __builtin_inff() : __builtin_nanf("")) : r[e];
     }
     uint2 c;
     if constexpr (SECOND) {
@@ -195,21 +214,13 @@ __device__ inline uint2 encode8(const double (&v)[RUN], uint32_t& byte) {
         c.x = __builtin_amdgcn_perm(w[1], w[0], 0x06040200u);
         c.y = __builtin_amdgcn_perm(w[3], w[2], 0x06040200u);
     } else {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) r[e] = __builtin_copysignf(r[e], f[e]);
         int a = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false), b = __builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
         a = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], a, true);
         b = __builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], b, true);
         c.x = (uint32_t)a;
         c.y = (uint32_t)b;
-    }
-    if (odd) {                                        // infinities and NaN
-#pragma unroll
-        for (int i = 0; i < RUN; ++i) {
-            const uint32_t h = high_word(v[i]) & 0x7fffffffu;
-            if (h < kNotFinite) continue;
-            const uint32_t code = !SECOND ? 127u : v[i] != v[i] ? 255u : 248u;
-            uint32_t& word = i < 4 ? c.x : c.y;
-            word = (word & ~(0xffu << (8 * (i & 3)))) | (code << (8 * (i & 3)));
-        }
     }
     return c;
 }
@@ -272,19 +283,23 @@ __device__ inline void step32(const AdamArgs& a, const Factors& f, float (&p)[RU
 __device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN], const float (&g)[RUN], uint2& mc, uint2& vc,
                              uint32_t& mb, uint32_t& vb) {
     float mf[RUN], vf[RUN];
-    decode8<false>(mc, block_unit(mb), mf);
-    decode8<true>(vc, block_unit(vb), vf);
-    const double r1 = 1.0 - a.beta1, r2 = 1.0 - a.beta2;
+    decode8<false>(mc, mf);
+    decode8<true>(vc, vf);
+    // (a block's unit is a power of two: in the factor it changes no rounding)
+    const double m1 = (double)block_unit(mb) * a.beta1, r1 = 1.0 - a.beta1;
+    const double m2 = (double)block_unit(vb) * a.beta2, r2 = 1.0 - a.beta2;
     double m[RUN], v[RUN];
 #pragma unroll
     for (int e = 0; e < RUN; ++e) {
         const double gd = (double)g[e] * f.scale;
-        m[e] = (double)mf[e] * a.beta1 + gd * r1;
-        v[e] = (double)vf[e] * a.beta2 + gd * gd * r2;
-        p[e] = updated(p[e], (float)m[e], (float)v[e], f, a.eps);
+        m[e] = (double)mf[e] * m1 + gd * r1;
+        v[e] = (double)vf[e] * m2 + gd * gd * r2;
+        mf[e] = (float)m[e];
+        vf[e] = (float)v[e];
+        p[e] = updated(p[e], mf[e], vf[e], f, a.eps);
     }
-    mc = encode8<false>(m, mb);
-    vc = encode8<true>(v, vb);
+    mc = encode8<false>(m, mf, mb);
+    vc = encode8<true>(v, vf, vb);
 }
 
 // A chunk of a tensor without gaps that lies inside it, of types P and G: every load is issued
@@ -407,12 +422,16 @@ __global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
         const float unit = block_unit(s[n + at / kAdamBlock]);
         float v[RUN];
         if (left >= RUN && t.cols[i] == 0) {
-            decode8<SECOND>(load_codes(s + at), unit, v);
+            decode8<SECOND>(load_codes(s + at), v);
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) v[e] *= unit;
             if (t.f32[i]) store_run<kGradF32>(t.out[i], v, at);
             else store_run<kGradBF16>(t.out[i], v, at);
         } else {
             const int count = left >= RUN ? RUN : (int)left;
-            decode8<SECOND>(load_codes(s + at, count), unit, v);
+            decode8<SECOND>(load_codes(s + at, count), v);
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) v[e] *= unit;
             each_value(at, count, t.cols[i], t.ld[i],
                        [&](int e, int64_t o) { put_at(t.out[i], t.f32[i] ? kGradF32 : kGradBF16, o, v[e]); });
         }

@@ -46,11 +46,13 @@ def encode(x, second):
     lv = levels(second).to(x.device)
     middle = (lv[1:] + lv[:-1]) / 2
     border, nan = (63488.0, 255) if second else (464.0, 127)
-    odd = ~(x.abs() < 1.9375 * 2.0 ** 127)
+    held = x.float().abs()                            # magnitudes are judged as FP32 holds them
+    odd = ~(held < 1.9375 * 2.0 ** 127)
+    held = torch.nn.functional.pad(torch.where(odd, 0.0, held), (0, -n % BLOCK)).reshape(-1, BLOCK).amax(1).double()
     a = torch.nn.functional.pad(torch.where(odd, 0.0, x.abs()), (0, -n % BLOCK)).reshape(-1, BLOCK)
     k = torch.full((a.shape[0],), -100, dtype=torch.int32, device=x.device)
     for _ in range(230):                              # the smallest k from -100 on that the largest fits under
-        k += (a.amax(1) >= border * power(k)).int()
+        k += (held >= border * power(k)).int()
     y = (a * power(-k)[:, None]).reshape(-1)[:n]
     code = torch.searchsorted(middle, y)              # the lower of two as near
     code += ((code % 2 == 1) & (code < middle.numel()) & (y == middle[code.clamp(max=middle.numel() - 1)])).long()
@@ -58,8 +60,15 @@ def encode(x, second):
         code = torch.where((y > 0) & (code == 0), 1, code)
         code = torch.where(odd, torch.where(x.isnan(), 255, 248), code)
     else:
-        code = torch.where(odd, 127, code) + 128 * ((x < 0) & (code > 0) & ~odd).long()
+        code = torch.where(odd, 127, code) + 128 * torch.signbit(x).long()
     return torch.cat([code.to(torch.uint8), (k + 127).to(torch.uint8)])
+
+
+def same_state(a, b, n, second):
+    """The same units, and codes that stand for the same numbers (a zero's sign, and which of the codes
+    for NaN, are not told apart)."""
+    x, y = decode(a, n, second), decode(b, n, second)
+    return torch.equal(a[n:], b[n:]) and bool(((x == y) | (x.isnan() & y.isnan())).all())
 
 
 def clip_scale(norm, max_norm):
