@@ -10,7 +10,7 @@ namespace lin {
 constexpr int kAdamTensors = 40;
 constexpr int kAdamRun = 8;                           // consecutive values of a thread
 constexpr int kAdamChunk = 256 * kAdamRun;            // values of one workgroup step
-constexpr int kAdamGrid = 2048;                       // most workgroups
+constexpr int kAdamGrid = 1 << 23;                    // most workgroups
 constexpr int kAdamBlock = 32;                        // values that share a power of two (8-bit moments)
 enum : int { kNoCopy = 3 };                           // beside kGradF16, kGradBF16 and kGradF32
 
@@ -29,6 +29,7 @@ struct AdamTable {
 struct AdamArgs {
     double lr, beta1, beta2, weight_decay;
     double bias1, bias2;             // 1 - beta^step; not read where device_step is given
+    float keep, rate, root;          // the kernel's Factors; not read where a device scalar is given
     float eps, max_norm;
     const float* norm;               // null: no clipping
     const float* device_lr;          // not null: read instead of lr

@@ -6,8 +6,9 @@
 //
 // One pass: weights, gradients and moments are read once, weights and moments written.  Up to
 // kAdamTensors tensors go into one launch, their table in the kernel's arguments; a tensor's
-// values, in row-major order, are cut into chunks of kAdamChunk, and workgroup w takes the w-th
-// share of all chunks in their order.  A thread takes 8 consecutive values.
+// values, in row-major order, are cut into chunks of kAdamChunk, one for each workgroup (shares of
+// many chunks a workgroup read and wrote as many distant streams at once: 10% slower).  A thread
+// takes 8 consecutive values.
 //
 // 8-bit moments: n codes, then a byte k + 127 for each block of 32 values, whose codes count in
 // units of 2^k.  The first moment's codes are a sign, 4 bits of exponent and 3 of mantissa (the
@@ -225,14 +226,15 @@ __device__ inline uint2 encode8(const double (&v)[RUN], const float (&f)[RUN], u
     return c;
 }
 
-// A step's factors.
+// A step's factors, the same on every thread.  What the host knows it has computed.
 struct Factors {
     double scale;                    // of the gradients
     float keep, rate, root;          // 1 - lr weight_decay, lr / bias1, 1 / sqrt(bias2)
 };
 
-__device__ inline Factors factors(const AdamArgs& a, Factors* shared) {
-    if (threadIdx.x == 0) {
+__device__ inline Factors factors(const AdamArgs& a) {
+    Factors f{1.0, a.keep, a.rate, a.root};
+    if (a.device_lr || a.device_step) {
         const double lr = a.device_lr ? (double)*a.device_lr : a.lr;
         double bias1 = a.bias1, bias2 = a.bias2;
         if (a.device_step) {
@@ -240,19 +242,15 @@ __device__ inline Factors factors(const AdamArgs& a, Factors* shared) {
             bias1 = 1.0 - pow(a.beta1, step);
             bias2 = 1.0 - pow(a.beta2, step);
         }
-        Factors f;
-        f.scale = 1.0;
-        if (a.norm) {
-            const double s = (double)a.max_norm / ((double)*a.norm + 1e-6);
-            f.scale = s >= 1.0 ? 1.0 : s;             // a NaN scale stays
-        }
         f.keep = (float)(1.0 - lr * a.weight_decay);
         f.rate = (float)(lr / bias1);
         f.root = (float)(1.0 / sqrt(bias2));
-        *shared = f;
     }
-    __syncthreads();
-    return *shared;
+    if (a.norm) {
+        const double s = (double)a.max_norm / ((double)*a.norm + 1e-6);
+        f.scale = s >= 1.0 ? 1.0 : s;                 // a NaN scale stays
+    }
+    return f;
 }
 
 // sqrt(v) within 2 FP32 steps, for subnormal v too (which the instruction takes for zero).
@@ -381,15 +379,24 @@ __device__ __forceinline__ void chunk_any(const AdamTable& t, const AdamArgs& a,
         each_value(at, count, cols, t.ldc[i], [&](int e, int64_t o) { put_at(t.copy[i], t.ctype[i], o, p[e]); });
 }
 
+// The tensor that holds chunk c: the last whose first chunk is <= c.
+template <typename Table>
+__device__ inline int tensor_of(const Table& t, int64_t c) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+// One chunk per workgroup, in their order (past the grid's limit the next ones after it).
 template <bool EIGHT>
 __global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
-    __shared__ Factors shared;
-    const Factors f = factors(a, &shared);
-    const int64_t chunks = t.first[t.count];
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    int i = 0;
-    for (int64_t c = c0; c < c1; ++c) {
-        while (c >= t.first[i + 1]) ++i;
+    const Factors f = factors(a);
+    for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+        const int i = tensor_of(t, c);
         const int64_t begin = (c - t.first[i]) * kAdamChunk, at = begin + threadIdx.x * RUN;
         if (t.cols[i] || begin + kAdamChunk > t.n[i]) {
             chunk_any<EIGHT>(t, a, f, i, at);
@@ -411,11 +418,8 @@ __global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
 
 template <bool SECOND>
 __global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
-    const int64_t chunks = t.first[t.count];
-    const int64_t c0 = chunks * blockIdx.x / gridDim.x, c1 = chunks * (blockIdx.x + 1) / gridDim.x;
-    int i = 0;
-    for (int64_t c = c0; c < c1; ++c) {
-        while (c >= t.first[i + 1]) ++i;
+    for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
+        const int i = tensor_of(t, c);
         const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
         if (left <= 0) continue;
         const uint8_t* s = t.state[i];

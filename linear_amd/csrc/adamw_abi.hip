@@ -118,6 +118,9 @@ int32_t linear_adamw(const linear_tensor* params, const linear_tensor* grads, vo
     a.weight_decay = o.weight_decay;
     a.bias1 = 1.0 - pow(o.beta1, (double)o.step);
     a.bias2 = 1.0 - pow(o.beta2, (double)o.step);
+    a.keep = (float)(1.0 - o.lr * o.weight_decay);
+    a.rate = (float)(o.lr / a.bias1);
+    a.root = (float)(1.0 / sqrt(a.bias2));
     a.eps = (float)o.eps;
     a.max_norm = o.max_norm;
     a.norm = o.norm;
