@@ -149,9 +149,23 @@ __device__ inline void decode8(uint2 codes, float (&out)[RUN]) {
 __device__ inline uint32_t high_word(double v) { return (uint32_t)(__builtin_bit_cast(uint64_t, v) >> 32); }
 __device__ inline double from_high(uint32_t hi) { return __builtin_bit_cast(double, (uint64_t)hi << 32); }
 
+// max(a, |b|, |c|) and min(a, b, c), a NaN left out (fmaxf makes three instructions of each maximum:
+// it quiets its operands first).
+__device__ inline float max3_abs(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, abs(%2), abs(%3)" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ inline float min3(float a, float b, float c) {
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
 template <int CTRL>
 __device__ inline float dpp_max(float v) {
-    return fmaxf(v, __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false)));
+    const float o = __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+    return max3_abs(v, o, o);
 }
 
 // The largest over the four lanes of a quad, which hold a block.
@@ -167,7 +181,7 @@ template <bool SECOND>
 __device__ inline uint2 encode8(const double (&v)[RUN], const float (&f)[RUN], uint32_t& byte) {
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < RUN; ++e) top = fmaxf(top, __builtin_fabsf(f[e]));   // (leaves out NaN)
+    for (int e = 0; e < RUN; e += 2) top = max3_abs(top, f[e], f[e + 1]);
     top = block_max(top);
     const bool endless = top >= kEndless;
     if (endless) {
@@ -193,9 +207,9 @@ __device__ inline uint2 encode8(const double (&v)[RUN], const float (&f)[RUN], u
         r[e] = (float)((__builtin_fabs(v[e]) + big) - big) * inverse;
     }
     if constexpr (SECOND) {
-        float least = r[0];
+        float least = __builtin_inff();
 #pragma unroll
-        for (int e = 1; e < RUN; ++e) least = fminf(least, r[e]);
+        for (int e = 0; e < RUN; e += 2) least = min3(least, r[e], r[e + 1]);
         if (least == 0.f) {
 #pragma unroll
             for (int e = 0; e < RUN; ++e) r[e] = r[e] == 0.f && v[e] > 0.0 ? 0x1p-17f : r[e];
@@ -260,8 +274,8 @@ __device__ inline float root_of(float v) {
     return low ? s * 0x1p-40f : s;
 }
 
-__device__ inline float updated(float p, float m, float v, const Factors& f, float eps) {
-    return p * f.keep - (f.rate * m) * __builtin_amdgcn_rcpf(root_of(v) * f.root + eps);
+__device__ inline float updated(float p, float m, float root, const Factors& f, float eps) {
+    return p * f.keep - (f.rate * m) * __builtin_amdgcn_rcpf(root * f.root + eps);
 }
 
 // The moments of 8 values after the step, and the values.
@@ -274,7 +288,7 @@ __device__ inline void step32(const AdamArgs& a, const Factors& f, float (&p)[RU
         const float gs = g[e] * s;
         m[e] = m[e] * b1 + gs * r1;
         v[e] = v[e] * b2 + gs * gs * r2;
-        p[e] = updated(p[e], m[e], v[e], f, a.eps);
+        p[e] = updated(p[e], m[e], root_of(v[e]), f, a.eps);
     }
 }
 
@@ -294,7 +308,14 @@ __device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN
         v[e] = (double)vf[e] * m2 + gd * gd * r2;
         mf[e] = (float)m[e];
         vf[e] = (float)v[e];
-        p[e] = updated(p[e], mf[e], vf[e], f, a.eps);
+    }
+    // the root of a subnormal v is under 2^-63: nothing beside an eps of 2^-36 or more
+    if (a.eps < 0x1p-36f) {                           // uniform
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) p[e] = updated(p[e], mf[e], root_of(vf[e]), f, a.eps);
+    } else {
+#pragma unroll
+        for (int e = 0; e < RUN; ++e) p[e] = updated(p[e], mf[e], __builtin_amdgcn_sqrtf(vf[e]), f, a.eps);
     }
     mc = encode8<false>(m, mf, mb);
     vc = encode8<true>(v, vf, vb);
