@@ -9,7 +9,13 @@ namespace lin {
 // Tensors of one launch, in its kernel arguments.
 constexpr int kAdamTensors = 40;
 constexpr int kAdamRun = 8;                           // consecutive values of a thread
-constexpr int kAdamChunk = 256 * kAdamRun;            // values of one workgroup step
+constexpr int kAdamRuns = 256 * kAdamRun;             // values of a workgroup's run
+// Runs of a workgroup's chunk: with 8-bit moments, and for their values, what a workgroup does
+// before its first load counts (486 M bf16 values: the step with one run 1210 us, with two 1080;
+// the values with one 350, with four 242).
+constexpr int adam_runs(bool eight) { return eight ? 2 : 1; }
+constexpr int adam_chunk(bool eight) { return adam_runs(eight) * kAdamRuns; }
+constexpr int kValueRuns = 4, kValueChunk = kValueRuns * kAdamRuns;
 constexpr int kAdamGrid = 1 << 23;                    // most workgroups
 constexpr int kAdamBlock = 32;                        // values that share a power of two (8-bit moments)
 enum : int { kNoCopy = 3 };                           // beside kGradF16, kGradBF16 and kGradF32

@@ -6,7 +6,7 @@
 //
 // One pass: weights, gradients and moments are read once, weights and moments written.  Up to
 // kAdamTensors tensors go into one launch, their table in the kernel's arguments; a tensor's
-// values, in row-major order, are cut into chunks of kAdamChunk, one for each workgroup (shares of
+// values, in row-major order, are cut into chunks, one for each workgroup (shares of
 // many chunks a workgroup read and wrote as many distant streams at once: 10% slower).  A thread
 // takes 8 consecutive values.
 //
@@ -296,19 +296,27 @@ __device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN
                              uint32_t& mb, uint32_t& vb) {
     float mf[RUN], vf[RUN];
     decode8<false>(mc, mf);
-    decode8<true>(vc, vf);
     // (a block's unit is a power of two: in the factor it changes no rounding)
-    const double m1 = (double)block_unit(mb) * a.beta1, r1 = 1.0 - a.beta1;
-    const double m2 = (double)block_unit(vb) * a.beta2, r2 = 1.0 - a.beta2;
-    double m[RUN], v[RUN];
+    const double m1 = (double)block_unit(mb) * a.beta1, m2 = (double)block_unit(vb) * a.beta2;
+    const double r1 = 1.0 - a.beta1, r2 = 1.0 - a.beta2;
+    // one moment after the other, held apart: together they take registers that waves could have
+    double gd[RUN], w[RUN];
 #pragma unroll
     for (int e = 0; e < RUN; ++e) {
-        const double gd = (double)g[e] * f.scale;
-        m[e] = (double)mf[e] * m1 + gd * r1;
-        v[e] = (double)vf[e] * m2 + gd * gd * r2;
-        mf[e] = (float)m[e];
-        vf[e] = (float)v[e];
+        gd[e] = (double)g[e] * f.scale;
+        w[e] = (double)mf[e] * m1 + gd[e] * r1;
+        mf[e] = (float)w[e];
     }
+    mc = encode8<false>(w, mf, mb);
+    __builtin_amdgcn_sched_barrier(0);
+    decode8<true>(vc, vf);
+#pragma unroll
+    for (int e = 0; e < RUN; ++e) {
+        w[e] = (double)vf[e] * m2 + gd[e] * gd[e] * r2;
+        vf[e] = (float)w[e];
+    }
+    vc = encode8<true>(w, vf, vb);
+    __builtin_amdgcn_sched_barrier(0);
     // the root of a subnormal v is under 2^-63: nothing beside an eps of 2^-36 or more
     if (a.eps < 0x1p-36f) {                           // uniform
 #pragma unroll
@@ -317,50 +325,70 @@ __device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN
 #pragma unroll
         for (int e = 0; e < RUN; ++e) p[e] = updated(p[e], mf[e], __builtin_amdgcn_sqrtf(vf[e]), f, a.eps);
     }
-    mc = encode8<false>(m, mf, mb);
-    vc = encode8<true>(v, vf, vb);
 }
 
 // A chunk of a tensor without gaps that lies inside it, of types P and G: every load is issued
 // before the first is used.
 template <bool EIGHT, int P, int G>
-__device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
-    const Run<P> pr = load_run<P>(t.param[i], at);
-    const Run<G> gr = load_run<G>(t.grad[i], at);
+__device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t begin) {
+    constexpr int U = adam_runs(EIGHT);
+    const int64_t at = begin + threadIdx.x * RUN;
+    Run<P> pr[U];
+    Run<G> gr[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        pr[u] = load_run<P>(t.param[i], at + u * kAdamRuns);
+        gr[u] = load_run<G>(t.grad[i], at + u * kAdamRuns);
+    }
     float p[RUN], g[RUN];
+    const auto leave = [&](int u) {
+        store_run<P>(t.param[i], p, at + u * kAdamRuns);
+        if (t.ctype[i] == kGradBF16) store_run<kGradBF16>(t.copy[i], p, at + u * kAdamRuns);
+        else if (t.ctype[i] == kGradF16) store_run<kGradF16>(t.copy[i], p, at + u * kAdamRuns);
+    };
     if constexpr (EIGHT) {
-        uint8_t *ms = (uint8_t*)t.m[i], *vs = (uint8_t*)t.v[i];
-        const int64_t block = t.n[i] + at / kAdamBlock;
-        uint2 mc = load_codes(ms + at), vc = load_codes(vs + at);
-        uint32_t mb = ms[block], vb = vs[block];
-        widen_run<P>(pr, p);
-        widen_run<G>(gr, g);
-        step8(a, f, p, g, mc, vc, mb, vb);
-        store_codes(ms + at, mc);
-        store_codes(vs + at, vc);
-        if ((threadIdx.x & 3) == 0) {
-            ms[block] = (uint8_t)mb;
-            vs[block] = (uint8_t)vb;
+        uint8_t *ms = (uint8_t*)t.m[i] + at, *vs = (uint8_t*)t.v[i] + at;
+        uint8_t *mk = (uint8_t*)t.m[i] + t.n[i] + at / kAdamBlock, *vk = (uint8_t*)t.v[i] + t.n[i] + at / kAdamBlock;
+        uint2 mc[U], vc[U];
+        uint32_t mb[U], vb[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            mc[u] = load_codes(ms + u * kAdamRuns);
+            vc[u] = load_codes(vs + u * kAdamRuns);
+            mb[u] = mk[u * kAdamRuns / kAdamBlock];
+            vb[u] = vk[u * kAdamRuns / kAdamBlock];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            widen_run<P>(pr[u], p);
+            widen_run<G>(gr[u], g);
+            step8(a, f, p, g, mc[u], vc[u], mb[u], vb[u]);
+            store_codes(ms + u * kAdamRuns, mc[u]);
+            store_codes(vs + u * kAdamRuns, vc[u]);
+            if ((threadIdx.x & 3) == 0) {
+                mk[u * kAdamRuns / kAdamBlock] = (uint8_t)mb[u];
+                vk[u * kAdamRuns / kAdamBlock] = (uint8_t)vb[u];
+            }
+            leave(u);
         }
     } else {
+        static_assert(U == 1, "one run");
         const Run<kGradF32> mr = load_run<kGradF32>(t.m[i], at), vr = load_run<kGradF32>(t.v[i], at);
         float m[RUN], v[RUN];
-        widen_run<P>(pr, p);
-        widen_run<G>(gr, g);
+        widen_run<P>(pr[0], p);
+        widen_run<G>(gr[0], g);
         widen_run<kGradF32>(mr, m);
         widen_run<kGradF32>(vr, v);
         step32(a, f, p, g, m, v);
         store_run<kGradF32>(t.m[i], m, at);
         store_run<kGradF32>(t.v[i], v, at);
+        leave(0);
     }
-    store_run<P>(t.param[i], p, at);
-    if (t.ctype[i] == kGradBF16) store_run<kGradBF16>(t.copy[i], p, at);
-    else if (t.ctype[i] == kGradF16) store_run<kGradF16>(t.copy[i], p, at);
 }
 
-// Any chunk.  Lanes past the end take part in their block's maximum with zeros.
+// Any run.  Lanes past the end take part in their block's maximum with zeros.
 template <bool EIGHT>
-__device__ __forceinline__ void chunk_any(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
+__device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
     const int64_t n = t.n[i], left = n - at, cols = t.cols[i];
     const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
     float p[RUN] = {}, g[RUN] = {};
@@ -414,25 +442,25 @@ __device__ inline int tensor_of(const Table& t, int64_t c) {
 
 // One chunk per workgroup, in their order (past the grid's limit the next ones after it).
 template <bool EIGHT>
-__global__ void __launch_bounds__(256) adamw(AdamTable t, AdamArgs a) {
+__global__ void __launch_bounds__(256, 4) adamw(AdamTable t, AdamArgs a) {
     const Factors f = factors(a);
     for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const int i = tensor_of(t, c);
-        const int64_t begin = (c - t.first[i]) * kAdamChunk, at = begin + threadIdx.x * RUN;
-        if (t.cols[i] || begin + kAdamChunk > t.n[i]) {
-            chunk_any<EIGHT>(t, a, f, i, at);
+        const int64_t begin = (c - t.first[i]) * adam_chunk(EIGHT);
+        if (t.cols[i] || begin + adam_chunk(EIGHT) > t.n[i]) {
+            for (int u = 0; u < adam_runs(EIGHT); ++u) run_any<EIGHT>(t, a, f, i, begin + u * kAdamRuns + threadIdx.x * RUN);
             continue;
         }
         switch (t.ptype[i] * 3 + t.gtype[i]) {        // uniform
-            case 0: chunk_fast<EIGHT, 0, 0>(t, a, f, i, at); break;
-            case 1: chunk_fast<EIGHT, 0, 1>(t, a, f, i, at); break;
-            case 2: chunk_fast<EIGHT, 0, 2>(t, a, f, i, at); break;
-            case 3: chunk_fast<EIGHT, 1, 0>(t, a, f, i, at); break;
-            case 4: chunk_fast<EIGHT, 1, 1>(t, a, f, i, at); break;
-            case 5: chunk_fast<EIGHT, 1, 2>(t, a, f, i, at); break;
-            case 6: chunk_fast<EIGHT, 2, 0>(t, a, f, i, at); break;
-            case 7: chunk_fast<EIGHT, 2, 1>(t, a, f, i, at); break;
-            default: chunk_fast<EIGHT, 2, 2>(t, a, f, i, at); break;
+            case 0: chunk_fast<EIGHT, 0, 0>(t, a, f, i, begin); break;
+            case 1: chunk_fast<EIGHT, 0, 1>(t, a, f, i, begin); break;
+            case 2: chunk_fast<EIGHT, 0, 2>(t, a, f, i, begin); break;
+            case 3: chunk_fast<EIGHT, 1, 0>(t, a, f, i, begin); break;
+            case 4: chunk_fast<EIGHT, 1, 1>(t, a, f, i, begin); break;
+            case 5: chunk_fast<EIGHT, 1, 2>(t, a, f, i, begin); break;
+            case 6: chunk_fast<EIGHT, 2, 0>(t, a, f, i, begin); break;
+            case 7: chunk_fast<EIGHT, 2, 1>(t, a, f, i, begin); break;
+            default: chunk_fast<EIGHT, 2, 2>(t, a, f, i, begin); break;
         }
     }
 }
@@ -441,23 +469,35 @@ template <bool SECOND>
 __global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
     for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const int i = tensor_of(t, c);
-        const int64_t n = t.n[i], at = (c - t.first[i]) * kAdamChunk + threadIdx.x * RUN, left = n - at;
-        if (left <= 0) continue;
-        const uint8_t* s = t.state[i];
-        const float unit = block_unit(s[n + at / kAdamBlock]);
+        const int64_t n = t.n[i], begin = (c - t.first[i]) * kValueChunk, at = begin + threadIdx.x * RUN;
+        const uint8_t *s = t.state[i] + at, *k = t.state[i] + n + at / kAdamBlock;
         float v[RUN];
-        if (left >= RUN && t.cols[i] == 0) {
-            decode8<SECOND>(load_codes(s + at), v);
+        if (t.cols[i] == 0 && begin + kValueChunk <= n) {
+            uint2 codes[kValueRuns];
+            uint32_t byte[kValueRuns];
 #pragma unroll
-            for (int e = 0; e < RUN; ++e) v[e] *= unit;
-            if (t.f32[i]) store_run<kGradF32>(t.out[i], v, at);
-            else store_run<kGradBF16>(t.out[i], v, at);
-        } else {
+            for (int u = 0; u < kValueRuns; ++u) {
+                codes[u] = load_codes(s + u * kAdamRuns);
+                byte[u] = k[u * kAdamRuns / kAdamBlock];
+            }
+#pragma unroll
+            for (int u = 0; u < kValueRuns; ++u) {
+                decode8<SECOND>(codes[u], v);
+#pragma unroll
+                for (int e = 0; e < RUN; ++e) v[e] *= block_unit(byte[u]);
+                if (t.f32[i]) store_run<kGradF32>(t.out[i], v, at + u * kAdamRuns);
+                else store_run<kGradBF16>(t.out[i], v, at + u * kAdamRuns);
+            }
+            continue;
+        }
+        for (int u = 0; u < kValueRuns; ++u) {
+            const int64_t left = n - at - u * kAdamRuns;
+            if (left <= 0) break;
             const int count = left >= RUN ? RUN : (int)left;
-            decode8<SECOND>(load_codes(s + at, count), v);
+            decode8<SECOND>(load_codes(s + u * kAdamRuns, count), v);
 #pragma unroll
-            for (int e = 0; e < RUN; ++e) v[e] *= unit;
-            each_value(at, count, t.cols[i], t.ld[i],
+            for (int e = 0; e < RUN; ++e) v[e] *= block_unit(k[u * kAdamRuns / kAdamBlock]);
+            each_value(at + u * kAdamRuns, count, t.cols[i], t.ld[i],
                        [&](int e, int64_t o) { put_at(t.out[i], t.f32[i] ? kGradF32 : kGradBF16, o, v[e]); });
         }
     }

@@ -145,7 +145,7 @@ int32_t linear_adamw(const linear_tensor* params, const linear_tensor* grads, vo
             t.ptype[k] = (uint8_t)p.type;
             t.gtype[k] = (uint8_t)g.type;
             t.ctype[k] = (uint8_t)(copies ? copies[i].type : (int64_t)kNoCopy);
-            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], kAdamChunk);
+            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], adam_chunk(o.state_bits == 8));
             t.count = k + 1;
         }
         if (t.count == kAdamTensors || (i + 1 == count && t.count > 0)) {
@@ -190,7 +190,7 @@ int32_t linear_adamw_values(const linear_tensor* out, const void* const* states,
             t.cols[k] = whole(y) ? 0 : y.cols;
             t.ld[k] = (int32_t)(y.rows == 1 ? 0 : y.ld);
             t.f32[k] = y.type == LINEAR_TYPE_F32;
-            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], kAdamChunk);
+            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], kValueChunk);
             t.count = k + 1;
         }
         if (t.count == kValueTensors || (i + 1 == count && t.count > 0)) {
