@@ -15,6 +15,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import itertools
 import operator
 import os
 
@@ -563,12 +564,28 @@ def _launch_stream(stream, *tensors):
     """_stream_handle's checks for tensors on one device and the current stream, the usual
     call, at less host time; anything else goes through it."""
     if stream is None:
-        devices = {t.get_device() for t in tensors if t is not None}    # -1 on the host
-        if len(devices) == 1:
-            index = devices.pop()
-            if index >= 0 and index == torch._C._cuda_getDevice():
-                return torch._C._cuda_getCurrentRawStream(index)
+        stream_of = _current_stream({t.get_device() for t in tensors if t is not None})
+        if stream_of is not None:
+            return stream_of
     return _stream_handle(stream, *tensors)
+
+
+def _many_launch_stream(stream, *lists):
+    """_launch_stream for lists of many tensors."""
+    if stream is None:
+        stream_of = _current_stream(set(map(torch.Tensor.get_device, itertools.chain(*lists))))
+        if stream_of is not None:
+            return stream_of
+    return _stream_handle(stream, *itertools.chain(*lists))
+
+
+def _current_stream(devices):
+    """The raw current stream where the devices (-1: the host) are the current one alone, else None."""
+    if len(devices) == 1:
+        index = devices.pop()
+        if index >= 0 and index == torch._C._cuda_getDevice():
+            return torch._C._cuda_getCurrentRawStream(index)
+    return None
 
 
 _NO_CONTEXT = contextlib.nullcontext()
@@ -974,15 +991,18 @@ def grad_workspace_bytes(count: int) -> int:
 def _tensor_table(tensors, name):
     """The tensors as an array of linear_tensor (five 64-bit fields each): contiguous ones of any
     shape, as one row, and matrices with unit inner stride."""
+    n = len(tensors)
+    types = list(map(_dtype_of, tensors))
     try:
-        kinds = array.array("q", map(_TENSOR_TYPES.__getitem__, map(_dtype_of, tensors)))
+        if n and types.count(types[0]) == n:          # (the usual case, at less host time)
+            kinds = array.array("q", (_TENSOR_TYPES[types[0]],)) * n
+        else:
+            kinds = array.array("q", map(_TENSOR_TYPES.__getitem__, types))
     except KeyError as e:
         raise TypeError("%s must be float16, bfloat16 or float32, got %s" % (name, e)) from None
-    n = len(tensors)
     sizes = array.array("q", map(torch.Tensor.numel, tensors))
-    table = array.array("q", bytes(40 * n))
+    table = array.array("q", (0, 1, 0, 0, 0)) * n
     table[0::5] = array.array("q", map(torch.Tensor.data_ptr, tensors))
-    table[1::5] = array.array("q", (1,)) * n
     table[2::5] = sizes
     table[3::5] = sizes
     table[4::5] = kinds
@@ -1069,7 +1089,7 @@ def _same_sizes(tables, tensors, names):
         raise ValueError("%s must have as many tensors as %s" % (" and ".join(names[1:]), names[0]))
     first = tables[0]
     for ts, name in zip(tensors[1:], names[1:]):
-        if any(a.shape != b.shape for a, b in zip(ts, tensors[0])):
+        if not all(map(torch.Tensor.is_same_size, ts, tensors[0])):
             raise ValueError("%s must have the shapes of %s" % (name, names[0]))
     if all(t[1::5] == first[1::5] for t in tables):
         return
@@ -1083,7 +1103,7 @@ def _same_sizes(tables, tensors, names):
 def _state_pointers(states, sizes, eight, name):
     """The states' addresses, after a check of their types and sizes."""
     want = torch.uint8 if eight else torch.float32
-    if len(states) != len(sizes) or any(d != want for d in map(_dtype_of, states)):
+    if len(states) != len(sizes) or set(map(_dtype_of, states)) - {want}:
         raise ValueError("%s must have a state for each tensor, all float32 or all uint8" % name)
     held = [n + -(-n // ADAMW_BLOCK) for n in sizes] if eight else sizes
     if list(map(torch.Tensor.numel, states)) != list(held) or not all(map(torch.Tensor.is_contiguous, states)):
@@ -1132,7 +1152,7 @@ def linear_adamw(params, grads, m, v, *, lr, step, beta1: float = 0.9, beta2: fl
         scalars.append(step)
     else:
         o.step = step
-    handle = _launch_stream(stream, *params, *grads, *m, *v, *scalars, *(copies or ()))
+    handle = _many_launch_stream(stream, params, grads, m, v, scalars, copies or ())
     rc = _lib().linear_adamw(tables[0].buffer_info()[0], tables[1].buffer_info()[0], mp.buffer_info()[0], vp.buffer_info()[0],
                              tables[2].buffer_info()[0] if copies is not None else None, len(params), ctypes.byref(o), handle)
     _check(rc, "linear_adamw")
@@ -1152,7 +1172,7 @@ def linear_adamw_values(states, second: bool, out=None, like=None, stream=None):
     out = list(out)
     table = _tensor_table(out, "out")
     sp = _state_pointers(states, list(map(torch.Tensor.numel, out)), True, "states")
-    handle = _launch_stream(stream, *states, *out)
+    handle = _many_launch_stream(stream, states, out)
     rc = _lib().linear_adamw_values(table.buffer_info()[0], sp.buffer_info()[0], int(bool(second)), len(out), handle)
     _check(rc, "linear_adamw_values")
     return out
