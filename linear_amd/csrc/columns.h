@@ -30,7 +30,8 @@ __device__ inline void column_block(const ColumnSumArgs& c, int block, int split
     float* part2 = lds + G * 65;                      // [H][64]
     const int tid = threadIdx.x, c8 = (tid & 7) * 8, g = tid >> 3;
     const int n = block * 64 + c8;
-    const int m0 = (int)((int64_t)c.M * split / c.splits), m1 = (int)((int64_t)c.M * (split + 1) / c.splits);
+    const int M = c.rows ? *c.rows : c.M;
+    const int m0 = (int)((int64_t)M * split / c.splits), m1 = (int)((int64_t)M * (split + 1) / c.splits);
     float sum[8] = {};
     for (int64_t m = m0 + g; m < m1; m += 4 * G) {
         u32x4 v[4];

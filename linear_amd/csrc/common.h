@@ -55,6 +55,7 @@ struct LinearArgs {
     uint16_t *gate, *up; // the kept projections [M, N], or nullptr
     int64_t ldw2, ldgate, ldup;
     int act;             // kEpiSilu, kEpiGeluTanh or kEpiGeluErf
+    const int32_t* list; // kOutList: row m of the tile's output is row list[m] of y
 };
 
 
@@ -65,8 +66,10 @@ enum : int { kF16 = 0, kBF16 = 1 };
 // round again); round only; store the FP32 sum itself; or round and run the
 // epilogue program of a.epi.  kOutGated: two projections per output, act(g) * u.
 // kOutF32Add: add the FP32 sum to the output.  kOutLse, kOutDz: the cross entropy's row
-// statistics and its gradient by the logits (loss_impl.h).
-enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 4, kOutF32Add = 5, kOutLse = 6, kOutDz = 7 };
+// statistics and its gradient by the logits (loss_impl.h).  kOutList: kOutRound with the
+// rows placed by a list.
+enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 4, kOutF32Add = 5, kOutLse = 6, kOutDz = 7,
+             kOutList = 8 };
 
 // Grouped contraction: group g is the activation slice x + g * gsx, the weight
 // block of rows g * N .. g * N + N - 1, y + g * gsy and the bias words g * N ..

@@ -223,8 +223,11 @@ __device__ inline void epi_tile(const LinearArgs& a, const unsigned char* tile, 
             }
         }
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
-            store8((uint16_t*)a.y + (int64_t)rr[k] * a.ldy + cc[k], rr[k] < a.M, cc[k], a.N, t[k]);
+        for (int k = 0; k < CH; ++k) {
+            int64_t row = rr[k];
+            if constexpr (MODE == kOutList) row = rr[k] < a.M ? a.list[rr[k]] : 0;
+            store8((uint16_t*)a.y + row * a.ldy + cc[k], rr[k] < a.M, cc[k], a.N, t[k]);
+        }
     }
 }
 
@@ -493,6 +496,11 @@ gemm_stream(Args a) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[LDSB];
 
     int tm, tn;
+    if constexpr (MODE == kOutDz) {
+        a.M = *a.rows;                               // only the rows that have a gradient
+        a.tiles_m = (a.M + BM - 1) / BM;
+        if ((int)blockIdx.x >= a.tiles_m * a.tiles_n) return;
+    }
     stream_tile<MODE>(a, tm, tn);
     constexpr bool GATED = MODE == kOutGated;
     const int m0 = tm * BM, n0 = tn * (GATED ? BN / 2 : BN);

@@ -89,10 +89,10 @@ constexpr int grad_lds = KG * STAGES * 64 * (BM + BN) * 2;   // bytes of the rin
 
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
 __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, unsigned char* smem) {
-    constexpr int BK = 64, R = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
+    constexpr int BK = 64, RB = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
     constexpr int NW = WM * WN;
     constexpr int TM = BM / WM, TN = BN / WN;
-    constexpr int FM = TM / R, FN = TN / R;
+    constexpr int FM = TM / RB, FN = TN / RB;
     constexpr int CROW = 2 * BN, RROW = ROWT ? 2 * BM : 2 * BK;   // LDS bytes per row of each panel
     constexpr int CBYTES = BK * CROW, RBYTES = BM * BK * 2;
     constexpr int SLICE = CBYTES + RBYTES;
@@ -100,7 +100,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     constexpr int GPW = GC + GR;
     static_assert(CBYTES % (1024 * NW) == 0 && RBYTES % (1024 * NW) == 0, "loads must divide evenly over the waves");
     static_assert(BN >= 64 && BM >= 64, "panel rows of 4 or more pairs");
-    static_assert(TM % R == 0 && TN % R == 0, "whole fragments");
+    static_assert(TM % RB == 0 && TN % RB == 0, "whole fragments");
     constexpr int RING = STAGES * SLICE;
     static_assert(STAGES >= 2 && KG * RING <= 160 * 1024, "LDS rings too large");
     static_assert(KG == 1 || (KG - 1) * BM * BN * 4 <= KG * RING, "the sets' sums must fit in the rings");
@@ -116,12 +116,22 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         }
     }
 
+    int R = a.R, L = a.L, tiles_r = a.tiles_r;
+    if (a.rows) {                                     // uniform
+        if constexpr (ROWT) {
+            L = *a.rows;
+        } else {
+            R = *a.rows;
+            tiles_r = (R + BM - 1) / BM;
+            if (block >= a.splits * a.groups * tiles_r * a.tiles_c) return;
+        }
+    }
     int tr, tc;
     // row tiles of every group of every split, stacked into one grid
-    tile_coords(block, a.splits * a.groups * a.tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
-    const int stack = tr / a.tiles_r;                 // split * groups + group
+    tile_coords(block, a.splits * a.groups * tiles_r, a.tiles_c, a.xcd_shift, tr, tc);
+    const int stack = tr / tiles_r;                   // split * groups + group
     const int split = stack / a.groups, group = stack - split * a.groups;
-    const int r0 = (tr - stack * a.tiles_r) * BM, c0 = tc * BN;
+    const int r0 = (tr - stack * tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
     float back = 1.f;                                 // (read here: its latency passes under the loop)
     if (a.unscale) back = *a.unscale;
@@ -148,18 +158,18 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             const int k = byte / row, c = (byte % row / 16) ^ (2 * (col ? panel_swz<BN>(k) : panel_swz<BM>(k)));
             const int at = (col ? c0 : r0) + 8 * c;
             const int line = col ? k & lines : k;
-            goff[j] = (int)(at < (col ? a.C : a.R)) & (int)(k % kLowRow < whole)
+            goff[j] = (int)(at < (col ? a.C : R)) & (int)(k % kLowRow < whole)
                           ? (uint32_t)((line * (int)(col ? a.ldc : a.ldr) + at) * 2) : kOOB;
         } else {
             const int r = byte / RROW, c = (byte % RROW / 16) ^ ((r >> 1) & 7);
             gk[(j - GC) % 2] = 8 * c;
-            goff[j] = r0 + r < a.R ? (uint32_t)((r * (int)a.ldr + 8 * c) * 2) : kOOB;
+            goff[j] = r0 + r < R ? (uint32_t)((r * (int)a.ldr + 8 * c) * 2) : kOOB;
         }
     }
 
     // slices: each segment's contraction in slices of BK, the segments one after the other
     // (split s takes a contiguous share of all of them, and a set of it)
-    const int per = (a.L + BK - 1) / BK;
+    const int per = (L + BK - 1) / BK;
     const int s0 = (int)((int64_t)per * a.segs * split / a.splits);
     const int s1 = (int)((int64_t)per * a.segs * (split + 1) / a.splits);
     const int nk = (s1 - s0 + KG - 1) / KG;           // slices a set runs
@@ -175,12 +185,12 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     const int first = (t0 - seg * per) * BK;
     const uint16_t* cp = a.c[seg] + (int64_t)first * a.ldc;
     const uint16_t* rp = ROWT ? rbase + (int64_t)first * a.ldr : rbase + r0 * a.ldr + (int64_t)t0 * BK;
-    int left = mine > 0 ? a.L - first : 0;            // contraction indices left in the segment
+    int left = mine > 0 ? L - first : 0;            // contraction indices left in the segment
     int todo = mine;                                  // slices left to request
     uint32_t fill = base;
     const int ldc = (int)a.ldc, ldr = (int)a.ldr;
-    const int cend = (a.C + 7) & ~7, rend = (a.R + 7) & ~7;
-    const int rbytes = ((min(BM, a.R - r0) - 1) * ldr + BK) * 2;
+    const int cend = (a.C + 7) & ~7, rend = (R + 7) & ~7;
+    const int rbytes = ((min(BM, R - r0) - 1) * ldr + BK) * 2;
     auto request = [&]<int J0, int J1>() {
         const int n = min(left, BK);
         const __amdgpu_buffer_rsrc_t rc = slice_rsrc(cp, ((n - 1) * ldc + cend) * 2);
@@ -199,7 +209,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         rp += ROWT ? BK * ldr : BK;
         if (left <= 0 && seg + 1 < a.segs) {
             ++seg;
-            left = a.L;
+            left = L;
             cp = a.c[1];
         }
         if (--todo <= 0) left = 0;
@@ -235,7 +245,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             const uint2 lo = lds_tr(p + 32 * ks * RROW), hi = lds_tr(p + (32 * ks + 4) * RROW);
             return (u32x4){lo.x, lo.y, hi.x, hi.y};
         } else {
-            return *(lds_u32x4*)(lds_at(slot + roff[ks]) + j * R * RROW);
+            return *(lds_u32x4*)(lds_at(slot + roff[ks]) + j * RB * RROW);
         }
     };
 
@@ -364,10 +374,11 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     }
 
     LinearArgs o;
-    o.M = !ROWT && a.fold ? a.fold : a.R;
+    o.M = !ROWT && a.fold ? a.fold : R;
     o.N = a.C;
+    o.list = a.list;
     if (a.splits > 1) {                               // FP32 partial sums (kOutF32)
-        o.y = a.partial + (int64_t)stack * o.M * a.ldp;
+        o.y = a.partial + (int64_t)stack * (!ROWT && a.fold ? a.fold : a.R) * a.ldp;
         o.ldy = a.ldp;
     } else {
         o.y = group ? a.y[1] : a.y[0];
@@ -380,11 +391,11 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         // 8192 x 4096 x 4096 214 -> 211 us, adding to the output 224 -> 218)
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
-            const int r = r0 + wm * TM + j * R + s;
+            const int r = r0 + wm * TM + j * RB + s;
             if (r >= o.M) continue;
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
-                const int c = c0 + wn * TN + i * R + 4 * q;
+                const int c = c0 + wn * TN + i * RB + 4 * q;
                 float* y = (float*)o.y + (int64_t)r * o.ldy + c;
                 if (c + 3 < o.N) {                     // at any alignment
                     f32x4 v = acc[i][j];
@@ -402,7 +413,7 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
             }
         }
     } else {
-        finish_tile<BM, BN, WM, WN, KG * RING, E, MODE, R>(o, smem, acc, r0, c0, wave, lane);
+        finish_tile<BM, BN, WM, WN, KG * RING, E, MODE, RB>(o, smem, acc, r0, c0, wave, lane);
     }
 }
 
@@ -442,6 +453,7 @@ static const void* grad_fn(bool rowt, int mode) {
     if (!rowt) {
         if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
         if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32Add>;
+        if (mode == kOutList) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutList>;
         return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
     }
     if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;

@@ -20,9 +20,16 @@ struct LossArgs : LinearArgs {
     RowPart* parts;          // [M, ldparts]: tile tn's statistics of row m at m * ldparts + tn
     int64_t ldparts;
     float* at_target;        // [M]: z at the target, where that is one of this launch's columns
-    // kOutDz: y is dz, 16-bit words; columns from N to the next multiple of 8 are zeroed
-    const float *lse, *dloss, *dlse;   // [M]; dlse may be null
-    const float* scale;      // dz is multiplied by *scale before its rounding
+    // kOutDz: y is dz, 16-bit words; columns from N to the next multiple of 8 are zeroed.  x, terms
+    // and y hold the rows that have a gradient, *rows of them
+    const struct RowTerms* terms;
+    const int32_t* rows;
+};
+
+// What a row's dz needs: rows exp(z - lse), less one at the target's column (-1: none).
+struct RowTerms {
+    float lse, rows, one;
+    int32_t column;
 };
 
 constexpr int kNumLossConfigs = 5;
@@ -53,13 +60,38 @@ struct LossJoinArgs {
 };
 hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream);
 
-// head[0], head[1]: the factor that dz is multiplied by before its rounding, as its inverse and
-// itself: 2^e over the largest finite |dloss| of the rows that count, with e such that the
-// largest |dloss + dlse| + |dloss| ends at 2^14 .. 2^15.  dz at a row's target is near -dloss
-// for most rows, the same number in each where the loss is a mean: unscaled, all would be
-// rounded the same way, up to half a step (1024 x 1024 x 768 bf16: dx, dW, db off by 1.9 times
-// one rounding; scaled, that number is a power of two).
-hipError_t launch_loss_scale(const int64_t* target, int64_t cols, const float* dloss, const float* dlse, int64_t M,
-                             float* head, hipStream_t stream);
+// The rows that have a gradient, those with d = dloss (of the rows that count) or d + dlse other
+// than zero: their number, their places (place[m]: m's place among them or -1; list: the rows of
+// the places) and their terms.  The others are left out of all that follows: their x may hold
+// anything, and in fine tuning, where most rows are a prompt's, they are most of the work.
+//
+// d and d + dlse are multiplied by head[1], whose inverse is head[0]: 2^e over the largest finite
+// |d|, with e such that the largest |d + dlse| + |d| ends at 2^14 .. 2^15.  dz at a row's target
+// is near -d for most rows, the same number in each where the loss is a mean: unscaled, all
+// would be rounded the same way, up to half a step (1024 x 1024 x 768 bf16: dx, dW, db off by 1.9
+// times one rounding; scaled, that number is a power of two).
+struct LossRowsArgs {
+    const int64_t* target;
+    const float *dloss, *dlse, *lse;   // dlse may be null
+    int64_t cols, M;
+    float* head;
+    int32_t *rows, *place, *list;
+    RowTerms* terms;
+};
+hipError_t launch_loss_rows(const LossRowsArgs& r, hipStream_t stream);
+
+// out [rows, ldo] = the rows of x [M, K] that have a place, there, with zeros past K (ldo a
+// multiple of 8); the rows of zeroed (may be null) that have none are set to zero.
+struct LossGatherArgs {
+    const uint16_t* x;
+    int64_t ldx, M;
+    int K;
+    const int32_t* place;
+    uint16_t* out;
+    int64_t ldo;
+    uint16_t* zeroed;
+    int64_t ldz;
+};
+hipError_t launch_loss_gather(const LossGatherArgs& g, hipStream_t stream);
 
 }  // namespace lin

@@ -1,5 +1,5 @@
 // loss.hip -- the row passes of the linear head's cross entropy: the tiles' statistics joined
-// into lse and loss, and the factor that dz is rounded under.
+// into lse and loss, and the rows that have a gradient.
 #include "loss.h"
 
 namespace lin {
@@ -41,28 +41,78 @@ __global__ void __launch_bounds__(256) loss_join(LossJoinArgs j) {
     }
 }
 
-__global__ void __launch_bounds__(1024) loss_scale(const int64_t* target, int64_t cols, const float* dloss,
-                                                   const float* dlse, int64_t M, float* head) {
+struct RowWeights {
+    float d, rows;
+    int32_t column;
+};
+__device__ inline RowWeights row_weights(const LossRowsArgs& a, int64_t m) {
+    const int64_t t = a.target[m];
+    const bool counts = t >= 0 && t < a.cols;
+    const float d = counts ? a.dloss[m] : 0.f;
+    return {d, a.dlse ? d + a.dlse[m] : d, counts ? (int32_t)t : -1};
+}
+
+// One workgroup (a few us at some thousand rows, and little beside the products at millions).
+__global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a) {
     __shared__ float lds[16];
+    __shared__ int counts[16];
     float base = 0.f, most = 0.f;
-    for (int64_t m = threadIdx.x; m < M; m += 1024) {
-        const int64_t t = target[m];
-        const float d = t >= 0 && t < cols ? dloss[m] : 0.f;
-        const float v = __builtin_fabsf(dlse ? d + dlse[m] : d) + __builtin_fabsf(d);
+    for (int64_t m = threadIdx.x; m < a.M; m += 1024) {
+        const RowWeights w = row_weights(a, m);
+        const float v = __builtin_fabsf(w.rows) + __builtin_fabsf(w.d);
         if (!(v < __builtin_inff())) continue;
-        base = fmaxf(base, __builtin_fabsf(d));
+        base = fmaxf(base, __builtin_fabsf(w.d));
         most = fmaxf(most, v);
     }
     const auto largest = [](float a, float b) { return fmaxf(a, b); };
     base = group_fold<16>(base, lds, largest);
     most = group_fold<16>(most, lds, largest);
-    if (threadIdx.x != 0) return;
     // (rows below 2^-80 are left smaller: the factor stays finite)
     base = fmaxf(base > 0.f ? base : most, 0x1p-80f);
     int x = 1;
     if (most > 0.f) __builtin_frexpf(most / base, &x);   // most / base < 2^x
-    head[0] = __builtin_ldexpf(base, x - 15);
-    head[1] = __builtin_ldexpf(1.f, 15 - x) / base;
+    const float scale = __builtin_ldexpf(1.f, 15 - x) / base;
+    // the rows with a gradient in their order: a ballot per wave, the waves' counts added up
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int taken = 0;
+    for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
+        const int64_t m = m0 + threadIdx.x;
+        RowWeights w{0.f, 0.f, -1};
+        if (m < a.M) w = row_weights(a, m);
+        const bool has = w.d != 0.f || w.rows != 0.f;    // (NaN too)
+        const uint64_t mask = __ballot(has);
+        __syncthreads();                             // the last counts have been read
+        if (lane == 0) counts[wave] = __popcll(mask);
+        __syncthreads();
+        int before = taken;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            before += i < wave ? counts[i] : 0;
+            taken += counts[i];
+        }
+        const int at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
+        if (m < a.M) a.place[m] = has ? at : -1;
+        if (has) {
+            a.list[at] = (int32_t)m;
+            a.terms[at] = RowTerms{a.lse[m], w.rows * scale, w.d * scale, w.column};
+        }
+    }
+    if (threadIdx.x == 0) {
+        a.head[0] = __builtin_ldexpf(base, x - 15);
+        a.head[1] = scale;
+        *a.rows = taken;
+    }
+}
+
+__global__ void __launch_bounds__(256) loss_gather(LossGatherArgs g) {
+    const int64_t chunks = g.ldo / 8, total = g.M * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / chunks;
+        const int c = (int)(i - m * chunks) * 8;
+        const int32_t at = g.place[m];
+        if (at >= 0) *(u32x4*)(g.out + at * g.ldo + c) = load8(g.x + m * g.ldx + c, true, c, g.K);
+        else if (g.zeroed) store8(g.zeroed + m * g.ldz + c, true, c, g.K, (u32x4){0u, 0u, 0u, 0u});
+    }
 }
 
 }  // namespace
@@ -73,10 +123,17 @@ hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream
     return launch_kernel((const void*)loss_join, dim3((unsigned)M), dim3(256), params, 0, stream);
 }
 
-hipError_t launch_loss_scale(const int64_t* target, int64_t cols, const float* dloss, const float* dlse, int64_t M,
-                             float* head, hipStream_t stream) {
-    void* params[] = {&target, &cols, &dloss, &dlse, &M, &head};
-    return launch_kernel((const void*)loss_scale, dim3(1), dim3(1024), params, 0, stream);
+hipError_t launch_loss_rows(const LossRowsArgs& r, hipStream_t stream) {
+    LossRowsArgs args = r;
+    void* params[] = {&args};
+    return launch_kernel((const void*)loss_rows, dim3(1), dim3(1024), params, 0, stream);
+}
+
+hipError_t launch_loss_gather(const LossGatherArgs& g, hipStream_t stream) {
+    LossGatherArgs args = g;
+    void* params[] = {&args};
+    const int64_t blocks = (g.M * (g.ldo / 8) + 255) / 256;
+    return launch_kernel((const void*)loss_gather, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
 }
 
 }  // namespace lin

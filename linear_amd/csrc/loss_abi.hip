@@ -175,16 +175,20 @@ LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     return p;
 }
 
-constexpr int64_t kLossHead = 256;
+constexpr int64_t kLossHead = 256;                    // the factor and its inverse, the number of rows
 int64_t sums_bytes(int64_t M, int64_t cols) { return M > 2048 ? round256(64 * cols * 4) : 0; }
 
-// Bytes ahead of the copies: the head, dz, dx's FP32 sums, the products' partial sums.
+// Bytes ahead of the copies: the head, the rows' places, list and terms, dz, dx's FP32 sums, the
+// products' partial sums.
 struct LossSpace {
-    int64_t dz, dx, partials, end;
+    int64_t place, list, terms, dz, dx, partials, end;
 };
 LossSpace space_of(const LossPlan& p, int64_t M, int64_t K) {
     LossSpace s;
-    s.dz = kLossHead;
+    s.place = kLossHead;
+    s.list = s.place + round256(M * 4);
+    s.terms = s.list + round256(M * 4);
+    s.dz = s.terms + round256(M * (int64_t)sizeof(RowTerms));
     s.dx = s.dz + round256(M * p.ldz * 2);
     s.partials = s.dx + (p.pieces > 1 ? round256(M * round8(K) * 4) : 0);
     s.end = s.partials + round256(std::max({partial_bytes(p.dx, 1, M, K), partial_bytes(p.dw, 1, p.cols, K), sums_bytes(M, p.cols)}));
@@ -215,24 +219,24 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
     const LossPlan p = plan_loss(M, N, K, packed);
     const LossSpace at = space_of(p, M, K);
     unsigned char* space = (unsigned char*)ws;
+    const bool any = M > 0 && N > 0;
     // dz is scaled; the products' sums are then multiplied by the factor's inverse
-    float* const head = M > 0 && N > 0 ? (float*)ws : nullptr;
+    float* const head = any ? (float*)ws : nullptr;
+    int32_t* const rows = any ? (int32_t*)ws + 2 : nullptr;
+    int32_t *place = (int32_t*)(space + at.place), *list = any ? (int32_t*)(space + at.list) : nullptr;
     uint16_t* dz = (uint16_t*)(space + at.dz);
     float* sums = (float*)(space + at.dx);
     void* partials = space + at.partials;
     const Copies copies = copies_at(space + at.end, M, K);
-    if (head && (st = launched(launch_loss_scale(target, N, dloss, dlse, M, head, stream))) != LINEAR_OK) return st;
-    if (M > 0 && N > 0 && !in_place(x, ldx, M, K)) {
-        if ((st = launched(launch_repack(x, ldx, M, (int)K, copies.x, round8(K), stream))) != LINEAR_OK) return st;
-        x = copies.x;
-        ldx = round8(K);
+    LossArgs a = loss_args(copies.x, round8(K), target, M, N, K, di);
+    if (any) {
+        a.terms = (RowTerms*)(space + at.terms);
+        a.rows = rows;
+        const LossRowsArgs r{target, dloss, dlse, lse, N, M, head, rows, place, list, (RowTerms*)(space + at.terms)};
+        if ((st = launched(launch_loss_rows(r, stream))) != LINEAR_OK) return st;
+        const LossGatherArgs g{x, ldx, M, (int)K, place, copies.x, round8(K), want_dx ? dx : nullptr, lddx};
+        if (K > 0 && (st = launched(launch_loss_gather(g, stream))) != LINEAR_OK) return st;
     }
-    ldx = row_stride(ldx, M, K);
-    LossArgs a = loss_args(x, ldx, target, M, N, K, di);
-    a.lse = lse;
-    a.dloss = dloss;
-    a.dlse = dlse;
-    a.scale = head ? head + 1 : nullptr;
     a.y = dz;
     a.ldy = p.ldz;
     for (int64_t piece = 0; piece < p.pieces; ++piece) {
@@ -267,7 +271,9 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
             s.L = (int)cols;
             s.segs = s.groups = 1;
             s.unscale = p.pieces > 1 ? nullptr : head;
-            const int mode = p.pieces == 1 ? kOutRound : piece == 0 ? kOutF32 : kOutF32Add;
+            s.rows = rows;
+            s.list = p.pieces > 1 ? nullptr : list;
+            const int mode = p.pieces > 1 ? (piece == 0 ? kOutF32 : kOutF32Add) : list ? kOutList : kOutRound;
             if ((st = launch_stream(elem, false, mode, s, p.dx, di, partials, stream)) != LINEAR_OK) return st;
         }
         if (!want_dw && !want_db) continue;
@@ -283,6 +289,7 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         c.f32 = f32;
         c.accumulate = accumulate != 0;
         c.unscale = head;
+        c.rows = rows;
         const GradConfig& g = kGradConfigs[p.dw.cfg];
         const bool with_sums = want_db && want_dw && c.splits == 1 && sums_fit(p.dw, 1, cols, K, di.cus);
         if (want_db && !with_sums && (st = launched(launch_column_sum(elem, c, stream))) != LINEAR_OK) return st;
@@ -290,8 +297,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         memset(&s, 0, sizeof s);
         s.r = dz;
         s.ldr = p.ldz;
-        s.c[0] = x;
-        s.ldc = ldx;
+        s.c[0] = copies.x;
+        s.ldc = round8(K);
         s.y[0] = (char*)dw + n * lddw * eb;
         s.ldy[0] = lddw;
         s.R = (int)cols;
@@ -299,6 +306,7 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         s.L = (int)M;
         s.segs = s.groups = 1;
         s.unscale = head;
+        s.rows = rows;
         if (with_sums) {
             s.sum_blocks = (int)tiles_of(cols, g.bm);
             s.sums = c;
@@ -317,6 +325,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
     s.C = (int)K;
     s.splits = s.groups = 1;
     s.sum_unscale = head;
+    s.rows = rows;
+    s.list = list;
     return launched(launch_split_sum(elem, false, s, stream));
 }
 

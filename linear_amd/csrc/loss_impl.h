@@ -9,7 +9,9 @@
 // exp(z - largest): 8 bytes for a row of 256 columns, 1/128 of the logits; loss_join adds
 // the tiles' sums.  The gradient: z is formed again (2MNK operations against 4MN bytes
 // written and read), and exp(z - lse) needs nothing but lse, so a tile's dz leaves at once
-// as words for the two products that follow (dx = dz W, dW = dz^T x).
+// as words for the two products that follow (dx = dz W, dW = dz^T x).  Rows without a gradient
+// are left out of all three: the others are gathered to the front, and their number, which the
+// host does not know, is read from memory.
 //
 // A row's reference is clamped to the finite range: a row of -inf then sums to exp(-inf) =
 // 0 and has lse -inf, one with +inf has a sum, and an lse, of +inf; NaN stays.
@@ -120,7 +122,6 @@ __device__ __forceinline__ void finish_dz(const Args& a, unsigned char* smem, Ac
     constexpr int G = R * R / 256;
     const int wn = wave % WN, wm = wave / WN;
     const int lr = lane % R, lh = lane / R;
-    const float scale = *a.scale;
     const bool ragged = n0 + BN > a.N;               // uniform
     if (a.b) {
 #pragma unroll
@@ -137,26 +138,16 @@ __device__ __forceinline__ void finish_dz(const Args& a, unsigned char* smem, Ac
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
         const int m = m0 + wm * TM + j * R + lr;
-        float lse = 0.f, rows = 0.f, one = 0.f;
-        int t = -1;
-        if (m < a.M) {
-            const int64_t target = a.target[m];
-            lse = a.lse[m];
-            one = target >= 0 && target < a.cols ? a.dloss[m] * scale : 0.f;
-            rows = a.dlse ? one + a.dlse[m] * scale : one;
-            t = launch_column(a, target);
-        }
-        // a row without weight gives zeros, whatever its logits
-        const bool none = rows == 0.f && one == 0.f;
-        t -= n0 + wn * TN;
+        RowTerms r{0.f, 0.f, 0.f, -1};
+        if (m < a.M) r = a.terms[m];
+        const int t = r.column - (int)a.col0 - n0 - wn * TN;   // (negative without a target)
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int v = 0; v < 4 * G; ++v) {
                 const int c = i * R + v / 4 * 8 + lh * 4 + v % 4;
-                float d = rows * __expf(acc[i][j][v] - lse) - (c == t ? one : 0.f);
-                if (none || (ragged && n0 + wn * TN + c >= a.N)) d = 0.f;
-                acc[i][j][v] = d;
+                const float d = r.rows * __expf(acc[i][j][v] - r.lse) - (c == t ? r.one : 0.f);
+                acc[i][j][v] = ragged && n0 + wn * TN + c >= a.N ? 0.f : d;
             }
     }
     LinearArgs o = a;

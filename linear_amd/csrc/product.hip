@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) repack(const uint16_t* in, int64_t ld, in
 template <int E, bool F32>
 __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
     const int chunks = (a.C + 3) / 4;
-    const int64_t total = (int64_t)a.groups * a.R * chunks, plane = (int64_t)a.groups * a.R * a.ldp;
+    const int64_t total = (a.rows ? (int64_t)*a.rows : (int64_t)a.groups * a.R) * chunks, plane = (int64_t)a.groups * a.R * a.ldp;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t gr = i / chunks;                   // group * R + row
         const int c = (int)(i - gr * chunks) * 4;
@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(256) split_sum(StreamProduct a) {
             if (s + j < a.splits) v += w[j];
         if (a.sum_unscale) v *= *a.sum_unscale;
         const int g = gr >= a.R ? 1 : 0;
-        const int64_t at = (gr - (int64_t)g * a.R) * a.ldy[g] + c;
+        const int64_t row = a.list ? a.list[gr] : gr - (int64_t)g * a.R;
+        const int64_t at = row * a.ldy[g] + c;
         const bool whole = c + 3 < a.C;                  // stored at any alignment
         if constexpr (F32) {
             float* y = (float*)a.y[g] + at;

@@ -53,6 +53,7 @@ struct ColumnSumArgs {
     int M, N, splits;
     int f32, accumulate;
     const float* unscale;    // not null: the sums are multiplied by *unscale
+    const int32_t* rows;     // not null: the rows are *rows, at most M
 };
 // Splits of the rows: enough workgroups of 64 columns for every CU, of 2048 rows at
 // least; one where the columns alone give half the chip work (a second launch costs
@@ -87,6 +88,10 @@ struct StreamProduct {
     int fold;
     // not null: the sums are multiplied by *unscale, the power of two that undoes the row operand's
     const float* unscale;
+    // not null: only the first *rows rows of the row operand are there (its R rows without
+    // splits or groups, or, contraction-major, its L), a count that the device found
+    const int32_t* rows;
+    const int32_t* list;               // kOutList
     int tiles_r, tiles_c;
     int xcd_shift;
     // the contraction's slices shared among `splits` sets of tiles (more than one:
@@ -96,6 +101,7 @@ struct StreamProduct {
     int64_t ldp;
     int accumulate;          // launch_split_sum into floats: y += sum
     const float* sum_unscale;   // launch_split_sum, not null: the totals are multiplied by *sum_unscale
+                                // (launch_split_sum with rows and list: as for the products)
     // the last sum_blocks workgroups take 64 columns of db each instead of a tile
     // (small tiles of dw, one split)
     int sum_blocks;
@@ -114,7 +120,7 @@ inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {64, 64, 2, 2, 2, 4},
     {128, 128, 2, 4, 1, 2},
 };
-// rowt: contraction-major row operand; mode kOutRound, kOutF32 or kOutF32Add.
+// rowt: contraction-major row operand; mode kOutRound, kOutF32, kOutF32Add or, without rowt, kOutList.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);

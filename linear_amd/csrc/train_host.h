@@ -229,7 +229,8 @@ inline void set_tiles(StreamProduct& a, const StreamPlan& p, const DevInfo& di) 
 inline int32_t launch_stream(int elem, bool rowt, int mode, StreamProduct& a, const StreamPlan& p, const DevInfo& di,
                       void* partial, hipStream_t stream) {
     const GradConfig& g = kGradConfigs[p.cfg];
-    const int64_t eb = mode == kOutRound ? 2 : 4;
+    const bool f32 = mode == kOutF32 || mode == kOutF32Add;
+    const int64_t eb = f32 ? 4 : 2;
     set_tiles(a, p, di);
     if (p.c1 > 0) {
         StreamProduct head = a;
@@ -254,7 +255,8 @@ inline int32_t launch_stream(int elem, bool rowt, int mode, StreamProduct& a, co
     const int32_t st = launched(launch_grad_stream(elem, p.cfg, rowt, kOutF32, a, stream));
     if (st != LINEAR_OK) return st;
     if (a.fold) a.R = a.fold;
-    return launched(launch_split_sum(elem, mode != kOutRound, a, stream));
+    if (rowt) a.rows = nullptr;                       // it counted the contraction, not the output's rows
+    return launched(launch_split_sum(elem, f32, a, stream));
 }
 
 // The weight call's partial sums: db's and dw's, one after the other in the same space.

@@ -104,6 +104,34 @@ def test_gradients_that_are_not_wanted(wanted, t):
             assert torch.equal(a, c)
 
 
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K,share", [(1, 70, 40, 1.0), (20, 300, 72, 0.7), (300, 1030, 136, 0.9), (2500, 520, 72, 0.5),
+                                         (2100, 1032, 520, 0.02), (5000, 300, 93, 0.995)])
+def test_rows_without_a_gradient_take_no_part(M, N, K, share, t):
+    """Rows that do not count, or of weight zero: their x and lse may hold anything, their dx is zero, and
+    the other rows' gradients are those of a call without them (up to the order of sums: the same bounds)."""
+    x, w, target, b, dloss, _ = make(M, N, K, t)
+    gen = torch.Generator().manual_seed(9)
+    off = (torch.rand(M, generator=gen) < share).to(DEV)
+    target[off] = -1
+    zero = ~off & (torch.rand(M, generator=gen) < 0.1).to(DEV)
+    dloss[zero] = 0.0
+    _, lse = fn("", t)(x, w, target, b)
+    want, bound = ref.backward64(dloss, None, x, w, target, b, t)
+    x[off | zero] = float("nan")
+    lse[off | zero] = float("nan")
+    dx = torch.full_like(x, 7.0)
+    got = fn("_backward", t)(dloss, x, w, target, lse, b, dx=dx)
+    for g, v, e, n in zip(got, want, bound, ("dx", "dw", "db")):
+        inside(g, v, e, n)
+    assert bool((dx[off | zero] == 0).all())
+    wide = fn("_backward_f32out", t)(dloss, x, w, target, lse, b, need_dx=False)
+    keep = ~(off | zero)
+    alone = fn("_backward_f32out", t)(dloss[keep], x[keep], w, target[keep], lse[keep], b, need_dx=False)
+    for g, v, e in zip(wide[1:], alone[1:], ref.backward64(dloss, None, x.nan_to_num(0), w, target, b, t, True)[1][1:]):
+        inside(g, v.double(), 2 * e, "with and without the rows")
+
+
 def padded(v, pad, shift, fill):
     """The matrix v with `pad` extra columns and a base `shift` words further on, in a sea of `fill`."""
     flat = torch.full((v.shape[0] * (v.shape[1] + pad) + shift + 64,), fill, dtype=v.dtype, device=v.device)
