@@ -428,17 +428,19 @@ grad_stream(StreamProduct a) {
 // 64 x 64 tiles of two sets, or 128 x 128) and dWg, dWu (128 x 128): where each alone
 // leaves CUs idle in its last round, the other's tiles fill them.  dx's tiles, the
 // longer ones, come first.
-template <bool SMALL, int E>
+template <bool SMALL, int E, int MODE>
 __global__ void __launch_bounds__(512) grad_pair(StreamProduct a, StreamProduct b) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[grad_lds<128, 128, 1, 4>];
     static_assert(grad_lds<64, 64, 2, 4> <= grad_lds<128, 128, 1, 4>, "one LDS block for both");
     const int tiles = a.tiles_r * a.tiles_c;
     if ((int)blockIdx.x < tiles) {
-        if constexpr (SMALL) grad_tile<64, 64, 2, 2, 2, 4, false, E, kOutRound>(a, blockIdx.x, smem);
-        else grad_tile<128, 128, 2, 4, 1, 4, false, E, kOutRound>(a, blockIdx.x, smem);
-    } else {
-        grad_tile<128, 128, 2, 4, 1, 4, true, E, kOutRound>(b, blockIdx.x - tiles, smem);
+        if constexpr (SMALL) grad_tile<64, 64, 2, 2, 2, 4, false, E, MODE>(a, blockIdx.x, smem);
+        else grad_tile<128, 128, 2, 4, 1, 4, false, E, MODE>(a, blockIdx.x, smem);
+        return;
     }
+    const int block = blockIdx.x - tiles, rest = block - b.groups * b.tiles_r * b.tiles_c;
+    if (rest < 0) grad_tile<128, 128, 2, 4, 1, 4, true, E, kOutRound>(b, block, smem);
+    else column_block<E, 512>(b.sums, rest, 0, (float*)smem);
 }
 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
@@ -478,9 +480,10 @@ template <int E>
 hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream) {
     StreamProduct aa = a, bb = b;
     void* params[] = {&aa, &bb};
-    return launch_kernel(small ? (const void*)grad_pair<true, E> : (const void*)grad_pair<false, E>,
-                           dim3((unsigned)(a.tiles_r * a.tiles_c + b.groups * b.tiles_r * b.tiles_c)), dim3(512), params, 0,
-                           stream);
+    const void* fn = a.list ? (small ? (const void*)grad_pair<true, E, kOutList> : (const void*)grad_pair<false, E, kOutList>)
+                            : (small ? (const void*)grad_pair<true, E, kOutRound> : (const void*)grad_pair<false, E, kOutRound>);
+    return launch_kernel(fn, dim3((unsigned)(a.tiles_r * a.tiles_c + b.groups * b.tiles_r * b.tiles_c + b.sum_blocks)), dim3(512),
+                         params, 0, stream);
 }
 
 }  // namespace lin

@@ -46,19 +46,32 @@ struct RowWeights {
     int32_t column;
 };
 __device__ inline RowWeights row_weights(const LossRowsArgs& a, int64_t m) {
-    const int64_t t = a.target[m];
+    const int64_t t = a.target[m];                   // (every load is issued before the first is used)
+    const float all = a.dloss[m], more = a.dlse ? a.dlse[m] : 0.f;
     const bool counts = t >= 0 && t < a.cols;
-    const float d = counts ? a.dloss[m] : 0.f;
-    return {d, a.dlse ? d + a.dlse[m] : d, counts ? (int32_t)t : -1};
+    const float d = counts ? all : 0.f;
+    return {d, a.dlse ? d + more : d, counts ? (int32_t)t : -1};
 }
 
-// One workgroup (a few us at some thousand rows, and little beside the products at millions).
-__global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a) {
+__device__ inline void gather_piece(const LossGatherArgs& g, int64_t m, int c, int32_t at) {
+    if (at >= 0) *(u32x4*)(g.out + at * g.ldo + c) = load8(g.x + m * g.ldx + c, true, c, g.K);
+    else if (g.zeroed) store8(g.zeroed + m * g.ldz + c, true, c, g.K, (u32x4){0u, 0u, 0u, 0u});
+}
+
+// SCAN: one workgroup, which leaves the places in memory (a few us at some thousand rows, little
+// beside the products at millions).  Else every workgroup keeps them in LDS and gathers its share
+// of x; the first leaves the rest in memory.
+template <bool SCAN>
+__global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs g) {
     __shared__ float lds[16];
     __shared__ int counts[16];
+    __shared__ int32_t places[SCAN ? 1 : kLossScanRows];
     float base = 0.f, most = 0.f;
+    RowWeights mine{0.f, 0.f, -1};                   // of row threadIdx.x
+#pragma unroll 4
     for (int64_t m = threadIdx.x; m < a.M; m += 1024) {
         const RowWeights w = row_weights(a, m);
+        if (m < 1024) mine = w;
         const float v = __builtin_fabsf(w.rows) + __builtin_fabsf(w.d);
         if (!(v < __builtin_inff())) continue;
         base = fmaxf(base, __builtin_fabsf(w.d));
@@ -74,11 +87,16 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a) {
     const float scale = __builtin_ldexpf(1.f, 15 - x) / base;
     // the rows with a gradient in their order: a ballot per wave, the waves' counts added up
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const bool first = blockIdx.x == 0;
     int taken = 0;
     for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
         const int64_t m = m0 + threadIdx.x;
         RowWeights w{0.f, 0.f, -1};
-        if (m < a.M) w = row_weights(a, m);
+        float lse = 0.f;
+        if (m < a.M) {
+            w = m < 1024 ? mine : row_weights(a, m);
+            lse = a.lse[m];
+        }
         const bool has = w.d != 0.f || w.rows != 0.f;    // (NaN too)
         const uint64_t mask = __ballot(has);
         __syncthreads();                             // the last counts have been read
@@ -91,27 +109,36 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a) {
             taken += counts[i];
         }
         const int at = before + __popcll(mask & ((uint64_t(1) << lane) - 1));
-        if (m < a.M) a.place[m] = has ? at : -1;
-        if (has) {
+        if (m < a.M) {
+            if constexpr (SCAN) a.place[m] = has ? at : -1;
+            else places[m] = has ? at : -1;
+        }
+        if (has && first) {
             a.list[at] = (int32_t)m;
-            a.terms[at] = RowTerms{a.lse[m], w.rows * scale, w.d * scale, w.column};
+            a.terms[at] = RowTerms{lse, w.rows * scale, w.d * scale, w.column};
         }
     }
-    if (threadIdx.x == 0) {
+    if (first && threadIdx.x == 0) {
         a.head[0] = __builtin_ldexpf(base, x - 15);
         a.head[1] = scale;
         *a.rows = taken;
     }
+    if constexpr (!SCAN) {
+        __syncthreads();
+        const int chunks = (int)(g.ldo / 8);
+        const int64_t total = a.M * chunks;
+        for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 1024) {
+            const int m = (int)(i / chunks);
+            gather_piece(g, m, (int)(i - (int64_t)m * chunks) * 8, places[m]);
+        }
+    }
 }
 
-__global__ void __launch_bounds__(256) loss_gather(LossGatherArgs g) {
-    const int64_t chunks = g.ldo / 8, total = g.M * chunks;
+__global__ void __launch_bounds__(256) loss_gather(LossRowsArgs a, LossGatherArgs g) {
+    const int64_t chunks = g.ldo / 8, total = a.M * chunks;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / chunks;
-        const int c = (int)(i - m * chunks) * 8;
-        const int32_t at = g.place[m];
-        if (at >= 0) *(u32x4*)(g.out + at * g.ldo + c) = load8(g.x + m * g.ldx + c, true, c, g.K);
-        else if (g.zeroed) store8(g.zeroed + m * g.ldz + c, true, c, g.K, (u32x4){0u, 0u, 0u, 0u});
+        gather_piece(g, m, (int)(i - m * chunks) * 8, a.place[m]);
     }
 }
 
@@ -123,16 +150,19 @@ hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream
     return launch_kernel((const void*)loss_join, dim3((unsigned)M), dim3(256), params, 0, stream);
 }
 
-hipError_t launch_loss_rows(const LossRowsArgs& r, hipStream_t stream) {
-    LossRowsArgs args = r;
-    void* params[] = {&args};
-    return launch_kernel((const void*)loss_rows, dim3(1), dim3(1024), params, 0, stream);
-}
-
-hipError_t launch_loss_gather(const LossGatherArgs& g, hipStream_t stream) {
-    LossGatherArgs args = g;
-    void* params[] = {&args};
-    const int64_t blocks = (g.M * (g.ldo / 8) + 255) / 256;
+hipError_t launch_loss_rows(const LossRowsArgs& r, const LossGatherArgs& g, hipStream_t stream) {
+    LossRowsArgs rows = r;
+    LossGatherArgs gather = g;
+    void* params[] = {&rows, &gather};
+    const int64_t pieces = r.M * (g.ldo / 8);
+    if (r.M <= kLossScanRows) {
+        const int64_t blocks = pieces / 1024 + 1;
+        return launch_kernel((const void*)loss_rows<false>, dim3((unsigned)(blocks < 512 ? blocks : 512)), dim3(1024), params, 0,
+                             stream);
+    }
+    const hipError_t e = launch_kernel((const void*)loss_rows<true>, dim3(1), dim3(1024), params, 0, stream);
+    if (e != hipSuccess || pieces == 0) return e;
+    const int64_t blocks = (pieces + 255) / 256;
     return launch_kernel((const void*)loss_gather, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), params, 0, stream);
 }
 

@@ -156,9 +156,11 @@ int32_t run_loss(int elem, const uint16_t* x, int64_t ldx, const uint16_t* w, in
 // tiles): dz of one piece is formed, multiplied into dx (FP32 sums over the pieces) and into
 // its rows of dw.  One piece where dz is at most 256 MiB; else pieces of 128 MiB (they stay in
 // the memory-side cache until both products have read them), of 8192 columns at least.
+// Both products in one launch where that is faster (plan_pair), with db's column sums.
 struct LossPlan {
     int64_t pieces, cols, ldz;
     StreamPlan dx, dw;
+    bool pair;
 };
 LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     LossPlan p;
@@ -172,6 +174,8 @@ LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     p.ldz = (p.cols + 63) / 64 * 64;
     p.dx = plan_stream(1, M, K, slices_of(p.cols));
     p.dw = plan_stream(1, p.cols, K, slices_of(M));
+    p.pair = p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
+             plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, slices_of(N), 1, N, slices_of(M), false);
     return p;
 }
 
@@ -233,9 +237,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         a.terms = (RowTerms*)(space + at.terms);
         a.rows = rows;
         const LossRowsArgs r{target, dloss, dlse, lse, N, M, head, rows, place, list, (RowTerms*)(space + at.terms)};
-        if ((st = launched(launch_loss_rows(r, stream))) != LINEAR_OK) return st;
-        const LossGatherArgs g{x, ldx, M, (int)K, place, copies.x, round8(K), want_dx ? dx : nullptr, lddx};
-        if (K > 0 && (st = launched(launch_loss_gather(g, stream))) != LINEAR_OK) return st;
+        const LossGatherArgs g{x, ldx, (int)K, copies.x, round8(K), want_dx ? dx : nullptr, lddx};
+        if ((st = launched(launch_loss_rows(r, g, stream))) != LINEAR_OK) return st;
     }
     a.y = dz;
     a.ldy = p.ldz;
@@ -257,26 +260,30 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
                 if (st != LINEAR_OK) return st;
             }
         }
-        StreamProduct s;
-        if (want_dx) {
-            memset(&s, 0, sizeof s);
-            s.r = dz;
-            s.ldr = p.ldz;
-            s.c[0] = wp;
-            s.ldc = ldp;
-            s.y[0] = p.pieces > 1 ? (void*)sums : (void*)dx;
-            s.ldy[0] = p.pieces > 1 ? round8(K) : lddx;
-            s.R = (int)M;
-            s.C = (int)K;
-            s.L = (int)cols;
-            s.segs = s.groups = 1;
-            s.unscale = p.pieces > 1 ? nullptr : head;
-            s.rows = rows;
-            s.list = p.pieces > 1 ? nullptr : list;
-            const int mode = p.pieces > 1 ? (piece == 0 ? kOutF32 : kOutF32Add) : list ? kOutList : kOutRound;
-            if ((st = launch_stream(elem, false, mode, s, p.dx, di, partials, stream)) != LINEAR_OK) return st;
-        }
-        if (!want_dw && !want_db) continue;
+        StreamProduct sx, sw;
+        memset(&sx, 0, sizeof sx);
+        memset(&sw, 0, sizeof sw);
+        sx.r = sw.r = dz;
+        sx.ldr = sw.ldr = p.ldz;
+        sx.segs = sx.groups = sw.segs = sw.groups = 1;
+        sx.rows = sw.rows = rows;
+        sx.c[0] = wp;
+        sx.ldc = ldp;
+        sx.y[0] = p.pieces > 1 ? (void*)sums : (void*)dx;
+        sx.ldy[0] = p.pieces > 1 ? round8(K) : lddx;
+        sx.R = (int)M;
+        sx.C = (int)K;
+        sx.L = (int)cols;
+        sx.unscale = p.pieces > 1 ? nullptr : head;
+        sx.list = p.pieces > 1 ? nullptr : list;
+        sw.c[0] = copies.x;
+        sw.ldc = round8(K);
+        sw.y[0] = (char*)dw + n * lddw * eb;
+        sw.ldy[0] = lddw;
+        sw.R = (int)cols;
+        sw.C = (int)K;
+        sw.L = (int)M;
+        sw.unscale = head;
         ColumnSumArgs c;
         memset(&c, 0, sizeof c);
         c.dy = dz;
@@ -290,29 +297,27 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         c.accumulate = accumulate != 0;
         c.unscale = head;
         c.rows = rows;
-        const GradConfig& g = kGradConfigs[p.dw.cfg];
-        const bool with_sums = want_db && want_dw && c.splits == 1 && sums_fit(p.dw, 1, cols, K, di.cus);
-        if (want_db && !with_sums && (st = launched(launch_column_sum(elem, c, stream))) != LINEAR_OK) return st;
-        if (!want_dw) continue;
-        memset(&s, 0, sizeof s);
-        s.r = dz;
-        s.ldr = p.ldz;
-        s.c[0] = copies.x;
-        s.ldc = round8(K);
-        s.y[0] = (char*)dw + n * lddw * eb;
-        s.ldy[0] = lddw;
-        s.R = (int)cols;
-        s.C = (int)K;
-        s.L = (int)M;
-        s.segs = s.groups = 1;
-        s.unscale = head;
-        s.rows = rows;
+        const bool together = p.pair && want_dx && want_dw && !f32 && any;
+        const bool with_sums = want_db && want_dw && c.splits == 1 && (together || sums_fit(p.dw, 1, cols, K, di.cus));
         if (with_sums) {
-            s.sum_blocks = (int)tiles_of(cols, g.bm);
-            s.sums = c;
+            sw.sum_blocks = (int)tiles_of(cols, 64);
+            sw.sums = c;
+        } else if (want_db && (st = launched(launch_column_sum(elem, c, stream))) != LINEAR_OK) {
+            return st;
         }
-        const int mode = !f32 ? kOutRound : accumulate ? kOutF32Add : kOutF32;
-        if ((st = launch_stream(elem, true, mode, s, p.dw, di, partials, stream)) != LINEAR_OK) return st;
+        if (together) {
+            set_tiles(sx, p.dx, di);
+            set_tiles(sw, p.dw, di);
+            return launched(launch_grad_pair(elem, p.dx.cfg == kPairSmall, sx, sw, stream));
+        }
+        if (want_dx) {
+            const int mode = p.pieces > 1 ? (piece == 0 ? kOutF32 : kOutF32Add) : list ? kOutList : kOutRound;
+            if ((st = launch_stream(elem, false, mode, sx, p.dx, di, partials, stream)) != LINEAR_OK) return st;
+        }
+        if (want_dw) {
+            const int mode = !f32 ? kOutRound : accumulate ? kOutF32Add : kOutF32;
+            if ((st = launch_stream(elem, true, mode, sw, p.dw, di, partials, stream)) != LINEAR_OK) return st;
+        }
     }
     if (!want_dx || p.pieces == 1) return LINEAR_OK;
     StreamProduct s;                                  // the sums over the pieces, rounded

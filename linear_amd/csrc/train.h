@@ -130,7 +130,8 @@ inline hipError_t launch_grad_stream(int elem, int cfg, bool rowt, int mode, con
 }
 
 // Two unsplit products in one launch: a (rowt false) on kGradConfigs[kPairSmall] or, not
-// small, [kPairTile], then b (rowt true) on [kPairTile]; both rounded.
+// small, [kPairTile], then b (rowt true) on [kPairTile]; both rounded, a's rows placed by its
+// list where it has one.  b.sum_blocks as for one product.
 constexpr int kPairSmall = 4, kPairTile = 2;
 template <int E> hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream);
 extern template hipError_t launch_grad_pair_t<kF16>(bool, const StreamProduct&, const StreamProduct&, hipStream_t);

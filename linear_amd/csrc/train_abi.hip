@@ -275,25 +275,7 @@ GatedPlan plan_gated(int64_t M, int64_t N, int64_t K) {
     const int64_t sx = 2 * slices_of(N), sw = slices_of(M);
     GatedPlan p{plan_stream(1, M, K, sx, low), plan_stream(2, N, K, sw), false};
     if (M == 0 || N == 0) return p;
-    double best = p.dx.time + p.dw.time + kLaunchGap;
-    const lin::GradConfig& gw = lin::kGradConfigs[lin::kPairTile];
-    const TileTime& tw = kGradTimes[lin::kPairTile];
-    const double wt = tw.fixed + tw.slice * (double)sw;
-    const double wsum = wt * 2.0 * (double)(tiles_of(N, gw.bm) * tiles_of(K, gw.bn));
-    for (int c : {lin::kPairSmall, lin::kPairTile}) {
-        const lin::GradConfig& g = lin::kGradConfigs[c];
-        if (low && g.bm != 64) continue;
-        const TileTime& t = kGradTimes[c];
-        const double xt = t.fixed + t.slice * (double)sx;
-        const double xsum = xt * (double)(tiles_of(M, g.bm) * tiles_of(K, g.bn));
-        const double all = std::max(std::max(xt, wt), (xsum + wsum) / kPlanCus + 0.5 * wt);
-        if (all < best) {
-            best = all;
-            p.pair = true;
-            p.dx = StreamPlan{c, 1, 0, 0, xt};
-            p.dw = StreamPlan{lin::kPairTile, 1, 0, 0, wt};
-        }
-    }
+    p.pair = plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, sx, 2, N, sw, low);
     return p;
 }
 

@@ -205,6 +205,33 @@ inline bool sums_fit(const StreamPlan& p, int64_t groups, int64_t R, int64_t C, 
     return groups * tiles_of(R, g.bm) * tiles_of(C, g.bn) + tiles_of(R, 64) <= (int64_t)cus * kGradTimes[p.cfg].per_cu;
 }
 
+// dx [R, C] over sx slices and dw (groups of [Rw, C]) over sw slices in one launch, where their
+// tiles together, spread over the CUs, take less than `time`: whether, and the tiles of both.
+// (Both then keep these plans, unsplit, launched together or alone.)  only64: dx on 64-row tiles.
+inline bool plan_pair(StreamPlan& dx, StreamPlan& dw, double time, int64_t R, int64_t C, int64_t sx, int64_t groups, int64_t Rw,
+                      int64_t sw, bool only64) {
+    bool pair = false;
+    const GradConfig& gw = kGradConfigs[kPairTile];
+    const TileTime& tw = kGradTimes[kPairTile];
+    const double wt = tw.fixed + tw.slice * (double)sw;
+    const double wsum = wt * (double)(groups * tiles_of(Rw, gw.bm) * tiles_of(C, gw.bn));
+    for (int c : {kPairSmall, kPairTile}) {
+        const GradConfig& g = kGradConfigs[c];
+        if (only64 && g.bm != 64) continue;
+        const TileTime& t = kGradTimes[c];
+        const double xt = t.fixed + t.slice * (double)sx;
+        const double xsum = xt * (double)(tiles_of(R, g.bm) * tiles_of(C, g.bn));
+        const double all = std::max(std::max(xt, wt), (xsum + wsum) / kPlanCus + 0.5 * wt);
+        if (all < time) {
+            time = all;
+            pair = true;
+            dx = StreamPlan{c, 1, 0, 0, xt};
+            dw = StreamPlan{kPairTile, 1, 0, 0, wt};
+        }
+    }
+    return pair;
+}
+
 // Bytes of partial sums of a product's plan.
 inline int64_t partial_bytes(const StreamPlan& p, int64_t groups, int64_t R, int64_t C) {
     return p.splits > 1 ? p.splits * groups * R * ((C + 7) / 8 * 8) * 4 : 0;
