@@ -15,6 +15,7 @@ import array
 import contextlib
 import ctypes
 import functools
+import importlib.util
 import itertools
 import operator
 import os
@@ -23,6 +24,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblinear_amd.so")
+MARSHAL_PATH = os.path.join(_HERE, "_marshal.so")
 
 LINEAR_OK = 0
 LINEAR_E_NULL = 1
@@ -215,6 +217,17 @@ def _lib():
     lib.linear_last_hip_error.restype = i32
     _LIB = lib
     return lib
+
+
+@functools.lru_cache(maxsize=None)
+def _marshal():
+    """The module that reads lists of tensors (csrc/marshal.cpp)."""
+    if not os.path.exists(MARSHAL_PATH):
+        raise RuntimeError("_marshal.so is not built (run `python -m linear_amd.build` or __graft_entry__.build())")
+    spec = importlib.util.spec_from_file_location("_marshal", MARSHAL_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def library_path() -> str:
@@ -1117,6 +1130,20 @@ def _device_scalar(t, name, dtype):
     return t.data_ptr()
 
 
+def _adamw_tables(params, grads, m, v, copies):
+    """The tables of an AdamW call's tensors, after checks that say what is wrong."""
+    tensors, names = [params, grads], ["params", "grads"]
+    if copies is not None:
+        tensors.append(copies)
+        names.append("copies")
+    tables = [_tensor_table(t, n) for t, n in zip(tensors, names)]
+    _same_sizes(tables, tensors, names)
+    eight = bool(m) and m[0].dtype == torch.uint8
+    sizes = list(map(torch.Tensor.numel, params))
+    mp, vp = _state_pointers(m, sizes, eight, "m"), _state_pointers(v, sizes, eight, "v")
+    return (*(t.tobytes() for t in tables), *(() if copies is not None else (None,)), mp.tobytes(), vp.tobytes(), eight)
+
+
 def linear_adamw(params, grads, m, v, *, lr, step, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                  weight_decay: float = 0.01, norm=None, max_norm=None, copies=None, stream=None):
     """One AdamW step, in place, over a sequence of parameters (float16, bfloat16, float32) and their gradients (of any
@@ -1125,36 +1152,34 @@ def linear_adamw(params, grads, m, v, *, lr, step, beta1: float = 0.9, beta2: fl
     copies: 16-bit tensors that the new parameters are also rounded into.  lr and step may be device tensors of one
     value (float32, int64), read when the step runs: a captured step then follows them.  Returns params."""
     params, grads, m, v = list(params), list(grads), list(m), list(v)
-    tensors, names = [params, grads], ["params", "grads"]
-    if copies is not None:
-        copies = list(copies)
-        tensors.append(copies)
-        names.append("copies")
-    tables = [_tensor_table(t, n) for t, n in zip(tensors, names)]
-    _same_sizes(tables, tensors, names)
-    eight = bool(m) and m[0].dtype == torch.uint8
-    sizes = list(map(torch.Tensor.numel, params))
-    mp, vp = _state_pointers(m, sizes, eight, "m"), _state_pointers(v, sizes, eight, "v")
+    copies = None if copies is None else list(copies)
+    scalars = [t for t in (norm, lr, step) if isinstance(t, torch.Tensor)]
+    packed = _marshal().adamw(params, grads, m, v, copies)    # None: not the plain case
+    if packed is not None:
+        pt, gt, ct, mp, vp, eight, device = packed
+        if stream is None and all(t.get_device() == device for t in scalars):
+            handle = _current_stream({device})
+        else:
+            handle = None
+    else:
+        pt, gt, ct, mp, vp, eight = _adamw_tables(params, grads, m, v, copies)
+        handle = None
+    if handle is None:
+        handle = _many_launch_stream(stream, params, grads, m, v, scalars, copies or ())
     if (norm is None) != (max_norm is None):
         raise ValueError("norm and max_norm belong together")
     o = _AdamwOptions(beta1=beta1, beta2=beta2, eps=eps, weight_decay=weight_decay, state_bits=8 if eight else 32)
-    scalars = []
     if norm is not None:
         o.norm, o.max_norm = _device_scalar(norm, "norm", torch.float32), max_norm
-        scalars.append(norm)
     if isinstance(lr, torch.Tensor):
         o.device_lr = _device_scalar(lr, "lr", torch.float32)
-        scalars.append(lr)
     else:
         o.lr = lr
     if isinstance(step, torch.Tensor):
         o.device_step = _device_scalar(step, "step", torch.int64)
-        scalars.append(step)
     else:
         o.step = step
-    handle = _many_launch_stream(stream, params, grads, m, v, scalars, copies or ())
-    rc = _lib().linear_adamw(tables[0].buffer_info()[0], tables[1].buffer_info()[0], mp.buffer_info()[0], vp.buffer_info()[0],
-                             tables[2].buffer_info()[0] if copies is not None else None, len(params), ctypes.byref(o), handle)
+    rc = _lib().linear_adamw(pt, gt, mp, vp, ct, len(params), ctypes.byref(o), handle)
     _check(rc, "linear_adamw")
     return params
 
@@ -1170,10 +1195,17 @@ def linear_adamw_values(states, second: bool, out=None, like=None, stream=None):
         with _on(stream, like[0].device if like else torch.device("cpu")):
             out = [torch.empty(t.shape, dtype=torch.bfloat16, device=t.device) for t in like]
     out = list(out)
-    table = _tensor_table(out, "out")
-    sp = _state_pointers(states, list(map(torch.Tensor.numel, out)), True, "states")
-    handle = _many_launch_stream(stream, states, out)
-    rc = _lib().linear_adamw_values(table.buffer_info()[0], sp.buffer_info()[0], int(bool(second)), len(out), handle)
+    packed = _marshal().states(out, states)
+    handle = None
+    if packed is not None:
+        table, sp, device = packed
+        handle = _current_stream({device}) if stream is None else None
+    else:
+        table = _tensor_table(out, "out").tobytes()
+        sp = _state_pointers(states, list(map(torch.Tensor.numel, out)), True, "states").tobytes()
+    if handle is None:
+        handle = _many_launch_stream(stream, states, out)
+    rc = _lib().linear_adamw_values(table, sp, int(bool(second)), len(out), handle)
     _check(rc, "linear_adamw_values")
     return out
 

@@ -11,6 +11,7 @@ import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -26,6 +27,10 @@ SOURCES = ["gemm_f16.hip", "gemm_bf16.hip", "skinny.hip", "epilogue.hip", "index
            "loss_f16.hip", "loss_bf16.hip", "loss.hip", "adamw.hip",
            "linear_abi.hip", "train_abi.hip", "loss_abi.hip",
            "adamw_abi.hip"]
+
+# the binding's marshalling of many tensors, host code against torch's headers
+MARSHAL = "marshal.cpp"
+MARSHAL_OUT = os.path.join(HERE, "_marshal.so")
 
 # sources whose kernels set m0 in inline assembly (lds_dma16_raw), which the compiler is not told
 RAW_M0_SOURCES = ("grad_f16.hip", "grad_bf16.hip")
@@ -118,14 +123,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_marshal() -> str:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    include = os.path.join(home, "include")
+    tmp = MARSHAL_OUT + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, MARSHAL), "-o", tmp,
+           "-L" + os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s" % (MARSHAL, r.stderr))
+    os.replace(tmp, MARSHAL_OUT)
+    return MARSHAL_OUT
+
+
 def build(verbose: bool = True) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     # a failed build must not leave the previous library behind for tests and
     # benchmarks to load
-    for out in (OUT, PROBE_OUT):
+    for out in (OUT, PROBE_OUT, MARSHAL_OUT):
         if os.path.exists(out):
             os.remove(out)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(SOURCES) + len(PROBE_SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_marshal)
         objs = list(ex.map(_compile, SOURCES + PROBE_SOURCES))
     for out, part in ((OUT, objs[:len(SOURCES)]), (PROBE_OUT, objs[len(SOURCES):])):
         tmp = out + ".tmp%d" % os.getpid()
@@ -134,6 +156,9 @@ def build(verbose: bool = True) -> str:
         os.replace(tmp, out)
         if verbose:
             print("built", out)
+    marshal.result()
+    if verbose:
+        print("built", MARSHAL_OUT)
     return OUT
 
 

@@ -89,9 +89,9 @@ struct LossGatherArgs {
     uint16_t* zeroed;
     int64_t ldz;
 };
-// Up to kLossScanRows rows one launch does both, every workgroup finding the places for itself (1024 x
-// 768: 6.4 us, 7.6 in two launches and their gap; 4096 x 4096: 25, 20);
-// past them one workgroup finds them first.
+// Up to kLossScanRows rows one launch does both, every workgroup finding the places for itself
+// (1024 x 768: 6.4 us, 7.6 in two launches and their gap; 4096 x 4096: 25, 20); past them one
+// workgroup finds them first.
 constexpr int kLossScanRows = 1024;
 hipError_t launch_loss_rows(const LossRowsArgs& r, const LossGatherArgs& g, hipStream_t stream);
 
