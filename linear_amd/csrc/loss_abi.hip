@@ -172,7 +172,7 @@ LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     p.cols = p.pieces == 1 ? N : std::min(tiles_of(tiles_of(N, p.pieces), 256) * 256, N);
     p.pieces = std::max<int64_t>(p.cols ? tiles_of(N, p.cols) : 1, 1);
     p.ldz = (p.cols + 63) / 64 * 64;
-    p.dx = plan_stream(1, M, K, slices_of(p.cols));
+    p.dx = plan_stream(1, M, K, slices_of(p.cols), false, true);
     p.dw = plan_stream(1, p.cols, K, slices_of(M));
     p.pair = p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
              plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, slices_of(N), 1, N, slices_of(M), false);

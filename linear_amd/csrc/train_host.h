@@ -159,8 +159,10 @@ inline double tile_time(int cfg, int64_t groups, int64_t R, int64_t C, int64_t s
     return splits == 1 ? main : main + 3.5 + 0.65e-6 * 4.0 * (double)splits * (double)groups * (double)R * (double)C;
 }
 
-// only64: one launch of a 64-row tile.
-inline StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices, bool only64 = false) {
+// only64: one launch of a 64-row tile.  split_large: the 256-row tiles may share a contraction too,
+// for those of a vocabulary's length (cross entropy, loss and gradients: 1000 x 128259 x 4096 3792 ->
+// 3489 us, 1999 x 32001 x 2048 982 -> 953).
+inline StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slices, bool only64 = false, bool split_large = false) {
     StreamPlan p{only64 ? kPairSmall : 0, 1, 0, 0, 0.0};
     double best = tile_time(p.cfg, groups, R, C, slices, 1);
     for (int c = 0; c < kNumGradConfigs; ++c) {
@@ -168,7 +170,7 @@ inline StreamPlan plan_stream(int64_t groups, int64_t R, int64_t C, int64_t slic
         for (int64_t s = 1; s <= 16 && (s == 1 || 2 * s <= slices); ++s) {
             // the large tiles fill the chip where splitting pays, and past twice the chip's
             // tiles a split only adds traffic
-            if (s > 1 && (kGradConfigs[c].bm == 256 || kGradConfigs[c].stages == 2)) break;
+            if (s > 1 && !split_large && (kGradConfigs[c].bm == 256 || kGradConfigs[c].stages == 2)) break;
             if (s > 1 && s * groups * tiles_of(R, kGradConfigs[c].bm) * tiles_of(C, kGradConfigs[c].bn) >
                              2 * kPlanCus * kGradTimes[c].per_cu)
                 break;
