@@ -161,20 +161,24 @@ struct LossPlan {
     int64_t pieces, cols, ldz;
     StreamPlan dx, dw;
     bool pair;
+    bool outer;                                       // dw by launch_outer, where its layout allows
 };
+constexpr int64_t kOuterValues = int64_t(1) << 20;
 LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     LossPlan p;
     int64_t most = std::max<int64_t>(N, 1);
     const int64_t rows = std::max<int64_t>(M, 1);
     if (rows * most > int64_t(1) << 27) most = std::max<int64_t>((int64_t(1) << 26) / rows, 8192);
     if (packed) most = std::min(most, std::max<int64_t>(pack_rows(N, K), 1));
+    most = std::min(most, kMaxLdIn / 256 * 256);      // a stride that the products' kernels read
     p.pieces = std::max<int64_t>(tiles_of(N, most), 1);
     p.cols = p.pieces == 1 ? N : std::min(tiles_of(tiles_of(N, p.pieces), 256) * 256, N);
     p.pieces = std::max<int64_t>(p.cols ? tiles_of(N, p.cols) : 1, 1);
     p.ldz = (p.cols + 63) / 64 * 64;
     p.dx = plan_stream(1, M, K, slices_of(p.cols), false, true);
     p.dw = plan_stream(1, p.cols, K, slices_of(M));
-    p.pair = p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
+    p.outer = M <= kOuterL && N * K >= kOuterValues;
+    p.pair = !p.outer && p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
              plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, slices_of(N), 1, N, slices_of(M), false);
     return p;
 }
@@ -298,7 +302,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         c.unscale = head;
         c.rows = rows;
         const bool together = p.pair && want_dx && want_dw && !f32 && any;
-        const bool with_sums = want_db && want_dw && c.splits == 1 && (together || sums_fit(p.dw, 1, cols, K, di.cus));
+        const bool outer = want_dw && p.outer && K % 8 == 0 && streamable(dw, lddw) && !(f32 && accumulate);
+        const bool with_sums = want_db && want_dw && !outer && c.splits == 1 && (together || sums_fit(p.dw, 1, cols, K, di.cus));
         if (with_sums) {
             sw.sum_blocks = (int)tiles_of(cols, 64);
             sw.sums = c;
@@ -314,7 +319,9 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
             const int mode = p.pieces > 1 ? (piece == 0 ? kOutF32 : kOutF32Add) : list ? kOutList : kOutRound;
             if ((st = launch_stream(elem, false, mode, sx, p.dx, di, partials, stream)) != LINEAR_OK) return st;
         }
-        if (want_dw) {
+        if (outer) {
+            if ((st = launched(launch_outer(elem, f32 ? kOutF32 : kOutRound, sw, stream))) != LINEAR_OK) return st;
+        } else if (want_dw) {
             const int mode = !f32 ? kOutRound : accumulate ? kOutF32Add : kOutF32;
             if ((st = launch_stream(elem, true, mode, sw, p.dw, di, partials, stream)) != LINEAR_OK) return st;
         }

@@ -1,0 +1,152 @@
+// outer_impl.h -- a weight's gradient from few rows (templates).
+//
+//     y[r, c] = sum_{k < L} row[k, r] * col[k, c]          L <= 64, both contraction-major
+//
+// With one slice of contraction indices the product is bound by writing y, and a tile that ends after
+// one slice overlaps its stores with nothing (262 MB of dW from 20 rows: 74 us on the 256 x 256 tile,
+// 3.5 TB/s).  Here a workgroup of 4 waves keeps its 256 columns of the column panel in registers, as
+// matrix-core operands, and walks down the rows in blocks of 64: a block's slice of the row operand
+// comes through an LDS ring by direct-to-LDS loads, three blocks ahead, and its sums leave from the
+// registers while later blocks are multiplied.
+//
+// Columns are dealt to a fragment's 16 rows so that a lane ends with 8 consecutive columns of a row
+// in two fragments: 32 p + 8 h + 4 b + e for fragment 2 p + b, lane group h, element e.  Four lanes
+// then store 64 bytes of a row (16-bit words), the next two fragments the 64 beside them.
+//
+// Loads and stores share a counter and finish in the order of their issue.  Stores go through a
+// buffer resource, masked by their offset and not by a branch, so that every block issues the same
+// number of them and the wait for a block's slice counts past the stores of three blocks.
+#pragma once
+
+#include "grad_impl.h"
+
+namespace lin {
+
+constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
+
+template <int E, int MODE>
+__global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
+    constexpr int CROW = 2 * kOuterCols, RROW = 2 * kOuterRows, SLOT = 64 * RROW;
+    constexpr int LOADS = SLOT / 4096;                // of a slice, per wave
+    constexpr int STORES = MODE == kOutRound ? 8 : 16;
+    static_assert(kOuterStages * SLOT == 64 * CROW, "the ring takes the column panel's place");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[64 * CROW];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int q = lane >> 4, s = lane & 15, kq = 8 * q + (s >> 2);
+    const int L = a.rows ? *a.rows : a.L;
+    const float back = a.unscale ? *a.unscale : 1.f;
+    const int c0 = (int)(blockIdx.x % a.tiles_c) * kOuterCols, share = (int)(blockIdx.x / a.tiles_c);
+    const int ldc = (int)a.ldc, ldr = (int)a.ldr;
+    const uint32_t base = lds_address(smem);
+
+    // the column panel: 64 rows of 512 bytes, 8 loads of 1 KB per wave; rows past L read zero
+    {
+        const __amdgpu_buffer_rsrc_t rc = slice_rsrc(a.c[0] + c0, L > 0 ? ((L - 1) * ldc + ((a.C + 7) & ~7) - c0) * 2 : 0);
+        static_for<0, 8>([&]<int j>() {
+            const int byte = (wave * 8 + j) * 1024 + 16 * lane, k = byte / CROW;
+            const int c = (byte % CROW / 16) ^ (2 * panel_swz<kOuterCols>(k));
+            lds_dma16_raw(rc, base + (wave * 8 + j) * 1024, c0 + 8 * c < a.C ? (uint32_t)((k * ldc + 8 * c) * 2) : kOOB);
+        });
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    lds_barrier();
+    u32x4 col[2][4];                                  // [K step][fragment]
+    static_for<0, 2>([&]<int ks>() {
+        static_for<0, 4>([&]<int i>() {
+            const int unit = wave * 4 + 2 * (i >> 1) + ((s & 3) >> 1);
+            lds_byte* p = lds_at(base + (kq + 32 * ks) * CROW + ((unit ^ panel_swz<kOuterCols>(kq)) << 5) + 16 * (s & 1) + 8 * (i & 1));
+            const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * CROW);
+            col[ks][i] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+        });
+    });
+    lds_barrier();                                    // the panel's place is the ring's from here on
+
+    uint32_t goff[LOADS];
+    static_for<0, LOADS>([&]<int j>() {
+        const int byte = (wave * LOADS + j) * 1024 + 16 * lane, k = byte / RROW;
+        goff[j] = (uint32_t)((k * ldr + 8 * ((byte % RROW / 16) ^ (2 * panel_swz<kOuterRows>(k)))) * 2);
+    });
+    const int blocks = (a.R + kOuterRows - 1) / kOuterRows, step = (int)(gridDim.x / a.tiles_c);
+    const int rend = (a.R + 7) & ~7;
+    int asked = share, fill = 0;                      // the next block to request, its slot
+    auto request = [&]() {
+        // (a resource of no bytes past the last block: nothing is read, and the count stays)
+        const bool some = asked < blocks && L > 0;
+        const int r0 = some ? asked * kOuterRows : 0;
+        const __amdgpu_buffer_rsrc_t rr = slice_rsrc(a.r + r0, some ? ((L - 1) * ldr + rend - r0) * 2 : 0);
+        static_for<0, LOADS>([&]<int j>() { lds_dma16_raw(rr, base + fill * SLOT + (wave * LOADS + j) * 1024, goff[j]); });
+        asked += step;
+        fill = (fill + 1) % kOuterStages;
+    };
+#pragma unroll
+    for (int t = 0; t < kOuterStages - 1; ++t) request();
+
+    constexpr int WORD = MODE == kOutRound ? 2 : 4;
+    const int cl = c0 + wave * 64 + 8 * q;            // this lane's first column; its others are 32 further on
+    int slot = 0, turn = 0;
+    for (int block = share; block < blocks; block += step) {
+        // the slice asked for kOuterStages - 1 blocks ago (or ahead of the loop) has landed once only
+        // what was issued after it is outstanding
+        static_for<0, kOuterStages>([&]<int k>() {
+            if (turn == k) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(k * STORES + (kOuterStages - 2) * LOADS) : "memory");
+        });
+        turn = turn < kOuterStages - 1 ? turn + 1 : turn;
+        lds_barrier();
+        request();
+        u32x4 row[2][4];
+        static_for<0, 2>([&]<int ks>() {
+            static_for<0, 4>([&]<int j>() {
+                lds_byte* p = lds_at(base + slot * SLOT + (kq + 32 * ks) * RROW + ((j ^ panel_swz<kOuterRows>(kq)) << 5) + 8 * (s & 3));
+                const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * RROW);
+                row[ks][j] = (u32x4){lo.x, lo.y, hi.x, hi.y};
+            });
+        });
+        slot = (slot + 1) % kOuterStages;
+        const int r0 = block * kOuterRows, left = min(a.R - r0, kOuterRows);
+        char* y = (char*)a.y[0] + (int64_t)r0 * a.ldy[0] * WORD;
+        const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc((void*)y, (short)0, 0x7fffffff, kRsrcWord3);
+        static_for<0, 4>([&]<int j>() {
+            f32x4 acc[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32<E>(col[0][i], row[0][j], (f32x4){});
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32<E>(col[1][i], row[1][j], acc[i]);
+            const int r = 16 * j + s;
+            static_for<0, 2>([&]<int p>() {
+                const int c = cl + 32 * p;
+                const uint32_t off = r < left && c < a.C ? (uint32_t)((r * (int)a.ldy[0] + c) * WORD) : kOOB;
+                if constexpr (MODE == kOutRound) {
+                    u32x4 w;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f32x4 v = acc[2 * p + e / 2] * back;
+                        w[e] = (uint32_t)narrow<E>(v[2 * (e & 1)]) | ((uint32_t)narrow<E>(v[2 * (e & 1) + 1]) << 16);
+                    }
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, 0);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const f32x4 v = acc[2 * p + b] * back;
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ry, off == kOOB ? kOOB : off + 16 * b, 0, 0);
+                    }
+                }
+            });
+        });
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the empty requests land before the LDS is released
+}
+
+// mode kOutRound or kOutF32.
+template <int E>
+hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream) {
+    StreamProduct args = a;
+    args.tiles_c = (a.C + kOuterCols - 1) / kOuterCols;
+    const int64_t blocks = ((int64_t)a.R + kOuterRows - 1) / kOuterRows;
+    // four workgroups for each of 256 CUs, each taking every shares-th block
+    const int64_t shares = (1024 + args.tiles_c - 1) / args.tiles_c;
+    void* params[] = {&args};
+    return launch_kernel(mode == kOutRound ? (const void*)outer_stream<E, kOutRound> : (const void*)outer_stream<E, kOutF32>,
+                         dim3((unsigned)((blocks < shares ? blocks : shares) * args.tiles_c)), dim3(256), params, 0, stream);
+}
+
+}  // namespace lin

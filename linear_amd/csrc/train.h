@@ -140,6 +140,17 @@ inline hipError_t launch_grad_pair(int elem, bool small, const StreamProduct& a,
     return elem == kBF16 ? launch_grad_pair_t<kBF16>(small, a, b, stream) : launch_grad_pair_t<kF16>(small, a, b, stream);
 }
 
+// One unsplit contraction-major product (rowt) of at most kOuterL contraction indices, bound by its
+// output's write: mode kOutRound or kOutF32; y 16-byte aligned, C and ldy multiples of 8, ldy at
+// most kMaxLdIn.
+constexpr int kOuterL = 64;
+template <int E> hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream);
+extern template hipError_t launch_outer_t<kF16>(int, const StreamProduct&, hipStream_t);
+extern template hipError_t launch_outer_t<kBF16>(int, const StreamProduct&, hipStream_t);
+inline hipError_t launch_outer(int elem, int mode, const StreamProduct& a, hipStream_t stream) {
+    return elem == kBF16 ? launch_outer_t<kBF16>(mode, a, stream) : launch_outer_t<kF16>(mode, a, stream);
+}
+
 // y[g] = the partial sums' total, in order of the splits: rounded to elem's type, or floats.
 hipError_t launch_split_sum(int elem, bool f32, const StreamProduct& a, hipStream_t stream);
 

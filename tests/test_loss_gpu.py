@@ -4,7 +4,7 @@ import torch
 
 import linear_amd as la
 import loss_refs as ref
-from train_refs import inside
+from train_refs import half_step, inside, tiny
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -73,6 +73,32 @@ def test_vocabulary_in_pieces(M, N, K, t):
     _, lse = check_forward(x, w, target, b, t)
     check_backward(dloss, dlse, x, w, target, lse, b, t)
     check_backward(dloss, None, x, w, target, lse, b, t, f32=True)
+
+
+# few rows against weights of a million values and more: column tiles and row blocks of every remainder,
+# outputs of aligned rows (and, with K odd or rows off alignment, the other kernels)
+FEW = [(1, 4096, 264), (2, 16500, 64), (20, 4103, 520), (33, 5000, 776), (63, 2049, 1032), (64, 70001, 256), (64, 1100, 2008),
+       (17, 3000, 513), (40, 524300, 8)]
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", FEW)
+def test_few_rows_and_a_large_vocabulary(M, N, K, t):
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = check_forward(x, w, target, b, t)
+    got = check_backward(dloss, dlse, x, w, target, lse, b, t)
+    wide = check_backward(dloss, dlse, x, w, target, lse, b, t, f32=True)
+    # the same sums times the factor's inverse, rounded to the type, or to FP32: half a step of each
+    size = wide[1].double().abs()
+    inside(got[1], wide[1].double(), (half_step(t) + 2.0 ** -24) * 1.001 * size + tiny(t), "dw of one rounding")
+    for pad in (8, 3):
+        dw, flat = padded(torch.zeros_like(w), pad, 8, 9.0)
+        again = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, dw=dw)
+        inside(again[1], got[1].double(), 2 * ref.backward64(dloss, dlse, x, w, target, b, t)[1][1], "dw in wide rows")
+        if pad == 8:
+            assert torch.equal(again[1], got[1])
+        dw.fill_(9.0)
+        assert bool((flat == 9.0).all()), "written outside"
 
 
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
