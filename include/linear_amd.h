@@ -523,7 +523,7 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
  *
  * N is the vocabulary.  A row whose target lies outside [0, N) does not count: its loss is
  * 0 (its lse is that of its logits all the same).  loss and lse are [M] floats; either may
- * be NULL.  target: [M] device int64.  b: [N] or NULL; an entry of -inf takes its column
+ * be NULL.  target: [M] device int64, needed in any case.  b: [N] or NULL; an entry of -inf takes its column
  * out.  A row of -inf logits has lse -inf, one with +inf (and no NaN) lse +inf.  N == 0
  * gives lse -inf; K == 0 gives z = b.  FP32 inside; reruns are bit-identical.
  *
@@ -677,7 +677,8 @@ int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, i
  *
  * norm: device memory (linear_grad_norm's), or NULL; a NaN norm makes everything NaN, an
  * infinite one s zero, as for linear_grad_clip.  device_lr, device_step: device memory read
- * instead of lr and step by the step's kernels, for captured graphs (NULL: not used).
+ * instead of lr and step by the step's kernels, for captured graphs (NULL: not used); the
+ * step there is 1 or more.
  * LINEAR_E_VALUE: state_bits neither 8 nor 32; lr, eps or weight_decay negative, infinite or
  * NaN; a beta outside [0, 1); step < 1 (without device_step); max_norm negative or NaN (with
  * norm); copies of 32-bit type.  No tensor, state, copy or device scalar may overlap another

@@ -55,10 +55,10 @@ struct LossJoinArgs {
     int64_t count;           // statistics per row
     const float* at_target;
     const int64_t* target;
-    int64_t cols;
+    int64_t cols, M;
     float *lse, *loss;
 };
-hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream);
+hipError_t launch_loss_join(const LossJoinArgs& j, hipStream_t stream);
 
 // The rows that have a gradient, those with d = dloss (of the rows that count) or d + dlse other
 // than zero: their number, their places (place[m]: m's place among them or -1; list: the rows of

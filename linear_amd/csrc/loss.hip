@@ -24,20 +24,21 @@ __device__ inline float group_fold(float v, float* lds, F f) {
 // to the common reference; the order is fixed.
 __global__ void __launch_bounds__(256) loss_join(LossJoinArgs j) {
     __shared__ float lds[4];
-    const int64_t m = blockIdx.x;
-    const RowPart* p = j.parts + m * j.ldparts;
-    float top = -3.402823466e38f;                    // no reference is lower
-    for (int64_t i = threadIdx.x; i < j.count; i += 256) top = fmaxf(top, p[i].ref);
-    top = group_fold<4>(top, lds, [](float a, float b) { return fmaxf(a, b); });
-    float sum = 0.f;
-    for (int64_t i = threadIdx.x; i < j.count; i += 256) sum += p[i].sum * __expf(p[i].ref - top);
-    sum = group_fold<4>(sum, lds, [](float a, float b) { return a + b; });
-    if (threadIdx.x != 0) return;
-    const float lse = top + logf(sum);
-    if (j.lse) j.lse[m] = lse;
-    if (j.loss) {
-        const int64_t t = j.target[m];
-        j.loss[m] = t >= 0 && t < j.cols ? lse - j.at_target[m] : 0.f;
+    for (int64_t m = blockIdx.x; m < j.M; m += gridDim.x) {
+        const RowPart* p = j.parts + m * j.ldparts;
+        float top = -3.402823466e38f;                // no reference is lower
+        for (int64_t i = threadIdx.x; i < j.count; i += 256) top = fmaxf(top, p[i].ref);
+        top = group_fold<4>(top, lds, [](float a, float b) { return fmaxf(a, b); });
+        float sum = 0.f;
+        for (int64_t i = threadIdx.x; i < j.count; i += 256) sum += p[i].sum * __expf(p[i].ref - top);
+        sum = group_fold<4>(sum, lds, [](float a, float b) { return a + b; });
+        if (threadIdx.x != 0) continue;
+        const float lse = top + logf(sum);
+        if (j.lse) j.lse[m] = lse;
+        if (j.loss) {
+            const int64_t t = j.target[m];
+            j.loss[m] = t >= 0 && t < j.cols ? lse - j.at_target[m] : 0.f;
+        }
     }
 }
 
@@ -80,8 +81,8 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     const auto largest = [](float a, float b) { return fmaxf(a, b); };
     base = group_fold<16>(base, lds, largest);
     most = group_fold<16>(most, lds, largest);
-    // (rows below 2^-80 are left smaller: the factor stays finite)
-    base = fmaxf(base > 0.f ? base : most, 0x1p-80f);
+    // (rows below 2^-80, and d below 2^-100 of the largest, are left smaller: the factors stay finite)
+    base = fmaxf(fmaxf(base > 0.f ? base : most, 0x1p-80f), most * 0x1p-100f);
     int x = 1;
     if (most > 0.f) __builtin_frexpf(most / base, &x);   // most / base < 2^x
     const float scale = __builtin_ldexpf(1.f, 15 - x) / base;
@@ -144,10 +145,11 @@ __global__ void __launch_bounds__(256) loss_gather(LossRowsArgs a, LossGatherArg
 
 }  // namespace
 
-hipError_t launch_loss_join(const LossJoinArgs& j, int64_t M, hipStream_t stream) {
+hipError_t launch_loss_join(const LossJoinArgs& j, hipStream_t stream) {
     LossJoinArgs args = j;
     void* params[] = {&args};
-    return launch_kernel((const void*)loss_join, dim3((unsigned)M), dim3(256), params, 0, stream);
+    const int64_t blocks = j.M < 1 << 20 ? j.M : 1 << 20;
+    return launch_kernel((const void*)loss_join, dim3((unsigned)blocks), dim3(256), params, 0, stream);
 }
 
 hipError_t launch_loss_rows(const LossRowsArgs& r, const LossGatherArgs& g, hipStream_t stream) {

@@ -148,8 +148,8 @@ int32_t run_loss(int elem, const uint16_t* x, int64_t ldx, const uint16_t* w, in
                           cols, stream);
         if (st != LINEAR_OK) return st;
     }
-    const LossJoinArgs j{parts, a.ldparts, a.ldparts, at_target, target, N, lse, loss};
-    return launched(launch_loss_join(j, M, stream));
+    const LossJoinArgs j{parts, a.ldparts, a.ldparts, at_target, target, N, M, lse, loss};
+    return launched(launch_loss_join(j, stream));
 }
 
 // The gradient call's plan.  The vocabulary is taken in pieces of `cols` columns (whole

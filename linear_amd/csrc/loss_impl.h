@@ -140,13 +140,14 @@ __device__ __forceinline__ void finish_dz(const Args& a, unsigned char* smem, Ac
         const int m = m0 + wm * TM + j * R + lr;
         RowTerms r{0.f, 0.f, 0.f, -1};
         if (m < a.M) r = a.terms[m];
-        const int t = r.column - (int)a.col0 - n0 - wn * TN;   // (negative without a target)
+        // the target as a column of this wave (in unsigned arithmetic: one before them, or -1, is far past them)
+        const uint32_t t = (uint32_t)r.column - ((uint32_t)a.col0 + (uint32_t)(n0 + wn * TN));
 #pragma unroll
         for (int i = 0; i < FN; ++i)
 #pragma unroll
             for (int v = 0; v < 4 * G; ++v) {
                 const int c = i * R + v / 4 * 8 + lh * 4 + v % 4;
-                const float d = r.rows * __expf(acc[i][j][v] - r.lse) - (c == t ? r.one : 0.f);
+                const float d = r.rows * __expf(acc[i][j][v] - r.lse) - ((uint32_t)c == t ? r.one : 0.f);
                 acc[i][j][v] = ragged && n0 + wn * TN + c >= a.N ? 0.f : d;
             }
     }

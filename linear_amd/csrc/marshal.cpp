@@ -66,8 +66,18 @@ PyObject* bytes_of(const std::vector<T>& v) {
     return PyBytes_FromStringAndSize((const char*)v.data(), (Py_ssize_t)(v.size() * sizeof(T)));
 }
 
+// f(args, nargs), or None where reading a tensor throws.
+template <PyObject* F(PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+    try {
+        return F(args, nargs);
+    } catch (...) {
+        Py_RETURN_NONE;
+    }
+}
+
 // adamw(params, grads, m, v, copies or None): (params, grads, copies or None, m, v, 8-bit moments, device).
-PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* adamw(PyObject* const* args, Py_ssize_t nargs) {
     List p, g, m, v, c;
     const bool copies = nargs == 5 && args[4] != Py_None;
     if (nargs != 5 || !p.take(args[0]) || !g.take(args[1]) || !m.take(args[2]) || !v.take(args[3]) ||
@@ -84,14 +94,12 @@ PyObject* adamw(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
         if (!state_of(m[i], pr[i].cols, eight, device, mp[i]) || !state_of(v[i], pr[i].cols, eight, device, vp[i])) Py_RETURN_NONE;
         if (copies && (!row_of(c[i], device, cr[i]) || p[i].sizes() != c[i].sizes())) Py_RETURN_NONE;
     }
-    PyObject* none = Py_None;
-    Py_INCREF(none);
-    return Py_BuildValue("(NNNNNii)", bytes_of(pr), bytes_of(gr), copies ? (Py_DECREF(none), bytes_of(cr)) : none, bytes_of(mp),
-                         bytes_of(vp), (int)eight, device);
+    if (!copies) return Py_BuildValue("(NNONNii)", bytes_of(pr), bytes_of(gr), Py_None, bytes_of(mp), bytes_of(vp), (int)eight, device);
+    return Py_BuildValue("(NNNNNii)", bytes_of(pr), bytes_of(gr), bytes_of(cr), bytes_of(mp), bytes_of(vp), (int)eight, device);
 }
 
 // states(out, states): (out, states, device) of 8-bit moments and the tensors they are read into.
-PyObject* states(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+PyObject* states(PyObject* const* args, Py_ssize_t nargs) {
     List o, s;
     if (nargs != 2 || !o.take(args[0]) || !s.take(args[1]) || o.count != s.count || o.count == 0) Py_RETURN_NONE;
     std::vector<Row> rows(o.count);
@@ -103,8 +111,8 @@ PyObject* states(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
 }
 
 PyMethodDef kMethods[] = {
-    {"adamw", (PyCFunction)(void (*)(void))adamw, METH_FASTCALL, nullptr},
-    {"states", (PyCFunction)(void (*)(void))states, METH_FASTCALL, nullptr},
+    {"adamw", (PyCFunction)(void (*)(void))guarded<adamw>, METH_FASTCALL, nullptr},
+    {"states", (PyCFunction)(void (*)(void))guarded<states>, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

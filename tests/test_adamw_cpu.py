@@ -133,3 +133,16 @@ def test_the_8_bit_forms(second):
     z = ref.decode(ref.encode(y, second), y.numel(), second)
     least = y.abs().max() * 2.0 ** (-31 if second else -17)
     assert bool(((z - y).abs() <= 2.0 ** -4 * y.abs() + least).all())
+
+
+def test_the_native_tables_leave_what_is_not_plain_to_the_checks():
+    """Anything but lists of contiguous GPU tensors of the right types and sizes gives None (here: host
+    tensors, wrong objects, lists of other lengths)."""
+    if not os.path.exists(la.MARSHAL_PATH):
+        pytest.skip("_marshal.so not built")
+    n, t = la._marshal(), [torch.zeros(4, 8)]
+    for args in ((t, t, t, t, None), (t, t, t, t, t), ([], [], [], [], None), (t, [], t, t, None), ([1], t, t, t, None),
+                 (t, t, t, "x", None), (t, t, t, t), (None,) * 5, ([t[0].to_sparse()], t, t, t, None)):
+        assert n.adamw(*args) is None
+    for args in ((t, t), ([], []), (t, None), (t,), ([3], [4])):
+        assert n.states(*args) is None

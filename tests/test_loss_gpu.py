@@ -360,3 +360,36 @@ def test_a_weight_past_2_31_words():
         part += dz[:, n:n + 5000] @ piece
         size += dz[:, n:n + 5000].abs() @ piece.abs()
     assert bool(((dx.double() - part).abs() <= (2.0 ** -8 * 1.1 + 4 * bound) * size + 2.0 ** -8 * part.abs()).all())
+
+
+def test_weights_of_extreme_ratios():
+    """dloss far below dlse, and the reverse: the factor that dz is rounded under stays finite."""
+    M, N, K = 33, 300, 72
+    for t in TYPES:
+        x, w, target, b, dloss, dlse = make(M, N, K, t)
+        _, lse = fn("", t)(x, w, target, b)
+        for one, more in ((1e-30, 1.0), (1.0, 1e-30), (1e-36, 1e30), (0.0, 1e-3), (1e-3, 0.0), (1e20, 1e20)):
+            d, e = dloss * one, dlse * more
+            want, bound = ref.backward64(d, e, x, w, target, b, t, True)
+            got = fn("_backward_f32out", t)(d, x, w, target, lse, b, dlse=e, need_dx=False)
+            inside(got[1], want[1], bound[1], "dw %g %g" % (one, more))
+            inside(got[2], want[2], bound[2], "db %g %g" % (one, more))
+
+
+def test_loss_alone_and_rows_of_one_target():
+    """lse without loss and loss without lse; every row with the same target."""
+    M, N, K = 200, 700, 64
+    for t in TYPES:
+        x, w, target, b, dloss, _ = make(M, N, K, t)
+        target.fill_(699)
+        loss, lse = check_forward(x, w, target, b, t)
+        check_backward(dloss, None, x, w, target, lse, b, t)
+        tag = "bf16" if t == torch.bfloat16 else "f16"
+        ws = torch.empty(la.cross_entropy_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV)
+        for keep in (0, 1):
+            out = torch.zeros(M, device=DEV)
+            args = [x.data_ptr(), K, w.data_ptr(), K, b.data_ptr(), target.data_ptr()] + [None, None]
+            args[6 + keep] = out.data_ptr()
+            rc = getattr(la._lib(), "linear_%s_cross_entropy" % tag)(*args, M, N, K, ws.data_ptr(), ws.numel(),
+                                                                      torch.cuda.current_stream().cuda_stream)
+            assert rc == la.LINEAR_OK and torch.equal(out, lse if keep else loss)
