@@ -392,16 +392,36 @@ __device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, c
     const int64_t n = t.n[i], left = n - at, cols = t.cols[i];
     const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
     float p[RUN] = {}, g[RUN] = {};
-    each_value(at, count, cols, t.ldp[i], [&](int e, int64_t o) { p[e] = value_at(t.param[i], t.ptype[i], o); });
-    each_value(at, count, cols, t.ldg[i], [&](int e, int64_t o) { g[e] = value_at(t.grad[i], t.gtype[i], o); });
+    const bool whole = cols == 0 && count == RUN;     // (of a tensor's last chunk, all runs but one)
+    const auto get = [&](const void* from, int type, int64_t ld, float (&out)[RUN]) {
+        if (!whole) each_value(at, count, cols, ld, [&](int e, int64_t o) { out[e] = value_at(from, type, o); });
+        else if (type == kGradF32) widen_run<kGradF32>(load_run<kGradF32>(from, at), out);
+        else if (type == kGradBF16) widen_run<kGradBF16>(load_run<kGradBF16>(from, at), out);
+        else widen_run<kGradF16>(load_run<kGradF16>(from, at), out);
+    };
+    const auto put = [&](void* to, int type, int64_t ld, const float (&v)[RUN]) {
+        if (!whole) each_value(at, count, cols, ld, [&](int e, int64_t o) { put_at(to, type, o, v[e]); });
+        else if (type == kGradF32) store_run<kGradF32>(to, v, at);
+        else if (type == kGradBF16) store_run<kGradBF16>(to, v, at);
+        else store_run<kGradF16>(to, v, at);
+    };
+    get(t.param[i], t.ptype[i], t.ldp[i], p);
+    get(t.grad[i], t.gtype[i], t.ldg[i], g);
     if constexpr (EIGHT) {
         uint8_t *ms = (uint8_t*)t.m[i], *vs = (uint8_t*)t.v[i];
         const int64_t block = n + at / kAdamBlock;
-        uint2 mc = load_codes(ms + at, count), vc = load_codes(vs + at, count);
+        const bool full = count == RUN;
+        uint2 mc = full ? load_codes(ms + at) : load_codes(ms + at, count);
+        uint2 vc = full ? load_codes(vs + at) : load_codes(vs + at, count);
         uint32_t mb = count ? ms[block] : 0u, vb = count ? vs[block] : 0u;
         step8(a, f, p, g, mc, vc, mb, vb);
-        store_codes(ms + at, mc, count);
-        store_codes(vs + at, vc, count);
+        if (full) {
+            store_codes(ms + at, mc);
+            store_codes(vs + at, vc);
+        } else {
+            store_codes(ms + at, mc, count);
+            store_codes(vs + at, vc, count);
+        }
         if (count && (threadIdx.x & 3) == 0) {
             ms[block] = (uint8_t)mb;
             vs[block] = (uint8_t)vb;
@@ -409,23 +429,30 @@ __device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, c
     } else {
         float *mp = (float*)t.m[i] + at, *vp = (float*)t.v[i] + at;
         float m[RUN] = {}, v[RUN] = {};
+        if (count == RUN) {
+            widen_run<kGradF32>(load_run<kGradF32>(mp, 0), m);
+            widen_run<kGradF32>(load_run<kGradF32>(vp, 0), v);
+            step32(a, f, p, g, m, v);
+            store_run<kGradF32>(mp, m, 0);
+            store_run<kGradF32>(vp, v, 0);
+        } else {
 #pragma unroll
-        for (int e = 0; e < RUN; ++e)
-            if (e < count) {
-                m[e] = mp[e];
-                v[e] = vp[e];
-            }
-        step32(a, f, p, g, m, v);
+            for (int e = 0; e < RUN; ++e)
+                if (e < count) {
+                    m[e] = mp[e];
+                    v[e] = vp[e];
+                }
+            step32(a, f, p, g, m, v);
 #pragma unroll
-        for (int e = 0; e < RUN; ++e)
-            if (e < count) {
-                mp[e] = m[e];
-                vp[e] = v[e];
-            }
+            for (int e = 0; e < RUN; ++e)
+                if (e < count) {
+                    mp[e] = m[e];
+                    vp[e] = v[e];
+                }
+        }
     }
-    each_value(at, count, cols, t.ldp[i], [&](int e, int64_t o) { put_at(t.param[i], t.ptype[i], o, p[e]); });
-    if (t.ctype[i] != kNoCopy)
-        each_value(at, count, cols, t.ldc[i], [&](int e, int64_t o) { put_at(t.copy[i], t.ctype[i], o, p[e]); });
+    put(t.param[i], t.ptype[i], t.ldp[i], p);
+    if (t.ctype[i] != kNoCopy) put(t.copy[i], t.ctype[i], t.ldc[i], p);
 }
 
 // The tensor that holds chunk c: the last whose first chunk is <= c.

@@ -1,9 +1,9 @@
 // outer_impl.h -- a weight's gradient from few rows (templates).
 //
-//     y[r, c] = sum_{k < L} row[k, r] * col[k, c]          L <= 64, both contraction-major
+//     y[r, c] = sum_{k < L} row[k, r] * col[k, c]          L <= 128, both contraction-major
 //
-// With one slice of contraction indices the product is bound by writing y, and a tile that ends after
-// one slice overlaps its stores with nothing (262 MB of dW from 20 rows: 74 us on the 256 x 256 tile,
+// With one or two slices of contraction indices the product is bound by writing y, and a tile that
+// ends after them overlaps its stores with nothing (262 MB of dW from 20 rows: 74 us on the 256 x 256 tile,
 // 3.5 TB/s).  Here a workgroup of 4 waves keeps its 256 columns of the column panel in registers, as
 // matrix-core operands, and walks down the rows in blocks of 64: a block's slice of the row operand
 // comes through an LDS ring by direct-to-LDS loads, three blocks ahead, and its sums leave from the
@@ -30,13 +30,14 @@ constexpr int kStream = 2 | 16;
 
 constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
 
-template <int E, int MODE>
+// KS: K steps of 32 contraction indices, 2 or 4.
+template <int KS, int E, int MODE>
 __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
-    constexpr int CROW = 2 * kOuterCols, RROW = 2 * kOuterRows, SLOT = 64 * RROW;
-    constexpr int LOADS = SLOT / 4096;                // of a slice, per wave
+    constexpr int BK = 32 * KS, CROW = 2 * kOuterCols, RROW = 2 * kOuterRows, SLOT = BK * RROW;
+    constexpr int LOADS = SLOT / 4096, CLOADS = BK * CROW / 4096;   // of a slice and of the panel, per wave
     constexpr int STORES = MODE == kOutRound ? 8 : 16;
-    static_assert(kOuterStages * SLOT == 64 * CROW, "the ring takes the column panel's place");
-    __shared__ __attribute__((aligned(1024))) unsigned char smem[64 * CROW];
+    static_assert(kOuterStages * SLOT == BK * CROW, "the ring takes the column panel's place");
+    __shared__ __attribute__((aligned(1024))) unsigned char smem[BK * CROW];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int q = lane >> 4, s = lane & 15, kq = 8 * q + (s >> 2);
     const int L = a.rows ? *a.rows : a.L;
@@ -45,19 +46,19 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
     const int ldc = (int)a.ldc, ldr = (int)a.ldr;
     const uint32_t base = lds_address(smem);
 
-    // the column panel: 64 rows of 512 bytes, 8 loads of 1 KB per wave; rows past L read zero
+    // the column panel: rows of 512 bytes in loads of 1 KB; rows past L read zero
     {
         const __amdgpu_buffer_rsrc_t rc = slice_rsrc(a.c[0] + c0, L > 0 ? ((L - 1) * ldc + ((a.C + 7) & ~7) - c0) * 2 : 0);
-        static_for<0, 8>([&]<int j>() {
-            const int byte = (wave * 8 + j) * 1024 + 16 * lane, k = byte / CROW;
+        static_for<0, CLOADS>([&]<int j>() {
+            const int byte = (wave * CLOADS + j) * 1024 + 16 * lane, k = byte / CROW;
             const int c = (byte % CROW / 16) ^ (2 * panel_swz<kOuterCols>(k));
-            lds_dma16_raw(rc, base + (wave * 8 + j) * 1024, c0 + 8 * c < a.C ? (uint32_t)((k * ldc + 8 * c) * 2) : kOOB);
+            lds_dma16_raw(rc, base + (wave * CLOADS + j) * 1024, c0 + 8 * c < a.C ? (uint32_t)((k * ldc + 8 * c) * 2) : kOOB);
         });
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
-    u32x4 col[2][4];                                  // [K step][fragment]
-    static_for<0, 2>([&]<int ks>() {
+    u32x4 col[KS][4];                                 // [K step][fragment]
+    static_for<0, KS>([&]<int ks>() {
         static_for<0, 4>([&]<int i>() {
             const int unit = wave * 4 + 2 * (i >> 1) + ((s & 3) >> 1);
             lds_byte* p = lds_at(base + (kq + 32 * ks) * CROW + ((unit ^ panel_swz<kOuterCols>(kq)) << 5) + 16 * (s & 1) + 8 * (i & 1));
@@ -99,24 +100,20 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
         turn = turn < kOuterStages - 1 ? turn + 1 : turn;
         lds_barrier();
         request();
-        u32x4 row[2][4];
-        static_for<0, 2>([&]<int ks>() {
-            static_for<0, 4>([&]<int j>() {
-                lds_byte* p = lds_at(base + slot * SLOT + (kq + 32 * ks) * RROW + ((j ^ panel_swz<kOuterRows>(kq)) << 5) + 8 * (s & 3));
-                const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * RROW);
-                row[ks][j] = (u32x4){lo.x, lo.y, hi.x, hi.y};
-            });
-        });
+        const uint32_t from = base + slot * SLOT + kq * RROW + 8 * (s & 3);
         slot = (slot + 1) % kOuterStages;
         const int r0 = block * kOuterRows, left = min(a.R - r0, kOuterRows);
         char* y = (char*)a.y[0] + (int64_t)r0 * a.ldy[0] * WORD;
         const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc((void*)y, (short)0, 0x7fffffff, kRsrcWord3);
         static_for<0, 4>([&]<int j>() {
-            f32x4 acc[4];
+            f32x4 acc[4] = {};
+            static_for<0, KS>([&]<int ks>() {
+                lds_byte* p = lds_at(from + 32 * ks * RROW + ((j ^ panel_swz<kOuterRows>(kq)) << 5));
+                const uint2 lo = lds_tr(p), hi = lds_tr(p + 4 * RROW);
+                const u32x4 row = (u32x4){lo.x, lo.y, hi.x, hi.y};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32<E>(col[0][i], row[0][j], (f32x4){});
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32<E>(col[1][i], row[1][j], acc[i]);
+                for (int i = 0; i < 4; ++i) acc[i] = mfma16x16x32<E>(col[ks][i], row, acc[i]);
+            });
             const int r = 16 * j + s;
             static_for<0, 2>([&]<int p>() {
                 const int c = cl + 32 * p;
@@ -151,8 +148,9 @@ hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream) 
     // eight workgroups for each of 256 CUs, each taking every shares-th block (four: 2 to 4% slower)
     const int64_t shares = (2048 + args.tiles_c - 1) / args.tiles_c;
     void* params[] = {&args};
-    return launch_kernel(mode == kOutRound ? (const void*)outer_stream<E, kOutRound> : (const void*)outer_stream<E, kOutF32>,
-                         dim3((unsigned)((blocks < shares ? blocks : shares) * args.tiles_c)), dim3(256), params, 0, stream);
+    const void* fn = a.L <= 64 ? (mode == kOutRound ? (const void*)outer_stream<2, E, kOutRound> : (const void*)outer_stream<2, E, kOutF32>)
+                               : (mode == kOutRound ? (const void*)outer_stream<4, E, kOutRound> : (const void*)outer_stream<4, E, kOutF32>);
+    return launch_kernel(fn, dim3((unsigned)((blocks < shares ? blocks : shares) * args.tiles_c)), dim3(256), params, 0, stream);
 }
 
 }  // namespace lin

@@ -77,7 +77,7 @@ def test_vocabulary_in_pieces(M, N, K, t):
 
 # few rows against weights of a million values and more: column tiles and row blocks of every remainder,
 # outputs of aligned rows (and, with K odd or rows off alignment, the other kernels)
-FEW = [(1, 4096, 264), (2, 16500, 64), (20, 4103, 520), (33, 5000, 776), (63, 2049, 1032), (64, 70001, 256), (64, 1100, 2008),
+FEW = [(65, 4099, 520), (100, 3000, 776), (127, 16500, 72), (128, 9001, 1032), (128, 1100, 2008), (1, 4096, 264), (2, 16500, 64), (20, 4103, 520), (33, 5000, 776), (63, 2049, 1032), (64, 70001, 256), (64, 1100, 2008),
        (17, 3000, 513), (40, 524300, 8)]
 
 
