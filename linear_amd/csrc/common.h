@@ -67,9 +67,13 @@ enum : int { kF16 = 0, kBF16 = 1 };
 // epilogue program of a.epi.  kOutGated: two projections per output, act(g) * u.
 // kOutF32Add: add the FP32 sum to the output.  kOutLse, kOutDz: the cross entropy's row
 // statistics and its gradient by the logits (loss_impl.h).  kOutList: kOutRound with the
-// rows placed by a list.
+// rows placed by a list.  kOutStream: kOutRound with stores past the caches (y 16-byte aligned, of
+// a stride up to kMaxLdIn).
 enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 4, kOutF32Add = 5, kOutLse = 6, kOutDz = 7,
-             kOutList = 8 };
+             kOutList = 8, kOutStream = 9 };
+
+// Cache policy of buffer stores past the caches: non-temporal, of device scope (bits nt and sc1).
+constexpr int kPastCaches = 2 | 16;
 
 // Grouped contraction: group g is the activation slice x + g * gsx, the weight
 // block of rows g * N .. g * N + N - 1, y + g * gsy and the bias words g * N ..

@@ -226,6 +226,14 @@ __device__ inline void epi_tile(const LinearArgs& a, const unsigned char* tile, 
         for (int k = 0; k < CH; ++k) {
             int64_t row = rr[k];
             if constexpr (MODE == kOutList) row = rr[k] < a.M ? a.list[rr[k]] : 0;
+            if constexpr (MODE == kOutStream) {
+                const __amdgpu_buffer_rsrc_t ry = __builtin_amdgcn_make_buffer_rsrc(
+                    (void*)((uint16_t*)a.y + (int64_t)m0 * a.ldy + n0), (short)0, 0x7fffffff, kRsrcWord3);
+                const bool inside = rr[k] < a.M && cc[k] + 7 < a.N;
+                __builtin_amdgcn_raw_buffer_store_b128(
+                    t[k], ry, inside ? (uint32_t)(((rr[k] - m0) * (int)a.ldy + cc[k] - n0) * 2) : kOOB, 0, kPastCaches);
+                if (inside) continue;
+            }
             store8((uint16_t*)a.y + row * a.ldy + cc[k], rr[k] < a.M, cc[k], a.N, t[k]);
         }
     }

@@ -460,6 +460,7 @@ static const void* grad_fn(bool rowt, int mode) {
     }
     if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;
     if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32Add>;
+    if (mode == kOutStream) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutStream>;
     return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutRound>;
 }
 

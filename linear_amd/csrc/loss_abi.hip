@@ -319,10 +319,12 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
             const int mode = p.pieces > 1 ? (piece == 0 ? kOutF32 : kOutF32Add) : list ? kOutList : kOutRound;
             if ((st = launch_stream(elem, false, mode, sx, p.dx, di, partials, stream)) != LINEAR_OK) return st;
         }
+        // dw's words go past the caches, which hold the weight and dz (256 x 32000 x 4096 bf16 loss and
+        // gradients: 376 us, 361; 4096 x 128259 x 4096 12.52 ms, 12.41)
         if (outer) {
             if ((st = launched(launch_outer(elem, f32 ? kOutF32 : kOutRound, sw, stream))) != LINEAR_OK) return st;
         } else if (want_dw) {
-            const int mode = !f32 ? kOutRound : accumulate ? kOutF32Add : kOutF32;
+            const int mode = !f32 ? (streamable(dw, lddw) ? kOutStream : kOutRound) : accumulate ? kOutF32Add : kOutF32;
             if ((st = launch_stream(elem, true, mode, sw, p.dw, di, partials, stream)) != LINEAR_OK) return st;
         }
     }

@@ -22,12 +22,9 @@
 
 namespace lin {
 
-// Cache policy of the stores: non-temporal, of device scope (bits nt and sc1).  y is larger than the
-// caches or is read by nobody soon, and the weight that the next call reads stays in them
-// (backward without dx, 64 x 128259 x 4096 bf16: 520 us with plain stores, 508 with nt, 417 with
-// both; 20 x 32000 x 4096: 133, 122, 96).
-constexpr int kStream = 2 | 16;
-
+// The stores go past the caches: y is larger than those or is read by nobody soon, and the weight
+// that the next call reads stays in them (backward without dx, 64 x 128259 x 4096 bf16: 520 us with
+// plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).
 constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
 
 // KS: K steps of 32 contraction indices, 2 or 4.
@@ -125,12 +122,12 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
                         const f32x4 v = acc[2 * p + e / 2] * back;
                         w[e] = (uint32_t)narrow<E>(v[2 * (e & 1)]) | ((uint32_t)narrow<E>(v[2 * (e & 1) + 1]) << 16);
                     }
-                    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, kStream);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, kPastCaches);
                 } else {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const f32x4 v = acc[2 * p + b] * back;
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ry, off == kOOB ? kOOB : off + 16 * b, 0, kStream);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ry, off == kOOB ? kOOB : off + 16 * b, 0, kPastCaches);
                     }
                 }
             });

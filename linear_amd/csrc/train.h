@@ -120,7 +120,8 @@ inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {64, 64, 2, 2, 2, 4},
     {128, 128, 2, 4, 1, 2},
 };
-// rowt: contraction-major row operand; mode kOutRound, kOutF32, kOutF32Add or, without rowt, kOutList.
+// rowt: contraction-major row operand; mode kOutRound, kOutF32, kOutF32Add or, without rowt, kOutList,
+// with it kOutStream.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);
