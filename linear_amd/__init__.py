@@ -2,8 +2,9 @@
 
 Also its bfloat16 form, the unrounded FP32 sums, multi-step epilogue programs,
 the grouped and indexed (per-row expert) contractions, the gated feed-forward
-block with its gradients, the layer's gradients, and the global gradient norm
-with clipping.  A thin ctypes binding over the C ABI of ``liblinear_amd.so`` (declared in
+block with its gradients, the layer's gradients, the global gradient norm
+with clipping, a linear head's softmax cross entropy with its gradients, and an
+AdamW step over many tensors.  A thin ctypes binding over the C ABI of ``liblinear_amd.so`` (declared in
 ``include/linear_amd.h``).  The functions carry the C entry points' names and
 only marshal arguments: every step of the computation runs in the library's
 HIP kernels.  PyTorch supplies device memory and the stream.  If the library

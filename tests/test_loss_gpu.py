@@ -393,3 +393,61 @@ def test_loss_alone_and_rows_of_one_target():
             rc = getattr(la._lib(), "linear_%s_cross_entropy" % tag)(*args, M, N, K, ws.data_ptr(), ws.numel(),
                                                                       torch.cuda.current_stream().cuda_stream)
             assert rc == la.LINEAR_OK and torch.equal(out, lse if keep else loss)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(5, 129, 192), (20, 4099, 520), (100, 3001, 776), (130, 515, 93), (300, 8201, 264), (1024, 1024, 768),
+                                   (2100, 1032, 520), (20000, 8300, 64)])
+def test_what_the_workspace_and_the_outputs_held_does_not_matter(M, N, K, t):
+    """All bits set: NaN as words and as floats, -1 as counts and places."""
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    loss, lse = fn("", t)(x, w, target, b, workspace=torch.zeros(la.cross_entropy_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV))
+    size = la.cross_entropy_backward_workspace_bytes(M, N, K)
+    for name in ("_backward", "_backward_f32out"):
+        clean = fn(name, t)(dloss, x, w, target, lse, b, dlse=dlse, workspace=torch.zeros(size, dtype=torch.uint8, device=DEV))
+        full = [torch.full_like(g, float("nan")) for g in clean]
+        got = fn(name, t)(dloss, x, w, target, lse, b, dlse=dlse, dx=full[0], dw=full[1], db=full[2],
+                          workspace=torch.full((size,), 255, dtype=torch.uint8, device=DEV))
+        assert all(torch.equal(u, v) for u, v in zip(clean, got))
+    again = fn("", t)(x, w, target, b, workspace=torch.full((la.cross_entropy_workspace_bytes(M, N, K),), 255, dtype=torch.uint8, device=DEV))
+    assert torch.equal(loss, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("M", [9, 1500])
+def test_targets_of_any_64_bit_value(M):
+    """Words whose lower halves look like columns do not count."""
+    t, N, K = torch.bfloat16, 300, 72
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    strange = torch.tensor([2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, -2 ** 63, -2 ** 32 + 7, 2 ** 31, -1], device=DEV)
+    target[1:8] = strange
+    _, lse = check_forward(x, w, target, b, t)
+    check_backward(dloss, dlse, x, w, target, lse, b, t)
+
+
+def test_two_calls_at_once():
+    """Two host threads, each with a stream, inputs and workspaces of its own."""
+    import threading
+    t = torch.bfloat16
+    sets = [make(300, 2049, 264, t, seed=s) for s in (0, 50)]
+    want = []
+    for x, w, target, b, dloss, dlse in sets:
+        loss, lse = fn("", t)(x, w, target, b)
+        want.append((loss, lse) + fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse))
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def work(i):
+        x, w, target, b, dloss, dlse = sets[i]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(8):
+                loss, lse = fn("", t)(x, w, target, b)
+                got[i] = (loss, lse) + fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse)
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    for g, v in zip(got, want):
+        assert g is not None and all(torch.equal(a, b) for a, b in zip(g, v))
