@@ -6,8 +6,6 @@
 
 namespace lin {
 
-// Tensors of one launch, in its kernel arguments.
-constexpr int kAdamTensors = 40;
 constexpr int kAdamRun = 8;                           // consecutive values of a thread
 constexpr int kAdamRuns = 256 * kAdamRun;             // values of a workgroup's run
 // Runs of a workgroup's chunk: with 8-bit moments, and for their values, what a workgroup does
@@ -20,16 +18,32 @@ constexpr int kAdamGrid = 1 << 23;                    // most workgroups
 constexpr int kAdamBlock = 32;                        // values that share a power of two (8-bit moments)
 enum : int { kNoCopy = 3 };                           // beside kGradF16, kGradBF16 and kGradF32
 
-struct AdamTable {
-    void* param[kAdamTensors];
-    const void* grad[kAdamTensors];
-    void *m[kAdamTensors], *v[kAdamTensors], *copy[kAdamTensors];
-    int64_t n[kAdamTensors];                          // values
-    int64_t first[kAdamTensors + 1];                  // first chunk of each tensor; the last: all chunks
-    int64_t cols[kAdamTensors];                       // values of a row; 0: no gaps between the rows
-    int32_t ldp[kAdamTensors], ldg[kAdamTensors], ldc[kAdamTensors];
-    uint8_t ptype[kAdamTensors], gtype[kAdamTensors], ctype[kAdamTensors];
+// The tensors of one launch, in its kernel arguments.
+template <int N>
+struct AdamTensors {
+    static constexpr int kMost = N;
+    void* param[N];
+    const void* grad[N];
+    void *m[N], *v[N];
+    int64_t n[N];                                     // values
+    int64_t first[N + 1];                             // first chunk of each tensor; the last: all chunks
+    uint8_t types[N];                                 // 3 * the parameter's + the gradient's
     int count;
+};
+
+// Copies, and gaps between rows: cols is the values of a row (0: no gaps), ld the row strides.
+struct AdamTable : AdamTensors<40> {
+    static constexpr bool kPlain = false;
+    void* copy[kMost];
+    int64_t cols[kMost];
+    int32_t ldp[kMost], ldg[kMost], ldc[kMost];
+    uint8_t ctype[kMost];
+};
+
+// Neither: more tensors in a launch (63 tensors of 66049 and 132355 values, FP32: 32.3 us in two
+// launches, 26.9 in one; with 8-bit moments and their values 48, 35).
+struct AdamPlainTable : AdamTensors<72> {
+    static constexpr bool kPlain = true;
 };
 
 struct AdamArgs {
@@ -41,8 +55,10 @@ struct AdamArgs {
     const float* device_lr;          // not null: read instead of lr
     const int64_t* device_step;      // not null: the step
 };
-static_assert(sizeof(AdamTable) + sizeof(AdamArgs) <= 3840, "the table travels as kernel arguments");
+static_assert(sizeof(AdamTable) + sizeof(AdamArgs) <= 3840 && sizeof(AdamPlainTable) + sizeof(AdamArgs) <= 3840,
+              "the table travels as kernel arguments");
 hipError_t launch_adamw(bool eight, const AdamTable& t, const AdamArgs& a, int grid, hipStream_t stream);
+hipError_t launch_adamw(bool eight, const AdamPlainTable& t, const AdamArgs& a, int grid, hipStream_t stream);
 
 // 8-bit moments as the numbers they stand for.
 constexpr int kValueTensors = 64;

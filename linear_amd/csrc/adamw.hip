@@ -5,7 +5,7 @@
 //     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
 //
 // One pass: weights, gradients and moments are read once, weights and moments written.  Up to
-// kAdamTensors tensors go into one launch, their table in the kernel's arguments; a tensor's
+// 72 tensors (40 with copies or gaps between rows) go into one launch, their table in its arguments; a tensor's
 // values, in row-major order, are cut into chunks, one for each workgroup (shares of
 // many chunks a workgroup read and wrote as many distant streams at once: 10% slower).  A thread
 // takes 8 consecutive values.
@@ -329,8 +329,8 @@ __device__ inline void step8(const AdamArgs& a, const Factors& f, float (&p)[RUN
 
 // A chunk of a tensor without gaps that lies inside it, of types P and G: every load is issued
 // before the first is used.
-template <bool EIGHT, int P, int G>
-__device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t begin) {
+template <bool EIGHT, int P, int G, typename Table>
+__device__ __forceinline__ void chunk_fast(const Table& t, const AdamArgs& a, const Factors& f, int i, int64_t begin) {
     constexpr int U = adam_runs(EIGHT);
     const int64_t at = begin + threadIdx.x * RUN;
     Run<P> pr[U];
@@ -343,8 +343,10 @@ __device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a
     float p[RUN], g[RUN];
     const auto leave = [&](int u) {
         store_run<P>(t.param[i], p, at + u * kAdamRuns);
-        if (t.ctype[i] == kGradBF16) store_run<kGradBF16>(t.copy[i], p, at + u * kAdamRuns);
-        else if (t.ctype[i] == kGradF16) store_run<kGradF16>(t.copy[i], p, at + u * kAdamRuns);
+        if constexpr (!Table::kPlain) {
+            if (t.ctype[i] == kGradBF16) store_run<kGradBF16>(t.copy[i], p, at + u * kAdamRuns);
+            else if (t.ctype[i] == kGradF16) store_run<kGradF16>(t.copy[i], p, at + u * kAdamRuns);
+        }
     };
     if constexpr (EIGHT) {
         uint8_t *ms = (uint8_t*)t.m[i] + at, *vs = (uint8_t*)t.v[i] + at;
@@ -387,9 +389,16 @@ __device__ __forceinline__ void chunk_fast(const AdamTable& t, const AdamArgs& a
 }
 
 // Any run.  Lanes past the end take part in their block's maximum with zeros.
-template <bool EIGHT>
-__device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
-    const int64_t n = t.n[i], left = n - at, cols = t.cols[i];
+template <bool EIGHT, typename Table>
+__device__ __forceinline__ void run_any(const Table& t, const AdamArgs& a, const Factors& f, int i, int64_t at) {
+    const int64_t n = t.n[i], left = n - at;
+    int64_t cols = 0, ldp = 0, ldg = 0;
+    if constexpr (!Table::kPlain) {
+        cols = t.cols[i];
+        ldp = t.ldp[i];
+        ldg = t.ldg[i];
+    }
+    const int ptype = t.types[i] / 3, gtype = t.types[i] % 3;
     const int count = left >= RUN ? RUN : left > 0 ? (int)left : 0;
     float p[RUN] = {}, g[RUN] = {};
     const bool whole = cols == 0 && count == RUN;     // (of a tensor's last chunk, all runs but one)
@@ -405,8 +414,8 @@ __device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, c
         else if (type == kGradBF16) store_run<kGradBF16>(to, v, at);
         else store_run<kGradF16>(to, v, at);
     };
-    get(t.param[i], t.ptype[i], t.ldp[i], p);
-    get(t.grad[i], t.gtype[i], t.ldg[i], g);
+    get(t.param[i], ptype, ldp, p);
+    get(t.grad[i], gtype, ldg, g);
     if constexpr (EIGHT) {
         uint8_t *ms = (uint8_t*)t.m[i], *vs = (uint8_t*)t.v[i];
         const int64_t block = n + at / kAdamBlock;
@@ -451,8 +460,9 @@ __device__ __forceinline__ void run_any(const AdamTable& t, const AdamArgs& a, c
                 }
         }
     }
-    put(t.param[i], t.ptype[i], t.ldp[i], p);
-    if (t.ctype[i] != kNoCopy) put(t.copy[i], t.ctype[i], t.ldc[i], p);
+    put(t.param[i], ptype, ldp, p);
+    if constexpr (!Table::kPlain)
+        if (t.ctype[i] != kNoCopy) put(t.copy[i], t.ctype[i], t.ldc[i], p);
 }
 
 // The tensor that holds chunk c: the last whose first chunk is <= c.
@@ -468,17 +478,20 @@ __device__ inline int tensor_of(const Table& t, int64_t c) {
 }
 
 // One chunk per workgroup, in their order (past the grid's limit the next ones after it).
-template <bool EIGHT>
-__global__ void __launch_bounds__(256, 4) adamw(AdamTable t, AdamArgs a) {
+template <bool EIGHT, typename Table>
+__global__ void __launch_bounds__(256, 4) adamw(Table t, AdamArgs a) {
     const Factors f = factors(a);
     for (int64_t c = blockIdx.x; c < t.first[t.count]; c += gridDim.x) {
         const int i = tensor_of(t, c);
         const int64_t begin = (c - t.first[i]) * adam_chunk(EIGHT);
-        if (t.cols[i] || begin + adam_chunk(EIGHT) > t.n[i]) {
-            for (int u = 0; u < adam_runs(EIGHT); ++u) run_any<EIGHT>(t, a, f, i, begin + u * kAdamRuns + threadIdx.x * RUN);
+        bool gaps = false;
+        if constexpr (!Table::kPlain) gaps = t.cols[i] != 0;
+        if (gaps || begin + adam_chunk(EIGHT) > t.n[i]) {
+            for (int u = 0; u < adam_runs(EIGHT) && begin + u * kAdamRuns < t.n[i]; ++u)
+                run_any<EIGHT>(t, a, f, i, begin + u * kAdamRuns + threadIdx.x * RUN);
             continue;
         }
-        switch (t.ptype[i] * 3 + t.gtype[i]) {        // uniform
+        switch (t.types[i]) {                         // uniform
             case 0: chunk_fast<EIGHT, 0, 0>(t, a, f, i, begin); break;
             case 1: chunk_fast<EIGHT, 0, 1>(t, a, f, i, begin); break;
             case 2: chunk_fast<EIGHT, 0, 2>(t, a, f, i, begin); break;
@@ -532,12 +545,20 @@ __global__ void __launch_bounds__(256) adamw_values(ValueTable t) {
 
 }  // namespace
 
-hipError_t launch_adamw(bool eight, const AdamTable& t, const AdamArgs& a, int grid, hipStream_t stream) {
-    AdamTable table = t;
+template <typename Table>
+static hipError_t launch_table(bool eight, const Table& t, const AdamArgs& a, int grid, hipStream_t stream) {
+    Table table = t;
     AdamArgs args = a;
     void* params[] = {&table, &args};
-    return launch_kernel(eight ? (const void*)adamw<true> : (const void*)adamw<false>, dim3((unsigned)grid), dim3(256), params, 0,
-                         stream);
+    return launch_kernel(eight ? (const void*)adamw<true, Table> : (const void*)adamw<false, Table>, dim3((unsigned)grid),
+                         dim3(256), params, 0, stream);
+}
+
+hipError_t launch_adamw(bool eight, const AdamTable& t, const AdamArgs& a, int grid, hipStream_t stream) {
+    return launch_table(eight, t, a, grid, stream);
+}
+hipError_t launch_adamw(bool eight, const AdamPlainTable& t, const AdamArgs& a, int grid, hipStream_t stream) {
+    return launch_table(eight, t, a, grid, stream);
 }
 
 hipError_t launch_adamw_values(bool second, const ValueTable& t, int grid, hipStream_t stream) {

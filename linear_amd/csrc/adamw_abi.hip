@@ -63,6 +63,42 @@ int32_t check_options(const linear_adamw_options& o) {
 
 int grid_of(int64_t chunks) { return (int)std::min<int64_t>(chunks, kAdamGrid); }
 
+// The launches over the tensors that are not empty.
+template <typename Table>
+int32_t launch_tables(const linear_tensor* params, const linear_tensor* grads, void* const* m, void* const* v,
+                      const linear_tensor* copies, int64_t count, bool eight, const AdamArgs& a, hipStream_t stream) {
+    Table t;
+    memset(&t, 0, sizeof t);
+    for (int64_t i = 0; i < count; ++i) {
+        const linear_tensor &p = params[i], &g = grads[i];
+        if (!empty(p)) {
+            const int k = t.count;
+            t.param[k] = p.data;
+            t.grad[k] = g.data;
+            t.m[k] = m[i];
+            t.v[k] = v[i];
+            t.n[k] = p.rows * p.cols;
+            t.types[k] = (uint8_t)(3 * p.type + g.type);
+            if constexpr (!Table::kPlain) {
+                t.copy[k] = copies ? copies[i].data : nullptr;
+                t.cols[k] = whole(p) && whole(g) && (!copies || whole(copies[i])) ? 0 : p.cols;
+                t.ldp[k] = (int32_t)(p.rows == 1 ? 0 : p.ld);
+                t.ldg[k] = (int32_t)(g.rows == 1 ? 0 : g.ld);
+                t.ldc[k] = (int32_t)(!copies || p.rows == 1 ? 0 : copies[i].ld);
+                t.ctype[k] = (uint8_t)(copies ? copies[i].type : (int64_t)kNoCopy);
+            }
+            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], adam_chunk(eight));
+            t.count = k + 1;
+        }
+        if (t.count == Table::kMost || (i + 1 == count && t.count > 0)) {
+            const int32_t st = launched(launch_adamw(eight, t, a, grid_of(t.first[t.count]), stream));
+            if (st != LINEAR_OK) return st;
+            t.count = 0;
+        }
+    }
+    return LINEAR_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,35 +162,10 @@ int32_t linear_adamw(const linear_tensor* params, const linear_tensor* grads, vo
     a.norm = o.norm;
     a.device_lr = o.device_lr;
     a.device_step = o.device_step;
-    AdamTable t;
-    memset(&t, 0, sizeof t);
-    for (int64_t i = 0; i < count; ++i) {
-        const linear_tensor &p = params[i], &g = grads[i];
-        if (!empty(p)) {
-            const int k = t.count;
-            t.param[k] = p.data;
-            t.grad[k] = g.data;
-            t.m[k] = m[i];
-            t.v[k] = v[i];
-            t.copy[k] = copies ? copies[i].data : nullptr;
-            t.n[k] = p.rows * p.cols;
-            t.cols[k] = whole(p) && whole(g) && (!copies || whole(copies[i])) ? 0 : p.cols;
-            t.ldp[k] = (int32_t)(p.rows == 1 ? 0 : p.ld);
-            t.ldg[k] = (int32_t)(g.rows == 1 ? 0 : g.ld);
-            t.ldc[k] = (int32_t)(!copies || p.rows == 1 ? 0 : copies[i].ld);
-            t.ptype[k] = (uint8_t)p.type;
-            t.gtype[k] = (uint8_t)g.type;
-            t.ctype[k] = (uint8_t)(copies ? copies[i].type : (int64_t)kNoCopy);
-            t.first[k + 1] = t.first[k] + tiles_of(t.n[k], adam_chunk(o.state_bits == 8));
-            t.count = k + 1;
-        }
-        if (t.count == kAdamTensors || (i + 1 == count && t.count > 0)) {
-            st = launched(launch_adamw(o.state_bits == 8, t, a, grid_of(t.first[t.count]), (hipStream_t)stream));
-            if (st != LINEAR_OK) return st;
-            t.count = 0;
-        }
-    }
-    return LINEAR_OK;
+    bool plain = !copies;
+    for (int64_t i = 0; i < count && plain; ++i) plain = empty(params[i]) || (whole(params[i]) && whole(grads[i]));
+    if (plain) return launch_tables<AdamPlainTable>(params, grads, m, v, nullptr, count, o.state_bits == 8, a, (hipStream_t)stream);
+    return launch_tables<AdamTable>(params, grads, m, v, copies, count, o.state_bits == 8, a, (hipStream_t)stream);
 }
 
 int32_t linear_adamw_values(const linear_tensor* out, const void* const* states, int32_t second, int64_t count, void* stream) {

@@ -349,3 +349,29 @@ def test_a_training_step_of_a_small_model(bits):
         grads = [dwg, dwu, dwo, dhead]
         norm = la.linear_grad_norm(grads)
         check_step(params, grads, m, v, step, ref.clip_scale(norm, 0.1), norm=norm, max_norm=0.1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("with_copies", [False, True], ids=["plain", "copies"])
+@pytest.mark.parametrize("count", [39, 40, 41, 71, 72, 73, 145])
+def test_tables_of_every_fill(count, with_copies, bits):
+    """Tensors that fill a launch's table, one less and one more, in the plain form and with copies; empty
+    tensors among them take no place."""
+    sizes = [(1 + (53 * i) % 97,) for i in range(count)]
+    sizes[3:3] = [(0,), (0, 5)]
+    p, g = make(sizes, TYPES, TYPES[::-1])
+    m, v = states(p, bits)
+    copies = [torch.empty_like(t, dtype=torch.bfloat16) for t in p] if with_copies else None
+    check_step(p, g, m, v, 1, copies=copies)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_one_tensor_with_gaps_among_plain_ones(bits):
+    sizes = [(1 + (53 * i) % 97, 3) for i in range(75)]
+    p, g = make(sizes, [torch.float32], [torch.bfloat16])
+    m, v = states(p, bits)
+    wide = torch.full((sizes[50][0], 8), 7.0, device=DEV)
+    wide[:, :3] = p[50]
+    p[50] = wide[:, :3]
+    check_step(p, g, m, v, 1)
+    assert bool((wide[:, 3:] == 7.0).all())
