@@ -877,7 +877,22 @@ def _vector(t, name, dtype, n):
     return t.data_ptr()
 
 
+def _new_scratch(need, device):
+    """A new workspace on a GPU and its address, at less host time than _scratch."""
+    made = _marshal().scratch(need, device)
+    return made if made is not None else _scratch(None, need, torch.device("cuda", device))[:2]
+
+
 def _cross_entropy_call(tag, dtype, x, weight, target, b, loss, lse, workspace, stream):
+    name = _CROSS_ENTROPY[tag]
+    if stream is None and workspace is None and loss is None and lse is None:
+        packed = _marshal().cross_entropy(x, weight, target, b, tag == "bf16")    # None: not the plain case
+        if packed is not None:
+            device, M, N, K, loss, lse, args = packed
+            need = cross_entropy_workspace_bytes(M, N, K)
+            workspace, wsp = _new_scratch(need, device)
+            _check(_entry(name)(*args, M, N, K, wsp, need, torch._C._cuda_getCurrentRawStream(device)), name)
+            return loss, lse
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [M, K] and weight [N, K]")
     M, K = x.shape
@@ -893,7 +908,6 @@ def _cross_entropy_call(tag, dtype, x, weight, target, b, loss, lse, workspace, 
         if lse is None:
             lse = torch.empty(M, dtype=torch.float32, device=x.device)
         workspace, wsp, wsn = _scratch(workspace, cross_entropy_workspace_bytes(M, N, K), x.device)
-    name = _CROSS_ENTROPY[tag]
     rc = _entry(name)(xp, ldx, wp, ldw, bp, tp, _vector(loss, "loss", torch.float32, M), _vector(lse, "lse", torch.float32, M),
                       M, N, K, wsp, wsn, handle)
     _check(rc, name)
@@ -917,10 +931,22 @@ def linear_bf16_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: tor
 
 def _cross_entropy_backward_call(tag, dtype, f32, dloss, x, weight, target, lse, b, dlse, need_dx, need_dw, bias, accumulate,
                                  dx, dw, db, workspace, stream):
+    name = _CROSS_ENTROPY_BACKWARD[tag, f32]
+    need_dx, need_dw = bool(need_dx or dx is not None), bool(need_dw or dw is not None)
+    bias = db is not None or (need_dw and b is not None if bias is None else bool(bias))
+    if stream is None and workspace is None and dx is None and dw is None and db is None and not accumulate and (
+            need_dx or need_dw or bias):
+        packed = _marshal().cross_entropy_backward(dloss, x, weight, target, lse, b, dlse, need_dx, need_dw, bias,
+                                                   tag == "bf16", f32)
+        if packed is not None:
+            device, M, N, K, dx, dw, db, args = packed
+            need = cross_entropy_backward_workspace_bytes(M, N, K)
+            workspace, wsp = _new_scratch(need, device)
+            flag = (0,) if f32 else ()
+            _check(_entry(name)(*args, *flag, M, N, K, wsp, need, torch._C._cuda_getCurrentRawStream(device)), name)
+            return dx, dw, db
     if x.dim() != 2 or weight.dim() != 2:
         raise ValueError("x must be [M, K] and weight [N, K]")
-    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
-    bias = db is not None or (need_dw and b is not None if bias is None else bias)
     if not (need_dx or need_dw or bias):
         raise ValueError("nothing to compute: no gradient is wanted")
     if accumulate and ((need_dw and dw is None) or (bias and db is None)):
@@ -941,7 +967,6 @@ def _cross_entropy_backward_call(tag, dtype, f32, dloss, x, weight, target, lse,
         if bias and db is None:
             db = torch.empty(N, dtype=odt, device=x.device)
         workspace, wsp, wsn = _scratch(workspace, cross_entropy_backward_workspace_bytes(M, N, K), x.device)
-    name = _CROSS_ENTROPY_BACKWARD[tag, f32]
     flag = (int(bool(accumulate)),) if f32 else ()
     rc = _entry(name)(vectors[0], vectors[1], xp, ldx, wp, ldw, bp, tp, vectors[2], *dxa, *dwa,
                       _vector(db, "db", odt, N) if bias else None, *flag, M, N, K, wsp, wsn, handle)

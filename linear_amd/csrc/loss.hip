@@ -43,19 +43,20 @@ __global__ void __launch_bounds__(256) loss_join(LossJoinArgs j) {
 }
 
 struct RowWeights {
-    float d, rows;
+    float d, rows, lse;
     int32_t column;
 };
 __device__ inline RowWeights row_weights(const LossRowsArgs& a, int64_t m) {
     const int64_t t = a.target[m];                   // (every load is issued before the first is used)
-    const float all = a.dloss[m], more = a.dlse ? a.dlse[m] : 0.f;
+    const float all = a.dloss[m], more = a.dlse ? a.dlse[m] : 0.f, lse = a.lse[m];
     const bool counts = t >= 0 && t < a.cols;
     const float d = counts ? all : 0.f;
-    return {d, a.dlse ? d + more : d, counts ? (int32_t)t : -1};
+    return {d, a.dlse ? d + more : d, lse, counts ? (int32_t)t : -1};
 }
 
-__device__ inline void gather_piece(const LossGatherArgs& g, int64_t m, int c, int32_t at) {
-    if (at >= 0) *(u32x4*)(g.out + at * g.ldo + c) = load8(g.x + m * g.ldx + c, true, c, g.K);
+__device__ inline u32x4 piece_of(const LossGatherArgs& g, int64_t m, int c) { return load8(g.x + m * g.ldx + c, true, c, g.K); }
+__device__ inline void leave_piece(const LossGatherArgs& g, int64_t m, int c, int32_t at, const u32x4& piece) {
+    if (at >= 0) *(u32x4*)(g.out + at * g.ldo + c) = piece;
     else if (g.zeroed) store8(g.zeroed + m * g.ldz + c, true, c, g.K, (u32x4){0u, 0u, 0u, 0u});
 }
 
@@ -68,7 +69,12 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     __shared__ int counts[16];
     __shared__ int32_t places[SCAN ? 1 : kLossScanRows];
     float base = 0.f, most = 0.f;
-    RowWeights mine{0.f, 0.f, -1};                   // of row threadIdx.x
+    RowWeights mine{0.f, 0.f, 0.f, -1};              // of row threadIdx.x
+    // the first piece of x that this thread moves, requested ahead of the places: most threads have no other
+    const int chunks = SCAN ? 1 : (int)(g.ldo / 8);
+    const int64_t total = SCAN ? 0 : a.M * chunks, i0 = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+    u32x4 piece = {};
+    if (i0 < total) piece = piece_of(g, i0 / chunks, (int)(i0 % chunks) * 8);
 #pragma unroll 4
     for (int64_t m = threadIdx.x; m < a.M; m += 1024) {
         const RowWeights w = row_weights(a, m);
@@ -92,12 +98,8 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     int taken = 0;
     for (int64_t m0 = 0; m0 < a.M; m0 += 1024) {
         const int64_t m = m0 + threadIdx.x;
-        RowWeights w{0.f, 0.f, -1};
-        float lse = 0.f;
-        if (m < a.M) {
-            w = m < 1024 ? mine : row_weights(a, m);
-            lse = a.lse[m];
-        }
+        RowWeights w{0.f, 0.f, 0.f, -1};
+        if (m < a.M) w = m < 1024 ? mine : row_weights(a, m);
         const bool has = w.d != 0.f || w.rows != 0.f;    // (NaN too)
         const uint64_t mask = __ballot(has);
         __syncthreads();                             // the last counts have been read
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
         }
         if (has && first) {
             a.list[at] = (int32_t)m;
-            a.terms[at] = RowTerms{lse, w.rows * scale, w.d * scale, w.column};
+            a.terms[at] = RowTerms{w.lse, w.rows * scale, w.d * scale, w.column};
         }
     }
     if (first && threadIdx.x == 0) {
@@ -126,11 +128,9 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     }
     if constexpr (!SCAN) {
         __syncthreads();
-        const int chunks = (int)(g.ldo / 8);
-        const int64_t total = a.M * chunks;
-        for (int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 1024) {
-            const int m = (int)(i / chunks);
-            gather_piece(g, m, (int)(i - (int64_t)m * chunks) * 8, places[m]);
+        for (int64_t i = i0; i < total; i += (int64_t)gridDim.x * 1024) {
+            const int m = (int)(i / chunks), c = (int)(i - (int64_t)m * chunks) * 8;
+            leave_piece(g, m, c, places[m], i == i0 ? piece : piece_of(g, m, c));
         }
     }
 }
@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(256) loss_gather(LossRowsArgs a, LossGatherArg
     const int64_t chunks = g.ldo / 8, total = a.M * chunks;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
         const int64_t m = i / chunks;
-        gather_piece(g, m, (int)(i - m * chunks) * 8, a.place[m]);
+        const int c = (int)(i - m * chunks) * 8;
+        const int32_t at = a.place[m];
+        leave_piece(g, m, c, at, at >= 0 ? piece_of(g, m, c) : (u32x4){});
     }
 }
 

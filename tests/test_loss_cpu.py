@@ -166,3 +166,18 @@ def test_the_bounds_catch_mistakes():
         inside(v.bfloat16(), v, e, "right")
         with pytest.raises(AssertionError):
             inside((v * 1.03).bfloat16(), v, e, "planted")
+
+
+def test_the_native_tables_leave_what_is_not_plain_to_the_checks():
+    """Anything but contiguous GPU tensors of the right types and sizes gives None (here: host tensors and
+    wrong objects)."""
+    if not os.path.exists(la.MARSHAL_PATH):
+        pytest.skip("_marshal.so not built")
+    n, x, f, target = la._marshal(), torch.zeros(4, 8, dtype=torch.float16), torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    for args in ((x, x, target, None, False), (x, x, target, x[0], True), (None, x, target, None, False), (x, 3, target, None, False),
+                 (x, x, None, None, False), (x.to_sparse(), x, target, None, False), (x, x, target), ()):
+        assert n.cross_entropy(*args) is None
+    good = [f, x, x, target, f, None, None, True, True, False, False, False]
+    for i, v in ((0, f), (0, None), (1, "x"), (3, f), (4, None), (5, 1)):
+        assert n.cross_entropy_backward(*good[:i], v, *good[i + 1:]) is None
+    assert n.cross_entropy_backward(*good[:5]) is None
