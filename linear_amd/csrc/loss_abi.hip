@@ -163,7 +163,11 @@ struct LossPlan {
     bool pair;
     bool outer;                                       // dw by launch_outer, where its layout allows
 };
-constexpr int64_t kOuterValues = int64_t(1) << 20;
+// From how many values of dw on launch_outer is the faster, for up to 128 rows and up to 256 (those with
+// whole cache lines in a row of dw: bf16 loss and gradients of 256 x 32000 x 4096 361 -> 324 us, 256 x
+// 16000 x 2048 117 -> 107; under the limit 256 x 5000 x 1000 55 -> 59, off the lines 250 x 34002 x 1144
+// 168 -> 179).
+constexpr int64_t kOuterValues = int64_t(1) << 20, kOuterLong = int64_t(1) << 24;
 LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     LossPlan p;
     int64_t most = std::max<int64_t>(N, 1);
@@ -177,7 +181,7 @@ LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     p.ldz = (p.cols + 63) / 64 * 64;
     p.dx = plan_stream(1, M, K, slices_of(p.cols), false, true);
     p.dw = plan_stream(1, p.cols, K, slices_of(M));
-    p.outer = M <= kOuterL && N * K >= kOuterValues;
+    p.outer = M <= 128 ? N * K >= kOuterValues : M <= kOuterL && K % 64 == 0 && N * K >= kOuterLong;
     p.pair = !p.outer && p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
              plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, slices_of(N), 1, N, slices_of(M), false);
     return p;
@@ -322,6 +326,7 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
         // dw's words go past the caches, which hold the weight and dz (256 x 32000 x 4096 bf16 loss and
         // gradients: 376 us, 361; 4096 x 128259 x 4096 12.52 ms, 12.41)
         if (outer) {
+            sw.xcd_shift = di.xcd_shift;
             if ((st = launched(launch_outer(elem, f32 ? kOutF32 : kOutRound, sw, stream))) != LINEAR_OK) return st;
         } else if (want_dw) {
             const int mode = !f32 ? (streamable(dw, lddw) ? kOutStream : kOutRound) : accumulate ? kOutF32Add : kOutF32;

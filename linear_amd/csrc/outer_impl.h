@@ -1,8 +1,8 @@
 // outer_impl.h -- a weight's gradient from few rows (templates).
 //
-//     y[r, c] = sum_{k < L} row[k, r] * col[k, c]          L <= 128, both contraction-major
+//     y[r, c] = sum_{k < L} row[k, r] * col[k, c]          L <= 256, both contraction-major
 //
-// With one or two slices of contraction indices the product is bound by writing y, and a tile that
+// With one to four slices of contraction indices the product is bound by writing y, and a tile that
 // ends after them overlaps its stores with nothing (262 MB of dW from 20 rows: 74 us on the 256 x 256 tile,
 // 3.5 TB/s).  Here a workgroup of 4 waves keeps its 256 columns of the column panel in registers, as
 // matrix-core operands, and walks down the rows in blocks of 64: a block's slice of the row operand
@@ -27,7 +27,7 @@ namespace lin {
 // plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).
 constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
 
-// KS: K steps of 32 contraction indices, 2 or 4.
+// KS: K steps of 32 contraction indices, 2, 4 or 8.
 template <int KS, int E, int MODE>
 __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
     constexpr int BK = 32 * KS, CROW = 2 * kOuterCols, RROW = 2 * kOuterRows, SLOT = BK * RROW;
@@ -39,7 +39,12 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
     const int q = lane >> 4, s = lane & 15, kq = 8 * q + (s >> 2);
     const int L = a.rows ? *a.rows : a.L;
     const float back = a.unscale ? *a.unscale : 1.f;
-    const int c0 = (int)(blockIdx.x % a.tiles_c) * kOuterCols, share = (int)(blockIdx.x / a.tiles_c);
+    const int step = (int)(gridDim.x / a.tiles_c), dies = 1 << a.xcd_shift;
+    int tile = (int)blockIdx.x;
+    // a share's column tiles on one XCD, whose L2 then reads a slice once for all of them (256 x 32000 x
+    // 4096 bf16 loss and gradients 331 -> 324 us; the shorter panels, whose slices are small, lose 1 to 2%)
+    if (KS == 8 && step % dies == 0) tile = (tile / dies / a.tiles_c * dies + tile % dies) * a.tiles_c + tile / dies % a.tiles_c;
+    const int c0 = tile % a.tiles_c * kOuterCols, share = tile / a.tiles_c;
     const int ldc = (int)a.ldc, ldr = (int)a.ldr;
     const uint32_t base = lds_address(smem);
 
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
         const int byte = (wave * LOADS + j) * 1024 + 16 * lane, k = byte / RROW;
         goff[j] = (uint32_t)((k * ldr + 8 * ((byte % RROW / 16) ^ (2 * panel_swz<kOuterRows>(k)))) * 2);
     });
-    const int blocks = (a.R + kOuterRows - 1) / kOuterRows, step = (int)(gridDim.x / a.tiles_c);
+    const int blocks = (a.R + kOuterRows - 1) / kOuterRows;
     const int rend = (a.R + 7) & ~7;
     int asked = share, fill = 0;                      // the next block to request, its slot
     auto request = [&]() {
@@ -92,7 +97,8 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
         // the slice asked for kOuterStages - 1 blocks ago (or ahead of the loop) has landed once only
         // what was issued after it is outstanding
         static_for<0, kOuterStages>([&]<int k>() {
-            if (turn == k) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(k * STORES + (kOuterStages - 2) * LOADS) : "memory");
+            constexpr int after = k * STORES + (kOuterStages - 2) * LOADS;   // (the counter's wait ends at 63)
+            if (turn == k) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(after < 63 ? after : 63) : "memory");
         });
         turn = turn < kOuterStages - 1 ? turn + 1 : turn;
         lds_barrier();
@@ -142,12 +148,17 @@ hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream) 
     StreamProduct args = a;
     args.tiles_c = (a.C + kOuterCols - 1) / kOuterCols;
     const int64_t blocks = ((int64_t)a.R + kOuterRows - 1) / kOuterRows;
-    // eight workgroups for each of 256 CUs, each taking every shares-th block (four: 2 to 4% slower)
-    const int64_t shares = (2048 + args.tiles_c - 1) / args.tiles_c;
+    // eight workgroups for each of 256 CUs, each taking every shares-th block (four: 2 to 4% slower);
+    // of the longest panels, which fill a CU's LDS, one
+    const int64_t shares = a.L <= 128 ? (2048 + args.tiles_c - 1) / args.tiles_c : args.tiles_c < 256 ? 256 / args.tiles_c : 1;
+    int64_t used = blocks < shares ? blocks : shares;
+    if (a.L > 128 && used >> a.xcd_shift) used = used >> a.xcd_shift << a.xcd_shift;
     void* params[] = {&args};
-    const void* fn = a.L <= 64 ? (mode == kOutRound ? (const void*)outer_stream<2, E, kOutRound> : (const void*)outer_stream<2, E, kOutF32>)
-                               : (mode == kOutRound ? (const void*)outer_stream<4, E, kOutRound> : (const void*)outer_stream<4, E, kOutF32>);
-    return launch_kernel(fn, dim3((unsigned)((blocks < shares ? blocks : shares) * args.tiles_c)), dim3(256), params, 0, stream);
+    const bool words = mode == kOutRound;
+    const void* fn = a.L <= 64    ? (words ? (const void*)outer_stream<2, E, kOutRound> : (const void*)outer_stream<2, E, kOutF32>)
+                     : a.L <= 128 ? (words ? (const void*)outer_stream<4, E, kOutRound> : (const void*)outer_stream<4, E, kOutF32>)
+                                  : (words ? (const void*)outer_stream<8, E, kOutRound> : (const void*)outer_stream<8, E, kOutF32>);
+    return launch_kernel(fn, dim3((unsigned)(used * args.tiles_c)), dim3(256), params, 0, stream);
 }
 
 }  // namespace lin

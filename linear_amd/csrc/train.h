@@ -144,7 +144,7 @@ inline hipError_t launch_grad_pair(int elem, bool small, const StreamProduct& a,
 // One unsplit contraction-major product (rowt) of at most kOuterL contraction indices, bound by its
 // output's write: mode kOutRound or kOutF32; y 16-byte aligned, C and ldy multiples of 8, ldy at
 // most kMaxLdIn.
-constexpr int kOuterL = 128;
+constexpr int kOuterL = 256;
 template <int E> hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_outer_t<kF16>(int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_outer_t<kBF16>(int, const StreamProduct&, hipStream_t);

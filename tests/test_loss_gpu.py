@@ -451,3 +451,23 @@ def test_two_calls_at_once():
         th.join()
     for g, v in zip(got, want):
         assert g is not None and all(torch.equal(a, b) for a, b in zip(g, v))
+
+
+# weight gradients of three and four slices on the few rows' kernel: column tiles and row blocks of every
+# remainder, one block a workgroup and many
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(129, 4096, 264), (200, 4099, 520), (193, 16500, 72), (255, 9001, 1032), (256, 1100, 2008),
+                                   (256, 70001, 256), (256, 3000, 776), (256, 524300, 8),
+                                   (256, 16500, 2048), (161, 33000, 1024), (200, 131200, 256), (130, 53001, 640)])
+def test_some_hundred_rows_and_a_large_vocabulary(M, N, K, t):
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = check_forward(x, w, target, b, t)
+    got = check_backward(dloss, dlse, x, w, target, lse, b, t)
+    check_backward(dloss, dlse, x, w, target, lse, b, t, f32=True)
+    again = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, bias=True)
+    assert all(torch.equal(u, v) for u, v in zip(got, again))
+    dw, flat = padded(torch.zeros_like(w), 8, 8, 9.0)
+    fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, dw=dw)
+    assert torch.equal(dw, got[1])
+    dw.fill_(9.0)
+    assert bool((flat == 9.0).all()), "written outside"
