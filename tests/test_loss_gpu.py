@@ -471,3 +471,13 @@ def test_some_hundred_rows_and_a_large_vocabulary(M, N, K, t):
     assert torch.equal(dw, got[1])
     dw.fill_(9.0)
     assert bool((flat == 9.0).all()), "written outside"
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(40, 66000, 2049), (300, 33100, 4099)])
+def test_copied_weights_in_pieces(M, N, K, t):
+    """Rows of odd length, more than are copied at a time."""
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    _, lse = check_forward(x, w, target, b, t)
+    check_backward(dloss, dlse, x, w, target, lse, b, t)
+    check_backward(dloss, None, x, w, target, lse, b, t, f32=True)
