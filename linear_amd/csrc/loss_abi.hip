@@ -164,10 +164,9 @@ struct LossPlan {
     bool pair;
     bool outer;                                       // dw by launch_outer, where its layout allows
 };
-// From how many values of dw on launch_outer is the faster, for up to 128 rows and up to 256 (those with
-// whole cache lines in a row of dw: bf16 loss and gradients of 256 x 32000 x 4096 361 -> 324 us, 256 x
-// 16000 x 2048 117 -> 107; under the limit 256 x 5000 x 1000 55 -> 59, off the lines 250 x 34002 x 1144
-// 168 -> 179).
+// From how many values of dw on launch_outer is the faster, for up to 128 rows and up to 256 (bf16
+// loss and gradients of 256 x 32000 x 4096 361 -> 324 us, 256 x 16000 x 2048 117 -> 107, 160 x 60000 x 520
+// 131 -> 125; under the limit 256 x 5000 x 1000 55 -> 59).
 constexpr int64_t kOuterValues = int64_t(1) << 20, kOuterLong = int64_t(1) << 24;
 LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     LossPlan p;
@@ -182,7 +181,7 @@ LossPlan plan_loss(int64_t M, int64_t N, int64_t K, bool packed) {
     p.ldz = (p.cols + 63) / 64 * 64;
     p.dx = plan_stream(1, M, K, slices_of(p.cols), false, true);
     p.dw = plan_stream(1, p.cols, K, slices_of(M));
-    p.outer = M <= 128 ? N * K >= kOuterValues : M <= kOuterL && K % 64 == 0 && N * K >= kOuterLong;
+    p.outer = M <= 128 ? N * K >= kOuterValues : M <= kOuterL && N * K >= kOuterLong;
     p.pair = !p.outer && p.pieces == 1 && M > 0 && N > 0 && K > 0 &&
              plan_pair(p.dx, p.dw, p.dx.time + p.dw.time + kLaunchGap, M, K, slices_of(N), 1, N, slices_of(M), false);
     return p;
@@ -330,7 +329,7 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
             sw.xcd_shift = di.xcd_shift;
             if ((st = launched(launch_outer(elem, f32 ? kOutF32 : kOutRound, sw, stream))) != LINEAR_OK) return st;
         } else if (want_dw) {
-            const int mode = !f32 ? (streamable(dw, lddw) ? kOutStream : kOutRound) : accumulate ? kOutF32Add : kOutF32;
+            const int mode = !f32 ? (streamable(dw, lddw) && whole_lines(dw, lddw, 2) ? kOutStream : kOutRound) : accumulate ? kOutF32Add : kOutF32;
             if ((st = launch_stream(elem, true, mode, sw, p.dw, di, partials, stream)) != LINEAR_OK) return st;
         }
     }

@@ -24,11 +24,13 @@ namespace lin {
 
 // The stores go past the caches: y is larger than those or is read by nobody soon, and the weight
 // that the next call reads stays in them (backward without dx, 64 x 128259 x 4096 bf16: 520 us with
-// plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).
+// plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).  Rows
+// that end inside a cache line keep plain stores, which the caches put together (loss
+// and gradients of 20 x 32000 x 4104 373 -> 253 us, of 2 x 11771 x 2248 90 -> 65).
 constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
 
-// KS: K steps of 32 contraction indices, 2, 4 or 8.
-template <int KS, int E, int MODE>
+// KS: K steps of 32 contraction indices, 2, 4 or 8; POLICY: the stores' cache policy.
+template <int KS, int E, int MODE, int POLICY>
 __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
     constexpr int BK = 32 * KS, CROW = 2 * kOuterCols, RROW = 2 * kOuterRows, SLOT = BK * RROW;
     constexpr int LOADS = SLOT / 4096, CLOADS = BK * CROW / 4096;   // of a slice and of the panel, per wave
@@ -128,18 +130,24 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
                         const f32x4 v = acc[2 * p + e / 2] * back;
                         w[e] = (uint32_t)narrow<E>(v[2 * (e & 1)]) | ((uint32_t)narrow<E>(v[2 * (e & 1) + 1]) << 16);
                     }
-                    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, kPastCaches);
+                    __builtin_amdgcn_raw_buffer_store_b128(w, ry, off, 0, POLICY);
                 } else {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const f32x4 v = acc[2 * p + b] * back;
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ry, off == kOOB ? kOOB : off + 16 * b, 0, kPastCaches);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ry, off == kOOB ? kOOB : off + 16 * b, 0, POLICY);
                     }
                 }
             });
         });
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the empty requests land before the LDS is released
+}
+
+template <int KS, int E>
+static const void* outer_fn(bool words, bool past) {
+    if (words) return past ? (const void*)outer_stream<KS, E, kOutRound, kPastCaches> : (const void*)outer_stream<KS, E, kOutRound, 0>;
+    return past ? (const void*)outer_stream<KS, E, kOutF32, kPastCaches> : (const void*)outer_stream<KS, E, kOutF32, 0>;
 }
 
 // mode kOutRound or kOutF32.
@@ -154,10 +162,10 @@ hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream) 
     int64_t used = blocks < shares ? blocks : shares;
     if (a.L > 128 && used >> a.xcd_shift) used = used >> a.xcd_shift << a.xcd_shift;
     void* params[] = {&args};
-    const bool words = mode == kOutRound;
-    const void* fn = a.L <= 64    ? (words ? (const void*)outer_stream<2, E, kOutRound> : (const void*)outer_stream<2, E, kOutF32>)
-                     : a.L <= 128 ? (words ? (const void*)outer_stream<4, E, kOutRound> : (const void*)outer_stream<4, E, kOutF32>)
-                                  : (words ? (const void*)outer_stream<8, E, kOutRound> : (const void*)outer_stream<8, E, kOutF32>);
+    const bool words = mode == kOutRound, past = whole_lines(a.y[0], a.ldy[0], words ? 2 : 4);
+    const void* fn = a.L <= 64    ? outer_fn<2, E>(words, past)
+                     : a.L <= 128 ? outer_fn<4, E>(words, past)
+                                  : outer_fn<8, E>(words, past);
     return launch_kernel(fn, dim3((unsigned)(used * args.tiles_c)), dim3(256), params, 0, stream);
 }
 

@@ -458,7 +458,7 @@ def test_two_calls_at_once():
 @pytest.mark.parametrize("t", TYPES, ids=IDS)
 @pytest.mark.parametrize("M,N,K", [(129, 4096, 264), (200, 4099, 520), (193, 16500, 72), (255, 9001, 1032), (256, 1100, 2008),
                                    (256, 70001, 256), (256, 3000, 776), (256, 524300, 8),
-                                   (256, 16500, 2048), (161, 33000, 1024), (200, 131200, 256), (130, 53001, 640)])
+                                   (256, 16500, 2048), (161, 33000, 1024), (200, 131200, 256), (130, 53001, 640), (200, 33001, 520), (256, 17001, 1000)])
 def test_some_hundred_rows_and_a_large_vocabulary(M, N, K, t):
     x, w, target, b, dloss, dlse = make(M, N, K, t)
     _, lse = check_forward(x, w, target, b, t)
