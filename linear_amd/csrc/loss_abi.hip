@@ -25,8 +25,8 @@ bool loss_dims_ok(int64_t M, int64_t N, int64_t K) {
     return M >= 0 && N >= 0 && K >= 0 && M <= kMaxLossRows && N <= kMaxSize && K <= kMaxLossK;
 }
 
-// kLossConfigs' times, near those measured at one tile a CU and set so that the choice is the fastest tile,
-// or within 3% of it, of all five at M from 1 to 2000, N from 8000 to 128259, K of 768 and 4096.
+// kLossConfigs' times, near those measured and set so that the choice is the fastest of the five tiles, or
+// close to it, at M from 1 to 2000, N from 8000 to 128259, K of 768 and 4096.
 constexpr TileTime kLossTimes[kNumLossConfigs] = {{6.5, 1.60, 1}, {5.3, 0.80, 1}, {4.9, 0.50, 1}, {2.0, 0.42, 2}, {2.0, 0.30, 3}};
 
 // The tile of a product of M rows and N columns (by sizes alone: workspaces depend on it).
