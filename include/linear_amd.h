@@ -562,10 +562,11 @@ int32_t linear_bf16_cross_entropy(const uint16_t* x, int64_t ldx,
  * lse is the forward call's.  The logits are formed again, a piece of the vocabulary at a
  * time; dz of a piece is kept in the workspace as the two products' operand, dx's sums over
  * the pieces in FP32.  c is a power of two over the rows' largest |d| that brings their
- * largest |d + dlse| + |d| to 2^14 .. 2^15: neither large nor small dloss loses precision in
- * binary16 (the outputs themselves have the type's range: scale dloss, as usual there), and
- * the -d of rows that share one d, as in a mean, is not rounded at all.  Rows with d = 0 and
- * dlse = 0 take no part (and no time): their dx is +0, whatever their x and lse are.
+ * largest |d + dlse| + |d| to 2^14 .. 2^15 (c is at most 2^125: weights that are all under
+ * 2^-111 end lower): neither large nor small dloss loses precision in binary16 (the outputs
+ * themselves have the type's range: scale dloss, as usual there), and the -d of rows that
+ * share one d, as in a mean, is not rounded at all.  d + dlse is an FP32 sum.  Rows with
+ * d = 0 and dlse = 0 take no part (and no time): their dx is +0, whatever their x and lse are.
  *
  * dx, dw and db may each be NULL (not wanted), not all three unless they are empty.  N == 0
  * gives dx = +0, M == 0 gives dw = db = +0.  The _f32out forms store dw and db as floats

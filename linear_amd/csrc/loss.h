@@ -66,7 +66,8 @@ hipError_t launch_loss_join(const LossJoinArgs& j, hipStream_t stream);
 // anything, and in fine tuning, where most rows are a prompt's, they are most of the work.
 //
 // d and d + dlse are multiplied by head[1], whose inverse is head[0]: 2^e over the largest finite
-// |d|, with e such that the largest |d + dlse| + |d| ends at 2^14 .. 2^15.  dz at a row's target
+// |d|, with e such that the largest |d + dlse| + |d| ends at 2^14 .. 2^15 (lower where it is under
+// 2^-111, so that both numbers stay normal ones).  dz at a row's target
 // is near -d for most rows, the same number in each where the loss is a mean: unscaled, all
 // would be rounded the same way, up to half a step (1024 x 1024 x 768 bf16: dx, dW, db off by 1.9
 // times one rounding; scaled, that number is a power of two).

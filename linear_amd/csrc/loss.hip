@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     __shared__ float lds[16];
     __shared__ int counts[16];
     __shared__ int32_t places[SCAN ? 1 : kLossScanRows];
-    float base = 0.f, most = 0.f;
+    float base = 0.f, most = 0.f;                    // the largest |d|, and half the largest weight
     RowWeights mine{0.f, 0.f, 0.f, -1};              // of row threadIdx.x
     // the first piece of x that this thread moves, requested ahead of the places: most threads have no other
     const int chunks = SCAN ? 1 : (int)(g.ldo / 8);
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     for (int64_t m = threadIdx.x; m < a.M; m += 1024) {
         const RowWeights w = row_weights(a, m);
         if (m < 1024) mine = w;
-        const float v = __builtin_fabsf(w.rows) + __builtin_fabsf(w.d);
+        const float v = 0.5f * __builtin_fabsf(w.rows) + 0.5f * __builtin_fabsf(w.d);   // (the sum may pass FP32's range)
         if (!(v < __builtin_inff())) continue;
         base = fmaxf(base, __builtin_fabsf(w.d));
         most = fmaxf(most, v);
@@ -87,10 +87,13 @@ __global__ void __launch_bounds__(1024) loss_rows(LossRowsArgs a, LossGatherArgs
     const auto largest = [](float a, float b) { return fmaxf(a, b); };
     base = group_fold<16>(base, lds, largest);
     most = group_fold<16>(most, lds, largest);
-    // (rows below 2^-80, and d below 2^-100 of the largest, are left smaller: the factors stay finite)
-    base = fmaxf(fmaxf(base > 0.f ? base : most, 0x1p-80f), most * 0x1p-100f);
-    int x = 1;
-    if (most > 0.f) __builtin_frexpf(most / base, &x);   // most / base < 2^x
+    // d below 2^-111, or 2^-100 of the largest weight, does not set the factor: with base from 2^-111 to
+    // 2^128 and x from 1 to 101, scale and its inverse lie between 2^-115 and 2^125.  Weights that are
+    // all under 2^-111 end below 2^14 (at 1 for FP32's smallest normal ones).
+    base = fmaxf(fmaxf(base > 0.f ? base : most, 0x1p-111f), most * 0x1p-99f);
+    int x = 0;
+    if (most > 0.f) __builtin_frexpf(most / base, &x);   // 2 most / base < 2^(x + 1)
+    x = max(x + 1, 1);
     const float scale = __builtin_ldexpf(1.f, 15 - x) / base;
     // the rows with a gradient in their order: a ballot per wave, the waves' counts added up
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;

@@ -481,3 +481,39 @@ def test_copied_weights_in_pieces(M, N, K, t):
     _, lse = check_forward(x, w, target, b, t)
     check_backward(dloss, dlse, x, w, target, lse, b, t)
     check_backward(dloss, None, x, w, target, lse, b, t, f32=True)
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("size", [1e-30, 1e-34, 3e-35, 1e-36, 1e-38, 1e-42])
+def test_row_weights_that_are_all_small(size, t):
+    """Weights down to FP32's subnormals: the factor that dz is rounded under, and its inverse, stay numbers."""
+    M, N, K = 33, 300, 72
+    x, w, target, b, dloss, _ = make(M, N, K, t)
+    _, lse = fn("", t)(x, w, target, b)
+    d = dloss * 10 * size
+    for dlse in (None, d * 0.5, d * -0.25):
+        want, bound = ref.backward64(d, dlse, x, w, target, b, t, True)
+        got = fn("_backward_f32out", t)(d, x, w, target, lse, b, dlse=dlse, bias=True)
+        # the factor ends at 2^125: half a spacing of binary16's subnormals, 2^-25, is 2^-150 of dz (with what
+        # the matrix unit makes of such words, as in backward64, 2^11 times that under its sums' error); outputs and the
+        # partial sums of up to 16 splits are rounded to multiples of FP32's 2^-149
+        dz = 2.0 ** -150 if t == torch.float16 else 0.0
+        for g, v, e, n, count, factor in zip(got, want, bound, ("dx", "dw", "db"), (N, M, M), (w, x, torch.ones(1, device=DEV))):
+            most = float(factor.double().abs().amax())
+            room = count * most * dz * (1 + 2 ** 11 * (count / 16 + 48) * 2.0 ** -23) + 17 * 2.0 ** -150
+            inside(g, v, e + room, "%s %g" % (n, size))
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+def test_row_weights_near_the_largest_number(t):
+    """|d + dlse| + |d| past FP32's range, d + dlse and the outputs inside it."""
+    M, N, K = 33, 300, 72
+    x, w, target, _, dloss, _ = make(M, N, K, t, bias=False)
+    x = x * 2.0 ** -8
+    _, lse = fn("", t)(x, w, target)
+    target = torch.where(ref.counted(target, N), target, 5)
+    one = dloss.sign() * (0.6 + dloss.abs().clamp(max=0.4))
+    for d, dlse in ((3.3e38 * one, None), (3e38 * one.sign(), None), (1.9e38 * one.sign(), 1.4e38 * one), (3.3e38 * one, -1e38 * one)):
+        want, bound = ref.backward64(d, dlse, x, w, target, None, t, True)
+        got = fn("_backward_f32out", t)(d, x, w, target, lse, None, dlse=dlse, need_dx=False, bias=False)
+        inside(got[1], want[1], bound[1], "dw")
