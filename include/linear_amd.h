@@ -525,7 +525,8 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
  * 0 (its lse is that of its logits all the same).  loss and lse are [M] floats; either may
  * be NULL.  target: [M] device int64, needed in any case.  b: [N] or NULL; an entry of -inf takes its column
  * out.  A row of -inf logits has lse -inf, one with +inf (and no NaN) lse +inf.  N == 0
- * gives lse -inf; K == 0 gives z = b.  FP32 inside; reruns are bit-identical.
+ * gives lse -inf; K == 0 gives z = b.  FP32 inside; loss is formed from differences to the
+ * row's largest logit, so its error does not grow with lse; reruns are bit-identical.
  *
  * Limits: M up to LINEAR_CROSS_ENTROPY_MAX_M, K up to LINEAR_CROSS_ENTROPY_MAX_K, N as for
  * the gated block.  Every layout runs the streaming kernels: operands off 16-byte alignment,

@@ -33,11 +33,13 @@ __global__ void __launch_bounds__(256) loss_join(LossJoinArgs j) {
         for (int64_t i = threadIdx.x; i < j.count; i += 256) sum += p[i].sum * __expf(p[i].ref - top);
         sum = group_fold<4>(sum, lds, [](float a, float b) { return a + b; });
         if (threadIdx.x != 0) continue;
-        const float lse = top + logf(sum);
-        if (j.lse) j.lse[m] = lse;
+        const float over = logf(sum);                // lse - top
+        if (j.lse) j.lse[m] = top + over;
         if (j.loss) {
+            // not lse - z: lse is rounded to its own size, which says nothing about the loss of a row that
+            // its target decides (lse of 300: steps of 3e-5)
             const int64_t t = j.target[m];
-            j.loss[m] = t >= 0 && t < j.cols ? lse - j.at_target[m] : 0.f;
+            j.loss[m] = t >= 0 && t < j.cols ? (top - j.at_target[m]) + over : 0.f;
         }
     }
 }

@@ -517,3 +517,27 @@ def test_row_weights_near_the_largest_number(t):
         want, bound = ref.backward64(d, dlse, x, w, target, None, t, True)
         got = fn("_backward_f32out", t)(d, x, w, target, lse, None, dlse=dlse, need_dx=False, bias=False)
         inside(got[1], want[1], bound[1], "dw")
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N", [(3, 64), (70, 1000), (300, 9001)])
+@pytest.mark.parametrize("base,gap", [(12, 8), (28, 12), (296, 10), (304, 14), (1992, 8), (1984, 16), (-2016, 16), (30464, 12)])
+def test_confident_rows_keep_their_loss(base, gap, M, N, t):
+    """Rows decided by their target (logits base + gap and base): a loss far under a step of lse has an
+    error that lse's size has no part in.  The logits are sums of two whole numbers, so they are exact."""
+    x, w = torch.zeros(M, 8, dtype=t, device=DEV), torch.zeros(N, 8, dtype=t, device=DEV)
+    x[:, 0], w[:, 0] = 1, base
+    target = (torch.arange(M, device=DEV) * 37) % N
+    group = 1 + torch.arange(M, device=DEV) % 7       # the rows of a group share the columns that are up
+    x[torch.arange(M, device=DEV), group] = 1
+    w[target, group] = gap
+    z = x.double() @ w.double().t()
+    assert float(w[0, 0]) == base
+    y = z - z.amax(1, keepdim=True)
+    want = torch.logsumexp(y, 1) - y.gather(1, target[:, None])[:, 0]
+    loss, _ = fn("", t)(x, w, target)
+    # the sum of the exponentials: up to 90 + N / 8192 additions (loss_refs) of half a step of FP32, relative to
+    # a sum of exp(want), and S (|y| + 8) on three factors of each term but the largest (exp 0 is 1); the
+    # logarithm and the addition
+    p = torch.where(y == 0, 0.0, torch.exp(y) * 3 * 2.0 ** -23 * (y.abs() + 8)).sum(1)
+    inside(loss, want, p + (90 + N / 8192) * 2.0 ** -24 + 4 * 2.0 ** -24 * want.abs(), "loss")
