@@ -659,13 +659,15 @@ int32_t linear_grad_clip(const linear_tensor* grads, const linear_tensor* out, i
  *     m = beta1 m + (1 - beta1) g        v = beta2 v + (1 - beta2) g^2
  *     p = p (1 - lr weight_decay) - lr / (1 - beta1^step) * m / (sqrt(v / (1 - beta2^step)) + eps)
  *
- * in FP32, p rounded to its type once.  params, grads: `count` tensors as for
- * linear_grad_clip, of the same sizes, each of any type and row stride.  m, v: for each
- * tensor linear_adamw_state_bytes(rows * cols, state_bits) bytes of device memory, which the
- * step reads and overwrites; values in row-major order without gaps, whatever the
- * parameter's stride; all bytes zero before the first step.  copies: NULL, or `count` tensors
- * of 16-bit types that p is also rounded into (the words of 32-bit weights that the next
- * forward pass reads).  The arrays and options are host memory, read during the call.
+ * in FP32, p rounded to its type once.  An eps over zero counts as 2^-126 at least, FP32's
+ * smallest normal number; with eps 0 a value of zero moments becomes NaN, the formula's 0 / 0.
+ * params, grads: `count` tensors as for linear_grad_clip, of the same sizes, each of any type
+ * and row stride.  m, v: for each tensor linear_adamw_state_bytes(rows * cols, state_bits)
+ * bytes of device memory, which the step reads and overwrites; values in row-major order
+ * without gaps, whatever the parameter's stride; all bytes zero before the first step.
+ * copies: NULL, or `count` tensors of 16-bit types that p is also rounded into (the words of
+ * 32-bit weights that the next forward pass reads).  The arrays and options are host memory,
+ * read during the call.
  *
  * state_bits 32: floats.  state_bits 8: rows * cols codes, then a byte k + 127 for each block
  * of LINEAR_ADAMW_BLOCK values, whose codes count in units of 2^k; k is the smallest from -100

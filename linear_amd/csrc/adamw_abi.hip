@@ -157,7 +157,9 @@ int32_t linear_adamw(const linear_tensor* params, const linear_tensor* grads, vo
     a.keep = (float)(1.0 - o.lr * o.weight_decay);
     a.rate = (float)(o.lr / a.bias1);
     a.root = (float)(1.0 / sqrt(a.bias2));
-    a.eps = (float)o.eps;
+    // the kernels' reciprocal takes a subnormal denominator for zero: 0 / eps would be NaN.  (Beside a root, of
+    // 2^-75 at least, an eps under 2^-126 is nothing.)
+    a.eps = o.eps > 0.0 ? std::max((float)o.eps, 0x1p-126f) : 0.f;
     a.max_norm = o.max_norm;
     a.norm = o.norm;
     a.device_lr = o.device_lr;

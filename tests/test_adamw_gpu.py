@@ -375,3 +375,21 @@ def test_one_tensor_with_gaps_among_plain_ones(bits):
     p[50] = wide[:, :3]
     check_step(p, g, m, v, 1)
     assert bool((wide[:, 3:] == 7.0).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-37, 1e-39, 1e-44, 1e-60, 1e-300])
+def test_an_eps_of_any_size_over_zero(eps, bits):
+    """Values with zero moments stay where they are (0 / eps is 0); the others take the formula's step."""
+    o = {**OPTIONS, "eps": eps, "weight_decay": 0.0}
+    p, g = make([(70, 33), (5,)], TYPES, TYPES[::-1])
+    for t in g:
+        t[::2] = 0
+    m, v = states(p, bits)
+    for step in (1, 2):
+        old, om, ov = [t.clone() for t in p], values(m, p, False), values(v, p, True)
+        la.linear_adamw(p, g, m, v, step=step, **o)
+        for i in range(len(p)):
+            want, bound = ref.step64(old[i], g[i], om[i], ov[i], o, step)
+            inside(p[i][1::2], want[0][1::2], ref.stored(want[0], bound[0], p[i].dtype)[1::2], "p %d" % i)
+            assert torch.equal(p[i][::2], old[i][::2])
