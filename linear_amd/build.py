@@ -72,6 +72,31 @@ def _resources(text: str) -> dict:
     return res
 
 
+def _asm_resources(asm: str) -> dict:
+    """The same from the kernels' metadata at the end of their assembly (with -save-temps hipcc makes no
+    remarks)."""
+    fields = {"vgpr_count": "VGPRs", "agpr_count": "AGPRs", "sgpr_count": "TotalSGPRs", "vgpr_spill_count": "VGPRs Spill",
+              "sgpr_spill_count": "SGPRs Spill", "private_segment_fixed_size": "ScratchSize [bytes/lane]",
+              "group_segment_fixed_size": "LDS Size [bytes/block]"}
+    res = {}
+    for entry in re.split(r"^  - ", asm.partition("amdhsa.kernels:")[2], flags=re.M)[1:]:
+        values = dict(re.findall(r"^ *\.(\w+): +(\S+)$", entry, flags=re.M))
+        if "name" in values:
+            res[values["name"]] = {label: values[key] for key, label in fields.items() if key in values}
+    return res
+
+
+def _check_resources(src: str, res: dict) -> None:
+    """Every kernel must run from registers and LDS: scratch memory (spills, or an argument copy indexed
+    at run time) costs a memory round trip per access."""
+    if not res and not src.endswith("_abi.hip"):          # (host code alone)
+        raise RuntimeError("no kernel's resources were found for %s" % src)
+    bad = {k: v for k, v in res.items()
+           if v.get("ScratchSize [bytes/lane]") != "0" or v.get("VGPRs Spill") != "0"}
+    if bad:
+        raise RuntimeError("kernels in %s use scratch memory: %s" % (src, ", ".join(sorted(bad))))
+
+
 def _other_m0_uses(asm: str) -> list:
     """The instructions naming m0 that are not lds_dma16_raw's three: m0's write, the wait states
     and the direct-to-LDS load that reads it.  Any other would be the compiler's own use, whose
@@ -104,22 +129,18 @@ def _compile(src: str) -> str:
         raise RuntimeError("hipcc failed for %s:\n%s" % (src, msg))
     if msg.strip():
         print(msg, file=sys.stderr)
-    # every kernel must run from registers and LDS: scratch memory (spills, or an
-    # argument copy indexed at run time) costs a memory round trip per access
-    res = _resources(out)
-    bad = {k: v for k, v in res.items()
-           if v.get("ScratchSize [bytes/lane]", "0") != "0" or v.get("VGPRs Spill", "0") != "0"}
+    asm = ""
+    if src in RAW_M0_SOURCES:
+        with open(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + "-hip-amdgcn-amd-amdhsa-gfx950.s")) as f:
+            asm = f.read()
+    res = _asm_resources(asm) if asm else _resources(out)
     with open(os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".resources.txt"), "w") as f:
         for k, v in sorted(res.items()):
             f.write("%s %s\n" % (k, " ".join("%s=%s" % (a.replace(" ", "_"), b) for a, b in v.items())))
-    if bad:
-        raise RuntimeError("kernels in %s use scratch memory: %s" % (src, ", ".join(sorted(bad))))
-    if src in RAW_M0_SOURCES:
-        asm = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + "-hip-amdgcn-amd-amdhsa-gfx950.s")
-        with open(asm) as f:
-            uses = _other_m0_uses(f.read())
-        if uses:
-            raise RuntimeError("%s: the compiler uses m0 itself beside the inline assembly: %s" % (src, uses[0]))
+    _check_resources(src, res)
+    uses = _other_m0_uses(asm)
+    if uses:
+        raise RuntimeError("%s: the compiler uses m0 itself beside the inline assembly: %s" % (src, uses[0]))
     return obj
 
 
