@@ -6,6 +6,7 @@ really compile); object files go to ``_build/`` at the repository root.
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import re
 import shutil
@@ -144,7 +145,27 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _compile_marshal() -> str:
+def _marshal_needs() -> str | None:
+    """What is missing here for the binding's module; the library itself needs none of it."""
+    if shutil.which("g++") is None:
+        return "g++"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's headers"
+    spec = importlib.util.find_spec("torch")
+    home = os.path.dirname(spec.origin) if spec is not None and spec.origin else ""
+    if not os.path.exists(os.path.join(home, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return "torch's headers"
+    if not os.path.exists(os.path.join(home, "lib", "libtorch_python.so")):
+        return "torch's libraries"
+    return None
+
+
+def _compile_marshal() -> str | None:
+    """Builds the binding's module; where something for it is missing, says what, and the binding does without."""
+    needs = _marshal_needs()
+    if needs is not None:
+        print("not built: %s (no %s); the binding reads tensors at more host time" % (MARSHAL_OUT, needs), file=sys.stderr)
+        return None
     import torch
     home = os.path.dirname(torch.__file__)
     include = os.path.join(home, "include")
@@ -177,8 +198,7 @@ def build(verbose: bool = True) -> str:
         os.replace(tmp, out)
         if verbose:
             print("built", out)
-    marshal.result()
-    if verbose:
+    if marshal.result() is not None and verbose:
         print("built", MARSHAL_OUT)
     return OUT
 

@@ -4,7 +4,9 @@ import os
 import shutil
 
 import pytest
+import torch
 
+import linear_amd as la
 from linear_amd import build
 
 LOAD = "\ts_mov_b32 m0, s53\n\ts_nop 3\n\tbuffer_load_dwordx4 v1, s[4:7], 0 offen lds\n"
@@ -53,3 +55,34 @@ def test_a_source_whose_kernels_are_not_found_fails_the_build():
     build._check_resources("train_abi.hip", {})
     with pytest.raises(RuntimeError, match="scratch"):
         build._check_resources("loss.hip", {"k": {"VGPRs Spill": "0"}})
+
+
+def test_the_library_is_built_without_what_the_bindings_module_needs(tmp_path, monkeypatch, capsys):
+    """g++, Python's and torch's headers are the module's alone; the library's build goes on without them."""
+    monkeypatch.setattr(build, "MARSHAL_OUT", str(tmp_path / "_marshal.so"))
+    with monkeypatch.context() as c:
+        c.setattr(build.shutil, "which", lambda name: None)
+        assert build._compile_marshal() is None and "no g++" in capsys.readouterr().err
+    with monkeypatch.context() as c:
+        c.setattr(build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+        assert build._compile_marshal() is None and "Python's headers" in capsys.readouterr().err
+    with monkeypatch.context() as c:
+        c.setattr(build.importlib.util, "find_spec", lambda name: None)
+        assert build._compile_marshal() is None and "torch's headers" in capsys.readouterr().err
+    assert not os.listdir(tmp_path)
+
+
+def test_the_binding_without_its_module(tmp_path, monkeypatch):
+    """The module's calls give None, so every call goes through the binding's checks."""
+    monkeypatch.setattr(la, "MARSHAL_PATH", str(tmp_path / "_marshal.so"))
+    la._marshal.cache_clear()
+    try:
+        with pytest.warns(UserWarning, match="not built"):
+            n = la._marshal()
+        t = torch.zeros(4)
+        assert n.adamw([t], [t], [t], [t], None) is None and n.states([t], [t]) is None and n.scratch(16, 0) is None
+        assert n.cross_entropy(t, t, t, None, False) is None and n.cross_entropy_backward() is None
+        with pytest.raises(ValueError):                # host tensors: the binding's own refusal
+            la.linear_adamw([t], [t], [t.clone()], [t.clone()], lr=0.1, step=1)
+    finally:
+        la._marshal.cache_clear()

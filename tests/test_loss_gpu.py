@@ -541,3 +541,21 @@ def test_confident_rows_keep_their_loss(base, gap, M, N, t):
     # logarithm and the addition
     p = torch.where(y == 0, 0.0, torch.exp(y) * 3 * 2.0 ** -23 * (y.abs() + 8)).sum(1)
     inside(loss, want, p + (90 + N / 8192) * 2.0 ** -24 + 4 * 2.0 ** -24 * want.abs(), "loss")
+
+
+def test_calls_without_the_bindings_module(monkeypatch):
+    """The same bits where tensors are read by the binding itself: the loss, its gradients, an AdamW step."""
+    t = torch.bfloat16
+    x, w, target, b, dloss, dlse = make(70, 300, 72, t)
+
+    def calls():
+        loss, lse = fn("", t)(x, w, target, b)
+        grads = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse)
+        wide = fn("_backward_f32out", t)(dloss, x, w, target, lse, b)
+        p, m, v = w.clone(), la.adamw_state(w, 8), la.adamw_state(w, 8)
+        la.linear_adamw([p], [grads[1]], [m], [v], lr=1e-2, step=1)
+        return [loss, lse, *grads, *wide, p, m, v, *la.linear_adamw_values([m], False, like=[p])]
+
+    want = calls()
+    monkeypatch.setattr(la, "_marshal", lambda: la._NoMarshal)
+    assert all(torch.equal(u, v) for u, v in zip(calls(), want))
