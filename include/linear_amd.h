@@ -534,11 +534,15 @@ int32_t linear_bf16_backward_weight_f32out(const uint16_t* dy, int64_t lddy,
  * the weight a piece at a time.
  *
  * workspace: linear_cross_entropy_workspace_bytes(M, N, K) bytes of device memory, 16-byte
- * aligned; ownership and overlaps as for the gated block's.
+ * aligned; ownership and overlaps as for the gated block's.  The .._aligned bytes are enough
+ * where nothing is copied: x and weight 16-byte aligned, K a multiple of 8, and the row
+ * strides (of more than one row) multiples of 8 up to LINEAR_CROSS_ENTROPY_MAX_K (one token of
+ * 128259 x 4096: 16 KB; with room for copies 256 MB).
  */
 #define LINEAR_CROSS_ENTROPY_MAX_M (1 << 24)
 #define LINEAR_CROSS_ENTROPY_MAX_K ((1 << 22) - 8)
 int64_t linear_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int64_t linear_cross_entropy_workspace_bytes_aligned(int64_t M, int64_t N, int64_t K);
 int32_t linear_f16_cross_entropy(const uint16_t* x, int64_t ldx,
                                  const uint16_t* weight, int64_t ldw,
                                  const uint16_t* b, const int64_t* target,
@@ -573,9 +577,11 @@ int32_t linear_bf16_cross_entropy(const uint16_t* x, int64_t ldx,
  * gives dx = +0, M == 0 gives dw = db = +0.  The _f32out forms store dw and db as floats
  * (unrounded sums), or with accumulate != 0 add them to what dw and db hold.
  *
- * workspace: linear_cross_entropy_backward_workspace_bytes(M, N, K) bytes, as above.
+ * workspace: linear_cross_entropy_backward_workspace_bytes(M, N, K) bytes, as above; .._aligned
+ * bytes are enough where the weight is as described there.
  */
 int64_t linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t N, int64_t K);   /* -1 if out of range */
+int64_t linear_cross_entropy_backward_workspace_bytes_aligned(int64_t M, int64_t N, int64_t K);
 int32_t linear_f16_cross_entropy_backward(const float* dloss, const float* dlse,
                                           const uint16_t* x, int64_t ldx,
                                           const uint16_t* weight, int64_t ldw,

@@ -72,6 +72,7 @@ ENTRY_POINTS = ("linear_f16", "linear_f16_nobias", "linear_f16_ex", "linear_f16_
                 "linear_f16_backward_weight", "linear_bf16_backward_weight",
                 "linear_f16_backward_weight_f32out", "linear_bf16_backward_weight_f32out",
                 "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes",
+                "linear_cross_entropy_workspace_bytes_aligned", "linear_cross_entropy_backward_workspace_bytes_aligned",
                 "linear_f16_cross_entropy", "linear_bf16_cross_entropy",
                 "linear_f16_cross_entropy_backward", "linear_bf16_cross_entropy_backward",
                 "linear_f16_cross_entropy_backward_f32out", "linear_bf16_cross_entropy_backward_f32out",
@@ -193,7 +194,8 @@ def _lib():
                                                    i64, vp, i64, vp]
         getattr(lib, name + "_f32out").restype = i32
     for name in ("linear_gated_forward_workspace_bytes", "linear_gated_workspace_bytes", "linear_backward_workspace_bytes",
-                 "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes"):
+                 "linear_cross_entropy_workspace_bytes", "linear_cross_entropy_backward_workspace_bytes",
+                 "linear_cross_entropy_workspace_bytes_aligned", "linear_cross_entropy_backward_workspace_bytes_aligned"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = i64
     lib.linear_grad_workspace_bytes.argtypes = [i64]
@@ -863,21 +865,34 @@ _CROSS_ENTROPY_BACKWARD = {(t, f): "linear_%s_cross_entropy_backward%s" % (t, "_
 
 
 @functools.lru_cache(maxsize=256)
-def cross_entropy_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Bytes of device workspace a cross entropy call needs."""
-    n = _lib().linear_cross_entropy_workspace_bytes(M, N, K)
+def cross_entropy_workspace_bytes(M: int, N: int, K: int, aligned: bool = False) -> int:
+    """Bytes of device workspace a cross entropy call needs; aligned: where x and weight are 16-byte aligned and
+    their row strides multiples of 8, so that neither is copied."""
+    lib = _lib()
+    n = (lib.linear_cross_entropy_workspace_bytes_aligned if aligned else lib.linear_cross_entropy_workspace_bytes)(M, N, K)
     if n < 0:
         raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
     return n
 
 
 @functools.lru_cache(maxsize=256)
-def cross_entropy_backward_workspace_bytes(M: int, N: int, K: int) -> int:
-    """Bytes of device workspace a cross entropy backward call needs."""
-    n = _lib().linear_cross_entropy_backward_workspace_bytes(M, N, K)
+def cross_entropy_backward_workspace_bytes(M: int, N: int, K: int, aligned: bool = False) -> int:
+    """Bytes of device workspace a cross entropy backward call needs; aligned: where weight is 16-byte aligned and
+    its row stride a multiple of 8, so that it is not copied."""
+    lib = _lib()
+    n = (lib.linear_cross_entropy_backward_workspace_bytes_aligned if aligned
+         else lib.linear_cross_entropy_backward_workspace_bytes)(M, N, K)
     if n < 0:
         raise ValueError("M=%d, N=%d, K=%d out of range" % (M, N, K))
     return n
+
+
+CROSS_ENTROPY_MAX_K = (1 << 22) - 8
+
+
+def _in_place(p, rows, ld):
+    """Whether rows of a multiple of 8 values are read where they are (see the workspaces)."""
+    return not p or (p % 16 == 0 and (rows <= 1 or (ld % 8 == 0 and ld <= CROSS_ENTROPY_MAX_K)))
 
 
 def _vector(t, name, dtype, n):
@@ -901,7 +916,7 @@ def _cross_entropy_call(tag, dtype, x, weight, target, b, loss, lse, workspace, 
         packed = _marshal().cross_entropy(x, weight, target, b, tag == "bf16")    # None: not the plain case
         if packed is not None:
             device, M, N, K, loss, lse, args = packed
-            need = cross_entropy_workspace_bytes(M, N, K)
+            need = cross_entropy_workspace_bytes(M, N, K, (args[0] | args[2]) % 16 == 0)
             workspace, wsp = _new_scratch(need, device)
             _check(_entry(name)(*args, M, N, K, wsp, need, torch._C._cuda_getCurrentRawStream(device)), name)
             return loss, lse
@@ -919,7 +934,8 @@ def _cross_entropy_call(tag, dtype, x, weight, target, b, loss, lse, workspace, 
             loss = torch.empty(M, dtype=torch.float32, device=x.device)
         if lse is None:
             lse = torch.empty(M, dtype=torch.float32, device=x.device)
-        workspace, wsp, wsn = _scratch(workspace, cross_entropy_workspace_bytes(M, N, K), x.device)
+        need = cross_entropy_workspace_bytes(M, N, K, _in_place(xp, M, ldx) and _in_place(wp, N, ldw))
+        workspace, wsp, wsn = _scratch(workspace, need, x.device)
     rc = _entry(name)(xp, ldx, wp, ldw, bp, tp, _vector(loss, "loss", torch.float32, M), _vector(lse, "lse", torch.float32, M),
                       M, N, K, wsp, wsn, handle)
     _check(rc, name)
@@ -931,7 +947,7 @@ def linear_f16_cross_entropy(x: torch.Tensor, weight: torch.Tensor, target: torc
     """(loss, lse) of the head x @ weight.T (+ b) (x [M, K], weight [N, K], b [N], float16; target int64 [M]):
     lse = log sum exp of a row's logits, loss = lse - the target's logit, float32 [M]; a target outside [0, N)
     (-100, say) gives loss 0.  The logits are never stored.  loss, lse: tensors to write.  workspace: a uint8
-    device tensor of at least cross_entropy_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    device tensor of at least cross_entropy_workspace_bytes(M, N, K, aligned) bytes (allocated per call when None)."""
     return _cross_entropy_call("f16", torch.float16, x, weight, target, b, loss, lse, workspace, stream)
 
 
@@ -952,7 +968,7 @@ def _cross_entropy_backward_call(tag, dtype, f32, dloss, x, weight, target, lse,
                                                    tag == "bf16", f32)
         if packed is not None:
             device, M, N, K, dx, dw, db, args = packed
-            need = cross_entropy_backward_workspace_bytes(M, N, K)
+            need = cross_entropy_backward_workspace_bytes(M, N, K, args[4] % 16 == 0)
             workspace, wsp = _new_scratch(need, device)
             flag = (0,) if f32 else ()
             _check(_entry(name)(*args, *flag, M, N, K, wsp, need, torch._C._cuda_getCurrentRawStream(device)), name)
@@ -978,7 +994,8 @@ def _cross_entropy_backward_call(tag, dtype, f32, dloss, x, weight, target, lse,
         dw, *dwa = _output(dw, "dw", odt, (N, K), x) if need_dw else none
         if bias and db is None:
             db = torch.empty(N, dtype=odt, device=x.device)
-        workspace, wsp, wsn = _scratch(workspace, cross_entropy_backward_workspace_bytes(M, N, K), x.device)
+        need = cross_entropy_backward_workspace_bytes(M, N, K, _in_place(wp, N, ldw))
+        workspace, wsp, wsn = _scratch(workspace, need, x.device)
     flag = (int(bool(accumulate)),) if f32 else ()
     rc = _entry(name)(vectors[0], vectors[1], xp, ldx, wp, ldw, bp, tp, vectors[2], *dxa, *dwa,
                       _vector(db, "db", odt, N) if bias else None, *flag, M, N, K, wsp, wsn, handle)
@@ -992,7 +1009,7 @@ def linear_f16_cross_entropy_backward(dloss: torch.Tensor, x: torch.Tensor, weig
     """(dx [M, K], dw [N, K], db [N]) of linear_f16_cross_entropy from dloss and, where lse enters the objective
     too, dlse (float32 [M]); lse is the forward call's.  Those not wanted are None; db is wanted with b and dw
     unless bias says otherwise.  workspace: a uint8 device tensor of at least
-    cross_entropy_backward_workspace_bytes(M, N, K) bytes (allocated per call when None)."""
+    cross_entropy_backward_workspace_bytes(M, N, K, aligned) bytes (allocated per call when None)."""
     return _cross_entropy_backward_call("f16", torch.float16, False, dloss, x, weight, target, lse, b, dlse, need_dx, need_dw,
                                         bias, False, dx, dw, db, workspace, stream)
 

@@ -52,8 +52,9 @@ int64_t pack_rows(int64_t N, int64_t K) {
     return std::min(rows, N);
 }
 
-// What both calls keep at the end of their workspace: copies of x and of a piece of the
-// weight, for layouts that the streaming kernels cannot read.
+// What both calls keep at the end of their workspace: copies of x and, behind it, of a piece of the
+// weight, for layouts that the streaming kernels cannot read.  (Calls that read the weight in place need,
+// and may be given, the workspace without them.)
 int64_t copies_bytes(int64_t M, int64_t N, int64_t K) {
     return round256(M * round8(K) * 2) + round256(pack_rows(N, K) * round8(K) * 2);
 }
@@ -116,7 +117,8 @@ int32_t run_loss(int elem, const uint16_t* x, int64_t ldx, const uint16_t* w, in
     if (!loss_dims_ok(M, N, K)) return LINEAR_E_SHAPE;
     if (M == 0) return LINEAR_OK;
     if (!target || (!loss && !lse)) return LINEAR_E_NULL;
-    const int64_t need = linear_cross_entropy_workspace_bytes(M, N, K);
+    const bool packed = !in_place(w, ldw, N, K), aligned = !packed && in_place(x, ldx, M, K);
+    const int64_t need = aligned ? linear_cross_entropy_workspace_bytes_aligned(M, N, K) : linear_cross_entropy_workspace_bytes(M, N, K);
     const Operand in[] = {{x, M, ldx, K}, {w, N, ldw, K}, {b, b ? 1 : 0, N, N}, {target, 1, M, M, 8}};
     const Operand out[] = {{loss, 1, M, M, 4}, {lse, 1, M, M, 4}, {ws, 1, need, need, 1}};
     int32_t st = check_operands(in, out);
@@ -138,7 +140,6 @@ int32_t run_loss(int elem, const uint16_t* x, int64_t ldx, const uint16_t* w, in
     LossArgs a = loss_args(x, row_stride(ldx, M, K), target, M, N, K, di);
     a.ldparts = tiles_of(N, g.bn);
     a.at_target = at_target;
-    const bool packed = !in_place(w, ldw, N, K);
     int64_t step = launch_columns(M, g);
     if (packed) step = std::min(step, pack_rows(N, K));
     for (int64_t n = 0; n < N; n += step) {          // (whole tiles, but for the last)
@@ -217,7 +218,10 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
     const bool want_dx = dx && M > 0 && K > 0, want_dw = dw && N > 0 && K > 0, want_db = db && N > 0;
     // (an empty output has no address, like one that is not wanted)
     if (!want_dx && !want_dw && !want_db) return M == 0 || N == 0 || K == 0 || dx || dw ? LINEAR_OK : LINEAR_E_NULL;
-    const int64_t need = linear_cross_entropy_backward_workspace_bytes(M, N, K), eb = f32 ? 4 : 2;
+    const bool packed = !in_place(w, ldw, N, K);
+    const int64_t need = packed ? linear_cross_entropy_backward_workspace_bytes(M, N, K)
+                                : linear_cross_entropy_backward_workspace_bytes_aligned(M, N, K);
+    const int64_t eb = f32 ? 4 : 2;
     const Operand in[] = {{x, M, ldx, N > 0 ? K : 0}, {w, M > 0 ? N : 0, ldw, K}, {b, b ? 1 : 0, N, N}, {target, 1, M, M, 8},
                           {lse, 1, M, M, 4}, {dloss, 1, M, M, 4}, {dlse, dlse ? 1 : 0, M, M, 4}};
     const Operand out[] = {{dx, M, lddx, K}, {dw, N, lddw, K, eb}, {db, 1, N, N, eb}, {ws, 1, need, need, 1}};
@@ -228,7 +232,6 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
     int dev = 0;
     DevInfo di;
     if ((st = check_device(&dev, &di)) != LINEAR_OK) return st;
-    const bool packed = !in_place(w, ldw, N, K);
     const LossPlan p = plan_loss(M, N, K, packed);
     const LossSpace at = space_of(p, M, K);
     unsigned char* space = (unsigned char*)ws;
@@ -359,10 +362,20 @@ int64_t linear_cross_entropy_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     return parts_bytes(M, N, K) + round256(M * 4) + copies_bytes(M, N, K);
 }
 
+int64_t linear_cross_entropy_workspace_bytes_aligned(int64_t M, int64_t N, int64_t K) {
+    if (K % 8 != 0 || !loss_dims_ok(M, N, K)) return linear_cross_entropy_workspace_bytes(M, N, K);
+    return parts_bytes(M, N, K) + round256(M * 4);
+}
+
 int64_t linear_cross_entropy_backward_workspace_bytes(int64_t M, int64_t N, int64_t K) {
     if (!loss_dims_ok(M, N, K)) return -1;
     const int64_t in_place = space_of(plan_loss(M, N, K, false), M, K).end, packed = space_of(plan_loss(M, N, K, true), M, K).end;
     return std::max(in_place, packed) + copies_bytes(M, N, K);
+}
+
+int64_t linear_cross_entropy_backward_workspace_bytes_aligned(int64_t M, int64_t N, int64_t K) {
+    if (K % 8 != 0 || !loss_dims_ok(M, N, K)) return linear_cross_entropy_backward_workspace_bytes(M, N, K);
+    return space_of(plan_loss(M, N, K, false), M, K).end + round256(M * K * 2);   // (x is gathered there in any layout)
 }
 
 int32_t linear_f16_cross_entropy(const uint16_t* x, int64_t ldx, const uint16_t* weight, int64_t ldw, const uint16_t* b,

@@ -181,3 +181,28 @@ def test_the_native_tables_leave_what_is_not_plain_to_the_checks():
     for i, v in ((0, f), (0, None), (1, "x"), (3, f), (4, None), (5, 1)):
         assert n.cross_entropy_backward(*good[:i], v, *good[i + 1:]) is None
     assert n.cross_entropy_backward(*good[:5]) is None
+
+
+@needs_lib
+def test_workspaces_without_copies():
+    """Operands that are read in place need no room for copies; others are refused with less."""
+    fwd, bwd = la.cross_entropy_workspace_bytes, la.cross_entropy_backward_workspace_bytes
+    assert fwd(1, 128259, 4096, True) < 1 << 16 and fwd(1, 128259, 4096) > 1 << 27
+    assert bwd(20, 32000, 4096) - bwd(20, 32000, 4096, True) > 1 << 27
+    for M in (0, 1, 63, 5000, 1 << 24):
+        for N in (0, 1, 777, 130000, (1 << 31) - 65536):
+            for K in (0, 1, 8, 4096, 4097, (1 << 22) - 8):
+                for f in (fwd, bwd):
+                    assert 0 <= f(M, N, K, True) <= f(M, N, K) and (K % 8 == 0 or f(M, N, K, True) == f(M, N, K))
+    for bad in ((-1, 2, 8), (1, 1 << 31, 8), (1, 2, 1 << 22), (1, 2, -8)):
+        for f in (fwd, bwd):
+            with pytest.raises(ValueError):
+                f(*bad, True)
+    for call, size in ((forward, fwd(8, 32, 64, True)), (backward, bwd(8, 32, 64, True))):
+        assert call(nws=size - 1) == SPACE
+        for kw in (dict(w=W + 2), dict(ldw=65), dict(ldw=(1 << 22) + 8), *((dict(x=X + 8), dict(ldx=68)) if call is forward else ())):
+            assert call(nws=size, **kw) == SPACE, kw
+        if not torch.cuda.is_available():
+            assert call(nws=size) == NODEV and call(nws=size, ldw=72, ldx=80) == NODEV
+            if call is backward:                       # x is gathered from any layout
+                assert call(nws=size, x=X + 2, ldx=65) == NODEV

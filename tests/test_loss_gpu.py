@@ -559,3 +559,33 @@ def test_calls_without_the_bindings_module(monkeypatch):
     want = calls()
     monkeypatch.setattr(la, "_marshal", lambda: la._NoMarshal)
     assert all(torch.equal(u, v) for u, v in zip(calls(), want))
+
+
+@pytest.mark.parametrize("t", TYPES, ids=IDS)
+@pytest.mark.parametrize("M,N,K", [(1, 8200, 4096), (20, 4099, 520), (300, 1030, 96), (1024, 1024, 768), (2100, 1032, 520), (20000, 8300, 64)])
+def test_workspaces_of_the_size_that_calls_in_place_need(M, N, K, t):
+    """The same bits as with a larger workspace, and nothing written past its end."""
+    x, w, target, b, dloss, dlse = make(M, N, K, t)
+    loss, lse = fn("", t)(x, w, target, b, workspace=torch.empty(la.cross_entropy_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV))
+    full = torch.empty(la.cross_entropy_backward_workspace_bytes(M, N, K), dtype=torch.uint8, device=DEV)
+    want = fn("_backward", t)(dloss, x, w, target, lse, b, dlse=dlse, workspace=full)
+    tight = la.cross_entropy_workspace_bytes(M, N, K, True)
+    ws = torch.full((tight + 4096,), 77, dtype=torch.uint8, device=DEV)
+    got = fn("", t)(x, w, target, b, workspace=ws[:tight])
+    assert torch.equal(got[0], loss) and torch.equal(got[1], lse) and bool((ws[tight:] == 77).all())
+    tight = la.cross_entropy_backward_workspace_bytes(M, N, K, True)
+    ws = torch.full((tight + 4096,), 77, dtype=torch.uint8, device=DEV)
+    for gx in (x, padded(x, 3, 1, float("nan"))[0]):   # x is gathered from any layout
+        got = fn("_backward", t)(dloss, gx, w, target, lse, b, dlse=dlse, workspace=ws[:tight])
+        assert all(torch.equal(u, v) for u, v in zip(got, want)) and bool((ws[tight:] == 77).all())
+
+
+def test_a_call_in_place_takes_no_room_for_copies():
+    t = torch.bfloat16
+    x, w, target, b, dloss, dlse = make(4, 40000, 1024, t)
+    torch.cuda.synchronize()
+    for call in (lambda: fn("", t)(x, w, target, b), lambda: fn("", t)(x, w, target, b, loss=torch.empty(4, device=DEV))):
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        call()
+        assert torch.cuda.max_memory_allocated() - before < 8 << 20
