@@ -75,10 +75,10 @@ enum : int { kOutBias = 0, kOutRound = 1, kOutF32 = 2, kOutEpi = 3, kOutGated = 
 // Cache policy of buffer stores past the caches: non-temporal, of device scope (bits nt and sc1).
 constexpr int kPastCaches = 2 | 16;
 
-// Whether an output's rows begin at cache lines: stores past the caches of rows that do not leave
+// Whether rows of 16-bit words begin at cache lines: stores past the caches of rows that do not leave
 // parts of lines to the memory.
-inline bool whole_lines(const void* p, int64_t ld, int word) {
-    return (uintptr_t)p % 128 == 0 && ld * word % 128 == 0;
+inline bool whole_lines(const void* p, int64_t ld) {
+    return (uintptr_t)p % 128 == 0 && ld % 64 == 0;
 }
 
 // Grouped contraction: group g is the activation slice x + g * gsx, the weight

@@ -22,11 +22,13 @@
 
 namespace lin {
 
-// The stores go past the caches: y is larger than those or is read by nobody soon, and the weight
+// Words are stored past the caches: y is larger than those or is read by nobody soon, and the weight
 // that the next call reads stays in them (backward without dx, 64 x 128259 x 4096 bf16: 520 us with
-// plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).  Rows
-// that end inside a cache line keep plain stores, which the caches put together (loss
-// and gradients of 20 x 32000 x 4104 373 -> 253 us, of 2 x 11771 x 2248 90 -> 65).
+// plain stores, 508 with the bit nt alone, 417 with nt and sc1; 20 x 32000 x 4096: 133, 122, 96).  Stores that do
+// not fill parts of lines at once keep to the caches, which put them together: rows that end inside a
+// cache line (loss and gradients of 20 x 32000 x 4104 373 -> 253 us, of 2 x 11771 x 2248 90 -> 65), and
+// floats, 16 of whose bytes a lane stores at a time, 32 apart (backward without dx, FP32 dW: 20 x 32000 x 4096 491
+// us past the caches, 197; 128 x 32000 x 4096 497, 226; on the 64-row tiles 212 and 247).
 constexpr int kOuterCols = 256, kOuterRows = 64, kOuterStages = 4;
 
 // KS: K steps of 32 contraction indices, 2, 4 or 8; POLICY: the stores' cache policy.
@@ -146,8 +148,8 @@ __global__ void __launch_bounds__(256) outer_stream(StreamProduct a) {
 
 template <int KS, int E>
 static const void* outer_fn(bool words, bool past) {
-    if (words) return past ? (const void*)outer_stream<KS, E, kOutRound, kPastCaches> : (const void*)outer_stream<KS, E, kOutRound, 0>;
-    return past ? (const void*)outer_stream<KS, E, kOutF32, kPastCaches> : (const void*)outer_stream<KS, E, kOutF32, 0>;
+    if (!words) return (const void*)outer_stream<KS, E, kOutF32, 0>;
+    return past ? (const void*)outer_stream<KS, E, kOutRound, kPastCaches> : (const void*)outer_stream<KS, E, kOutRound, 0>;
 }
 
 // mode kOutRound or kOutF32.
@@ -162,7 +164,7 @@ hipError_t launch_outer_t(int mode, const StreamProduct& a, hipStream_t stream) 
     int64_t used = blocks < shares ? blocks : shares;
     if (a.L > 128 && used >> a.xcd_shift) used = used >> a.xcd_shift << a.xcd_shift;
     void* params[] = {&args};
-    const bool words = mode == kOutRound, past = whole_lines(a.y[0], a.ldy[0], words ? 2 : 4);
+    const bool words = mode == kOutRound, past = words && whole_lines(a.y[0], a.ldy[0]);
     const void* fn = a.L <= 64    ? outer_fn<2, E>(words, past)
                      : a.L <= 128 ? outer_fn<4, E>(words, past)
                                   : outer_fn<8, E>(words, past);
