@@ -574,8 +574,10 @@ int32_t linear_bf16_cross_entropy(const uint16_t* x, int64_t ldx,
  * d = 0 and dlse = 0 take no part (and no time): their dx is +0, whatever their x and lse are.
  *
  * dx, dw and db may each be NULL (not wanted), not all three unless they are empty.  N == 0
- * gives dx = +0, M == 0 gives dw = db = +0.  The _f32out forms store dw and db as floats
- * (unrounded sums), or with accumulate != 0 add them to what dw and db hold.
+ * gives dx = +0, M == 0 gives dw = db = +0.  The _f32out forms store dw and db as floats (the
+ * sums without a rounding of their own; dz is rounded all the same, so they are those of
+ * linear_bf16_backward_weight_f32out on a dy of words: each product is off by up to
+ * 2^-8 of itself, 2^-11 in binary16), or with accumulate != 0 add them to what dw and db hold.
  *
  * workspace: linear_cross_entropy_backward_workspace_bytes(M, N, K) bytes, as above; .._aligned
  * bytes are enough where the weight is as described there.

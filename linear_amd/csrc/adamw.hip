@@ -240,7 +240,9 @@ __device__ inline uint2 encode8(const double (&v)[RUN], const float (&f)[RUN], u
     return c;
 }
 
-// A step's factors, the same on every thread.  What the host knows it has computed.
+// A step's factors, the same on every thread.  What the host knows it has computed; a step or rate in
+// device memory costs every thread two powers in FP64 (486 M bf16 values, device lr and step: 32-bit moments
+// 1967 -> 1977 us, 8-bit ones, whose step is bound by its instructions, 922 -> 1171).
 struct Factors {
     double scale;                    // of the gradients
     float keep, rate, root;          // 1 - lr weight_decay, lr / bias1, 1 / sqrt(bias2)

@@ -26,7 +26,9 @@ bool loss_dims_ok(int64_t M, int64_t N, int64_t K) {
 }
 
 // kLossConfigs' times, near those measured and set so that the choice is the fastest of the five tiles, or
-// close to it, at M from 1 to 2000, N from 8000 to 128259, K of 768 and 4096.
+// close to it, at M from 1 to 2000, N from 8000 to 128259, K of 768 and 4096.  Measured beside those, with every
+// tile (bf16 loss; M of 1, 16, 48, 100, 200, 400, 700, 1500, N of 16000 and 50000, K of 384, 1536, 2048, 2560, 6144):
+// 76 of the 80 within 4% of the fastest, the others 6 to 14% (700 x 16000 x 6144 172 us, 151 on 256 x 256).
 constexpr TileTime kLossTimes[kNumLossConfigs] = {{6.5, 1.60, 1}, {5.3, 0.80, 1}, {4.9, 0.50, 1}, {2.0, 0.42, 2}, {2.0, 0.30, 3}};
 
 // The tile of a product of M rows and N columns (by sizes alone: workspaces depend on it).
