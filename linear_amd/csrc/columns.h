@@ -5,9 +5,10 @@
 
 namespace lin {
 
-template <int E>
+// COUNTED: of the first *c.rows rows, times *c.unscale.
+template <int E, bool COUNTED>
 __device__ inline void store_sum(const ColumnSumArgs& c, int n, float sum) {
-    if (c.unscale) sum *= *c.unscale;
+    if constexpr (COUNTED) sum *= *c.unscale;
     if (c.f32) {
         float* y = (float*)c.db + n;
         *y = c.accumulate ? *y + sum : sum;
@@ -23,14 +24,14 @@ constexpr int column_lds(int threads) { return threads / 8 * 65 + threads; }
 // columns 8 (t % 8) of every (NT / 8)-th row from t / 8, four rows' loads in flight;
 // then NT / 64 threads per column add 8 row groups each, and one adds theirs.  A
 // fixed order.  A single split stores db itself.
-template <int E, int NT>
+template <int E, int NT, bool COUNTED>
 __device__ inline void column_block(const ColumnSumArgs& c, int block, int split, float* lds) {
     constexpr int G = NT / 8, H = NT / 64;            // row groups, threads per column
     float* part = lds;                                // [G][65]
     float* part2 = lds + G * 65;                      // [H][64]
     const int tid = threadIdx.x, c8 = (tid & 7) * 8, g = tid >> 3;
     const int n = block * 64 + c8;
-    const int M = c.rows ? *c.rows : c.M;
+    const int M = COUNTED ? *c.rows : c.M;
     const int m0 = (int)((int64_t)M * split / c.splits), m1 = (int)((int64_t)M * (split + 1) / c.splits);
     float sum[8] = {};
     for (int64_t m = m0 + g; m < m1; m += 4 * G) {
@@ -56,7 +57,7 @@ __device__ inline void column_block(const ColumnSumArgs& c, int block, int split
     t = part2[tid];
 #pragma unroll
     for (int i = 1; i < H; ++i) t += part2[i * 64 + tid];
-    if (c.splits == 1) store_sum<E>(c, out, t);
+    if (c.splits == 1) store_sum<E, COUNTED>(c, out, t);
     else c.partial[(int64_t)split * c.N + out] = t;
 }
 

@@ -84,10 +84,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t slice_rsrc(const uint16_t* p, 
 // and add their sums in LDS at the end: a small tile's slice is bound by the latency of
 // its reads, so several in flight cost one's time (no traffic, unlike a split over
 // workgroups).  The sets run the same number of slices, empty ones at the end.
+//
+// COUNTED: the row operand's rows (or the contraction) are as many as a.rows says.  Instances of their
+// own: asking for it at run time cost the other calls 0.1 to 0.3 us (81 x 136 x 608 f16 gradients 8.25
+// -> 8.12 us, 7 x 11232 x 288 20.9 -> 20.6).
 template <int BM, int BN, int KG, int STAGES>
 constexpr int grad_lds = KG * STAGES * 64 * (BM + BN) * 2;   // bytes of the rings
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE, bool COUNTED>
 __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, unsigned char* smem) {
     constexpr int BK = 64, RB = 16, KS = 2;            // slice, MFMA block, K steps of 32 per slice
     constexpr int NW = WM * WN;
@@ -111,20 +115,18 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         const int tiles = a.splits * a.groups * a.tiles_r * a.tiles_c;
         if (block >= tiles) {
             static_assert(column_lds(KG * NW * 64) * 4 <= KG * RING, "the column sums fit in the rings");
-            column_block<E, KG * NW * 64>(a.sums, block - tiles, 0, (float*)smem);
+            column_block<E, KG * NW * 64, COUNTED>(a.sums, block - tiles, 0, (float*)smem);
             return;
         }
     }
 
     int R = a.R, L = a.L, tiles_r = a.tiles_r;
-    if (a.rows) {                                     // uniform
-        if constexpr (ROWT) {
-            L = *a.rows;
-        } else {
-            R = *a.rows;
-            tiles_r = (R + BM - 1) / BM;
-            if (block >= a.splits * a.groups * tiles_r * a.tiles_c) return;
-        }
+    if constexpr (COUNTED && ROWT) {
+        L = *a.rows;
+    } else if constexpr (COUNTED) {
+        R = *a.rows;
+        tiles_r = (R + BM - 1) / BM;
+        if (block >= a.splits * a.groups * tiles_r * a.tiles_c) return;
     }
     int tr, tc;
     // row tiles of every group of every split, stacked into one grid
@@ -133,8 +135,11 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     const int split = stack / a.groups, group = stack - split * a.groups;
     const int r0 = (tr - stack * tiles_r) * BM, c0 = tc * BN;
     const uint16_t* rbase = a.r + group * a.rgroup;
+    constexpr bool UNSCALED = COUNTED || (E == kF16 && MODE != kOutF32Add);   // the calls that scale their row operand
     float back = 1.f;                                 // (read here: its latency passes under the loop)
-    if (a.unscale) back = *a.unscale;
+    if constexpr (UNSCALED) {
+        if (a.unscale) back = *a.unscale;
+    }
 
     const int lane = threadIdx.x & 63;
     const int set = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x / (NW * 64));
@@ -366,11 +371,13 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
         }
     }
 
-    if (a.unscale) {                                  // uniform
+    if constexpr (UNSCALED) {
+        if (a.unscale) {                              // uniform
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+            for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < FM; ++j) acc[i][j] *= back;
+                for (int j = 0; j < FM; ++j) acc[i][j] *= back;
+        }
     }
 
     LinearArgs o;
@@ -417,62 +424,81 @@ __device__ __forceinline__ void grad_tile(const StreamProduct& a, int block, uns
     }
 }
 
-template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE>
+template <int BM, int BN, int WM, int WN, int KG, int STAGES, bool ROWT, int E, int MODE, bool COUNTED>
 __global__ void __launch_bounds__(KG * WM * WN * 64)
 grad_stream(StreamProduct a) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[grad_lds<BM, BN, KG, STAGES>];
-    grad_tile<BM, BN, WM, WN, KG, STAGES, ROWT, E, MODE>(a, blockIdx.x, smem);
+    grad_tile<BM, BN, WM, WN, KG, STAGES, ROWT, E, MODE, COUNTED>(a, blockIdx.x, smem);
 }
 
 // Two products that do not depend on each other in one launch, the gated block's dx (on
 // 64 x 64 tiles of two sets, or 128 x 128) and dWg, dWu (128 x 128): where each alone
 // leaves CUs idle in its last round, the other's tiles fill them.  dx's tiles, the
 // longer ones, come first.
-template <bool SMALL, int E, int MODE>
+template <bool SMALL, int E, bool COUNTED>
 __global__ void __launch_bounds__(512) grad_pair(StreamProduct a, StreamProduct b) {
     __shared__ __attribute__((aligned(1024))) unsigned char smem[grad_lds<128, 128, 1, 4>];
     static_assert(grad_lds<64, 64, 2, 4> <= grad_lds<128, 128, 1, 4>, "one LDS block for both");
+    constexpr int MODE = COUNTED ? kOutList : kOutRound;
     const int tiles = a.tiles_r * a.tiles_c;
     if ((int)blockIdx.x < tiles) {
-        if constexpr (SMALL) grad_tile<64, 64, 2, 2, 2, 4, false, E, MODE>(a, blockIdx.x, smem);
-        else grad_tile<128, 128, 2, 4, 1, 4, false, E, MODE>(a, blockIdx.x, smem);
+        if constexpr (SMALL) grad_tile<64, 64, 2, 2, 2, 4, false, E, MODE, COUNTED>(a, blockIdx.x, smem);
+        else grad_tile<128, 128, 2, 4, 1, 4, false, E, MODE, COUNTED>(a, blockIdx.x, smem);
         return;
     }
-    const int block = blockIdx.x - tiles, rest = block - b.groups * b.tiles_r * b.tiles_c;
-    if (rest < 0) grad_tile<128, 128, 2, 4, 1, 4, true, E, kOutRound>(b, block, smem);
-    else column_block<E, 512>(b.sums, rest, 0, (float*)smem);
+    const int block = blockIdx.x - tiles;
+    if constexpr (COUNTED) {                          // the bias gradient's workgroups
+        const int rest = block - b.groups * b.tiles_r * b.tiles_c;
+        if (rest >= 0) {
+            column_block<E, 512, true>(b.sums, rest, 0, (float*)smem);
+            return;
+        }
+    }
+    grad_tile<128, 128, 2, 4, 1, 4, true, E, kOutRound, COUNTED>(b, block, smem);
 }
 
 static hipError_t launch_product(const void* fn, const StreamProduct& a, int threads, hipStream_t stream) {
+    if (!fn) return hipErrorInvalidValue;             // no call has this product
     StreamProduct args = a;
     void* params[] = {&args};
     return launch_kernel(fn, dim3((unsigned)(a.splits * a.groups * a.tiles_r * a.tiles_c + a.sum_blocks)), dim3(threads),
                            params, 0, stream);
 }
 
+// rowt, mode, counted: as train.h's launch_grad_stream says.
 template <int BM, int BN, int WM, int WN, int KG, int STAGES, int E>
-static const void* grad_fn(bool rowt, int mode) {
-    if (!rowt) {
-        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32>;
-        if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32Add>;
-        if (mode == kOutList) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutList>;
-        return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound>;
+static const void* grad_fn(bool rowt, int mode, bool counted) {
+    if (counted) {
+        if (!rowt) {
+            if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32, true>;
+            if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32Add, true>;
+            return mode == kOutList ? (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutList, true> : nullptr;
+        }
+        if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32, true>;
+        if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32Add, true>;
+        if (mode == kOutStream) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutStream, true>;
+        return mode == kOutRound ? (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutRound, true> : nullptr;
     }
-    if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32>;
-    if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32Add>;
-    if (mode == kOutStream) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutStream>;
-    return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutRound>;
+    if (!rowt) {
+        if constexpr (BM < 256 && STAGES > 2)         // partial sums (the tiles that split contractions take)
+            if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutF32, false>;
+        return mode == kOutRound ? (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, false, E, kOutRound, false> : nullptr;
+    }
+    if (mode == kOutF32) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32, false>;
+    if (mode == kOutF32Add) return (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutF32Add, false>;
+    return mode == kOutRound ? (const void*)grad_stream<BM, BN, WM, WN, KG, STAGES, true, E, kOutRound, false> : nullptr;
 }
 
 template <int E>
 hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream) {
+    const bool counted = a.rows != nullptr;
     switch (cfg) {
-        case 0: return launch_product(grad_fn<256, 256, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
-        case 1: return launch_product(grad_fn<256, 128, 4, 2, 1, 3, E>(rowt, mode), a, 512, stream);
-        case 2: return launch_product(grad_fn<128, 128, 2, 4, 1, 4, E>(rowt, mode), a, 512, stream);
-        case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 5, E>(rowt, mode), a, 256, stream);
-        case 4: return launch_product(grad_fn<64, 64, 2, 2, 2, 4, E>(rowt, mode), a, 512, stream);
-        case 5: return launch_product(grad_fn<128, 128, 2, 4, 1, 2, E>(rowt, mode), a, 512, stream);
+        case 0: return launch_product(grad_fn<256, 256, 2, 4, 1, 2, E>(rowt, mode, counted), a, 512, stream);
+        case 1: return launch_product(grad_fn<256, 128, 4, 2, 1, 3, E>(rowt, mode, counted), a, 512, stream);
+        case 2: return launch_product(grad_fn<128, 128, 2, 4, 1, 4, E>(rowt, mode, counted), a, 512, stream);
+        case 3: return launch_product(grad_fn<64, 64, 2, 2, 1, 5, E>(rowt, mode, counted), a, 256, stream);
+        case 4: return launch_product(grad_fn<64, 64, 2, 2, 2, 4, E>(rowt, mode, counted), a, 512, stream);
+        case 5: return launch_product(grad_fn<128, 128, 2, 4, 1, 2, E>(rowt, mode, counted), a, 512, stream);
         default: return hipErrorInvalidValue;
     }
 }
@@ -481,8 +507,8 @@ template <int E>
 hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream) {
     StreamProduct aa = a, bb = b;
     void* params[] = {&aa, &bb};
-    const void* fn = a.list ? (small ? (const void*)grad_pair<true, E, kOutList> : (const void*)grad_pair<false, E, kOutList>)
-                            : (small ? (const void*)grad_pair<true, E, kOutRound> : (const void*)grad_pair<false, E, kOutRound>);
+    const void* fn = a.rows ? (small ? (const void*)grad_pair<true, E, true> : (const void*)grad_pair<false, E, true>)
+                            : (small ? (const void*)grad_pair<true, E, false> : (const void*)grad_pair<false, E, false>);
     return launch_kernel(fn, dim3((unsigned)(a.tiles_r * a.tiles_c + b.groups * b.tiles_r * b.tiles_c + b.sum_blocks)), dim3(512),
                          params, 0, stream);
 }

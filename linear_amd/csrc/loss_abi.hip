@@ -335,7 +335,8 @@ int32_t run_loss_backward(int elem, bool f32, const float* dloss, const float* d
             sw.xcd_shift = di.xcd_shift;
             if ((st = launched(launch_outer(elem, f32 ? kOutF32 : kOutRound, sw, stream))) != LINEAR_OK) return st;
         } else if (want_dw) {
-            const int mode = !f32 ? (streamable(dw, lddw) && whole_lines(dw, lddw) ? kOutStream : kOutRound) : accumulate ? kOutF32Add : kOutF32;
+            const int mode = !f32 ? (any && streamable(dw, lddw) && whole_lines(dw, lddw) ? kOutStream : kOutRound)
+                                  : accumulate ? kOutF32Add : kOutF32;
             if ((st = launch_stream(elem, true, mode, sw, p.dw, di, partials, stream)) != LINEAR_OK) return st;
         }
     }

@@ -414,21 +414,21 @@ __global__ void __launch_bounds__(256) gated_grad(GatedGradArgs g) {
     }
 }
 
-template <int E>
+template <int E, bool COUNTED>
 __global__ void __launch_bounds__(1024) column_partials(ColumnSumArgs c) {
     __shared__ float lds[column_lds(1024)];
-    column_block<E, 1024>(c, blockIdx.x, blockIdx.y, lds);
+    column_block<E, 1024, COUNTED>(c, blockIdx.x, blockIdx.y, lds);
 }
 
 // The splits' sums, in their order.
-template <int E>
+template <int E, bool COUNTED>
 __global__ void __launch_bounds__(64) column_finish(ColumnSumArgs c) {
     const int n = blockIdx.x * 64 + threadIdx.x;
     if (n >= c.N) return;
     float sum = c.partial[n];
 #pragma unroll 8
     for (int s = 1; s < c.splits; ++s) sum += c.partial[(int64_t)s * c.N + n];
-    store_sum<E>(c, n, sum);
+    store_sum<E, COUNTED>(c, n, sum);
 }
 
 template <int T, int E>
@@ -507,11 +507,17 @@ hipError_t launch_column_sum(int elem, const ColumnSumArgs& c, hipStream_t strea
         return hipSuccess;
     }
     const unsigned gx = (unsigned)((c.N + 63) / 64);
-    hipError_t e = launch_kernel(elem == kBF16 ? (const void*)column_partials<kBF16> : (const void*)column_partials<kF16>,
-                                   dim3(gx, (unsigned)c.splits), dim3(1024), params, 0, stream);
+    const void *sums, *finish;
+    if (c.rows) {
+        sums = elem == kBF16 ? (const void*)column_partials<kBF16, true> : (const void*)column_partials<kF16, true>;
+        finish = elem == kBF16 ? (const void*)column_finish<kBF16, true> : (const void*)column_finish<kF16, true>;
+    } else {
+        sums = elem == kBF16 ? (const void*)column_partials<kBF16, false> : (const void*)column_partials<kF16, false>;
+        finish = elem == kBF16 ? (const void*)column_finish<kBF16, false> : (const void*)column_finish<kF16, false>;
+    }
+    hipError_t e = launch_kernel(sums, dim3(gx, (unsigned)c.splits), dim3(1024), params, 0, stream);
     if (e != hipSuccess || c.splits == 1) return e;
-    return launch_kernel(elem == kBF16 ? (const void*)column_finish<kBF16> : (const void*)column_finish<kF16>,
-                           dim3(gx), dim3(64), params, 0, stream);
+    return launch_kernel(finish, dim3(gx), dim3(64), params, 0, stream);
 }
 
 }  // namespace lin

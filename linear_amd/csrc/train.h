@@ -52,8 +52,8 @@ struct ColumnSumArgs {
     void* db;                // 16-bit words or floats
     int M, N, splits;
     int f32, accumulate;
-    const float* unscale;    // not null: the sums are multiplied by *unscale
-    const int32_t* rows;     // not null: the rows are *rows, at most M
+    const int32_t* rows;     // not null: the rows are *rows, at most M, and
+    const float* unscale;    // the sums are multiplied by *unscale
 };
 // Splits of the rows: enough workgroups of 64 columns for every CU, of 2048 rows at
 // least; one where the columns alone give half the chip work (a second launch costs
@@ -120,8 +120,8 @@ inline constexpr GradConfig kGradConfigs[kNumGradConfigs] = {
     {64, 64, 2, 2, 2, 4},
     {128, 128, 2, 4, 1, 2},
 };
-// rowt: contraction-major row operand; mode kOutRound, kOutF32, kOutF32Add or, without rowt, kOutList,
-// with it kOutStream.
+// rowt: contraction-major row operand; mode kOutRound, kOutF32 or, with rowt, kOutF32Add.  With a.rows: without
+// rowt kOutList (not kOutRound), kOutF32 or kOutF32Add, with it kOutStream too.
 template <int E> hipError_t launch_grad_stream_t(int cfg, bool rowt, int mode, const StreamProduct& a, hipStream_t stream);
 extern template hipError_t launch_grad_stream_t<kF16>(int, bool, int, const StreamProduct&, hipStream_t);
 extern template hipError_t launch_grad_stream_t<kBF16>(int, bool, int, const StreamProduct&, hipStream_t);
@@ -131,8 +131,8 @@ inline hipError_t launch_grad_stream(int elem, int cfg, bool rowt, int mode, con
 }
 
 // Two unsplit products in one launch: a (rowt false) on kGradConfigs[kPairSmall] or, not
-// small, [kPairTile], then b (rowt true) on [kPairTile]; both rounded, a's rows placed by its
-// list where it has one.  b.sum_blocks as for one product.
+// small, [kPairTile], then b (rowt true) on [kPairTile]; both rounded.  Both with rows or neither: with
+// them a's rows are placed by its list, and b.sum_blocks is as for one product.
 constexpr int kPairSmall = 4, kPairTile = 2;
 template <int E> hipError_t launch_grad_pair_t(bool small, const StreamProduct& a, const StreamProduct& b, hipStream_t stream);
 extern template hipError_t launch_grad_pair_t<kF16>(bool, const StreamProduct&, const StreamProduct&, hipStream_t);
