@@ -592,9 +592,11 @@ def _launch_stream(stream, *tensors):
     """_stream_handle's checks for tensors on one device and the current stream, the usual
     call, at less host time; anything else goes through it."""
     if stream is None:
-        stream_of = _current_stream({t.get_device() for t in tensors if t is not None})
-        if stream_of is not None:
-            return stream_of
+        devices = {t.get_device() for t in tensors if t is not None}    # -1 on the host
+        if len(devices) == 1:
+            index = devices.pop()
+            if index >= 0 and index == torch._C._cuda_getDevice():
+                return torch._C._cuda_getCurrentRawStream(index)
     return _stream_handle(stream, *tensors)
 
 
